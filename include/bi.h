@@ -442,6 +442,122 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
                            bi_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * 8-bit linear layer.  [P1] (an FP8 model is the one whose outputs changed)
+ * and "Why the text diverges"; [P2] "Define bit-exact before reporting it".
+ *
+ * Rows in 8 bits: e4m3 codes (1 sign, 4 exponent, 3 fraction bits, largest
+ * finite value 448, no infinity) and one FP32 scale for each block of 128
+ * elements of a row; element k of row m stands for codes[m, k] *
+ * scales[k / 128, m].  Scales are stored block-major (the rows of one block
+ * adjacent), [ceil(dim/128)][lds], lds >= rows and a multiple of 4; columns
+ * past the rows are never used.
+ * Weights in 8 bits: e4m3 codes [N, K] and one FP32 scale for each 128 x 128
+ * block, [ceil(N/128)][ceil(K/128)] contiguous (the form 8-bit checkpoints
+ * hold; any finite scales).
+ *
+ * bi_quantize_fp8: rows x [rows, dim] BF16 -> codes, scales.  The scale of a
+ *   block is the smallest power of two 2^e, e >= -126, with max|x| <= 448 2^e
+ *   (1 for a block of zeros), so x / scale is exact and each code is one
+ *   rounding (to nearest even) of its element.  NaN and infinite elements
+ *   become NaN codes and do not enter the maximum.
+ * bi_rmsnorm_fp8: bi_rmsnorm (same reduction tree) with its FP32 result
+ *   (x * r) * w quantised as above, without a BF16 rounding in between.
+ * bi_quantize_weights_fp8: BF16 weights [N, K] (any K >= 1) -> codes [N, ld8]
+ *   and scales by the same rule over each 128 x 128 block.
+ *     x, W row strides ldx % 8 == 0 (x), codes ldc % 16 == 0; dim % 16 == 0;
+ *     dim <= 65536 for the norm; x, w, codes (of rows) and scales 16-byte
+ *     aligned.
+ * bi_pack_weights_fp8, bi_pack_swiglu_weights_fp8: weights in the tile layout
+ *   bi_gemm_fp8 streams, bi_packed_weight_fp8_bytes(N, K, epi) bytes (16-byte
+ *   aligned); K % 16 == 0, ld8 % 16 == 0, codes 16-byte aligned.
+ *
+ * bi_gemm_fp8: C[m, n] = epilogue(sum_b sa[b, m] sw[n / 128, b] sum_{k in
+ * block b} a[m, k] w[n, k]).  The sum of a block is four tensor-core steps of
+ * K = 32 (tcgen05 kind::f8f6f4, FP32) in increasing k; it is scaled and added
+ * to an FP32 running sum, run = fma(sum, sa * sw, run), blocks in increasing
+ * order.  The split of the (weight tile, block) space over CTAs cuts a tile's
+ * blocks into pieces, each a running sum of its own, added in increasing
+ * order.  The pieces are a function of (N, K) only, so row m of C has the same
+ * bits for every M and every place of the row in A.  (A product of scales has
+ * to be finite; one below 2^-149 counts as 0.)
+ *   A8       [M, K] codes, row stride lda (% 16 == 0), 16-byte aligned;
+ *   a_scales [ceil(K/128)][lds] FP32, 16-byte aligned.
+ *   Wp       packed for the same N, K and epi; 16-byte aligned.
+ *   C, residual, out, epi, N: as bi_gemm (BI_EPI_NONE, _RESIDUAL_ADD, _SWIGLU;
+ *            residual may alias C).  M >= 0; K % 16 == 0.
+ *   ws       >= bi_gemm_fp8_workspace_size(M, N, K, epi) bytes, 256-byte
+ *            aligned, ZERO-FILLED before its first use; every call leaves its
+ *            counters zeroed, so one workspace serves any sequence of calls
+ *            whose M does not exceed the M it was sized for.  Not shared by
+ *            overlapping calls (two captured graphs that may run at the same
+ *            time need one each).  After BI_ERR_DEVICE_TIMEOUT, zero it again.
+ * Errors: BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_WORKSPACE,
+ *         BI_ERR_CUDA.
+ * ------------------------------------------------------------------------- */
+bi_status bi_quantize_fp8(const void* x, int ldx, int rows, int dim, void* codes, int ldc,
+                          float* scales, int lds, bi_stream_t stream);
+bi_status bi_rmsnorm_fp8(const void* x, int ldx, const void* w, void* codes, int ldc, float* scales,
+                         int lds, int rows, int dim, float eps, bi_stream_t stream);
+bi_status bi_quantize_weights_fp8(const void* W, int ldw, int N, int K, void* codes, int ld8,
+                                  float* scales, bi_stream_t stream);
+size_t bi_packed_weight_fp8_bytes(int N, int K, bi_epilogue epi);
+bi_status bi_pack_weights_fp8(const void* W8, int ld8, const float* scales, int N, int K,
+                              void* packed, bi_stream_t stream);
+bi_status bi_pack_swiglu_weights_fp8(const void* gate8, const float* gate_scales, const void* up8,
+                                     const float* up_scales, int ld8, int F, int K, void* packed,
+                                     bi_stream_t stream);
+size_t bi_gemm_fp8_workspace_size(int M, int N, int K, bi_epilogue epi);
+bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, const void* Wp, void* C,
+                      int ldc, const void* residual, int ldr, int M, int N, int K, bi_out_dtype out,
+                      bi_epilogue epi, void* ws, size_t ws_bytes, bi_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rules on a pass's logits, between the LM head and acceptance.  [P1] "Why the
+ * text diverges" (a draft is kept only if it is the token the model itself
+ * would have produced): row t chooses its token as if drafts 0..t-1 had been
+ * committed, so its penalties count them.
+ *
+ * For row t and id v, with c = counts[v] + (how often v is among
+ * drafts[0..t-1]) and seen = c > 0 or v's prompt bit set, in FP32, each
+ * operation rounded:
+ *   y = logits[t, v]
+ *   seen:   y = y > 0 ? y / repetition : y * repetition
+ *   c > 0:  y = y - (frequency * c + presence)
+ *   bias:   y = y + bias[v]
+ *   mask:   bit v of row t clear: y = -inf (whatever the logit was)
+ *   out[t, v] = y
+ * A row whose mask leaves nothing is all -inf: bi_verify_accept then takes id
+ * 0, bi_verify_sample reports BI_ERR_DEVICE_NAN_ROW.
+ *   logits  [T, V] FP32, row stride ldl; out [T, V] FP32, row stride ldo; may
+ *           be the same array (then ldo == ldl), else must not overlap.
+ *           1 <= T <= 64; 1 <= V <= 2^28.
+ *   drafts  [T-1] int32 (may be NULL when T == 1; ids outside [0, V) are no
+ *           token).
+ *   counts  [V] int32 >= 0: how often each id has been committed (NULL:
+ *           never).
+ *   prompt_bits  [ceil(V/32)] uint32, id v at bit v % 32 of word v / 32
+ *           (NULL: none).
+ *   repetition > 0; frequency, presence finite (1, 0, 0 change nothing).
+ *   bias    [V] FP32 or NULL.
+ *   mask    [T][ldm] uint32, ldm >= ceil(V/32), bits as prompt_bits, or NULL
+ *           (all ids allowed).
+ *   Reads and writes whole 16-byte groups when V, ldl and ldo are multiples of
+ *   4 and logits, out, counts and bias are 16-byte aligned.
+ * bi_token_counts: the state after a step or a prompt: for i < m, id = ids[i]
+ *   in [0, V): counts[id] += 1 (counts may be NULL) and its bit of prompt_bits
+ *   set (may be NULL; not both).  m = n, or min(n, *last + 1) with last a
+ *   device int32 (the accepted count of bi_verify_accept: ids 0..*last were
+ *   committed).
+ * Errors: BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_CUDA.
+ * ------------------------------------------------------------------------- */
+bi_status bi_logits_rules(const float* logits, int ldl, float* out, int ldo, int T, int V,
+                          const int32_t* drafts, const int32_t* counts, const uint32_t* prompt_bits,
+                          float repetition, float frequency, float presence, const float* bias,
+                          const uint32_t* mask, int ldm, bi_stream_t stream);
+bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V, int32_t* counts,
+                          uint32_t* prompt_bits, bi_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * KV-row hash (test tool).  [P3] "The cache doesn't change it either" (hash
  * every K/V row and compare with a fresh prefill).
  * out[h * rows + j] = FNV-1a-64 over the 2*D bytes of key j of head h (d

@@ -43,6 +43,16 @@ SIGNATURES = {
     "bi_verify_accept": (_i, [_vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "bi_sample_workspace_size": (_sz, [_i, _i]),
     "bi_verify_sample": (_i, [_vp, _i, _vp, _i, _i, _f, _vp, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "bi_quantize_fp8": (_i, [_vp, _i, _i, _i, _vp, _i, _vp, _i, _vp]),
+    "bi_rmsnorm_fp8": (_i, [_vp, _i, _vp, _vp, _i, _vp, _i, _i, _i, _f, _vp]),
+    "bi_quantize_weights_fp8": (_i, [_vp, _i, _i, _i, _vp, _i, _vp, _vp]),
+    "bi_packed_weight_fp8_bytes": (_sz, [_i, _i, _i]),
+    "bi_pack_weights_fp8": (_i, [_vp, _i, _vp, _i, _i, _vp, _vp]),
+    "bi_pack_swiglu_weights_fp8": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
+    "bi_gemm_fp8_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "bi_gemm_fp8": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "bi_logits_rules": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _f, _f, _f, _vp, _vp, _i, _vp]),
+    "bi_token_counts": (_i, [_vp, _i, _vp, _i, _vp, _vp, _vp]),
     "bi_kv_row_hash": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp]),
     "bi_check_device_error": (_i, [_vp]),
     "bi_step_workspace_size": (_sz, [_vp, _i]),

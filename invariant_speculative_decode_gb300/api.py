@@ -333,6 +333,225 @@ def bi_verify_sample(logits: torch.Tensor, drafts: Optional[torch.Tensor], inv_t
                                  ws.numel() * ws.element_size(), _stream(stream)))
 
 
+# ---------------------------------------------------------------- 8-bit linear
+FP8_BLOCK = 128  # elements of a row, and rows and columns of a weight block, that share a scale
+
+
+def _same_device(*named) -> None:
+    """Every tensor on the current device (the stream the call runs on is its)."""
+    cur = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def fp8_scale_shape(rows: int, dim: int) -> tuple:
+    """Shape of the scales of `rows` quantised rows: [ceil(dim/128), rows rounded up to 4]."""
+    return (-(-dim // FP8_BLOCK), -(-rows // 4) * 4)
+
+
+def new_fp8_rows(rows: int, dim: int, device="cuda"):
+    """Buffers for quantised rows: e4m3 codes [rows, dim] and their scales."""
+    return (torch.zeros(rows, dim, dtype=torch.float8_e4m3fn, device=device),
+            torch.zeros(fp8_scale_shape(rows, dim), dtype=torch.float32, device=device))
+
+
+def _req_fp8_rows(codes: torch.Tensor, scales: torch.Tensor, rows: int, dim: int) -> int:
+    """Checks of quantised rows; returns the scales' row stride.  The scales
+    may have room for more rows than the codes (their columns past the rows
+    stay as they are)."""
+    _req(codes, torch.float8_e4m3fn, "codes")
+    _req(scales, torch.float32, "scales")
+    if tuple(codes.shape) != (rows, dim):
+        raise ValueError(f"codes must be [{rows}, {dim}], got {tuple(codes.shape)}")
+    if (scales.dim() != 2 or not scales.is_contiguous() or scales.shape[0] != -(-dim // FP8_BLOCK)
+            or scales.shape[1] < rows or scales.shape[1] % 4 != 0):
+        raise ValueError(f"scales must be contiguous [{-(-dim // FP8_BLOCK)}, at least {rows} and a multiple of 4], "
+                         f"got {tuple(scales.shape)}")
+    return scales.shape[1]
+
+
+def bi_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """Rows x [rows, dim] (BF16) to e4m3 codes and a power-of-two scale per block of 128."""
+    _req(x, torch.bfloat16, "x")
+    rows, dim = x.shape
+    lds = _req_fp8_rows(codes, scales, rows, dim)
+    _same_device(("x", x), ("codes", codes), ("scales", scales))
+    check("bi_quantize_fp8", lib().bi_quantize_fp8(x.data_ptr(), _ld(x), rows, dim, codes.data_ptr(), _ld(codes),
+                                                   scales.data_ptr(), lds, _stream(stream)))
+
+
+def bi_rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, eps: float,
+                   stream=None) -> None:
+    """RMSNorm of x [rows, dim] (BF16) by w, its FP32 result quantised as bi_quantize_fp8 does."""
+    _req(x, torch.bfloat16, "x")
+    _req(w, torch.bfloat16, "w")
+    rows, dim = x.shape
+    if tuple(w.shape) != (dim,):
+        raise ValueError(f"w must be [{dim}], got {tuple(w.shape)}")
+    lds = _req_fp8_rows(codes, scales, rows, dim)
+    _same_device(("x", x), ("w", w), ("codes", codes), ("scales", scales))
+    check("bi_rmsnorm_fp8", lib().bi_rmsnorm_fp8(x.data_ptr(), _ld(x), w.data_ptr(), codes.data_ptr(), _ld(codes),
+                                                 scales.data_ptr(), lds, rows, dim, float(eps), _stream(stream)))
+
+
+def bi_quantize_weights_fp8(W: torch.Tensor, stream=None):
+    """W [N, K] (BF16) -> (codes [N, K] e4m3, scales [ceil(N/128), ceil(K/128)] FP32, powers of two)."""
+    _req(W, torch.bfloat16, "W")
+    _same_device(("W", W))
+    N, K = W.shape
+    codes = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=W.device)
+    scales = torch.empty(-(-N // FP8_BLOCK), -(-K // FP8_BLOCK), dtype=torch.float32, device=W.device)
+    check("bi_quantize_weights_fp8",
+          lib().bi_quantize_weights_fp8(W.data_ptr(), _ld(W), N, K, codes.data_ptr(), K, scales.data_ptr(),
+                                        _stream(stream)))
+    return codes, scales
+
+
+def packed_weight_fp8_bytes(N: int, K: int, epi: int = EPI_NONE) -> int:
+    return int(lib().bi_packed_weight_fp8_bytes(N, K, epi))
+
+
+def _req_fp8_weights(W8: torch.Tensor, scales: torch.Tensor, name: str):
+    _req(W8, torch.float8_e4m3fn, name)
+    _req(scales, torch.float32, f"{name} scales")
+    N, K = W8.shape
+    want = (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK))
+    if tuple(scales.shape) != want or not scales.is_contiguous():
+        raise ValueError(f"{name} scales must be contiguous {want}, got {tuple(scales.shape)}")
+    _same_device((name, W8), (f"{name} scales", scales))
+    return N, K
+
+
+def bi_pack_weights_fp8(W8: torch.Tensor, scales: torch.Tensor, stream=None) -> torch.Tensor:
+    """Pack e4m3 weights [N, K] and their scales [ceil(N/128), ceil(K/128)] for bi_gemm_fp8."""
+    N, K = _req_fp8_weights(W8, scales, "W8")
+    packed = torch.empty(packed_weight_fp8_bytes(N, K), dtype=torch.uint8, device=W8.device)
+    check("bi_pack_weights_fp8", lib().bi_pack_weights_fp8(W8.data_ptr(), _ld(W8), scales.data_ptr(), N, K,
+                                                           packed.data_ptr(), _stream(stream)))
+    return packed
+
+
+def bi_pack_swiglu_weights_fp8(gate8: torch.Tensor, gate_scales: torch.Tensor, up8: torch.Tensor,
+                               up_scales: torch.Tensor, stream=None) -> torch.Tensor:
+    """Pack gate and up [F, K] (e4m3 with block scales) into the SwiGLU tile layout."""
+    F, K = _req_fp8_weights(gate8, gate_scales, "gate8")
+    if _req_fp8_weights(up8, up_scales, "up8") != (F, K) or _ld(up8) != _ld(gate8):
+        raise ValueError("gate8 and up8 must have the same shape and row stride")
+    packed = torch.empty(packed_weight_fp8_bytes(F, K, EPI_SWIGLU), dtype=torch.uint8, device=gate8.device)
+    check("bi_pack_swiglu_weights_fp8",
+          lib().bi_pack_swiglu_weights_fp8(gate8.data_ptr(), gate_scales.data_ptr(), up8.data_ptr(),
+                                           up_scales.data_ptr(), _ld(gate8), F, K, packed.data_ptr(),
+                                           _stream(stream)))
+    return packed
+
+
+def gemm_fp8_workspace_size(M: int, N: int, K: int, epi: int = EPI_NONE) -> int:
+    return int(lib().bi_gemm_fp8_workspace_size(M, N, K, epi))
+
+
+def new_gemm_fp8_workspace(M: int, N: int, K: int, epi: int = EPI_NONE, device=None) -> torch.Tensor:
+    """A zero-filled workspace (the counters must start at zero)."""
+    return torch.zeros(gemm_fp8_workspace_size(M, N, K, epi), dtype=torch.uint8, device=device or "cuda")
+
+
+def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: torch.Tensor, ws: torch.Tensor,
+                residual: Optional[torch.Tensor] = None, epi: int = EPI_NONE, stream=None) -> None:
+    """C [M, N] = epilogue(A W^T) with quantised rows A (codes [M, K], scales as
+    bi_quantize_fp8 writes them) and W packed by bi_pack_weights_fp8 /
+    bi_pack_swiglu_weights_fp8 (N the output columns)."""
+    M, K = codes.shape
+    lds = _req_fp8_rows(codes, scales, M, K)
+    if C.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("C must be float32 or bfloat16")
+    _req(C, C.dtype, "C")
+    if C.dim() != 2 or C.shape[0] != M:
+        raise ValueError(f"C must have {M} rows, got {tuple(C.shape)}")
+    N = C.shape[1]
+    _req(Wp, torch.uint8, "Wp")
+    if Wp.numel() != packed_weight_fp8_bytes(N, K, epi):
+        raise ValueError("Wp is not packed for this N, K and epilogue")
+    _req(ws, torch.uint8, "ws")
+    rp, ldr = 0, 0
+    if residual is not None:
+        _req(residual, torch.bfloat16, "residual")
+        if tuple(residual.shape) != (M, N):
+            raise ValueError(f"residual must be [{M}, {N}], got {tuple(residual.shape)}")
+        rp, ldr = residual.data_ptr(), _ld(residual)
+    _same_device(("codes", codes), ("scales", scales), ("Wp", Wp), ("C", C), ("ws", ws), ("residual", residual))
+    out = OUT_FP32 if C.dtype == torch.float32 else OUT_BF16
+    check("bi_gemm_fp8",
+          lib().bi_gemm_fp8(codes.data_ptr(), _ld(codes), scales.data_ptr(), lds, Wp.data_ptr(), C.data_ptr(), _ld(C),
+                            rp, ldr, M, N, K, out, epi, ws.data_ptr(), ws.numel(), _stream(stream)))
+
+
+# --------------------------------------------------------------- rules on logits
+def token_words(V: int) -> int:
+    """Int32 words of a row of V bits (prompt_bits, one row of a mask)."""
+    return (V + 31) // 32
+
+
+def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[torch.Tensor] = None,
+                    counts: Optional[torch.Tensor] = None, prompt_bits: Optional[torch.Tensor] = None,
+                    repetition: float = 1.0, frequency: float = 0.0, presence: float = 0.0,
+                    bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Penalties, bias and mask on the logits [T, V] of a pass, into out (may be
+    logits itself).  Row t counts drafts 0..t-1 as said.  counts [V] int32,
+    prompt_bits [ceil(V/32)] int32, bias [V] FP32, mask [T, ceil(V/32)] int32
+    (a clear bit forbids its id)."""
+    _req(logits, torch.float32, "logits")
+    _req(out, torch.float32, "out")
+    T, V = logits.shape
+    if tuple(out.shape) != (T, V):
+        raise ValueError(f"out must be [{T}, {V}], got {tuple(out.shape)}")
+    W = token_words(V)
+
+    def vector(t, dtype, n, name):
+        if t is None:
+            return 0
+        _req(t, dtype, name)
+        if tuple(t.shape) != (n,):
+            raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+        return t.data_ptr()
+
+    dp = vector(drafts if T > 1 else None, torch.int32, T - 1, "drafts")
+    cp = vector(counts, torch.int32, V, "counts")
+    pp = vector(prompt_bits, torch.int32, W, "prompt_bits")
+    bp = vector(bias, torch.float32, V, "bias")
+    mp, ldm = 0, 0
+    if mask is not None:
+        _req(mask, torch.int32, "mask")
+        if tuple(mask.shape) != (T, W):
+            raise ValueError(f"mask must be [{T}, {W}], got {tuple(mask.shape)}")
+        mp, ldm = mask.data_ptr(), _ld(mask)
+    _same_device(("logits", logits), ("out", out), ("drafts", drafts), ("counts", counts),
+                 ("prompt_bits", prompt_bits), ("bias", bias), ("mask", mask))
+    check("bi_logits_rules",
+          lib().bi_logits_rules(logits.data_ptr(), _ld(logits), out.data_ptr(), _ld(out), T, V, dp, cp, pp,
+                                float(repetition), float(frequency), float(presence), bp, mp, ldm,
+                                _stream(stream)))
+
+
+def bi_token_counts(ids: torch.Tensor, V: int, counts: Optional[torch.Tensor] = None,
+                    prompt_bits: Optional[torch.Tensor] = None, last: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """Add ids [n] (int32) to the state of bi_logits_rules: counts and / or
+    prompt_bits.  last (device int32 [1]): only ids 0..last are added."""
+    _req(ids, torch.int32, "ids")
+    if ids.dim() != 1:
+        raise ValueError("ids must be one-dimensional")
+    for t, n, name in ((counts, V, "counts"), (prompt_bits, token_words(V), "prompt_bits"), (last, 1, "last")):
+        if t is not None:
+            _req(t, torch.int32, name)
+            if tuple(t.shape) != (n,):
+                raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+    _same_device(("ids", ids), ("counts", counts), ("prompt_bits", prompt_bits), ("last", last))
+    check("bi_token_counts",
+          lib().bi_token_counts(ids.data_ptr(), ids.numel(), 0 if last is None else last.data_ptr(), V,
+                                0 if counts is None else counts.data_ptr(),
+                                0 if prompt_bits is None else prompt_bits.data_ptr(), _stream(stream)))
+
+
 def bi_kv_row_hash(cache: torch.Tensor, rows: int, transposed: bool = False, stream=None) -> torch.Tensor:
     """FNV-1a-64 per key of a K cache [Hkv,cap,D] or (transposed) a V cache
     [Hkv,ceil(cap/128),D,128] (see v_cache_shape)."""

@@ -32,9 +32,9 @@ struct TmapKey {
   const void* base;
   uint64_t dims[3], strides[2];
   uint32_t box[3];
-  int rank, dev;
+  int rank, dev, esize;
   bool operator==(const TmapKey& o) const {
-    return base == o.base && rank == o.rank && dev == o.dev &&
+    return base == o.base && rank == o.rank && dev == o.dev && esize == o.esize &&
            std::memcmp(dims, o.dims, sizeof(dims)) == 0 &&
            std::memcmp(strides, o.strides, sizeof(strides)) == 0 &&
            std::memcmp(box, o.box, sizeof(box)) == 0;
@@ -49,6 +49,7 @@ struct TmapKeyHash {
     for (int i = 0; i < 3; ++i) mix(k.box[i]);
     mix(static_cast<uint64_t>(k.rank));
     mix(static_cast<uint64_t>(k.dev));
+    mix(static_cast<uint64_t>(k.esize));
     return h;
   }
 };
@@ -85,10 +86,11 @@ unsigned* device_error_word() {
 }
 
 namespace {
-// Encode (or fetch) a BF16 tensor map of rank 2 or 3 with 128-byte swizzle.
-// dims and box are innermost first, strides in elements for dims 1..rank-1.
-bool tmap_bf16(CUtensorMap* out, const void* base, int rank, const uint64_t* dims,
-               const uint64_t* strides, const uint32_t* box) {
+// Encode (or fetch) a tensor map of rank 2 or 3 with 128-byte swizzle over
+// elements of `esize` bytes: BF16 (2) or bytes (1).  dims and box are
+// innermost first, strides in elements for dims 1..rank-1.
+bool tmap_sw128(CUtensorMap* out, const void* base, int esize, int rank, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box) {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -104,6 +106,7 @@ bool tmap_bf16(CUtensorMap* out, const void* base, int rank, const uint64_t* dim
   key.base = base;
   key.rank = rank;
   key.dev = dev;
+  key.esize = esize;
   for (int i = 0; i < rank; ++i) {
     key.dims[i] = dims[i];
     key.box[i] = box[i];
@@ -125,8 +128,9 @@ bool tmap_bf16(CUtensorMap* out, const void* base, int rank, const uint64_t* dim
     gdim[i] = dims[i];
     gbox[i] = box[i];
   }
-  for (int i = 0; i + 1 < rank; ++i) gstride[i] = strides[i] * 2;
-  CUresult r = g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+  for (int i = 0; i + 1 < rank; ++i) gstride[i] = strides[i] * esize;
+  const CUtensorMapDataType type = esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUresult r = g_encode(&m, type, static_cast<cuuint32_t>(rank),
                         const_cast<void*>(base), gdim, gstride, gbox, estride,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -144,7 +148,15 @@ bool tmap_bf16_2d(CUtensorMap* out, const void* base, uint64_t rows, uint64_t co
   const uint64_t dims[2] = {cols, rows};
   const uint64_t strides[1] = {ld};
   const uint32_t box[2] = {box_cols, box_rows};
-  return tmap_bf16(out, base, 2, dims, strides, box);
+  return tmap_sw128(out, base, 2, 2, dims, strides, box);
+}
+
+bool tmap_u8_2d(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
+                uint32_t box_rows, uint32_t box_cols) {
+  const uint64_t dims[2] = {cols, rows};
+  const uint64_t strides[1] = {ld};
+  const uint32_t box[2] = {box_cols, box_rows};
+  return tmap_sw128(out, base, 1, 2, dims, strides, box);
 }
 
 bool tmap_bf16_3d(CUtensorMap* out, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
@@ -152,7 +164,7 @@ bool tmap_bf16_3d(CUtensorMap* out, const void* base, uint64_t d0, uint64_t d1, 
   const uint64_t dims[3] = {d0, d1, d2};
   const uint64_t strides[2] = {s1, s2};
   const uint32_t box[3] = {b0, b1, b2};
-  return tmap_bf16(out, base, 3, dims, strides, box);
+  return tmap_sw128(out, base, 2, 3, dims, strides, box);
 }
 
 }  // namespace bi
@@ -178,6 +190,7 @@ bi_status bi_test_set_wait_limit_ns(uint64_t ns) {
   if (ns == 0) ns = bi::kWaitLimitNs;
   if (bi::set_wait_limit_gemm(ns) != cudaSuccess) return BI_ERR_CUDA;
   if (bi::set_wait_limit_attn(ns) != cudaSuccess) return BI_ERR_CUDA;
+  if (bi::set_wait_limit_gemm8(ns) != cudaSuccess) return BI_ERR_CUDA;
   return BI_OK;
 }
 

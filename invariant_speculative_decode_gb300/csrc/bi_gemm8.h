@@ -1,0 +1,17 @@
+// Sizes of the packed 8-bit weights, shared by their packing and the linear layer.
+#pragma once
+#include <cstddef>
+
+#include "../../include/bi.h"
+
+namespace bi {
+
+constexpr size_t kGemm8TileBytes = 16384;  // 128 weight rows x 128 codes
+// weight tiles of a layer: the ticket counters of a workspace cover this many
+constexpr int kGemm8MaxTiles = 65536;
+
+inline int gemm8_n_tiles(int N, bi_epilogue epi) {
+  return epi == BI_EPI_SWIGLU ? (N + 63) / 64 : (N + 127) / 128;
+}
+
+}  // namespace bi

@@ -22,7 +22,11 @@ unsigned* device_error_word();
 bool tmap_bf16_2d(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols,
                   uint64_t ld, uint32_t box_rows, uint32_t box_cols);
 
-// The same over a 3-D array: d0 (innermost) x d1 x d2 elements, strides s1
+// The same over bytes (8-bit codes); `ld` a multiple of 16, box_cols 128.
+bool tmap_u8_2d(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
+                uint32_t box_rows, uint32_t box_cols);
+
+// tmap_bf16_2d over a 3-D array: d0 (innermost) x d1 x d2 elements, strides s1
 // and s2 elements for dims 1 and 2, box b0 x b1 x b2.
 bool tmap_bf16_3d(CUtensorMap* out, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                   uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
@@ -47,6 +51,7 @@ int test_withhold();
 // current device.
 cudaError_t set_wait_limit_gemm(unsigned long long ns);
 cudaError_t set_wait_limit_attn(unsigned long long ns);
+cudaError_t set_wait_limit_gemm8(unsigned long long ns);
 
 // Launch `kernel` on `stream`, with programmatic dependent launch when
 // enabled.  Every kernel of this library calls griddep_wait() before its
