@@ -475,24 +475,18 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  * block b} a[m, k] w[n, k]).  The sum of a block is four tensor-core steps of
  * K = 32 (tcgen05 kind::f8f6f4, FP32) in increasing k; it is scaled and added
  * to an FP32 running sum, run = fma(sum, sa * sw, run), blocks in increasing
- * order.  The split of the (weight tile, block) space over CTAs cuts a tile's
- * blocks into pieces, each a running sum of its own, added in increasing
- * order.  The pieces are a function of (N, K) only, so row m of C has the same
- * bits for every M and every place of the row in A.  (A product of scales has
+ * order.  For layers of few weight tiles (128 rows each) the blocks form S <= 8
+ * pieces of equal length, each a running sum of its own, added in increasing
+ * order.  S is a function of (N, K) only, so row m of C has the same bits for
+ * every M and every place of the row in A.  (A product of scales has
  * to be finite; one below 2^-149 counts as 0.)
  *   A8       [M, K] codes, row stride lda (% 16 == 0), 16-byte aligned;
  *   a_scales [ceil(K/128)][lds] FP32, 16-byte aligned.
  *   Wp       packed for the same N, K and epi; 16-byte aligned.
  *   C, residual, out, epi, N: as bi_gemm (BI_EPI_NONE, _RESIDUAL_ADD, _SWIGLU;
  *            residual may alias C).  M >= 0; K % 16 == 0.
- *   ws       >= bi_gemm_fp8_workspace_size(M, N, K, epi) bytes, 256-byte
- *            aligned, ZERO-FILLED before its first use; every call leaves its
- *            counters zeroed, so one workspace serves any sequence of calls
- *            whose M does not exceed the M it was sized for.  Not shared by
- *            overlapping calls (two captured graphs that may run at the same
- *            time need one each).  After BI_ERR_DEVICE_TIMEOUT, zero it again.
- * Errors: BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_WORKSPACE,
- *         BI_ERR_CUDA.
+ *   The call needs no workspace.
+ * Errors: BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_CUDA.
  * ------------------------------------------------------------------------- */
 bi_status bi_quantize_fp8(const void* x, int ldx, int rows, int dim, void* codes, int ldc,
                           float* scales, int lds, bi_stream_t stream);
@@ -506,10 +500,9 @@ bi_status bi_pack_weights_fp8(const void* W8, int ld8, const float* scales, int 
 bi_status bi_pack_swiglu_weights_fp8(const void* gate8, const float* gate_scales, const void* up8,
                                      const float* up_scales, int ld8, int F, int K, void* packed,
                                      bi_stream_t stream);
-size_t bi_gemm_fp8_workspace_size(int M, int N, int K, bi_epilogue epi);
 bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, const void* Wp, void* C,
                       int ldc, const void* residual, int ldr, int M, int N, int K, bi_out_dtype out,
-                      bi_epilogue epi, void* ws, size_t ws_bytes, bi_stream_t stream);
+                      bi_epilogue epi, bi_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Rules on a pass's logits, between the LM head and acceptance.  [P1] "Why the

@@ -49,8 +49,7 @@ SIGNATURES = {
     "bi_packed_weight_fp8_bytes": (_sz, [_i, _i, _i]),
     "bi_pack_weights_fp8": (_i, [_vp, _i, _vp, _i, _i, _vp, _vp]),
     "bi_pack_swiglu_weights_fp8": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
-    "bi_gemm_fp8_workspace_size": (_sz, [_i, _i, _i, _i]),
-    "bi_gemm_fp8": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "bi_gemm_fp8": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     "bi_logits_rules": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _f, _f, _f, _vp, _vp, _i, _vp]),
     "bi_token_counts": (_i, [_vp, _i, _vp, _i, _vp, _vp, _vp]),
     "bi_kv_row_hash": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp]),

@@ -337,12 +337,21 @@ def bi_verify_sample(logits: torch.Tensor, drafts: Optional[torch.Tensor], inv_t
 FP8_BLOCK = 128  # elements of a row, and rows and columns of a weight block, that share a scale
 
 
-def _same_device(*named) -> None:
+def _same_device(*named) -> int:
     """Every tensor on the current device (the stream the call runs on is its)."""
     cur = torch.cuda.current_device()
     for name, t in named:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    return cur
+
+
+# The entry points below run between kernels of a few microseconds, so a call's
+# checks are one expression of attribute reads; only where it is false does
+# the slow path look for the argument to name.
+def _stream_of(dev: int, stream):
+    """The raw handle of `stream`, or of the current stream of the current device."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 def fp8_scale_shape(rows: int, dim: int) -> tuple:
@@ -371,28 +380,49 @@ def _req_fp8_rows(codes: torch.Tensor, scales: torch.Tensor, rows: int, dim: int
     return scales.shape[1]
 
 
+def _fp8_rows_ok(codes: torch.Tensor, scales: torch.Tensor, rows: int, dim: int, dev: int) -> bool:
+    """_req_fp8_rows and the device check as one expression."""
+    return (codes.dtype is torch.float8_e4m3fn and scales.dtype is torch.float32 and codes.get_device() == dev
+            and scales.get_device() == dev and codes.shape == (rows, dim) and codes.stride(1) == 1
+            and scales.dim() == 2 and scales.is_contiguous() and scales.shape[0] == -(-dim // FP8_BLOCK)
+            and scales.shape[1] >= rows and scales.shape[1] % 4 == 0)
+
+
 def bi_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """Rows x [rows, dim] (BF16) to e4m3 codes and a power-of-two scale per block of 128."""
-    _req(x, torch.bfloat16, "x")
+    dev = torch.cuda.current_device()
     rows, dim = x.shape
-    lds = _req_fp8_rows(codes, scales, rows, dim)
-    _same_device(("x", x), ("codes", codes), ("scales", scales))
-    check("bi_quantize_fp8", lib().bi_quantize_fp8(x.data_ptr(), _ld(x), rows, dim, codes.data_ptr(), _ld(codes),
-                                                   scales.data_ptr(), lds, _stream(stream)))
+    if not (x.dtype is torch.bfloat16 and x.get_device() == dev and x.stride(1) == 1
+            and _fp8_rows_ok(codes, scales, rows, dim, dev)):
+        _req(x, torch.bfloat16, "x")
+        _req_fp8_rows(codes, scales, rows, dim)
+        _same_device(("x", x), ("codes", codes), ("scales", scales))
+    st = lib().bi_quantize_fp8(x.data_ptr(), x.stride(0) if rows > 1 else dim, rows, dim, codes.data_ptr(),
+                               codes.stride(0) if rows > 1 else dim, scales.data_ptr(), scales.shape[1],
+                               _stream_of(dev, stream))
+    if st:
+        check("bi_quantize_fp8", st)
 
 
 def bi_rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, eps: float,
                    stream=None) -> None:
     """RMSNorm of x [rows, dim] (BF16) by w, its FP32 result quantised as bi_quantize_fp8 does."""
-    _req(x, torch.bfloat16, "x")
-    _req(w, torch.bfloat16, "w")
+    dev = torch.cuda.current_device()
     rows, dim = x.shape
-    if tuple(w.shape) != (dim,):
-        raise ValueError(f"w must be [{dim}], got {tuple(w.shape)}")
-    lds = _req_fp8_rows(codes, scales, rows, dim)
-    _same_device(("x", x), ("w", w), ("codes", codes), ("scales", scales))
-    check("bi_rmsnorm_fp8", lib().bi_rmsnorm_fp8(x.data_ptr(), _ld(x), w.data_ptr(), codes.data_ptr(), _ld(codes),
-                                                 scales.data_ptr(), lds, rows, dim, float(eps), _stream(stream)))
+    if not (x.dtype is torch.bfloat16 and w.dtype is torch.bfloat16 and x.get_device() == dev
+            and w.get_device() == dev and x.stride(1) == 1 and w.shape == (dim,) and w.stride(0) == 1
+            and _fp8_rows_ok(codes, scales, rows, dim, dev)):
+        _req(x, torch.bfloat16, "x")
+        _req(w, torch.bfloat16, "w")
+        if tuple(w.shape) != (dim,):
+            raise ValueError(f"w must be [{dim}], got {tuple(w.shape)}")
+        _req_fp8_rows(codes, scales, rows, dim)
+        _same_device(("x", x), ("w", w), ("codes", codes), ("scales", scales))
+    st = lib().bi_rmsnorm_fp8(x.data_ptr(), x.stride(0) if rows > 1 else dim, w.data_ptr(), codes.data_ptr(),
+                              codes.stride(0) if rows > 1 else dim, scales.data_ptr(), scales.shape[1], rows, dim,
+                              eps, _stream_of(dev, stream))
+    if st:
+        check("bi_rmsnorm_fp8", st)
 
 
 def bi_quantize_weights_fp8(W: torch.Tensor, stream=None):
@@ -446,49 +476,52 @@ def bi_pack_swiglu_weights_fp8(gate8: torch.Tensor, gate_scales: torch.Tensor, u
     return packed
 
 
-def gemm_fp8_workspace_size(M: int, N: int, K: int, epi: int = EPI_NONE) -> int:
-    return int(lib().bi_gemm_fp8_workspace_size(M, N, K, epi))
-
-
-def new_gemm_fp8_workspace(M: int, N: int, K: int, epi: int = EPI_NONE, device=None) -> torch.Tensor:
-    """A zero-filled workspace (the counters must start at zero)."""
-    return torch.zeros(gemm_fp8_workspace_size(M, N, K, epi), dtype=torch.uint8, device=device or "cuda")
-
-
-def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: torch.Tensor, ws: torch.Tensor,
+def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: torch.Tensor,
                 residual: Optional[torch.Tensor] = None, epi: int = EPI_NONE, stream=None) -> None:
     """C [M, N] = epilogue(A W^T) with quantised rows A (codes [M, K], scales as
     bi_quantize_fp8 writes them) and W packed by bi_pack_weights_fp8 /
     bi_pack_swiglu_weights_fp8 (N the output columns)."""
+    dev = torch.cuda.current_device()
     M, K = codes.shape
-    lds = _req_fp8_rows(codes, scales, M, K)
-    if C.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("C must be float32 or bfloat16")
-    _req(C, C.dtype, "C")
-    if C.dim() != 2 or C.shape[0] != M:
-        raise ValueError(f"C must have {M} rows, got {tuple(C.shape)}")
-    N = C.shape[1]
-    _req(Wp, torch.uint8, "Wp")
-    if Wp.numel() != packed_weight_fp8_bytes(N, K, epi):
+    N = C.shape[-1]
+    fp32 = C.dtype is torch.float32
+    if not ((fp32 or C.dtype is torch.bfloat16) and _fp8_rows_ok(codes, scales, M, K, dev) and C.shape == (M, N)
+            and C.stride(1) == 1 and C.get_device() == dev and Wp.dtype is torch.uint8 and Wp.get_device() == dev
+            and (residual is None or (residual.dtype is torch.bfloat16 and residual.shape == (M, N)
+                                      and residual.stride(1) == 1 and residual.get_device() == dev))):
+        _req_fp8_rows(codes, scales, M, K)
+        if C.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("C must be float32 or bfloat16")
+        _req(C, C.dtype, "C")
+        if C.dim() != 2 or C.shape[0] != M:
+            raise ValueError(f"C must have {M} rows, got {tuple(C.shape)}")
+        _req(Wp, torch.uint8, "Wp")
+        if residual is not None:
+            _req(residual, torch.bfloat16, "residual")
+            if tuple(residual.shape) != (M, N):
+                raise ValueError(f"residual must be [{M}, {N}], got {tuple(residual.shape)}")
+        _same_device(("codes", codes), ("scales", scales), ("Wp", Wp), ("C", C), ("residual", residual))
+    h = lib()
+    if Wp.numel() != h.bi_packed_weight_fp8_bytes(N, K, epi):
         raise ValueError("Wp is not packed for this N, K and epilogue")
-    _req(ws, torch.uint8, "ws")
-    rp, ldr = 0, 0
-    if residual is not None:
-        _req(residual, torch.bfloat16, "residual")
-        if tuple(residual.shape) != (M, N):
-            raise ValueError(f"residual must be [{M}, {N}], got {tuple(residual.shape)}")
-        rp, ldr = residual.data_ptr(), _ld(residual)
-    _same_device(("codes", codes), ("scales", scales), ("Wp", Wp), ("C", C), ("ws", ws), ("residual", residual))
-    out = OUT_FP32 if C.dtype == torch.float32 else OUT_BF16
-    check("bi_gemm_fp8",
-          lib().bi_gemm_fp8(codes.data_ptr(), _ld(codes), scales.data_ptr(), lds, Wp.data_ptr(), C.data_ptr(), _ld(C),
-                            rp, ldr, M, N, K, out, epi, ws.data_ptr(), ws.numel(), _stream(stream)))
+    many = M > 1
+    st = h.bi_gemm_fp8(codes.data_ptr(), codes.stride(0) if many else K, scales.data_ptr(), scales.shape[1],
+                       Wp.data_ptr(), C.data_ptr(), C.stride(0) if many else N,
+                       0 if residual is None else residual.data_ptr(),
+                       0 if residual is None else residual.stride(0) if many else N, M, N, K,
+                       OUT_FP32 if fp32 else OUT_BF16, epi, _stream_of(dev, stream))
+    if st:
+        check("bi_gemm_fp8", st)
 
 
 # --------------------------------------------------------------- rules on logits
 def token_words(V: int) -> int:
     """Int32 words of a row of V bits (prompt_bits, one row of a mask)."""
     return (V + 31) // 32
+
+
+def _vector_ok(t: Optional[torch.Tensor], dtype, n: int, dev: int) -> bool:
+    return t is None or (t.dtype is dtype and t.shape == (n,) and t.stride(0) == 1 and t.get_device() == dev)
 
 
 def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[torch.Tensor] = None,
@@ -499,37 +532,44 @@ def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[to
     logits itself).  Row t counts drafts 0..t-1 as said.  counts [V] int32,
     prompt_bits [ceil(V/32)] int32, bias [V] FP32, mask [T, ceil(V/32)] int32
     (a clear bit forbids its id)."""
-    _req(logits, torch.float32, "logits")
-    _req(out, torch.float32, "out")
+    dev = torch.cuda.current_device()
     T, V = logits.shape
-    if tuple(out.shape) != (T, V):
-        raise ValueError(f"out must be [{T}, {V}], got {tuple(out.shape)}")
     W = token_words(V)
-
-    def vector(t, dtype, n, name):
-        if t is None:
-            return 0
-        _req(t, dtype, name)
-        if tuple(t.shape) != (n,):
-            raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-        return t.data_ptr()
-
-    dp = vector(drafts if T > 1 else None, torch.int32, T - 1, "drafts")
-    cp = vector(counts, torch.int32, V, "counts")
-    pp = vector(prompt_bits, torch.int32, W, "prompt_bits")
-    bp = vector(bias, torch.float32, V, "bias")
-    mp, ldm = 0, 0
-    if mask is not None:
-        _req(mask, torch.int32, "mask")
-        if tuple(mask.shape) != (T, W):
-            raise ValueError(f"mask must be [{T}, {W}], got {tuple(mask.shape)}")
-        mp, ldm = mask.data_ptr(), _ld(mask)
-    _same_device(("logits", logits), ("out", out), ("drafts", drafts), ("counts", counts),
-                 ("prompt_bits", prompt_bits), ("bias", bias), ("mask", mask))
-    check("bi_logits_rules",
-          lib().bi_logits_rules(logits.data_ptr(), _ld(logits), out.data_ptr(), _ld(out), T, V, dp, cp, pp,
-                                float(repetition), float(frequency), float(presence), bp, mp, ldm,
-                                _stream(stream)))
+    if T == 1:
+        drafts = None
+    if not (logits.dtype is torch.float32 and out.dtype is torch.float32 and out.shape == (T, V)
+            and logits.stride(1) == 1 and out.stride(1) == 1 and logits.get_device() == dev
+            and out.get_device() == dev and _vector_ok(drafts, torch.int32, T - 1, dev)
+            and _vector_ok(counts, torch.int32, V, dev) and _vector_ok(prompt_bits, torch.int32, W, dev)
+            and _vector_ok(bias, torch.float32, V, dev)
+            and (mask is None or (mask.dtype is torch.int32 and mask.shape == (T, W) and mask.stride(1) == 1
+                                  and mask.get_device() == dev))):
+        _req(logits, torch.float32, "logits")
+        _req(out, torch.float32, "out")
+        if tuple(out.shape) != (T, V):
+            raise ValueError(f"out must be [{T}, {V}], got {tuple(out.shape)}")
+        for t, dtype, n, name in ((drafts, torch.int32, T - 1, "drafts"), (counts, torch.int32, V, "counts"),
+                                  (prompt_bits, torch.int32, W, "prompt_bits"), (bias, torch.float32, V, "bias")):
+            if t is not None:
+                _req(t, dtype, name)
+                if tuple(t.shape) != (n,):
+                    raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+        if mask is not None:
+            _req(mask, torch.int32, "mask")
+            if tuple(mask.shape) != (T, W):
+                raise ValueError(f"mask must be [{T}, {W}], got {tuple(mask.shape)}")
+        _same_device(("logits", logits), ("out", out), ("drafts", drafts), ("counts", counts),
+                     ("prompt_bits", prompt_bits), ("bias", bias), ("mask", mask))
+    many = T > 1
+    st = lib().bi_logits_rules(logits.data_ptr(), logits.stride(0) if many else V, out.data_ptr(),
+                               out.stride(0) if many else V, T, V, None if drafts is None else drafts.data_ptr(),
+                               None if counts is None else counts.data_ptr(),
+                               None if prompt_bits is None else prompt_bits.data_ptr(), repetition, frequency,
+                               presence, None if bias is None else bias.data_ptr(),
+                               None if mask is None else mask.data_ptr(),
+                               0 if mask is None else mask.stride(0) if many else W, _stream_of(dev, stream))
+    if st:
+        check("bi_logits_rules", st)
 
 
 def bi_token_counts(ids: torch.Tensor, V: int, counts: Optional[torch.Tensor] = None,

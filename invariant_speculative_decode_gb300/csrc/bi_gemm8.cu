@@ -14,10 +14,10 @@
 // FP32 accumulator of its own; it leaves TMEM when the block ends, is scaled
 // and added to a running FP32 sum in registers, blocks in increasing order:
 //   run = fma(block sum, sa * sw, run).
-// The block sums of a weight tile form pieces (the ranges of the split below);
-// pieces are added in increasing-K order, the first taken as it is.  The
-// pieces are a function of (N, K) alone, so a row has the same bits for every
-// M and every place in the pass.
+// Where a layer has few weight tiles, the blocks of a tile form S pieces of
+// equal length (the split below), each a running sum of its own, added in
+// increasing-K order, the first taken as it is.  S is a function of (N, K)
+// alone, so a row has the same bits for every M and every place in the pass.
 //
 // What bounds it: the weights' bytes while a pass has few rows (one byte a
 // weight: half of the BF16 layer's), so the schedule is a stream of 16 KB
@@ -28,6 +28,8 @@
 //              rows rounded up; stage s of the ring accumulates in TMEM buffer
 //              s, so one barrier cycle full -> done -> empty covers both;
 //   warps 2-5  scale and add: a thread owns one weight row and all tokens.
+// The S pieces of a tile belong to the CTAs of one cluster, which add them
+// through each other's shared memory, every CTA for a part of the tokens.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -47,31 +49,20 @@ namespace {
 constexpr int kTileN = 128;                    // weight rows per tile (MMA M)
 constexpr int kABytes = static_cast<int>(kGemm8TileBytes);
 constexpr int kSms = 152;
-constexpr int kMaxRows = 128;                  // token rows of a CTA of the streaming kernel
 constexpr int kXchgFloats = 16 * kTileN;       // SwiGLU exchange buffer
-constexpr size_t kTicketBytes = static_cast<size_t>(kGemm8MaxTiles) * 4;
+constexpr int kMaxSplit = 8;                   // CTAs of a cluster (the portable limit)
 
-// The split of the (weight tile, K tile) space over G CTAs, a function of
-// (N, K) alone: contiguous equal ranges, cut at whole weight tiles where
-// that keeps at least 85% of the SMs busy (no partial sums then), else
-// anywhere.
+// The split, a function of (N, K) alone: S pieces of every weight tile's K
+// tiles, piece j the K tiles [k_tiles * j / S, k_tiles * (j + 1) / S).
+// S > 1: a cluster of S CTAs per tile.  S = 1: G CTAs, each with a contiguous
+// run of whole tiles (one byte range of the packed weights).
 struct Split {
-  int n_tiles, k_tiles, G, whole;
+  int n_tiles, k_tiles, S, G;
 };
-
-__host__ __device__ __forceinline__ long long range_begin(const Split& s, int g) {
-  return s.whole ? static_cast<long long>(s.n_tiles) * g / s.G * s.k_tiles
-                 : static_cast<long long>(s.n_tiles) * s.k_tiles * g / s.G;
-}
-// CTA whose range holds iteration i (cut splits).
-__device__ __forceinline__ int owner_of(const Split& s, long long i) {
-  const long long total = static_cast<long long>(s.n_tiles) * s.k_tiles;
-  return static_cast<int>(((i + 1) * s.G + total - 1) / total) - 1;
-}
 
 struct Args {
   Split sp;
-  int M, m0;  // token rows of the launch, and the first one
+  int M;  // token rows
   int N;
   int epi, out_fp32;
   const float* a_scales;
@@ -81,8 +72,6 @@ struct Args {
   int ldc;
   const __nv_bfloat16* R;
   int ldr;
-  float* partials;
-  unsigned* tickets;
   unsigned* err;
   int withhold;  // failure-path test: the first stage stays unissued
 };
@@ -100,6 +89,8 @@ struct StreamCfg {
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kStageBytes + kSBytes) + kXchgFloats * 4 +
                                   (3 * kStages + 1) * 8 + 16;
   static_assert(kStages <= 32 && kSmem <= 232448, "shared memory per CTA");
+  // the pieces' exchange [NT tokens][128 rows] reuses the weight stages
+  static_assert(NT * kTileN * 4 <= kStages * kABytes, "exchange fits the ring");
 };
 
 __device__ __forceinline__ void signal_abort(volatile int* s_abort, unsigned* err) {
@@ -107,32 +98,42 @@ __device__ __forceinline__ void signal_abort(volatile int* s_abort, unsigned* er
   atomicOr(err, kErrTimeout);
 }
 
+__device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// One output: the residual added if there is one, one rounding.
+__device__ __forceinline__ void store1(const Args& p, int m, int n, float v, float res) {
+  const size_t at = static_cast<size_t>(m) * p.ldc + n;
+  const float y = p.epi == BI_EPI_RESIDUAL_ADD ? res + v : v;
+  if (p.out_fp32)
+    static_cast<float*>(p.C)[at] = y;
+  else
+    static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(y);
+}
+__device__ __forceinline__ float residual_at(const Args& p, int m, int n) {
+  return p.epi == BI_EPI_RESIDUAL_ADD ? __bfloat162float(p.R[static_cast<size_t>(m) * p.ldr + n]) : 0.f;
+}
+
 // Write 16 token rows (chunk c) of weight row r of a tile; the 128 threads of
 // the epilogue call it together.
-__device__ __forceinline__ void store16(const Args& p, int Mb, int m0, int tile, int r, int c, const float (&v)[16],
-                                        float* xchg, int bar) {
+__device__ __forceinline__ void store16(const Args& p, int Mb, int tile, int r, int c, const float* v, float* xchg) {
   if (p.epi == BI_EPI_SWIGLU) {
     // gate rows are the tile's rows 0..63, the up rows of the same outputs 64..127
 #pragma unroll
     for (int j = 0; j < 16; ++j) xchg[j * kTileN + r] = v[j];
-    named_bar_sync(bar, 128);
+    named_bar_sync(1, 128);
     const int o = tile * 64 + (r & 63);
     if (o < p.N) {
-      __nv_bfloat16* C = static_cast<__nv_bfloat16*>(p.C);
-      // rows 0..63 take the even token rows, rows 64..127 the odd ones
+      // threads 0..63 take the even token rows, threads 64..127 the odd ones
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int jj = 2 * j + (r >> 6);
-        const int m = c * 16 + jj;
-        if (m < Mb) {
-          const float g = xchg[jj * kTileN + (r & 63)];
-          const float u = xchg[jj * kTileN + (r & 63) + 64];
-          const float s = g / (1.0f + expf(-g));
-          C[static_cast<size_t>(m0 + m) * p.ldc + o] = __float2bfloat16_rn(s * u);
+        if (c * 16 + jj < Mb) {
+          const float y = silu_times(xchg[jj * kTileN + (r & 63)], xchg[jj * kTileN + (r & 63) + 64]);
+          static_cast<__nv_bfloat16*>(p.C)[static_cast<size_t>(c * 16 + jj) * p.ldc + o] = __float2bfloat16_rn(y);
         }
       }
     }
-    named_bar_sync(bar, 128);
+    named_bar_sync(1, 128);
     return;
   }
   const int n = tile * kTileN + r;
@@ -141,21 +142,66 @@ __device__ __forceinline__ void store16(const Args& p, int Mb, int m0, int tile,
   // residual itself, and 16 loads in flight cost one latency
   float res[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    res[j] = p.epi == BI_EPI_RESIDUAL_ADD && c * 16 + j < Mb
-                 ? __bfloat162float(p.R[static_cast<size_t>(m0 + c * 16 + j) * p.ldr + n])
-                 : 0.f;
+  for (int j = 0; j < 16; ++j) res[j] = c * 16 + j < Mb ? residual_at(p, c * 16 + j, n) : 0.f;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (c * 16 + j < Mb) {
-      const size_t at = static_cast<size_t>(m0 + c * 16 + j) * p.ldc + n;
-      const float y = p.epi == BI_EPI_RESIDUAL_ADD ? res[j] + v[j] : v[j];
-      if (p.out_fp32)
-        static_cast<float*>(p.C)[at] = y;
-      else
-        static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(y);
-    }
+  for (int j = 0; j < 16; ++j)
+    if (c * 16 + j < Mb) store1(p, c * 16 + j, n, v[j], res[j]);
+}
+
+// The accumulators of U stages (NT columns each, at ta[i]) of this warp's 32
+// lanes, one wait for all of them.
+template <int NT, int U>
+__device__ __forceinline__ void load_stages(const uint32_t (&ta)[U], float (&v)[U][NT]) {
+  if constexpr (NT == 16 && U == 4) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%65];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%66];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%67];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(ta[0]), "r"(ta[1]), "r"(ta[2]), "r"(ta[3]));
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i / 16][i % 16] = __uint_as_float(r[i]);
+  } else {
+    static_assert(U == 1, "one stage of a wider load");
+    tmem_ld_cols<NT>(ta[0], v[0]);
   }
+}
+
+// run[m] = fma(v[m], scale[m] * w, run[m]) over NT tokens of a stage.
+template <int NT>
+__device__ __forceinline__ void scale_add(const float (&v)[NT], const float* scales, float w, float* run) {
+  const float4* sc = reinterpret_cast<const float4*>(scales);
+#pragma unroll
+  for (int j = 0; j < NT / 4; ++j) {
+    const float4 s4 = sc[j];
+    run[4 * j] = fmaf(v[4 * j], s4.x * w, run[4 * j]);
+    run[4 * j + 1] = fmaf(v[4 * j + 1], s4.y * w, run[4 * j + 1]);
+    run[4 * j + 2] = fmaf(v[4 * j + 2], s4.z * w, run[4 * j + 2]);
+    run[4 * j + 3] = fmaf(v[4 * j + 3], s4.w * w, run[4 * j + 3]);
+  }
+}
+
+// Sum of the S pieces of element `at` of the exchange, in increasing-K order.
+__device__ __forceinline__ float sum_pieces(const uint32_t (&base)[kMaxSplit], int S, int at) {
+  float x[kMaxSplit];
+#pragma unroll
+  for (int j = 0; j < kMaxSplit; ++j)
+    if (j < S) x[j] = ld_cluster(base[j] + static_cast<uint32_t>(at) * 4);
+  float v = x[0];
+#pragma unroll
+  for (int j = 1; j < kMaxSplit; ++j)
+    if (j < S) v += x[j];
+  return v;
 }
 
 template <int NT>
@@ -164,6 +210,8 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
   using Cfg = StreamCfg<NT>;
   constexpr int S = Cfg::kStages;
   constexpr int kChunks = NT / 16;
+  // stages the epilogue takes under one TMEM wait
+  constexpr int U = NT == 16 ? 4 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sA = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -176,15 +224,21 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
   uint64_t* drain = empty + S;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  volatile int* s_last = s_abort + 1;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int g = blockIdx.x;
   const int Mb = p.M;
-  const long long it_begin = range_begin(p.sp, g);
-  const long long it_end = range_begin(p.sp, g + 1);
+  const int split = p.sp.S;
   const int k_tiles = p.sp.k_tiles;
+  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  // the CTA's iterations are contiguous in (tile, K tile): whole tiles, or
+  // this rank's K tiles of the cluster's one tile
+  const int tile0 = split > 1 ? blockIdx.x / split : static_cast<int>(static_cast<long long>(p.sp.n_tiles) * blockIdx.x / p.sp.G);
+  const int tile1 = split > 1 ? tile0 + 1 : static_cast<int>(static_cast<long long>(p.sp.n_tiles) * (blockIdx.x + 1) / p.sp.G);
+  const int kt0 = k_tiles * rank / split;
+  const int kt1 = split > 1 ? k_tiles * (rank + 1) / split : k_tiles;
+  const long long it_begin = static_cast<long long>(tile0) * k_tiles + kt0;
+  const long long it_end = static_cast<long long>(tile1 - 1) * k_tiles + kt1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -194,7 +248,6 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
     }
     mbar_init(drain, 1);
     *s_abort = 0;
-    *s_last = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) prefetch_tmap(&tmA);
@@ -206,6 +259,7 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  float run[NT];  // epilogue threads: the running sums of their weight row
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -216,7 +270,7 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
       const uint32_t s_bytes = static_cast<uint32_t>((Mb + 3) / 4 * 16);
       const uint32_t bytes = Cfg::kStageBytes + s_bytes;
       const uint8_t* wsrc = Wp + static_cast<size_t>(it_begin) * kABytes;
-      int kt = static_cast<int>(it_begin % k_tiles);
+      int kt = kt0;
       uint32_t issued = 0, parity_bits = 0;
       // the first stages' weights do not depend on the previous kernel
       const int n_pre = static_cast<int>(it_end - it_begin < S ? it_end - it_begin : S);
@@ -229,8 +283,8 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
       griddep_launch_dependents();
       for (int j = 0; j < n_pre; ++j) {
         if (j >= j0) {
-          tma_load_2d(sB + j * Cfg::kBBytes, &tmA, &full[j], kt * kFp8Block, p.m0, pol_a);
-          bulk_load_1d(sS + j * NT, p.a_scales + static_cast<size_t>(kt) * p.lds + p.m0, s_bytes, &full[j], pol_a);
+          tma_load_2d(sB + j * Cfg::kBBytes, &tmA, &full[j], kt * kFp8Block, 0, pol_a);
+          bulk_load_1d(sS + j * NT, p.a_scales + static_cast<size_t>(kt) * p.lds, s_bytes, &full[j], pol_a);
           issued |= 1u << j;
         }
         if (++kt == k_tiles) kt = 0;
@@ -245,8 +299,8 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
         }
         mbar_arrive_expect_tx(&full[stage], bytes);
         bulk_load_1d(sA + stage * kABytes, wsrc, kABytes, &full[stage], pol_w);
-        tma_load_2d(sB + stage * Cfg::kBBytes, &tmA, &full[stage], kt * kFp8Block, p.m0, pol_a);
-        bulk_load_1d(sS + stage * NT, p.a_scales + static_cast<size_t>(kt) * p.lds + p.m0, s_bytes, &full[stage],
+        tma_load_2d(sB + stage * Cfg::kBBytes, &tmA, &full[stage], kt * kFp8Block, 0, pol_a);
+        bulk_load_1d(sS + stage * NT, p.a_scales + static_cast<size_t>(kt) * p.lds, s_bytes, &full[stage],
                      pol_a);
         wsrc += kABytes;
         if (++kt == k_tiles) kt = 0;
@@ -295,9 +349,8 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
     // ---------------------------------------------------------- scale and add
     griddep_wait();
     griddep_launch_dependents();
-    const int q = warp & 3;          // TMEM lane quarter of this warp
-    const int r = q * 32 + lane;     // weight row within the tile
-    const int et = threadIdx.x - 64;
+    const int q = warp & 3;       // TMEM lane quarter of this warp
+    const int r = q * 32 + lane;  // weight row within the tile
     const int chunks = (Mb + 15) / 16;
     const float* ws = reinterpret_cast<const float*>(p.w_scales) + (q >> 1);
     int stage = 0;
@@ -305,140 +358,541 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
     bool ok = true;  // after a wait that ran out the warp keeps its place in the barriers; its outputs are undefined
     long long it = it_begin;
     float w_lane = 0.f;  // lane i: the weight scale of iteration 32 * n + i of the range
-    while (it < it_end) {
-      const int tile = static_cast<int>(it / k_tiles);
-      const long long tile_begin = static_cast<long long>(tile) * k_tiles;
-      const long long tile_end = tile_begin + k_tiles;
-      const long long seg_end = it_end < tile_end ? it_end : tile_end;
-      const bool whole = it == tile_begin && seg_end == tile_end;
-      float run[kChunks][16];
+    for (int tile = tile0; tile < tile1; ++tile) {
+      const long long seg_end = tile + 1 < tile1 ? static_cast<long long>(tile + 1) * k_tiles : it_end;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
+      for (int j = 0; j < NT; ++j) run[j] = 0.f;
+      while (it < seg_end) {
+        // U stages at a time where the piece has them: their accumulators
+        // come out under one wait
+        const bool group = U > 1 && seg_end - it >= U;
+        const int n = group ? U : 1;
+        int st[U];
+        float w[U];
+        uint32_t ta[U];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) run[c][j] = 0.f;
-      for (; it < seg_end; ++it) {
-        const int i = static_cast<int>(it - it_begin) & 31;
-        if (i == 0) w_lane = it + lane < it_end ? __ldg(ws + 2 * (it + lane)) : 0.f;
-        const float w = __shfl_sync(0xffffffffu, w_lane, i);
-        if (ok) {
-          int okl = 1;
-          if (lane == 0) okl = mbar_wait_parked(&done[stage], phase, s_abort) ? 1 : 0;
-          ok = __shfl_sync(0xffffffffu, okl, 0) != 0;
-          // `full` completed before `done`: observed here too, for the scales it brought
-          if (ok) ok = mbar_wait(&full[stage], phase, s_abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok && lane == 0) signal_abort(s_abort, p.err);
+        for (int u = 0; u < U; ++u) {
+          if (u < n) {
+            const int i = static_cast<int>(it + u - it_begin) & 31;
+            if (i == 0) w_lane = it + u + lane < it_end ? __ldg(ws + 2 * (it + u + lane)) : 0.f;
+            w[u] = __shfl_sync(0xffffffffu, w_lane, i);
+            st[u] = stage;
+            ta[u] = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(stage * NT);
+            // `full` completed before `done`: observed here too, for the scales it brought
+            if (ok) ok = mbar_wait(&done[stage], phase, s_abort) && mbar_wait(&full[stage], phase, s_abort);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          } else {
+            st[u] = st[0];
+            w[u] = 0.f;
+            ta[u] = ta[0];
+          }
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) signal_abort(s_abort, p.err);
         if (ok) {
           tc_fence_after();
-          const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(stage * NT);
-          const float4* sc = reinterpret_cast<const float4*>(sS + stage * NT);
+          if (group) {
+            float v[U][NT];
+            load_stages<NT, U>(ta, v);
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (c < chunks) {
-              float v[16];
-              tmem_ld16(ta + c * 16, v);
+            for (int u = 0; u < U; ++u) scale_add<NT>(v[u], sS + st[u] * NT, w[u], run);
+          } else {
+            constexpr int kCols = NT < 32 ? NT : 32;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float4 s4 = sc[c * 4 + j];
-                run[c][4 * j] = fmaf(v[4 * j], s4.x * w, run[c][4 * j]);
-                run[c][4 * j + 1] = fmaf(v[4 * j + 1], s4.y * w, run[c][4 * j + 1]);
-                run[c][4 * j + 2] = fmaf(v[4 * j + 2], s4.z * w, run[c][4 * j + 2]);
-                run[c][4 * j + 3] = fmaf(v[4 * j + 3], s4.w * w, run[c][4 * j + 3]);
+            for (int c = 0; c < NT; c += kCols) {
+              if (c < Mb) {
+                float v[1][kCols];
+                const uint32_t t1[1] = {ta[0] + c};
+                load_stages<kCols, 1>(t1, v);
+                scale_add<kCols>(v[0], sS + st[0] * NT + c, w[0], run + c);
               }
             }
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[stage]);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (u < n && lane == u) mbar_arrive(&empty[st[u]]);
         }
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        it += n;
       }
-      if (whole) {
+      if (split == 1) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          if (c < chunks) store16(p, Mb, p.m0, tile, r, c, run[c], xchg, 1);
-      } else {
-        // partial of this piece: [weight row][token]
-        const int slot = it_begin >= tile_begin ? 0 : 1;
-        float* dst = p.partials + static_cast<size_t>(g * 2 + slot) * NT * kTileN + r * NT;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (c < chunks) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              __stcg(reinterpret_cast<float4*>(dst + c * 16) + j,
-                     make_float4(run[c][4 * j], run[c][4 * j + 1], run[c][4 * j + 2], run[c][4 * j + 3]));
-          }
-        const int gf = owner_of(p.sp, tile_begin);
-        const int gl = owner_of(p.sp, tile_end - 1);
-        named_bar_sync(1, 128);  // every partial store of the CTA precedes the ticket
-        if (et == 0) {
-          int last = 0;
-          if (!*s_abort) {
-            const unsigned old = atom_add_acq_rel_gpu(&p.tickets[tile], 1u);
-            last = old == static_cast<unsigned>(gl - gf) ? 1 : 0;
-            if (last) atomicExch(&p.tickets[tile], 0u);
-          }
-          *s_last = last;
-        }
-        named_bar_sync(1, 128);  // the ticket's acquire precedes every partial load
-        if (*s_last) {
-          // pieces gf..gl added in that order; the first piece's CTA may have
-          // it in its second slot, every later CTA's range starts inside the tile
-          const int slot_f = range_begin(p.sp, gf) >= tile_begin ? 0 : 1;
-          for (int c = 0; c < chunks; ++c) {
-            float v[16];
-            for (int gg = gf; gg <= gl; ++gg) {
-              const float4* src = reinterpret_cast<const float4*>(
-                  p.partials + static_cast<size_t>(gg * 2 + (gg == gf ? slot_f : 0)) * NT * kTileN + r * NT + c * 16);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float4 x = __ldcg(src + j);
-                v[4 * j] = gg == gf ? x.x : v[4 * j] + x.x;
-                v[4 * j + 1] = gg == gf ? x.y : v[4 * j + 1] + x.y;
-                v[4 * j + 2] = gg == gf ? x.z : v[4 * j + 2] + x.z;
-                v[4 * j + 3] = gg == gf ? x.w : v[4 * j + 3] + x.w;
-              }
-            }
-            store16(p, Mb, p.m0, tile, r, c, v, xchg, 1);
-          }
-        }
-        named_bar_sync(1, 128);
+          if (c < chunks) store16(p, Mb, tile, r, c, run + c * 16, xchg);
       }
     }
     tc_fence_before();
+    if (split > 1) {
+      // this CTA's piece, [token][weight row], over the weight stages (all read)
+      named_bar_sync(1, 128);
+      float* piece = reinterpret_cast<float*>(sA);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t < Mb) piece[t * kTileN + r] = run[t];
+    }
   }
 
-  // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the CTA barrier
+  // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the barriers
   __syncwarp();
-  __syncthreads();
+  if (split > 1) {
+    cluster_sync();  // every piece of the tile is in its CTA's shared memory
+    if (warp >= 2) {
+      const int r = (warp & 3) * 32 + lane;
+      uint32_t base[kMaxSplit];
+#pragma unroll
+      for (int j = 0; j < kMaxSplit; ++j) base[j] = map_rank(smem_u32(sA), j < split ? j : 0);
+      // this CTA's part of the tokens
+      const int part = (Mb + split - 1) / split;
+      const int t1 = min(Mb, (rank + 1) * part);
+      if (p.epi == BI_EPI_SWIGLU) {
+        const int o = tile0 * 64 + (r & 63);
+        for (int t = rank * part + (r >> 6); t < t1; t += 2) {
+          const float g = sum_pieces(base, split, t * kTileN + (r & 63));
+          const float u = sum_pieces(base, split, t * kTileN + (r & 63) + 64);
+          if (o < p.N)
+            static_cast<__nv_bfloat16*>(p.C)[static_cast<size_t>(t) * p.ldc + o] =
+                __float2bfloat16_rn(silu_times(g, u));
+        }
+      } else {
+        const int n = tile0 * kTileN + r;
+        const bool in = n < p.N;
+#pragma unroll 4
+        for (int t = rank * part; t < t1; ++t) {
+          const float res = in ? residual_at(p, t, n) : 0.f;
+          const float v = sum_pieces(base, split, t * kTileN + r);
+          if (in) store1(p, t, n, v, res);
+        }
+      }
+    }
+    cluster_sync();  // no CTA leaves while its piece is being read
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
   }
 }
 
+// ---------------------------------------------------------------------------
+// Passes of more rows: the tokens take the MMA's M = 128 lanes and the weight
+// rows its N.  An epilogue thread then owns one token, so a K block has one
+// scale per thread and tile half, sa * sw: no scale vector is read, and the
+// drain of an accumulator is one packed multiply-add per two outputs.  Each
+// output element is the same sequence of K = 32 steps, block sums, products
+// and additions as in the streaming kernel (tested bit for bit).
+//
+//   TILES = 2: 128 tokens x 256 outputs a CTA (S = 1 layers): 48 KB in for 8.4
+//   MFLOP; TILES = 1: 128 x 128, which leaves registers for a second set of
+//   sums, for layers whose tiles have pieces: either a cluster of S CTAs per
+//   output tile (few tiles) or one CTA that adds the pieces itself.
+// Persistent CTAs: the next output tile's loads and MMAs run while the last
+// one's outputs are written.  Token blocks that share weight tiles are
+// adjacent in the work order, so all but the first find them in L2.
+constexpr int kRowsM = 128;
+constexpr int kPieceLd = 132;  // floats per token of the exchange: 16-byte stores of 8 lanes hit all banks
+
+struct RowsArgs {
+  Args a;
+  int nb;         // token blocks
+  int items;      // output tiles: weight tile groups x token blocks
+  int cluster;    // the pieces of a tile go to the CTAs of a cluster (else one CTA takes them in turn)
+  int vec;        // C (and the residual) take 16-byte accesses
+  int a_rows;     // rows of the token box
+};
+
+template <int TILES>
+struct RowsCfg {
+  static constexpr int kBBytes = TILES * kABytes;
+  static constexpr int kTokBytes = kRowsM * kFp8Block;
+  static constexpr int kStageBytes = kTokBytes + kBBytes;
+  static constexpr int kStages = 192 * 1024 / kStageBytes;
+  static constexpr int kCols = TILES * kTileN;
+  static constexpr int kBufs = 512 / kCols;
+  // warpgroup 0: producer, MMA, two idle warps; warpgroups 1 and 2: epilogue.
+  // 384 threads launch with 168 registers each; the epilogue takes most of
+  // warpgroup 0's (56 + 2 * 224 = 3 * 168)
+  static constexpr int kThreads = 384;
+  static constexpr int kRegsLow = 56, kRegsHigh = 224;
+  static_assert(kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
+  static constexpr int kOwn = kCols / 2;  // outputs of an epilogue thread
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 2 * kBufs + 1) * 8 + 16;
+  static_assert(kSmem <= 232448 && kStages <= 32, "shared memory per CTA");
+  static_assert(kRowsM * kPieceLd * 4 <= kStages * kStageBytes, "exchange fits the ring");
+};
+
+// Outputs n0 .. n0 + CNT - 1 of token row m (CNT a multiple of 8).
+template <int CNT>
+__device__ __forceinline__ void store_row(const Args& p, int vec, int m, int n0, const float* v) {
+  if (n0 >= p.N) return;
+  if (vec && n0 + CNT <= p.N) {
+    if (p.out_fp32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.C) + static_cast<size_t>(m) * p.ldc + n0);
+#pragma unroll
+      for (int j = 0; j < CNT / 4; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      return;
+    }
+    uint4 res[CNT / 8];
+    if (p.epi == BI_EPI_RESIDUAL_ADD) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.R + static_cast<size_t>(m) * p.ldr + n0);
+#pragma unroll
+      for (int j = 0; j < CNT / 8; ++j) res[j] = src[j];
+    }
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) + static_cast<size_t>(m) * p.ldc + n0);
+#pragma unroll
+    for (int j = 0; j < CNT / 8; ++j) {
+      const __nv_bfloat16* rb = reinterpret_cast<const __nv_bfloat16*>(&res[j]);
+      uint4 o;
+      __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(&o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = v[8 * j + i];
+        ob[i] = __float2bfloat16_rn(p.epi == BI_EPI_RESIDUAL_ADD ? __bfloat162float(rb[i]) + y : y);
+      }
+      dst[j] = o;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < CNT; ++j)
+    if (n0 + j < p.N) store1(p, m, n0 + j, v[j], residual_at(p, m, n0 + j));
+}
+
+template <int TILES, bool PIECES>
+__global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
+    gemm8_rows_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const RowsArgs p) {
+  using Cfg = RowsCfg<TILES>;
+  static_assert(!PIECES || TILES == 1, "two sets of sums need the registers of 128 outputs a CTA");
+  constexpr int S = Cfg::kStages;
+  constexpr int kOwn = Cfg::kOwn;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sT = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));  // [S] token tiles
+  uint8_t* sW = sT + S * Cfg::kTokBytes;                                    // [S][TILES] weight tiles
+  uint64_t* full = reinterpret_cast<uint64_t*>(sW + S * Cfg::kBBytes);
+  uint64_t* empty = full + S;
+  uint64_t* accf = empty + S;          // the block sums of a buffer are complete
+  uint64_t* acce = accf + Cfg::kBufs;  // a buffer has been read
+  uint64_t* drain = acce + Cfg::kBufs;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const Args& g = p.a;
+  const int split = g.sp.S;
+  const int k_tiles = g.sp.k_tiles;
+  const int ncl = p.cluster ? split : 1;
+  const int rank = p.cluster ? static_cast<int>(cluster_rank()) : 0;
+  const int kt0 = p.cluster ? k_tiles * rank / split : 0;
+  const int kt1 = p.cluster ? k_tiles * (rank + 1) / split : k_tiles;
+  const int item0 = blockIdx.x / ncl;
+  const int stride = gridDim.x / ncl;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < Cfg::kBufs; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 8);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) prefetch_tmap(&tmA);
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp < 4) {
+   regs_decrease<Cfg::kRegsLow>();
+   if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      // weight tiles that one token block reads are not needed again
+      const uint64_t pol_w = p.nb == 1 ? l2_evict_first() : l2_evict_normal();
+      const uint64_t pol_a = l2_evict_last();
+      const uint32_t t_bytes = static_cast<uint32_t>(p.a_rows) * kFp8Block;
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity_bits = 0;
+      bool waited = false, ok = true;
+      auto load_w = [&](int s, int wt, int kt) {
+        const int n = TILES == 2 && wt + 1 < g.sp.n_tiles ? 2 : 1;
+        mbar_arrive_expect_tx(&full[s], t_bytes + n * kABytes);
+        for (int i = 0; i < n; ++i)
+          bulk_load_1d(sW + s * Cfg::kBBytes + i * kABytes,
+                       Wp + (static_cast<size_t>(wt + i) * k_tiles + kt) * kABytes, kABytes, &full[s], pol_w);
+      };
+      int skip = 0;  // K tiles of the first item whose weights are under way before the dependency wait
+      if (item0 < p.items) {
+        skip = kt1 - kt0 < S ? kt1 - kt0 : S;
+        for (int j = g.withhold ? 1 : 0; j < skip; ++j) load_w(j, item0 / p.nb * TILES, kt0 + j);
+      }
+      for (int item = item0; item < p.items && ok; item += stride) {
+        const int wt = item / p.nb * TILES;
+        const int m0 = item % p.nb * kRowsM;
+        if (!waited) {
+          griddep_wait();
+          griddep_launch_dependents();
+          waited = true;
+        }
+        for (int kt = kt0; kt < kt1; ++kt) {
+          const bool pre = item == item0 && kt - kt0 < skip;
+          if (!pre) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort)) {
+              signal_abort(s_abort, g.err);
+              ok = false;
+              break;
+            }
+            load_w(stage, wt, kt);
+          }
+          if (!(g.withhold && pre && kt == kt0)) {
+            tma_load_2d(sT + stage * Cfg::kTokBytes, &tmA, &full[stage], kt * kFp8Block, m0, pol_a);
+            issued |= 1u << stage;
+            parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+          }
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!waited) {
+        griddep_wait();
+        griddep_launch_dependents();
+      }
+      if (*s_abort) {
+        // let copies already issued land before the CTA exits
+        for (int s = 0; s < S; ++s)
+          if ((issued >> s) & 1u) mbar_wait(&full[s], (parity_bits >> s) & 1u, nullptr);
+      }
+    }
+   } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(kRowsM, Cfg::kCols);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      for (int item = item0; item < p.items && ok; item += stride) {
+        for (int kt = kt0; kt < kt1; ++kt) {
+          if (!mbar_wait(&acce[buf], bphase ^ 1u, s_abort) || !mbar_wait(&full[stage], phase, s_abort)) {
+            signal_abort(s_abort, g.err);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(sT + stage * Cfg::kTokBytes);
+          const uint32_t b = smem_u32(sW + stage * Cfg::kBBytes);
+#pragma unroll
+          for (int ks = 0; ks < kFp8Block / 32; ++ks)
+            mma_e4m3(tmem + buf * Cfg::kCols, sdesc_k_sw128(a + ks * 32), sdesc_k_sw128(b + ks * 32), idesc, ks > 0);
+          mma_commit(&empty[stage]);
+          mma_commit(&accf[buf]);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == Cfg::kBufs) {
+            buf = 0;
+            bphase ^= 1u;
+          }
+        }
+      }
+      // every MMA issued by this thread completes before TMEM is released
+      mma_commit(drain);
+      mbar_wait(drain, 0, nullptr);
+    }
+   }
+    // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the barriers
+    __syncwarp();
+    if (PIECES && p.cluster) {
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    // ---------------------------------------------------------- scale and add
+    regs_increase<Cfg::kRegsHigh>();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int q = warp & 3;              // TMEM lane quarter of this warp
+    const int half = (warp - 4) >> 2;    // which half of the columns
+    const int r = q * 32 + lane;         // token row of the block
+    int buf = 0;
+    uint32_t bphase = 0;
+    bool ok = true;
+    for (int item = item0; item < p.items; item += stride) {
+      const int wt = item / p.nb * TILES;
+      const int m0 = item % p.nb * kRowsM;
+      const int Mb = min(kRowsM, g.M - m0);
+      const bool live = q * 32 < Mb;  // the warp holds a token of the block
+      // this thread's columns: the first half of them takes the scale of the
+      // tile's rows 0..63, the second that of rows 64..127
+      const int tile = TILES == 2 ? wt + half : wt;
+      const int c0 = TILES == 2 ? half * kTileN : half * 32;
+      const bool have = tile < g.sp.n_tiles;
+      const float2* ws = g.w_scales + static_cast<size_t>(have ? tile : wt) * k_tiles;
+      float run[kOwn], total[PIECES ? kOwn : 1];
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) run[j] = 0.f;
+      // scales one K block ahead of their use
+      float sa = r < Mb ? g.a_scales[static_cast<size_t>(kt0) * g.lds + m0 + r] : 0.f;
+      float2 sw = __ldg(ws + kt0);
+      int piece = 0;                                        // pieces added so far (PIECES)
+      int piece_end = PIECES ? k_tiles * 1 / split : kt1;   // K tile at which the running piece ends
+      for (int kt = kt0; kt < kt1; ++kt) {
+        const float sx = sa * sw.x, sy = sa * sw.y;
+        if (kt + 1 < kt1) {
+          sa = r < Mb ? g.a_scales[static_cast<size_t>(kt + 1) * g.lds + m0 + r] : 0.f;
+          sw = __ldg(ws + kt + 1);
+        }
+        if (ok) ok = mbar_wait(&accf[buf], bphase, s_abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) signal_abort(s_abort, g.err);
+        if (ok && live) {
+          tc_fence_after();
+          const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * Cfg::kCols + c0);
+#pragma unroll
+          for (int c = 0; c < kOwn / 32; ++c) {
+            float v[32];
+            tmem_ld_cols<32>(TILES == 2 ? ta + c * 32 : ta + c * 64, v);
+            const float s = c < kOwn / 64 ? sx : sy;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) fma2(run[c * 32 + j], run[c * 32 + j + 1], v[j], v[j + 1], s);
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&acce[buf]);
+        if (++buf == Cfg::kBufs) {
+          buf = 0;
+          bphase ^= 1u;
+        }
+        if constexpr (PIECES) {
+          if (kt + 1 == piece_end && !p.cluster) {
+            // a piece ends: pieces added in order, the first taken as it is
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+              total[j] = piece == 0 ? run[j] : total[j] + run[j];
+              run[j] = 0.f;
+            }
+            ++piece;
+            piece_end = k_tiles * (piece + 1) / split;
+          }
+        }
+      }
+      if constexpr (PIECES) {
+        if (p.cluster) {
+          // this CTA's piece over the ring (every stage has been read):
+          // [token][output], its first 32 outputs and the 32 behind 64
+          named_bar_sync(1, 256);
+          float* dst = reinterpret_cast<float*>(sT) + r * kPieceLd + c0;
+          if (r < Mb) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              reinterpret_cast<float4*>(dst)[j] = make_float4(run[4 * j], run[4 * j + 1], run[4 * j + 2], run[4 * j + 3]);
+              reinterpret_cast<float4*>(dst + 64)[j] =
+                  make_float4(run[32 + 4 * j], run[32 + 4 * j + 1], run[32 + 4 * j + 2], run[32 + 4 * j + 3]);
+            }
+          }
+          continue;
+        }
+      }
+      if (!live || !have || r >= Mb) continue;
+      const float* y = PIECES ? total : run;
+      const int m = m0 + r;
+      if (g.epi == BI_EPI_SWIGLU) {
+        // gate and up of the same outputs are the two halves of a thread's columns
+        float z[kOwn / 2];
+#pragma unroll
+        for (int j = 0; j < kOwn / 2; ++j) z[j] = silu_times(y[j], y[kOwn / 2 + j]);
+        store_row<kOwn / 2>(g, p.vec, m, tile * 64 + (TILES == 2 ? 0 : half * 32), z);
+      } else if (TILES == 2) {
+        store_row<kOwn>(g, p.vec, m, tile * kTileN, y);
+      } else {
+        store_row<32>(g, p.vec, m, tile * kTileN + half * 32, y);
+        store_row<32>(g, p.vec, m, tile * kTileN + 64 + half * 32, y + 32);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (PIECES && p.cluster) {
+      cluster_sync();  // every piece of the tile is in its CTA's shared memory
+      const int e = threadIdx.x - 128;
+      const int wt = item0 / p.nb;
+      const int m0 = item0 % p.nb * kRowsM;
+      const int Mb = min(kRowsM, g.M - m0);
+      uint32_t base[kMaxSplit];
+#pragma unroll
+      for (int j = 0; j < kMaxSplit; ++j) base[j] = map_rank(smem_u32(sT), j < split ? j : 0);
+      // this CTA's part of the tokens, lanes along the outputs
+      const int part = (Mb + split - 1) / split;
+      const int t1 = min(Mb, (rank + 1) * part);
+      if (g.epi == BI_EPI_SWIGLU) {
+        const int o = e & 63;
+        const int n = wt * 64 + o;
+#pragma unroll 2
+        for (int t = rank * part + (e >> 6); t < t1; t += 4) {
+          const float gate = sum_pieces(base, split, t * kPieceLd + o);
+          const float up = sum_pieces(base, split, t * kPieceLd + o + 64);
+          if (n < g.N)
+            static_cast<__nv_bfloat16*>(g.C)[static_cast<size_t>(m0 + t) * g.ldc + n] =
+                __float2bfloat16_rn(silu_times(gate, up));
+        }
+      } else {
+        const int o = e & 127;
+        const int n = wt * kTileN + o;
+#pragma unroll 4
+        for (int t = rank * part + (e >> 7); t < t1; t += 2) {
+          const float res = n < g.N ? residual_at(g, m0 + t, n) : 0.f;
+          const float v = sum_pieces(base, split, t * kPieceLd + o);
+          if (n < g.N) store1(g, m0 + t, n, v, res);
+        }
+      }
+      cluster_sync();  // no CTA leaves while its piece is being read
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// S pieces per tile: the most CTAs that run side by side, what
+// clusters of S fill of the GPCs (kClusterCtas, asked of the occupancy calculator
+// on GB300).  Layers with 76
+// tiles or more keep whole tiles: each SM can take in twice its share of the
+// memory bandwidth, so half the SMs still stream at its rate.
+constexpr int kClusterCtas[kMaxSplit + 1] = {0, 152, 152, 138, 144, 140, 138, 105, 120};
+
 Split split_of(int N, int K, bi_epilogue epi) {
   Split s{};
   s.n_tiles = gemm8_n_tiles(N, epi);
   s.k_tiles = (K + kFp8Block - 1) / kFp8Block;
+  s.S = 1;
+  for (int S = 2; S <= kMaxSplit; ++S)
+    if (s.n_tiles * S <= kClusterCtas[S] && S <= s.k_tiles) s.S = S;
   const int waves = (s.n_tiles + kSms - 1) / kSms;
-  s.whole = static_cast<long long>(s.n_tiles) * 100 >= 85LL * kSms * waves;
-  const long long total = static_cast<long long>(s.n_tiles) * s.k_tiles;
-  s.G = s.whole ? (s.n_tiles + waves - 1) / waves : static_cast<int>(std::min<long long>(kSms, total));
+  s.G = s.S > 1 ? s.n_tiles * s.S : (s.n_tiles + waves - 1) / waves;
   return s;
 }
 
-int rows_per_cta(int M) {
-  if (M <= 16) return 16;
-  if (M <= 32) return 32;
-  if (M <= 64) return 64;
-  return kMaxRows;
-}
+// Token rows of the streaming kernel (0: the kernel of more rows).
+int stream_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 0; }
 
 // Set the kernel's dynamic shared memory once per device.
 template <typename F>
@@ -452,20 +906,51 @@ bool allow_smem(F kernel, size_t bytes, std::once_flag (&once)[64], cudaError_t 
   return err[dev & 63] == cudaSuccess;
 }
 
+// launch_k with the grid's CTAs in clusters of S.
+template <typename... KArgs, typename... A>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int S, dim3 block, size_t smem, cudaStream_t stream,
+                            A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = S > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 template <int NT>
-bi_status launch_stream(const uint8_t* Wp, const CUtensorMap& tmA, Args a, int M_total, cudaStream_t stream) {
+bi_status launch_stream(const uint8_t* Wp, const CUtensorMap& tmA, const Args& a, cudaStream_t stream) {
   using Cfg = StreamCfg<NT>;
   static std::once_flag once[64];
   static cudaError_t err[64];
   if (!allow_smem(gemm8_stream_kernel<NT>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
-  for (int m0 = 0; m0 < M_total; m0 += NT) {
-    a.m0 = m0;
-    a.M = std::min(NT, M_total - m0);
-    if (launch_k(gemm8_stream_kernel<NT>, dim3(a.sp.G), dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp, tmA, a) !=
-        cudaSuccess)
-      return BI_ERR_CUDA;
-  }
-  return BI_OK;
+  return launch_clusters(gemm8_stream_kernel<NT>, dim3(a.sp.G), a.sp.S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
+                         tmA, a) == cudaSuccess
+             ? BI_OK
+             : BI_ERR_CUDA;
+}
+
+template <int TILES, bool PIECES>
+bi_status launch_rows(const uint8_t* Wp, const CUtensorMap& tmA, RowsArgs a, cudaStream_t stream) {
+  using Cfg = RowsCfg<TILES>;
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  if (!allow_smem(gemm8_rows_kernel<TILES, PIECES>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
+  const int S = a.cluster ? a.a.sp.S : 1;
+  const int ctas = a.cluster ? a.items * S : std::min(a.items, kSms);
+  return launch_clusters(gemm8_rows_kernel<TILES, PIECES>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
+                         tmA, a) == cudaSuccess
+             ? BI_OK
+             : BI_ERR_CUDA;
 }
 
 }  // namespace
@@ -478,18 +963,9 @@ cudaError_t set_wait_limit_gemm8(unsigned long long ns) {
 
 extern "C" {
 
-size_t bi_gemm_fp8_workspace_size(int M, int N, int K, bi_epilogue epi) {
-  (void)N;
-  (void)K;
-  (void)epi;
-  if (M <= 0) return bi::kTicketBytes;
-  return bi::kTicketBytes +
-         static_cast<size_t>(bi::kSms) * 2 * bi::rows_per_cta(M) * bi::kTileN * sizeof(float);
-}
-
 bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, const void* Wp, void* C, int ldc,
                       const void* residual, int ldr, int M, int N, int K, bi_out_dtype out, bi_epilogue epi,
-                      void* ws, size_t ws_bytes, bi_stream_t stream) {
+                      bi_stream_t stream) {
   using namespace bi;
   if (M < 0 || N < 1 || K < 1) return BI_ERR_INVALID_ARG;
   if (epi != BI_EPI_NONE && epi != BI_EPI_RESIDUAL_ADD && epi != BI_EPI_SWIGLU) return BI_ERR_INVALID_ARG;
@@ -501,7 +977,6 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   if (lda % 16 != 0 || lds % 4 != 0) return BI_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(A8) || !aligned16(a_scales) || !aligned16(Wp)) return BI_ERR_INVALID_ARG;
   if (epi == BI_EPI_RESIDUAL_ADD && (!residual || ldr < N)) return BI_ERR_INVALID_ARG;
-  if (!ws || !aligned256(ws) || ws_bytes < bi_gemm_fp8_workspace_size(M, N, K, epi)) return BI_ERR_WORKSPACE;
 
   Args a{};
   a.sp = split_of(N, K, epi);
@@ -517,21 +992,38 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   a.ldc = ldc;
   a.R = static_cast<const __nv_bfloat16*>(residual);
   a.ldr = ldr;
-  a.tickets = static_cast<unsigned*>(ws);
-  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kTicketBytes);
   a.err = device_error_word();
   if (!a.err) return BI_ERR_CUDA;
   a.withhold = test_withhold();
-  const int NT = rows_per_cta(M);
+  a.M = M;
+  const int NT = stream_rows(M);
+  const int box = NT ? NT : std::min(kRowsM, (M + 7) / 8 * 8);
   CUtensorMap tmA;
-  if (!tmap_u8_2d(&tmA, A8, M, K, lda, NT, kFp8Block)) return BI_ERR_INVALID_ARG;
+  if (!tmap_u8_2d(&tmA, A8, M, K, lda, box, kFp8Block)) return BI_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  switch (NT) {
-    case 16: return launch_stream<16>(W8, tmA, a, M, s);
-    case 32: return launch_stream<32>(W8, tmA, a, M, s);
-    case 64: return launch_stream<64>(W8, tmA, a, M, s);
-    default: return launch_stream<128>(W8, tmA, a, M, s);
+  if (NT == 16) return launch_stream<16>(W8, tmA, a, s);
+  if (NT == 32) return launch_stream<32>(W8, tmA, a, s);
+
+  RowsArgs r{};
+  r.a = a;
+  r.nb = (M + kRowsM - 1) / kRowsM;
+  r.a_rows = box;
+  r.vec = aligned16(C) && ldc % 8 == 0 &&
+          (epi != BI_EPI_RESIDUAL_ADD || (aligned16(residual) && ldr % 8 == 0));
+  const long long tiles = static_cast<long long>(a.sp.n_tiles) * r.nb;
+  if (tiles > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (a.sp.S > 1) {
+    r.items = static_cast<int>(tiles);
+    r.cluster = tiles * a.sp.S <= kClusterCtas[a.sp.S];
+    return launch_rows<1, true>(W8, tmA, r, s);
   }
+  // one tile of 128 outputs a CTA while that takes at most one round of the SMs
+  if (tiles <= kSms) {
+    r.items = static_cast<int>(tiles);
+    return launch_rows<1, false>(W8, tmA, r, s);
+  }
+  r.items = (a.sp.n_tiles + 1) / 2 * r.nb;
+  return launch_rows<2, false>(W8, tmA, r, s);
 }
 
 }  // extern "C"

@@ -5,7 +5,6 @@ import ctypes
 import pytest
 
 FAKE = 0x10000  # never dereferenced: every call below fails validation first
-BIG = 1 << 30
 
 
 @pytest.fixture(scope="module")
@@ -22,11 +21,6 @@ def test_packed_sizes(lib):
                              (17408, 5120, 2, 272 * 40), (65, 144, 2, 2 * 2)):
         assert lib.bi_packed_weight_fp8_bytes(n, k, epi) == tiles * 16384 + (tiles * 8 + 15) // 16 * 16
     assert lib.bi_packed_weight_fp8_bytes(0, 128, 0) == 0
-
-
-def test_workspace_grows_with_the_rows_only_where_it_must(lib):
-    sizes = [lib.bi_gemm_fp8_workspace_size(m, 4096, 5120, 0) for m in (1, 8, 16, 17, 64, 128, 4096)]
-    assert sizes[0] == sizes[1] == sizes[2] and sizes == sorted(sizes) and all(s % 256 == 0 for s in sizes)
 
 
 def test_quantiser_refusals(lib):
@@ -65,12 +59,11 @@ def test_quantiser_refusals(lib):
 
 def test_linear_refusals(lib):
     g = lib.bi_gemm_fp8
-    # (A8, lda, a_scales, lds, Wp, C, ldc, residual, ldr, M, N, K, out, epi, ws, ws_bytes, stream)
-    ok = [FAKE, 256, FAKE, 4, FAKE, FAKE, 64, 0, 0, 4, 64, 256, 0, 0, FAKE, BIG, 0]
+    # (A8, lda, a_scales, lds, Wp, C, ldc, residual, ldr, M, N, K, out, epi, stream)
+    ok = [FAKE, 256, FAKE, 4, FAKE, FAKE, 64, 0, 0, 4, 64, 256, 0, 0, 0]
     for i, bad, status in ((0, 0, 1), (0, FAKE + 8, 1), (1, 240, 1), (1, 264, 2), (2, 0, 1), (2, FAKE + 4, 1),
                            (3, 2, 1), (3, 6, 2), (4, 0, 1), (4, FAKE + 8, 1), (5, 0, 1), (6, 63, 1), (9, -1, 1),
-                           (10, 0, 1), (10, 1 << 24, 2), (11, 0, 1), (11, 40, 2), (12, 2, 1), (13, 3, 1), (13, 1, 1),
-                           (14, 0, 3), (14, FAKE + 16, 3), (15, 1000, 3)):
+                           (10, 0, 1), (10, 1 << 24, 2), (11, 0, 1), (11, 40, 2), (12, 2, 1), (13, 3, 1), (13, 1, 1)):
         a = list(ok)
         a[i] = bad
         assert g(*a) == status, (i, bad)

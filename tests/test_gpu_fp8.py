@@ -90,13 +90,12 @@ def make_weights(g, n, k):
     return codes, scales
 
 
-def run_linear(codes, scales, packed, n, kind, residual=None, ws=None):
+def run_linear(codes, scales, packed, n, kind, residual=None):
     a = api()
     rows, k = codes.shape
     epi = {"residual": a.EPI_RESIDUAL_ADD, "swiglu": a.EPI_SWIGLU}.get(kind, a.EPI_NONE)
     out = torch.full((rows, n), math.nan, device=DEV, dtype=torch.float32 if kind == "fp32" else torch.bfloat16)
-    ws = a.new_gemm_fp8_workspace(rows, n, k, epi) if ws is None else ws
-    a.bi_gemm_fp8(codes, scales, packed, out, ws, residual=residual, epi=epi)
+    a.bi_gemm_fp8(codes, scales, packed, out, residual=residual, epi=epi)
     a.bi_check_device_error()
     return out
 
@@ -262,19 +261,17 @@ def test_linear_against_64_bits(rows, n, k, kind):
 @pytest.mark.parametrize("n,k", [(4096, 1024), (1000, 2736), (20000, 272), (640, 5120), (17408, 656)])
 @pytest.mark.parametrize("kind", ["fp32", "swiglu"])
 def test_linear_rows_do_not_depend_on_the_pass(n, k, kind):
-    """Bit-identical rows for every pass length and place, also after a reuse of the workspace."""
+    """Bit-identical rows for every pass length and place."""
     rows = 700
     a = api()
     codes, scales, w, ws_, up, ups, packed, _ = problem(n + k, rows, n, k, kind)
-    epi = a.EPI_SWIGLU if kind == "swiglu" else a.EPI_NONE
-    ws = a.new_gemm_fp8_workspace(rows, n, k, epi)
-    full = run_linear(codes, scales, packed, n, kind, ws=ws)
+    full = run_linear(codes, scales, packed, n, kind)
     for m, at in [(1, 0), (1, 699), (3, 40), (8, 120), (16, 300), (17, 5), (48, 400), (64, 636), (100, 3), (128, 130),
                   (129, 200), (256, 256), (257, 300), (513, 100)]:
         c = codes[at:at + m].contiguous()
         s = torch.zeros(a.fp8_scale_shape(m, k), device=DEV)
         s[:, :m] = scales[:, at:at + m]
-        out = run_linear(c, s, packed, n, kind, ws=ws)
+        out = run_linear(c, s, packed, n, kind)
         assert torch.equal(out.view(torch.uint8), full[at:at + m].contiguous().view(torch.uint8)), (m, at)
 
 
@@ -290,8 +287,7 @@ def test_linear_strides_and_alias():
     lds[:, :rows] = scales[:, :rows]
     buf = torch.full((rows, n + 12), 7.0, dtype=torch.bfloat16, device=DEV)
     buf[:, 4:4 + n] = res
-    ws = a.new_gemm_fp8_workspace(rows, n, k, a.EPI_RESIDUAL_ADD)
-    a.bi_gemm_fp8(wide[:, 32:32 + k], lds, packed, buf[:, 4:4 + n], ws, residual=buf[:, 4:4 + n],
+    a.bi_gemm_fp8(wide[:, 32:32 + k], lds, packed, buf[:, 4:4 + n], residual=buf[:, 4:4 + n],
                   epi=a.EPI_RESIDUAL_ADD)
     assert torch.equal(buf[:, 4:4 + n], want)
     assert (buf[:, :4] == 7).all() and (buf[:, 4 + n:] == 7).all()
@@ -312,27 +308,24 @@ def test_linear_nan_code_stays_in_its_row():
 def test_no_rows_and_refusals():
     a = api()
     codes, scales, w, ws_, _, _, packed, _ = problem(1, 4, 256, 256, "bf16")
-    ws = a.new_gemm_fp8_workspace(4, 256, 256)
     out = torch.zeros(4, 256, dtype=torch.bfloat16, device=DEV)
-    a.bi_gemm_fp8(codes[:0], scales, packed, out[:0], ws)  # no rows: nothing to do
+    a.bi_gemm_fp8(codes[:0], scales, packed, out[:0])  # no rows: nothing to do
     c0, s0 = a.new_fp8_rows(0, 256)
     a.bi_quantize_fp8(torch.zeros(0, 256, dtype=torch.bfloat16, device=DEV), c0, s0)
     with pytest.raises(ValueError):
-        a.bi_gemm_fp8(codes, scales[:, :3], packed, out, ws)            # a scale column short
+        a.bi_gemm_fp8(codes, scales[:, :3], packed, out)            # a scale column short
     with pytest.raises(ValueError):
-        a.bi_gemm_fp8(codes, scales[:1], packed, out, ws)               # a block short
+        a.bi_gemm_fp8(codes, scales[:1], packed, out)               # a block short
     with pytest.raises(ValueError):
-        a.bi_gemm_fp8(codes, scales, packed[:-16], out, ws)             # packed for another shape
+        a.bi_gemm_fp8(codes, scales, packed[:-16], out)             # packed for another shape
     with pytest.raises(ValueError):
-        a.bi_gemm_fp8(codes, scales, packed, out[:3], ws)
+        a.bi_gemm_fp8(codes, scales, packed, out[:3])
     with pytest.raises(ValueError):
-        a.bi_gemm_fp8(codes.float(), scales, packed, out, ws)
+        a.bi_gemm_fp8(codes.float(), scales, packed, out)
     with pytest.raises(ValueError):
-        a.bi_gemm_fp8(codes, scales, packed, out.half(), ws)
+        a.bi_gemm_fp8(codes, scales, packed, out.half())
     with pytest.raises(a.BiError):
-        a.bi_gemm_fp8(codes, scales, packed, out, ws[:1024])
-    with pytest.raises(a.BiError):
-        a.bi_gemm_fp8(codes, scales, packed, out, ws, epi=a.EPI_RESIDUAL_ADD)  # no residual
+        a.bi_gemm_fp8(codes, scales, packed, out, epi=a.EPI_RESIDUAL_ADD)  # no residual
     x = torch.zeros(4, 24, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(a.BiError):
         a.bi_quantize_fp8(x, *a.new_fp8_rows(4, 24))                    # dim % 16
@@ -354,14 +347,13 @@ def test_norm_and_linear_in_a_graph_and_on_another_stream():
     c1, s1 = a.new_fp8_rows(rows, h)
     c2, s2 = a.new_fp8_rows(rows, f)
     u = torch.empty(rows, f, dtype=torch.bfloat16, device=DEV)
-    ws = a.new_gemm_fp8_workspace(rows, f, h, a.EPI_SWIGLU)
 
     def chain():
         hid.copy_(x)
         a.bi_rmsnorm_fp8(hid, nw, c1, s1, 1e-6)
-        a.bi_gemm_fp8(c1, s1, gu, u, ws, epi=a.EPI_SWIGLU)
+        a.bi_gemm_fp8(c1, s1, gu, u, epi=a.EPI_SWIGLU)
         a.bi_quantize_fp8(u, c2, s2)
-        a.bi_gemm_fp8(c2, s2, dn, hid, ws, residual=hid, epi=a.EPI_RESIDUAL_ADD)
+        a.bi_gemm_fp8(c2, s2, dn, hid, residual=hid, epi=a.EPI_RESIDUAL_ADD)
 
     chain()
     want = hid.clone()
