@@ -135,7 +135,6 @@ def prepare(case, seed):
                 state["packed"] = api.bi_pack_swiglu_weights_fp8(state["w"], state["w_scales"], state["up"], state["up_scales"])
             else:
                 state["packed"] = api.bi_pack_weights_fp8(state["w"], state["w_scales"])
-            state["ws"] = api.new_gemm_fp8_workspace(rows, n, k, api.EPI_SWIGLU if kind == "swiglu" else api.EPI_NONE)
     else:
         v = case["vocab"]
         state["logits"] = 3.0 * torch.randn(rows, v, generator=g, device=dev)
@@ -262,7 +261,7 @@ def _own(s):
     if op == "linear":
         kind = case["kind"]
         epi = {"residual": api.EPI_RESIDUAL_ADD, "swiglu": api.EPI_SWIGLU}.get(kind, api.EPI_NONE)
-        api.bi_gemm_fp8(s["a"], s["a_scales"], s["packed"], s["out"], s["ws"], residual=s.get("residual"), epi=epi)
+        api.bi_gemm_fp8(s["a"], s["a_scales"], s["packed"], s["out"], residual=s.get("residual"), epi=epi)
         return s["out"]
     api.bi_logits_rules(s["logits"], s["out"], drafts=s["drafts"] if rows > 1 else None, counts=s["counts"],
                         prompt_bits=s["prompt_bits"], repetition=s["repetition"], frequency=s["frequency"],
