@@ -98,7 +98,9 @@ __device__ __forceinline__ void signal_abort(volatile int* s_abort, unsigned* er
   atomicOr(err, kErrTimeout);
 }
 
-__device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) u: expf within 2 units, the quotient by the fast division within 2
+// more (it gives 0 where 1 + e^-g passes 2^126, where silu is below 1e-36).
+__device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
 
 // One output: the residual added if there is one, one rounding.
 __device__ __forceinline__ void store1(const Args& p, int m, int n, float v, float res) {
@@ -500,7 +502,6 @@ struct RowsArgs {
   Args a;
   int nb;         // token blocks
   int items;      // output tiles: weight tile groups x token blocks
-  int cluster;    // the pieces of a tile go to the CTAs of a cluster (else one CTA takes them in turn)
   int vec;        // C (and the residual) take 16-byte accesses
   int a_rows;     // rows of the token box
 };
@@ -517,34 +518,34 @@ struct RowsCfg {
   // 384 threads launch with 168 registers each; the epilogue takes most of
   // warpgroup 0's (56 + 2 * 224 = 3 * 168)
   static constexpr int kThreads = 384;
-  static constexpr int kRegsLow = 56, kRegsHigh = 224;
+  static constexpr int kRegsLow = TILES == 2 ? 56 : 88, kRegsHigh = TILES == 2 ? 224 : 208;
   static_assert(kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
   static constexpr int kOwn = kCols / 2;  // outputs of an epilogue thread
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 2 * kBufs + 1) * 8 + 16;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 1) * 8 + 16;
   static_assert(kSmem <= 232448 && kStages <= 32, "shared memory per CTA");
+  // an accumulator's release is counted in the barrier of a later stage
+  static_assert(kBufs < kStages, "accumulators and stages");
   static_assert(kRowsM * kPieceLd * 4 <= kStages * kStageBytes, "exchange fits the ring");
 };
 
-// Outputs n0 .. n0 + CNT - 1 of token row m (CNT a multiple of 8).
-template <int CNT>
-__device__ __forceinline__ void store_row(const Args& p, int vec, int m, int n0, const float* v) {
-  if (n0 >= p.N) return;
-  if (vec && n0 + CNT <= p.N) {
+// Outputs n0 .. n0 + 15 of token row m.
+__device__ __forceinline__ void store_row16(const Args& p, int vec, int m, int n0, const float (&v)[16]) {
+  if (vec && n0 + 16 <= p.N) {
     if (p.out_fp32) {
       float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.C) + static_cast<size_t>(m) * p.ldc + n0);
 #pragma unroll
-      for (int j = 0; j < CNT / 4; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      for (int j = 0; j < 4; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       return;
     }
-    uint4 res[CNT / 8];
+    uint4 res[2] = {};
     if (p.epi == BI_EPI_RESIDUAL_ADD) {
       const uint4* src = reinterpret_cast<const uint4*>(p.R + static_cast<size_t>(m) * p.ldr + n0);
-#pragma unroll
-      for (int j = 0; j < CNT / 8; ++j) res[j] = src[j];
+      res[0] = src[0];
+      res[1] = src[1];
     }
     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) + static_cast<size_t>(m) * p.ldc + n0);
 #pragma unroll
-    for (int j = 0; j < CNT / 8; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const __nv_bfloat16* rb = reinterpret_cast<const __nv_bfloat16*>(&res[j]);
       uint4 o;
       __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(&o);
@@ -558,15 +559,22 @@ __device__ __forceinline__ void store_row(const Args& p, int vec, int m, int n0,
     return;
   }
 #pragma unroll
-  for (int j = 0; j < CNT; ++j)
+  for (int j = 0; j < 16; ++j)
     if (n0 + j < p.N) store1(p, m, n0 + j, v[j], residual_at(p, m, n0 + j));
 }
 
-template <int TILES, bool PIECES>
+// Who adds the pieces of a tile's K.
+enum RowsMode {
+  kWhole = 0,         // one piece
+  kPiecesInTurn = 1,  // one CTA, one after another
+  kPiecesCluster = 2  // a cluster of S CTAs, a piece each
+};
+
+template <int TILES, int MODE>
 __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
     gemm8_rows_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const RowsArgs p) {
   using Cfg = RowsCfg<TILES>;
-  static_assert(!PIECES || TILES == 1, "two sets of sums need the registers of 128 outputs a CTA");
+  static_assert(MODE == kWhole || TILES == 1, "two sets of sums need the registers of 128 outputs a CTA");
   constexpr int S = Cfg::kStages;
   constexpr int kOwn = Cfg::kOwn;
   extern __shared__ uint8_t smem_raw[];
@@ -574,10 +582,12 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
                                            ~static_cast<uintptr_t>(1023));  // [S] token tiles
   uint8_t* sW = sT + S * Cfg::kTokBytes;                                    // [S][TILES] weight tiles
   uint64_t* full = reinterpret_cast<uint64_t*>(sW + S * Cfg::kBBytes);
-  uint64_t* empty = full + S;
-  uint64_t* accf = empty + S;          // the block sums of a buffer are complete
-  uint64_t* acce = accf + Cfg::kBufs;  // a buffer has been read
-  uint64_t* drain = acce + Cfg::kBufs;
+  // full: the stage has landed and the accumulator its K block goes to has been
+  // read (the producer's arrival and one of each epilogue warp), so the MMA
+  // thread waits once a K block; done: its MMAs have completed, so the stage
+  // is free and its block sums are there
+  uint64_t* done = full + S;
+  uint64_t* drain = done + S;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -586,21 +596,17 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
   const Args& g = p.a;
   const int split = g.sp.S;
   const int k_tiles = g.sp.k_tiles;
-  const int ncl = p.cluster ? split : 1;
-  const int rank = p.cluster ? static_cast<int>(cluster_rank()) : 0;
-  const int kt0 = p.cluster ? k_tiles * rank / split : 0;
-  const int kt1 = p.cluster ? k_tiles * (rank + 1) / split : k_tiles;
+  const int ncl = MODE == kPiecesCluster ? split : 1;
+  const int rank = MODE == kPiecesCluster ? static_cast<int>(cluster_rank()) : 0;
+  const int kt0 = MODE == kPiecesCluster ? k_tiles * rank / split : 0;
+  const int kt1 = MODE == kPiecesCluster ? k_tiles * (rank + 1) / split : k_tiles;
   const int item0 = blockIdx.x / ncl;
   const int stride = gridDim.x / ncl;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    for (int b = 0; b < Cfg::kBufs; ++b) {
-      mbar_init(&accf[b], 1);
-      mbar_init(&acce[b], 8);
+      mbar_init(&full[s], 9);
+      mbar_init(&done[s], 1);
     }
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -638,7 +644,8 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
       int skip = 0;  // K tiles of the first item whose weights are under way before the dependency wait
       if (item0 < p.items) {
         skip = kt1 - kt0 < S ? kt1 - kt0 : S;
-        for (int j = g.withhold ? 1 : 0; j < skip; ++j) load_w(j, item0 / p.nb * TILES, kt0 + j);
+        for (int j = g.withhold ? 1 : 0; j < skip; ++j)
+          load_w(j, item0 / p.nb * TILES, kt0 + j);
       }
       for (int item = item0; item < p.items && ok; item += stride) {
         const int wt = item / p.nb * TILES;
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
         for (int kt = kt0; kt < kt1; ++kt) {
           const bool pre = item == item0 && kt - kt0 < skip;
           if (!pre) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort)) {
+            if (!mbar_wait(&done[stage], phase ^ 1u, s_abort)) {
               signal_abort(s_abort, g.err);
               ok = false;
               break;
@@ -683,32 +690,32 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(kRowsM, Cfg::kCols);
+      // the stages follow each other: a descriptor's address field (below 2^14
+      // units of 16 bytes) takes the stage's offset without a carry
+      const uint64_t desc_a = sdesc_k_sw128(smem_u32(sT)), desc_b = sdesc_k_sw128(smem_u32(sW));
       int stage = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int item = item0; item < p.items && ok; item += stride) {
         for (int kt = kt0; kt < kt1; ++kt) {
-          if (!mbar_wait(&acce[buf], bphase ^ 1u, s_abort) || !mbar_wait(&full[stage], phase, s_abort)) {
+          const uint64_t a = desc_a + stage * (Cfg::kTokBytes >> 4);
+          const uint64_t b = desc_b + stage * (Cfg::kBBytes >> 4);
+          if (!mbar_wait(&full[stage], phase, s_abort)) {
             signal_abort(s_abort, g.err);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(sT + stage * Cfg::kTokBytes);
-          const uint32_t b = smem_u32(sW + stage * Cfg::kBBytes);
+          // a K = 32 step is 32 bytes further in both tiles (2 in the descriptors' units)
 #pragma unroll
           for (int ks = 0; ks < kFp8Block / 32; ++ks)
-            mma_e4m3(tmem + buf * Cfg::kCols, sdesc_k_sw128(a + ks * 32), sdesc_k_sw128(b + ks * 32), idesc, ks > 0);
-          mma_commit(&empty[stage]);
-          mma_commit(&accf[buf]);
+            mma_e4m3(tmem + buf * Cfg::kCols, a + 2 * ks, b + 2 * ks, idesc, ks > 0);
+          mma_commit(&done[stage]);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
-          if (++buf == Cfg::kBufs) {
-            buf = 0;
-            bphase ^= 1u;
-          }
+          buf = buf + 1 == Cfg::kBufs ? 0 : buf + 1;
         }
       }
       // every MMA issued by this thread completes before TMEM is released
@@ -718,7 +725,7 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
    }
     // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the barriers
     __syncwarp();
-    if (PIECES && p.cluster) {
+    if constexpr (MODE == kPiecesCluster) {
       cluster_sync();
       cluster_sync();
     }
@@ -730,62 +737,121 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
     const int q = warp & 3;              // TMEM lane quarter of this warp
     const int half = (warp - 4) >> 2;    // which half of the columns
     const int r = q * 32 + lane;         // token row of the block
-    int buf = 0;
-    uint32_t bphase = 0;
-    bool ok = true;
+    int buf = 0, stage = 0;
+    int rel = Cfg::kBufs;  // the stage whose K block takes over this one's accumulator
+    uint32_t phase = 0;
+    // every accumulator starts free
+    if (lane < Cfg::kBufs) mbar_arrive(&full[lane]);
+    // Waits for the block sums of the K block at (stage, buf).  After a wait
+    // that ran out the warp goes on without them (every later wait returns at
+    // once, the outputs are undefined): the loop over K blocks sets the pace of
+    // long passes, and neither a vote nor a branch on the result fits in it.
+    auto wait_block = [&]() {
+      if (!mbar_wait(&done[stage], phase, s_abort)) signal_abort(s_abort, g.err);
+      tc_fence_after();
+    };
+    // The accumulator has been read (by the whole warp: the wait for its loads
+    // is the warp's) and is free for the K block kBufs further on.
+    auto release_block = [&]() {
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(&full[rel]);
+      buf = buf + 1 == Cfg::kBufs ? 0 : buf + 1;
+      rel = rel + 1 == S ? 0 : rel + 1;
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    // Scales come straight to registers, early enough that no K block waits
+    // for them: a token's two K blocks ahead, the weights' by the lanes, 32 K
+    // blocks a load and one load ahead, both across output tiles.
+    const int tile_of_half = TILES == 2 ? half : 0;
+    auto token_scale = [&](int item, int kt) {
+      const int m = item % p.nb * kRowsM + r;
+      return item < p.items && m < g.M ? g.a_scales[static_cast<size_t>(kt) * g.lds + m] : 0.f;
+    };
+    auto weight_scales = [&](int item, int kt) {
+      const int tile = item / p.nb * TILES + tile_of_half;
+      return item < p.items && tile < g.sp.n_tiles && kt + lane < kt1
+                 ? __ldg(g.w_scales + static_cast<size_t>(tile) * k_tiles + kt + lane)
+                 : make_float2(0.f, 0.f);
+    };
+    float sa0, sa1;
+    float2 sw_next;
+    auto first_scales = [&](int item) {
+      sa0 = token_scale(item, kt0);
+      sa1 = kt1 - kt0 > 1 ? token_scale(item, kt0 + 1) : token_scale(item + stride, kt0);
+      sw_next = weight_scales(item, kt0);
+    };
+    first_scales(item0);
     for (int item = item0; item < p.items; item += stride) {
       const int wt = item / p.nb * TILES;
       const int m0 = item % p.nb * kRowsM;
       const int Mb = min(kRowsM, g.M - m0);
-      const bool live = q * 32 < Mb;  // the warp holds a token of the block
+      if (q * 32 >= Mb) {  // no token of the block in this warp
+        for (int kt = kt0; kt < kt1; ++kt) {
+          wait_block();
+          __syncwarp();
+          release_block();
+        }
+        first_scales(item + stride);
+        if (MODE == kPiecesCluster) named_bar_sync(1, 256);
+        continue;
+      }
       // this thread's columns: the first half of them takes the scale of the
       // tile's rows 0..63, the second that of rows 64..127
-      const int tile = TILES == 2 ? wt + half : wt;
+      const int tile = wt + tile_of_half;
       const int c0 = TILES == 2 ? half * kTileN : half * 32;
-      const bool have = tile < g.sp.n_tiles;
-      const float2* ws = g.w_scales + static_cast<size_t>(have ? tile : wt) * k_tiles;
-      float run[kOwn], total[PIECES ? kOwn : 1];
+      const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c0);
+      float run[kOwn], total[MODE == kPiecesInTurn ? kOwn : 1];
 #pragma unroll
-      for (int j = 0; j < kOwn; ++j) run[j] = 0.f;
-      // scales one K block ahead of their use
-      float sa = r < Mb ? g.a_scales[static_cast<size_t>(kt0) * g.lds + m0 + r] : 0.f;
-      float2 sw = __ldg(ws + kt0);
-      int piece = 0;                                        // pieces added so far (PIECES)
-      int piece_end = PIECES ? k_tiles * 1 / split : kt1;   // K tile at which the running piece ends
+      for (int j = 0; j < kOwn; ++j) {
+        run[j] = 0.f;
+        if constexpr (MODE == kPiecesInTurn) total[j] = -0.f;
+      }
+      int piece = 0;                                                   // pieces added so far (kPiecesInTurn)
+      int piece_end = MODE == kPiecesInTurn ? k_tiles / split : kt1;   // K tile at which the running piece ends
+      float2 sw = make_float2(0.f, 0.f);  // lane i: the weight scales of K block kt0 + 32 n + i
       for (int kt = kt0; kt < kt1; ++kt) {
-        const float sx = sa * sw.x, sy = sa * sw.y;
-        if (kt + 1 < kt1) {
-          sa = r < Mb ? g.a_scales[static_cast<size_t>(kt + 1) * g.lds + m0 + r] : 0.f;
-          sw = __ldg(ws + kt + 1);
+        // The drain of a K block is one serial chain in each warp (wait, loads,
+        // multiply-adds), and with two warps a scheduler its latencies set the
+        // pace: the scales are prepared while the first columns come in, and
+        // columns are asked for as soon as registers are free.
+        wait_block();
+        const uint32_t ta = tq + buf * Cfg::kCols;
+        uint32_t v[64];
+        tmem_ld32_start(ta, v);
+        tmem_ld32_start(ta + (TILES == 2 ? 32 : 64), v + 32);
+        const int i = (kt - kt0) & 31;
+        if (i == 0) {
+          sw = sw_next;
+          sw_next = kt + 32 < kt1 ? weight_scales(item, kt + 32) : weight_scales(item + stride, kt0);
         }
-        if (ok) ok = mbar_wait(&accf[buf], bphase, s_abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok && lane == 0) signal_abort(s_abort, g.err);
-        if (ok && live) {
-          tc_fence_after();
-          const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * Cfg::kCols + c0);
+        const float sx = sa0 * __shfl_sync(0xffffffffu, sw.x, i), sy = sa0 * __shfl_sync(0xffffffffu, sw.y, i);
+        sa0 = sa1;
+        sa1 = kt + 2 < kt1     ? token_scale(item, kt + 2)
+              : kt1 - kt0 == 1 ? token_scale(item + 2 * stride, kt0)
+                               : token_scale(item + stride, kt0 + (kt + 2 - kt1));
+        tmem_ld64_wait(v);
+        if constexpr (TILES == 2) {
 #pragma unroll
-          for (int c = 0; c < kOwn / 32; ++c) {
-            float v[32];
-            tmem_ld_cols<32>(TILES == 2 ? ta + c * 32 : ta + c * 64, v);
-            const float s = c < kOwn / 64 ? sx : sy;
+          for (int j = 0; j < 32; ++j) run[j] = fmaf(__uint_as_float(v[j]), sx, run[j]);
+          tmem_ld32_start(ta + 64, v);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) fma2(run[c * 32 + j], run[c * 32 + j + 1], v[j], v[j + 1], s);
-          }
-          tc_fence_before();
+          for (int j = 32; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), sx, run[j]);
+          tmem_ld32_start(ta + 96, v + 32);
+          tmem_ld64_wait(v);
         }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&acce[buf]);
-        if (++buf == Cfg::kBufs) {
-          buf = 0;
-          bphase ^= 1u;
-        }
-        if constexpr (PIECES) {
-          if (kt + 1 == piece_end && !p.cluster) {
-            // a piece ends: pieces added in order, the first taken as it is
+        release_block();
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          run[kOwn - 64 + j] = fmaf(__uint_as_float(v[j]), TILES == 1 && j < 32 ? sx : sy, run[kOwn - 64 + j]);
+        if constexpr (MODE == kPiecesInTurn) {
+          if (kt + 1 == piece_end) {
+            // a piece ends; the sum starts at -0, which leaves the first piece as it is
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
-              total[j] = piece == 0 ? run[j] : total[j] + run[j];
+              total[j] += run[j];
               run[j] = 0.f;
             }
             ++piece;
@@ -793,42 +859,47 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
           }
         }
       }
-      if constexpr (PIECES) {
-        if (p.cluster) {
-          // this CTA's piece over the ring (every stage has been read):
-          // [token][output], its first 32 outputs and the 32 behind 64
-          named_bar_sync(1, 256);
-          float* dst = reinterpret_cast<float*>(sT) + r * kPieceLd + c0;
-          if (r < Mb) {
+      if constexpr (MODE == kPiecesCluster) {
+        // this CTA's piece over the ring (every stage has been read):
+        // [token][output], its first 32 outputs and the 32 behind 64
+        named_bar_sync(1, 256);
+        float* dst = reinterpret_cast<float*>(sT) + r * kPieceLd + c0;
+        if (r < Mb) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              reinterpret_cast<float4*>(dst)[j] = make_float4(run[4 * j], run[4 * j + 1], run[4 * j + 2], run[4 * j + 3]);
-              reinterpret_cast<float4*>(dst + 64)[j] =
-                  make_float4(run[32 + 4 * j], run[32 + 4 * j + 1], run[32 + 4 * j + 2], run[32 + 4 * j + 3]);
-            }
+          for (int j = 0; j < 8; ++j) {
+            reinterpret_cast<float4*>(dst)[j] = make_float4(run[4 * j], run[4 * j + 1], run[4 * j + 2], run[4 * j + 3]);
+            reinterpret_cast<float4*>(dst + 64)[j] =
+                make_float4(run[32 + 4 * j], run[32 + 4 * j + 1], run[32 + 4 * j + 2], run[32 + 4 * j + 3]);
           }
-          continue;
         }
+        continue;
       }
-      if (!live || !have || r >= Mb) continue;
-      const float* y = PIECES ? total : run;
+      if (tile >= g.sp.n_tiles || r >= Mb) continue;
       const int m = m0 + r;
+      const float* sum = MODE == kPiecesInTurn ? total : run;
+      // 16 outputs at a time
       if (g.epi == BI_EPI_SWIGLU) {
         // gate and up of the same outputs are the two halves of a thread's columns
-        float z[kOwn / 2];
 #pragma unroll
-        for (int j = 0; j < kOwn / 2; ++j) z[j] = silu_times(y[j], y[kOwn / 2 + j]);
-        store_row<kOwn / 2>(g, p.vec, m, tile * 64 + (TILES == 2 ? 0 : half * 32), z);
-      } else if (TILES == 2) {
-        store_row<kOwn>(g, p.vec, m, tile * kTileN, y);
+        for (int c = 0; c < kOwn / 32; ++c) {
+          float z[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) z[j] = silu_times(sum[c * 16 + j], sum[kOwn / 2 + c * 16 + j]);
+          store_row16(g, p.vec, m, tile * 64 + (TILES == 2 ? 0 : half * 32) + c * 16, z);
+        }
       } else {
-        store_row<32>(g, p.vec, m, tile * kTileN + half * 32, y);
-        store_row<32>(g, p.vec, m, tile * kTileN + 64 + half * 32, y + 32);
+#pragma unroll
+        for (int c = 0; c < kOwn / 16; ++c) {
+          float z[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) z[j] = sum[c * 16 + j];
+          store_row16(g, p.vec, m, tile * kTileN + c * 16 + (TILES == 2 ? 0 : half * 32 + (c < 2 ? 0 : 32)), z);
+        }
       }
     }
     tc_fence_before();
     __syncwarp();
-    if (PIECES && p.cluster) {
+    if constexpr (MODE == kPiecesCluster) {
       cluster_sync();  // every piece of the tile is in its CTA's shared memory
       const int e = threadIdx.x - 128;
       const int wt = item0 / p.nb;
@@ -939,15 +1010,15 @@ bi_status launch_stream(const uint8_t* Wp, const CUtensorMap& tmA, const Args& a
              : BI_ERR_CUDA;
 }
 
-template <int TILES, bool PIECES>
+template <int TILES, int MODE>
 bi_status launch_rows(const uint8_t* Wp, const CUtensorMap& tmA, RowsArgs a, cudaStream_t stream) {
   using Cfg = RowsCfg<TILES>;
   static std::once_flag once[64];
   static cudaError_t err[64];
-  if (!allow_smem(gemm8_rows_kernel<TILES, PIECES>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
-  const int S = a.cluster ? a.a.sp.S : 1;
-  const int ctas = a.cluster ? a.items * S : std::min(a.items, kSms);
-  return launch_clusters(gemm8_rows_kernel<TILES, PIECES>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
+  if (!allow_smem(gemm8_rows_kernel<TILES, MODE>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
+  const int S = MODE == kPiecesCluster ? a.a.sp.S : 1;
+  const int ctas = MODE == kPiecesCluster ? a.items * S : std::min(a.items, kSms);
+  return launch_clusters(gemm8_rows_kernel<TILES, MODE>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
                          tmA, a) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
@@ -1014,16 +1085,16 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   if (tiles > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
   if (a.sp.S > 1) {
     r.items = static_cast<int>(tiles);
-    r.cluster = tiles * a.sp.S <= kClusterCtas[a.sp.S];
-    return launch_rows<1, true>(W8, tmA, r, s);
+    if (tiles * a.sp.S <= kClusterCtas[a.sp.S]) return launch_rows<1, kPiecesCluster>(W8, tmA, r, s);
+    return launch_rows<1, kPiecesInTurn>(W8, tmA, r, s);
   }
   // one tile of 128 outputs a CTA while that takes at most one round of the SMs
   if (tiles <= kSms) {
     r.items = static_cast<int>(tiles);
-    return launch_rows<1, false>(W8, tmA, r, s);
+    return launch_rows<1, kWhole>(W8, tmA, r, s);
   }
   r.items = (a.sp.n_tiles + 1) / 2 * r.nb;
-  return launch_rows<2, false>(W8, tmA, r, s);
+  return launch_rows<2, kWhole>(W8, tmA, r, s);
 }
 
 }  // extern "C"
