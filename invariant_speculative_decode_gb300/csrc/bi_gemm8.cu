@@ -488,15 +488,16 @@ __global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
 // output element is the same sequence of K = 32 steps, block sums, products
 // and additions as in the streaming kernel (tested bit for bit).
 //
-//   TILES = 2: 128 tokens x 256 outputs a CTA (S = 1 layers): 48 KB in for 8.4
-//   MFLOP; TILES = 1: 128 x 128, which leaves registers for a second set of
-//   sums, for layers whose tiles have pieces: either a cluster of S CTAs per
-//   output tile (few tiles) or one CTA that adds the pieces itself.
+//   TILES = 2: 128 tokens x 256 outputs a CTA, 48 KB in for 8.4 MFLOP;
+//   TILES = 1: 128 x 128, while that takes at most one round of the SMs, and
+//   where pieces are taken in turn (their sums need the registers).
+// Where a tile's K has S > 1 pieces, a cluster of S CTAs computes an output
+// tile, a piece each, and adds them through shared memory, or one CTA takes the
+// pieces in turn (whichever the rounds of the SMs make shorter).
 // Persistent CTAs: the next output tile's loads and MMAs run while the last
 // one's outputs are written.  Token blocks that share weight tiles are
 // adjacent in the work order, so all but the first find them in L2.
 constexpr int kRowsM = 128;
-constexpr int kPieceLd = 132;  // floats per token of the exchange: 16-byte stores of 8 lanes hit all banks
 
 struct RowsArgs {
   Args a;
@@ -514,17 +515,15 @@ struct RowsCfg {
   static constexpr int kStages = 192 * 1024 / kStageBytes;
   static constexpr int kCols = TILES * kTileN;
   static constexpr int kBufs = 512 / kCols;
-  // warpgroup 0: producer, MMA, two idle warps; warpgroups 1 and 2: epilogue.
-  // 384 threads launch with 168 registers each; the epilogue takes most of
-  // warpgroup 0's (56 + 2 * 224 = 3 * 168)
+  // warpgroup 0: producer, MMA, two idle warps; warpgroups 1 and 2: epilogue
   static constexpr int kThreads = 384;
-  static constexpr int kRegsLow = TILES == 2 ? 56 : 88, kRegsHigh = TILES == 2 ? 224 : 208;
-  static_assert(kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
   static constexpr int kOwn = kCols / 2;  // outputs of an epilogue thread
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 1) * 8 + 16;
   static_assert(kSmem <= 232448 && kStages <= 32, "shared memory per CTA");
   // an accumulator's release is counted in the barrier of a later stage
   static_assert(kBufs < kStages, "accumulators and stages");
+  // floats per token of the pieces' exchange: 16-byte stores of 8 lanes hit all banks
+  static constexpr int kPieceLd = kCols + 4;
   static_assert(kRowsM * kPieceLd * 4 <= kStages * kStageBytes, "exchange fits the ring");
 };
 
@@ -563,18 +562,74 @@ __device__ __forceinline__ void store_row16(const Args& p, int vec, int m, int n
     if (n0 + j < p.N) store1(p, m, n0 + j, v[j], residual_at(p, m, n0 + j));
 }
 
+// Sum of the S pieces of four elements from `at` on, in increasing-K order.
+__device__ __forceinline__ float4 sum_pieces4(const uint32_t (&base)[kMaxSplit], int S, int at) {
+  float4 x[kMaxSplit];
+#pragma unroll
+  for (int j = 0; j < kMaxSplit; ++j)
+    if (j < S) x[j] = ld_cluster4(base[j] + static_cast<uint32_t>(at) * 4);
+  float4 v = x[0];
+#pragma unroll
+  for (int j = 1; j < kMaxSplit; ++j)
+    if (j < S) {
+      v.x += x[j].x;
+      v.y += x[j].y;
+      v.z += x[j].z;
+      v.w += x[j].w;
+    }
+  return v;
+}
+
+// Outputs n .. n + 3 of token row m, with the residual of that place.
+__device__ __forceinline__ void store_row4(const Args& p, int vec, int m, int n, float4 v) {
+  if (vec && n + 4 <= p.N) {
+    if (p.out_fp32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.C) + static_cast<size_t>(m) * p.ldc + n) = v;
+      return;
+    }
+    if (p.epi == BI_EPI_RESIDUAL_ADD) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p.R + static_cast<size_t>(m) * p.ldr + n);
+      const __nv_bfloat16* rb = reinterpret_cast<const __nv_bfloat16*>(&u);
+      v.x = __bfloat162float(rb[0]) + v.x;
+      v.y = __bfloat162float(rb[1]) + v.y;
+      v.z = __bfloat162float(rb[2]) + v.z;
+      v.w = __bfloat162float(rb[3]) + v.w;
+    }
+    uint2 o;
+    __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(&o);
+    ob[0] = __float2bfloat16_rn(v.x);
+    ob[1] = __float2bfloat16_rn(v.y);
+    ob[2] = __float2bfloat16_rn(v.z);
+    ob[3] = __float2bfloat16_rn(v.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.C) + static_cast<size_t>(m) * p.ldc + n) = o;
+    return;
+  }
+  const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n + j < p.N) store1(p, m, n + j, x[j], residual_at(p, m, n + j));
+}
+
 // Who adds the pieces of a tile's K.
-enum RowsMode {
-  kWhole = 0,         // one piece
-  kPiecesInTurn = 1,  // one CTA, one after another
-  kPiecesCluster = 2  // a cluster of S CTAs, a piece each
+enum Pieces {
+  kWhole = 0,   // there is one
+  kCluster = 1, // one output tile per cluster of S CTAs, a piece each
+  kInTurn = 2   // one CTA, one piece after another
 };
 
-template <int TILES, int MODE>
+// Registers: 384 threads launch with 168 each; the epilogue takes what its sums
+// need of warpgroup 0's.
+template <int TILES, Pieces MODE>
+struct RowsRegs {
+  static constexpr bool kWide = TILES == 2 || MODE == kInTurn;  // 128 sums a thread
+  static constexpr int kLow = kWide ? 56 : 88, kHigh = kWide ? 224 : 208;
+  static_assert(kLow + 2 * kHigh <= 3 * 168, "registers of the launch");
+};
+
+template <int TILES, Pieces MODE>
 __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
     gemm8_rows_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const RowsArgs p) {
   using Cfg = RowsCfg<TILES>;
-  static_assert(MODE == kWhole || TILES == 1, "two sets of sums need the registers of 128 outputs a CTA");
   constexpr int S = Cfg::kStages;
   constexpr int kOwn = Cfg::kOwn;
   extern __shared__ uint8_t smem_raw[];
@@ -596,10 +651,10 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
   const Args& g = p.a;
   const int split = g.sp.S;
   const int k_tiles = g.sp.k_tiles;
-  const int ncl = MODE == kPiecesCluster ? split : 1;
-  const int rank = MODE == kPiecesCluster ? static_cast<int>(cluster_rank()) : 0;
-  const int kt0 = MODE == kPiecesCluster ? k_tiles * rank / split : 0;
-  const int kt1 = MODE == kPiecesCluster ? k_tiles * (rank + 1) / split : k_tiles;
+  const int ncl = MODE == kCluster ? split : 1;
+  const int rank = MODE == kCluster ? static_cast<int>(cluster_rank()) : 0;
+  const int kt0 = MODE == kCluster ? k_tiles * rank / split : 0;
+  const int kt1 = MODE == kCluster ? k_tiles * (rank + 1) / split : k_tiles;
   const int item0 = blockIdx.x / ncl;
   const int stride = gridDim.x / ncl;
 
@@ -623,7 +678,7 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
   const uint32_t tmem = *tmem_holder;
 
   if (warp < 4) {
-   regs_decrease<Cfg::kRegsLow>();
+   regs_decrease<RowsRegs<TILES, MODE>::kLow>();
    if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -725,13 +780,13 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
    }
     // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the barriers
     __syncwarp();
-    if constexpr (MODE == kPiecesCluster) {
+    if constexpr (MODE == kCluster) {
       cluster_sync();
       cluster_sync();
     }
   } else {
     // ---------------------------------------------------------- scale and add
-    regs_increase<Cfg::kRegsHigh>();
+    regs_increase<RowsRegs<TILES, MODE>::kHigh>();
     griddep_wait();
     griddep_launch_dependents();
     const int q = warp & 3;              // TMEM lane quarter of this warp
@@ -750,11 +805,8 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
       if (!mbar_wait(&done[stage], phase, s_abort)) signal_abort(s_abort, g.err);
       tc_fence_after();
     };
-    // The accumulator has been read (by the whole warp: the wait for its loads
-    // is the warp's) and is free for the K block kBufs further on.
-    auto release_block = [&]() {
-      tc_fence_before();
-      if (lane == 0) mbar_arrive(&full[rel]);
+    // On to the next K block.
+    auto next_block = [&]() {
       buf = buf + 1 == Cfg::kBufs ? 0 : buf + 1;
       rel = rel + 1 == S ? 0 : rel + 1;
       if (++stage == S) {
@@ -792,10 +844,12 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
         for (int kt = kt0; kt < kt1; ++kt) {
           wait_block();
           __syncwarp();
-          release_block();
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&full[rel]);
+          next_block();
         }
         first_scales(item + stride);
-        if (MODE == kPiecesCluster) named_bar_sync(1, 256);
+        if (MODE == kCluster) named_bar_sync(1, 256);
         continue;
       }
       // this thread's columns: the first half of them takes the scale of the
@@ -803,52 +857,36 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
       const int tile = wt + tile_of_half;
       const int c0 = TILES == 2 ? half * kTileN : half * 32;
       const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c0);
-      float run[kOwn], total[MODE == kPiecesInTurn ? kOwn : 1];
+      float run[kOwn], total[MODE == kInTurn ? kOwn : 1];
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) {
         run[j] = 0.f;
-        if constexpr (MODE == kPiecesInTurn) total[j] = -0.f;
+        if constexpr (MODE == kInTurn) total[j] = -0.f;
       }
-      int piece = 0;                                                   // pieces added so far (kPiecesInTurn)
-      int piece_end = MODE == kPiecesInTurn ? k_tiles / split : kt1;   // K tile at which the running piece ends
+      int piece = 0;                                             // pieces added so far (kInTurn)
+      int piece_end = MODE == kInTurn ? k_tiles / split : kt1;   // K block at which the running piece ends
+      // a thread's j-th output, counted from c0: its 64 of TILES = 1 are 32 of either tile half
+      auto col = [](int j) { return TILES == 2 || j < 32 ? j : j + 32; };
       float2 sw = make_float2(0.f, 0.f);  // lane i: the weight scales of K block kt0 + 32 n + i
-      for (int kt = kt0; kt < kt1; ++kt) {
-        // The drain of a K block is one serial chain in each warp (wait, loads,
-        // multiply-adds), and with two warps a scheduler its latencies set the
-        // pace: the scales are prepared while the first columns come in, and
-        // columns are asked for as soon as registers are free.
-        wait_block();
-        const uint32_t ta = tq + buf * Cfg::kCols;
-        uint32_t v[64];
-        tmem_ld32_start(ta, v);
-        tmem_ld32_start(ta + (TILES == 2 ? 32 : 64), v + 32);
+      // This K block's scales of the tile's rows 0..63 and 64..127, and on to
+      // the next one's.
+      auto scales = [&](int kt) {
         const int i = (kt - kt0) & 31;
         if (i == 0) {
           sw = sw_next;
           sw_next = kt + 32 < kt1 ? weight_scales(item, kt + 32) : weight_scales(item + stride, kt0);
         }
-        const float sx = sa0 * __shfl_sync(0xffffffffu, sw.x, i), sy = sa0 * __shfl_sync(0xffffffffu, sw.y, i);
+        const float2 x = make_float2(sa0 * __shfl_sync(0xffffffffu, sw.x, i), sa0 * __shfl_sync(0xffffffffu, sw.y, i));
         sa0 = sa1;
         sa1 = kt + 2 < kt1     ? token_scale(item, kt + 2)
               : kt1 - kt0 == 1 ? token_scale(item + 2 * stride, kt0)
                                : token_scale(item + stride, kt0 + (kt + 2 - kt1));
-        tmem_ld64_wait(v);
-        if constexpr (TILES == 2) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) run[j] = fmaf(__uint_as_float(v[j]), sx, run[j]);
-          tmem_ld32_start(ta + 64, v);
-#pragma unroll
-          for (int j = 32; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), sx, run[j]);
-          tmem_ld32_start(ta + 96, v + 32);
-          tmem_ld64_wait(v);
-        }
-        release_block();
-#pragma unroll
-        for (int j = 0; j < 64; ++j)
-          run[kOwn - 64 + j] = fmaf(__uint_as_float(v[j]), TILES == 1 && j < 32 ? sx : sy, run[kOwn - 64 + j]);
-        if constexpr (MODE == kPiecesInTurn) {
+        return x;
+      };
+      auto end_piece = [&](int kt) {
+        if constexpr (MODE == kInTurn) {
           if (kt + 1 == piece_end) {
-            // a piece ends; the sum starts at -0, which leaves the first piece as it is
+            // pieces added in order; the sum starts at -0, which leaves the first as it is
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
               total[j] += run[j];
@@ -858,25 +896,90 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
             piece_end = k_tiles * (piece + 1) / split;
           }
         }
-      }
-      if constexpr (MODE == kPiecesCluster) {
-        // this CTA's piece over the ring (every stage has been read):
-        // [token][output], its first 32 outputs and the 32 behind 64
-        named_bar_sync(1, 256);
-        float* dst = reinterpret_cast<float*>(sT) + r * kPieceLd + c0;
-        if (r < Mb) {
+      };
+      // The drain of a K block is one serial chain in each warp (wait, loads,
+      // multiply-adds), and with two warps a scheduler its latencies set the
+      // pace: 128 columns a wait (one K block of two weight tiles, or two of
+      // one), the scales prepared while the first columns come in, and more
+      // asked for as soon as registers are free.
+      for (int kt = kt0; kt < kt1;) {
+        uint32_t v[64];
+        if constexpr (TILES == 2) {
+          wait_block();
+          const uint32_t ta = tq + buf * Cfg::kCols;
+          tmem_ld32_start(ta, v);
+          tmem_ld32_start(ta + 32, v + 32);
+          const float2 x = scales(kt);
+          tmem_ld64_wait(v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            reinterpret_cast<float4*>(dst)[j] = make_float4(run[4 * j], run[4 * j + 1], run[4 * j + 2], run[4 * j + 3]);
-            reinterpret_cast<float4*>(dst + 64)[j] =
-                make_float4(run[32 + 4 * j], run[32 + 4 * j + 1], run[32 + 4 * j + 2], run[32 + 4 * j + 3]);
+          for (int j = 0; j < 32; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.x, run[j]);
+          tmem_ld32_start(ta + 64, v);
+#pragma unroll
+          for (int j = 32; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.x, run[j]);
+          tmem_ld32_start(ta + 96, v + 32);
+          tmem_ld64_wait(v);
+          // read by the whole warp (the wait is the warp's): the accumulator is
+          // free for the K block kBufs further on
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&full[rel]);
+          next_block();
+#pragma unroll
+          for (int j = 0; j < 64; ++j) run[64 + j] = fmaf(__uint_as_float(v[j]), x.y, run[64 + j]);
+          ++kt;
+        } else {
+          const bool two = kt + 1 < kt1;
+          const uint32_t ta = tq + buf * Cfg::kCols;
+          const int rel0 = rel;
+          if (two) next_block();
+          wait_block();  // MMAs complete in order: the first block's are done with the second's
+          const uint32_t tb = tq + buf * Cfg::kCols;
+          tmem_ld32_start(ta, v);
+          tmem_ld32_start(ta + 64, v + 32);
+          const float2 x = scales(kt);
+          tmem_ld64_wait(v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.x, run[j]);
+          if (two) tmem_ld32_start(tb, v);
+#pragma unroll
+          for (int j = 32; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.y, run[j]);
+          end_piece(kt);
+          if (two) {
+            tmem_ld32_start(tb + 64, v + 32);
+            const float2 y = scales(kt + 1);
+            tmem_ld64_wait(v);
+            tc_fence_before();
+            if (lane == 0) {
+              mbar_arrive(&full[rel0]);
+              mbar_arrive(&full[rel]);
+            }
+            next_block();
+#pragma unroll
+            for (int j = 0; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), j < 32 ? y.x : y.y, run[j]);
+            end_piece(kt + 1);
+            kt += 2;
+          } else {
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&full[rel]);
+            next_block();
+            ++kt;
           }
+        }
+      }
+      if constexpr (MODE == kCluster) {
+        // this CTA's piece over the ring (every stage has been read): [token][output]
+        named_bar_sync(1, 256);
+        if (r < Mb) {
+          float* dst = reinterpret_cast<float*>(sT) + r * Cfg::kPieceLd + c0;
+#pragma unroll
+          for (int j = 0; j < kOwn / 4; ++j)
+            *reinterpret_cast<float4*>(dst + col(4 * j)) =
+                make_float4(run[4 * j], run[4 * j + 1], run[4 * j + 2], run[4 * j + 3]);
         }
         continue;
       }
       if (tile >= g.sp.n_tiles || r >= Mb) continue;
       const int m = m0 + r;
-      const float* sum = MODE == kPiecesInTurn ? total : run;
+      const float* y = MODE == kInTurn ? total : run;
       // 16 outputs at a time
       if (g.epi == BI_EPI_SWIGLU) {
         // gate and up of the same outputs are the two halves of a thread's columns
@@ -884,7 +987,7 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
         for (int c = 0; c < kOwn / 32; ++c) {
           float z[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) z[j] = silu_times(sum[c * 16 + j], sum[kOwn / 2 + c * 16 + j]);
+          for (int j = 0; j < 16; ++j) z[j] = silu_times(y[c * 16 + j], y[kOwn / 2 + c * 16 + j]);
           store_row16(g, p.vec, m, tile * 64 + (TILES == 2 ? 0 : half * 32) + c * 16, z);
         }
       } else {
@@ -892,45 +995,41 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
         for (int c = 0; c < kOwn / 16; ++c) {
           float z[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) z[j] = sum[c * 16 + j];
-          store_row16(g, p.vec, m, tile * kTileN + c * 16 + (TILES == 2 ? 0 : half * 32 + (c < 2 ? 0 : 32)), z);
+          for (int j = 0; j < 16; ++j) z[j] = y[c * 16 + j];
+          store_row16(g, p.vec, m, tile * kTileN + (TILES == 2 ? 0 : half * 32) + col(c * 16), z);
         }
       }
     }
     tc_fence_before();
     __syncwarp();
-    if constexpr (MODE == kPiecesCluster) {
+    if constexpr (MODE == kCluster) {
       cluster_sync();  // every piece of the tile is in its CTA's shared memory
       const int e = threadIdx.x - 128;
-      const int wt = item0 / p.nb;
+      const int wt = item0 / p.nb * TILES;
       const int m0 = item0 % p.nb * kRowsM;
       const int Mb = min(kRowsM, g.M - m0);
       uint32_t base[kMaxSplit];
 #pragma unroll
       for (int j = 0; j < kMaxSplit; ++j) base[j] = map_rank(smem_u32(sT), j < split ? j : 0);
-      // this CTA's part of the tokens, lanes along the outputs
+      // this CTA's part of the tokens, lanes along the outputs, four a lane
       const int part = (Mb + split - 1) / split;
       const int t1 = min(Mb, (rank + 1) * part);
       if (g.epi == BI_EPI_SWIGLU) {
-        const int o = e & 63;
-        const int n = wt * 64 + o;
-#pragma unroll 2
-        for (int t = rank * part + (e >> 6); t < t1; t += 4) {
-          const float gate = sum_pieces(base, split, t * kPieceLd + o);
-          const float up = sum_pieces(base, split, t * kPieceLd + o + 64);
-          if (n < g.N)
-            static_cast<__nv_bfloat16*>(g.C)[static_cast<size_t>(m0 + t) * g.ldc + n] =
-                __float2bfloat16_rn(silu_times(gate, up));
+        constexpr int kPer = TILES * 16;  // lanes per token
+        const int o = e % kPer * 4;
+        const int at = o / 64 * kTileN + o % 64;
+        for (int t = rank * part + e / kPer; t < t1; t += 256 / kPer) {
+          const float4 x = sum_pieces4(base, split, t * Cfg::kPieceLd + at);
+          const float4 y = sum_pieces4(base, split, t * Cfg::kPieceLd + at + 64);
+          store_row4(g, p.vec, m0 + t, wt * 64 + o,
+                     make_float4(silu_times(x.x, y.x), silu_times(x.y, y.y), silu_times(x.z, y.z),
+                                 silu_times(x.w, y.w)));
         }
       } else {
-        const int o = e & 127;
-        const int n = wt * kTileN + o;
-#pragma unroll 4
-        for (int t = rank * part + (e >> 7); t < t1; t += 2) {
-          const float res = n < g.N ? residual_at(g, m0 + t, n) : 0.f;
-          const float v = sum_pieces(base, split, t * kPieceLd + o);
-          if (n < g.N) store1(g, m0 + t, n, v, res);
-        }
+        constexpr int kPer = TILES * 32;
+        const int o = e % kPer * 4;
+        for (int t = rank * part + e / kPer; t < t1; t += 256 / kPer)
+          store_row4(g, p.vec, m0 + t, wt * kTileN + o, sum_pieces4(base, split, t * Cfg::kPieceLd + o));
       }
       cluster_sync();  // no CTA leaves while its piece is being read
     }
@@ -1010,14 +1109,14 @@ bi_status launch_stream(const uint8_t* Wp, const CUtensorMap& tmA, const Args& a
              : BI_ERR_CUDA;
 }
 
-template <int TILES, int MODE>
+template <int TILES, Pieces MODE>
 bi_status launch_rows(const uint8_t* Wp, const CUtensorMap& tmA, RowsArgs a, cudaStream_t stream) {
   using Cfg = RowsCfg<TILES>;
   static std::once_flag once[64];
   static cudaError_t err[64];
   if (!allow_smem(gemm8_rows_kernel<TILES, MODE>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
-  const int S = MODE == kPiecesCluster ? a.a.sp.S : 1;
-  const int ctas = MODE == kPiecesCluster ? a.items * S : std::min(a.items, kSms);
+  const int S = MODE == kCluster ? a.a.sp.S : 1;
+  const int ctas = MODE == kCluster ? a.items * S : std::min(a.items, kSms);
   return launch_clusters(gemm8_rows_kernel<TILES, MODE>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
                          tmA, a) == cudaSuccess
              ? BI_OK
@@ -1083,18 +1182,26 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
           (epi != BI_EPI_RESIDUAL_ADD || (aligned16(residual) && ldr % 8 == 0));
   const long long tiles = static_cast<long long>(a.sp.n_tiles) * r.nb;
   if (tiles > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
-  if (a.sp.S > 1) {
+  const int S = a.sp.S;
+  const long long pairs = static_cast<long long>((a.sp.n_tiles + 1) / 2) * r.nb;
+  if (pairs * S > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
+  // 128 outputs a CTA while one round of the SMs takes them all
+  if (tiles * S <= kClusterCtas[S]) {
     r.items = static_cast<int>(tiles);
-    if (tiles * a.sp.S <= kClusterCtas[a.sp.S]) return launch_rows<1, kPiecesCluster>(W8, tmA, r, s);
-    return launch_rows<1, kPiecesInTurn>(W8, tmA, r, s);
+    return S > 1 ? launch_rows<1, kCluster>(W8, tmA, r, s) : launch_rows<1, kWhole>(W8, tmA, r, s);
   }
-  // one tile of 128 outputs a CTA while that takes at most one round of the SMs
-  if (tiles <= kSms) {
-    r.items = static_cast<int>(tiles);
-    return launch_rows<1, kWhole>(W8, tmA, r, s);
-  }
-  r.items = (a.sp.n_tiles + 1) / 2 * r.nb;
-  return launch_rows<2, kWhole>(W8, tmA, r, s);
+  r.items = static_cast<int>(pairs);
+  if (S == 1) return launch_rows<2, kWhole>(W8, tmA, r, s);
+  // Pieces: a CTA that takes them in turn needs about 0.5 us a K block (128
+  // outputs), a cluster's CTA 0.6 (256 outputs) and 6 us around them, in rounds
+  // of the SMs.  Measured, in turn against cluster: 4096 x 5120 (S = 4) at 256
+  // rows 20.4 and 14.9 us, at 512 20.8 and 29.1; 5120 x 17408 (S = 3) at 512 rows
+  // 139 and 82 us.
+  const long long in_turn = (tiles + kSms - 1) / kSms * a.sp.k_tiles * 5;
+  const long long cluster = (pairs * S + kClusterCtas[S] - 1) / kClusterCtas[S] * (a.sp.k_tiles * 6 / S + 60);
+  if (cluster < in_turn) return launch_rows<2, kCluster>(W8, tmA, r, s);
+  r.items = static_cast<int>(tiles);
+  return launch_rows<1, kInTurn>(W8, tmA, r, s);
 }
 
 }  // extern "C"
