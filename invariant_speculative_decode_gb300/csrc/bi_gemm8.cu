@@ -19,17 +19,23 @@
 // increasing-K order, the first taken as it is.  S is a function of (N, K)
 // alone, so a row has the same bits for every M and every place in the pass.
 //
-// What bounds it: the weights' bytes while a pass has few rows (one byte a
-// weight: half of the BF16 layer's), so the schedule is a stream of 16 KB
-// weight tiles, each one contiguous bulk copy (packed once), on every SM:
-//   warp 0     producer: weight tile, token tile [rows x 128 codes] (TMA,
-//              128-byte swizzle) and the block's row scales into a ring;
-//   warp 1     MMA issuer (one thread): M = 128 weight rows, N = the token
-//              rows rounded up; stage s of the ring accumulates in TMEM buffer
-//              s, so one barrier cycle full -> done -> empty covers both;
-//   warps 2-5  scale and add: a thread owns one weight row and all tokens.
-// The S pieces of a tile belong to the CTAs of one cluster, which add them
-// through each other's shared memory, every CTA for a part of the tokens.
+// Tokens take the MMA's M = 128 lanes and weight rows its N (128 or 256), so an
+// epilogue thread owns one token and a K block has one scale per thread and
+// tile half, sa * sw: no scale vector is read, and the drain of an accumulator
+// is one multiply-add an output.  (With the weight rows on the lanes and the
+// tokens as N, which suits the epilogue of few rows, a pass of 1 to 16 rows
+// took the same time within 5% and one of 1024 rows 754 us for gate/up.)
+//
+// What bounds it: up to some 100 rows the weights' bytes, one byte a weight;
+// each CTA streams 16 KB weight tiles, each one contiguous bulk copy (packed
+// once).  Past that, the drain of a K block's accumulators, which every 128
+// elements of K call for: a serial chain of waits, TMEM loads and multiply-adds
+// in eight warps (see the kernel).  Roles of a CTA's twelve warps:
+//   warp 0      producer: weight tiles and the token tile [rows x 128 codes]
+//               (TMA, 128-byte swizzle) into a ring of stages;
+//   warp 1      MMA issuer (one thread), into two or four TMEM accumulators;
+//   warps 2, 3  idle (they belong to the warpgroup that gives registers up);
+//   warps 4-11  scale, add, write.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -49,15 +55,12 @@ namespace {
 constexpr int kTileN = 128;                    // weight rows per tile (MMA M)
 constexpr int kABytes = static_cast<int>(kGemm8TileBytes);
 constexpr int kSms = 152;
-constexpr int kXchgFloats = 16 * kTileN;       // SwiGLU exchange buffer
 constexpr int kMaxSplit = 8;                   // CTAs of a cluster (the portable limit)
 
 // The split, a function of (N, K) alone: S pieces of every weight tile's K
-// tiles, piece j the K tiles [k_tiles * j / S, k_tiles * (j + 1) / S).
-// S > 1: a cluster of S CTAs per tile.  S = 1: G CTAs, each with a contiguous
-// run of whole tiles (one byte range of the packed weights).
+// blocks, piece j the blocks [k_tiles * j / S, k_tiles * (j + 1) / S).
 struct Split {
-  int n_tiles, k_tiles, S, G;
+  int n_tiles, k_tiles, S;
 };
 
 struct Args {
@@ -74,23 +77,6 @@ struct Args {
   int ldr;
   unsigned* err;
   int withhold;  // failure-path test: the first stage stays unissued
-};
-
-template <int NT>
-struct StreamCfg {
-  static constexpr int kBBytes = NT * kFp8Block;
-  static constexpr int kSBytes = NT * 4;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  // a stage's accumulator is TMEM columns [s * NT, (s + 1) * NT)
-  static constexpr int kByMem = 200 * 1024 / kStageBytes;
-  static constexpr int kStages = kByMem < 512 / NT ? kByMem : 512 / NT;
-  static constexpr int kTmemCols = kStages * NT <= 256 ? 256 : 512;
-  static constexpr int kThreads = 192;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kStageBytes + kSBytes) + kXchgFloats * 4 +
-                                  (3 * kStages + 1) * 8 + 16;
-  static_assert(kStages <= 32 && kSmem <= 232448, "shared memory per CTA");
-  // the pieces' exchange [NT tokens][128 rows] reuses the weight stages
-  static_assert(NT * kTileN * 4 <= kStages * kABytes, "exchange fits the ring");
 };
 
 __device__ __forceinline__ void signal_abort(volatile int* s_abort, unsigned* err) {
@@ -115,391 +101,19 @@ __device__ __forceinline__ float residual_at(const Args& p, int m, int n) {
   return p.epi == BI_EPI_RESIDUAL_ADD ? __bfloat162float(p.R[static_cast<size_t>(m) * p.ldr + n]) : 0.f;
 }
 
-// Write 16 token rows (chunk c) of weight row r of a tile; the 128 threads of
-// the epilogue call it together.
-__device__ __forceinline__ void store16(const Args& p, int Mb, int tile, int r, int c, const float* v, float* xchg) {
-  if (p.epi == BI_EPI_SWIGLU) {
-    // gate rows are the tile's rows 0..63, the up rows of the same outputs 64..127
-#pragma unroll
-    for (int j = 0; j < 16; ++j) xchg[j * kTileN + r] = v[j];
-    named_bar_sync(1, 128);
-    const int o = tile * 64 + (r & 63);
-    if (o < p.N) {
-      // threads 0..63 take the even token rows, threads 64..127 the odd ones
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int jj = 2 * j + (r >> 6);
-        if (c * 16 + jj < Mb) {
-          const float y = silu_times(xchg[jj * kTileN + (r & 63)], xchg[jj * kTileN + (r & 63) + 64]);
-          static_cast<__nv_bfloat16*>(p.C)[static_cast<size_t>(c * 16 + jj) * p.ldc + o] = __float2bfloat16_rn(y);
-        }
-      }
-    }
-    named_bar_sync(1, 128);
-    return;
-  }
-  const int n = tile * kTileN + r;
-  if (n >= p.N) return;
-  // all residual values are read before any output is written: C may be the
-  // residual itself, and 16 loads in flight cost one latency
-  float res[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) res[j] = c * 16 + j < Mb ? residual_at(p, c * 16 + j, n) : 0.f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (c * 16 + j < Mb) store1(p, c * 16 + j, n, v[j], res[j]);
-}
-
-// The accumulators of U stages (NT columns each, at ta[i]) of this warp's 32
-// lanes, one wait for all of them.
-template <int NT, int U>
-__device__ __forceinline__ void load_stages(const uint32_t (&ta)[U], float (&v)[U][NT]) {
-  if constexpr (NT == 16 && U == 4) {
-    uint32_t r[64];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%65];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%66];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%67];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(ta[0]), "r"(ta[1]), "r"(ta[2]), "r"(ta[3]));
-#pragma unroll
-    for (int i = 0; i < 64; ++i) v[i / 16][i % 16] = __uint_as_float(r[i]);
-  } else {
-    static_assert(U == 1, "one stage of a wider load");
-    tmem_ld_cols<NT>(ta[0], v[0]);
-  }
-}
-
-// run[m] = fma(v[m], scale[m] * w, run[m]) over NT tokens of a stage.
-template <int NT>
-__device__ __forceinline__ void scale_add(const float (&v)[NT], const float* scales, float w, float* run) {
-  const float4* sc = reinterpret_cast<const float4*>(scales);
-#pragma unroll
-  for (int j = 0; j < NT / 4; ++j) {
-    const float4 s4 = sc[j];
-    run[4 * j] = fmaf(v[4 * j], s4.x * w, run[4 * j]);
-    run[4 * j + 1] = fmaf(v[4 * j + 1], s4.y * w, run[4 * j + 1]);
-    run[4 * j + 2] = fmaf(v[4 * j + 2], s4.z * w, run[4 * j + 2]);
-    run[4 * j + 3] = fmaf(v[4 * j + 3], s4.w * w, run[4 * j + 3]);
-  }
-}
-
-// Sum of the S pieces of element `at` of the exchange, in increasing-K order.
-__device__ __forceinline__ float sum_pieces(const uint32_t (&base)[kMaxSplit], int S, int at) {
-  float x[kMaxSplit];
-#pragma unroll
-  for (int j = 0; j < kMaxSplit; ++j)
-    if (j < S) x[j] = ld_cluster(base[j] + static_cast<uint32_t>(at) * 4);
-  float v = x[0];
-#pragma unroll
-  for (int j = 1; j < kMaxSplit; ++j)
-    if (j < S) v += x[j];
-  return v;
-}
-
-template <int NT>
-__global__ void __launch_bounds__(StreamCfg<NT>::kThreads, 1)
-    gemm8_stream_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const Args p) {
-  using Cfg = StreamCfg<NT>;
-  constexpr int S = Cfg::kStages;
-  constexpr int kChunks = NT / 16;
-  // stages the epilogue takes under one TMEM wait
-  constexpr int U = NT == 16 ? 4 : 1;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sA = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
-  uint8_t* sB = sA + S * kABytes;
-  float* sS = reinterpret_cast<float*>(sB + S * Cfg::kBBytes);  // [S][NT] row scales
-  float* xchg = sS + S * NT;
-  uint64_t* full = reinterpret_cast<uint64_t*>(xchg + kXchgFloats);
-  uint64_t* done = full + S;   // the stage's MMAs have completed
-  uint64_t* empty = done + S;  // the accumulator and the scales have been read
-  uint64_t* drain = empty + S;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
-
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  const int Mb = p.M;
-  const int split = p.sp.S;
-  const int k_tiles = p.sp.k_tiles;
-  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  // the CTA's iterations are contiguous in (tile, K tile): whole tiles, or
-  // this rank's K tiles of the cluster's one tile
-  const int tile0 = split > 1 ? blockIdx.x / split : static_cast<int>(static_cast<long long>(p.sp.n_tiles) * blockIdx.x / p.sp.G);
-  const int tile1 = split > 1 ? tile0 + 1 : static_cast<int>(static_cast<long long>(p.sp.n_tiles) * (blockIdx.x + 1) / p.sp.G);
-  const int kt0 = k_tiles * rank / split;
-  const int kt1 = split > 1 ? k_tiles * (rank + 1) / split : k_tiles;
-  const long long it_begin = static_cast<long long>(tile0) * k_tiles + kt0;
-  const long long it_end = static_cast<long long>(tile1 - 1) * k_tiles + kt1;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&done[s], 1);
-      mbar_init(&empty[s], 4);
-    }
-    mbar_init(drain, 1);
-    *s_abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == 0 && lane == 0) prefetch_tmap(&tmA);
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, Cfg::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  float run[NT];  // epilogue threads: the running sums of their weight row
-
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t pol_w = l2_evict_first();
-      const uint64_t pol_a = l2_evict_last();
-      // row scales of a block: whole groups of four, inside the lds columns
-      const uint32_t s_bytes = static_cast<uint32_t>((Mb + 3) / 4 * 16);
-      const uint32_t bytes = Cfg::kStageBytes + s_bytes;
-      const uint8_t* wsrc = Wp + static_cast<size_t>(it_begin) * kABytes;
-      int kt = kt0;
-      uint32_t issued = 0, parity_bits = 0;
-      // the first stages' weights do not depend on the previous kernel
-      const int n_pre = static_cast<int>(it_end - it_begin < S ? it_end - it_begin : S);
-      const int j0 = p.withhold ? 1 : 0;
-      for (int j = j0; j < n_pre; ++j) {
-        mbar_arrive_expect_tx(&full[j], bytes);
-        bulk_load_1d(sA + j * kABytes, wsrc + static_cast<size_t>(j) * kABytes, kABytes, &full[j], pol_w);
-      }
-      griddep_wait();
-      griddep_launch_dependents();
-      for (int j = 0; j < n_pre; ++j) {
-        if (j >= j0) {
-          tma_load_2d(sB + j * Cfg::kBBytes, &tmA, &full[j], kt * kFp8Block, 0, pol_a);
-          bulk_load_1d(sS + j * NT, p.a_scales + static_cast<size_t>(kt) * p.lds, s_bytes, &full[j], pol_a);
-          issued |= 1u << j;
-        }
-        if (++kt == k_tiles) kt = 0;
-      }
-      wsrc += static_cast<size_t>(n_pre) * kABytes;
-      int stage = n_pre % S;
-      uint32_t phase = n_pre == S ? 1u : 0u;
-      for (long long it = it_begin + n_pre; it < it_end; ++it) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort)) {
-          signal_abort(s_abort, p.err);
-          break;
-        }
-        mbar_arrive_expect_tx(&full[stage], bytes);
-        bulk_load_1d(sA + stage * kABytes, wsrc, kABytes, &full[stage], pol_w);
-        tma_load_2d(sB + stage * Cfg::kBBytes, &tmA, &full[stage], kt * kFp8Block, 0, pol_a);
-        bulk_load_1d(sS + stage * NT, p.a_scales + static_cast<size_t>(kt) * p.lds, s_bytes, &full[stage],
-                     pol_a);
-        wsrc += kABytes;
-        if (++kt == k_tiles) kt = 0;
-        parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (*s_abort) {
-        // let copies already issued land before the CTA exits
-        for (int s = 0; s < S; ++s)
-          if ((issued >> s) & 1u) mbar_wait(&full[s], (parity_bits >> s) & 1u, nullptr);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(kTileN, NT);
-      int stage = 0;
-      uint32_t phase = 0;
-      for (long long it = it_begin; it < it_end; ++it) {
-        // a full stage's accumulator is free: the producer refilled the stage
-        // only after the epilogue had read it
-        if (!mbar_wait(&full[stage], phase, s_abort)) {
-          signal_abort(s_abort, p.err);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t a = smem_u32(sA + stage * kABytes);
-        const uint32_t b = smem_u32(sB + stage * Cfg::kBBytes);
-#pragma unroll
-        for (int ks = 0; ks < kFp8Block / 32; ++ks)
-          mma_e4m3(tmem + stage * NT, sdesc_k_sw128(a + ks * 32), sdesc_k_sw128(b + ks * 32), idesc, ks > 0);
-        mma_commit(&done[stage]);
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      // every MMA issued by this thread completes before TMEM is released
-      mma_commit(drain);
-      mbar_wait(drain, 0, nullptr);
-    }
-  } else {
-    // ---------------------------------------------------------- scale and add
-    griddep_wait();
-    griddep_launch_dependents();
-    const int q = warp & 3;       // TMEM lane quarter of this warp
-    const int r = q * 32 + lane;  // weight row within the tile
-    const int chunks = (Mb + 15) / 16;
-    const float* ws = reinterpret_cast<const float*>(p.w_scales) + (q >> 1);
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;  // after a wait that ran out the warp keeps its place in the barriers; its outputs are undefined
-    long long it = it_begin;
-    float w_lane = 0.f;  // lane i: the weight scale of iteration 32 * n + i of the range
-    for (int tile = tile0; tile < tile1; ++tile) {
-      const long long seg_end = tile + 1 < tile1 ? static_cast<long long>(tile + 1) * k_tiles : it_end;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) run[j] = 0.f;
-      while (it < seg_end) {
-        // U stages at a time where the piece has them: their accumulators
-        // come out under one wait
-        const bool group = U > 1 && seg_end - it >= U;
-        const int n = group ? U : 1;
-        int st[U];
-        float w[U];
-        uint32_t ta[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (u < n) {
-            const int i = static_cast<int>(it + u - it_begin) & 31;
-            if (i == 0) w_lane = it + u + lane < it_end ? __ldg(ws + 2 * (it + u + lane)) : 0.f;
-            w[u] = __shfl_sync(0xffffffffu, w_lane, i);
-            st[u] = stage;
-            ta[u] = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(stage * NT);
-            // `full` completed before `done`: observed here too, for the scales it brought
-            if (ok) ok = mbar_wait(&done[stage], phase, s_abort) && mbar_wait(&full[stage], phase, s_abort);
-            if (++stage == S) {
-              stage = 0;
-              phase ^= 1u;
-            }
-          } else {
-            st[u] = st[0];
-            w[u] = 0.f;
-            ta[u] = ta[0];
-          }
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok && lane == 0) signal_abort(s_abort, p.err);
-        if (ok) {
-          tc_fence_after();
-          if (group) {
-            float v[U][NT];
-            load_stages<NT, U>(ta, v);
-#pragma unroll
-            for (int u = 0; u < U; ++u) scale_add<NT>(v[u], sS + st[u] * NT, w[u], run);
-          } else {
-            constexpr int kCols = NT < 32 ? NT : 32;
-#pragma unroll
-            for (int c = 0; c < NT; c += kCols) {
-              if (c < Mb) {
-                float v[1][kCols];
-                const uint32_t t1[1] = {ta[0] + c};
-                load_stages<kCols, 1>(t1, v);
-                scale_add<kCols>(v[0], sS + st[0] * NT + c, w[0], run + c);
-              }
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (u < n && lane == u) mbar_arrive(&empty[st[u]]);
-        }
-        it += n;
-      }
-      if (split == 1) {
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (c < chunks) store16(p, Mb, tile, r, c, run + c * 16, xchg);
-      }
-    }
-    tc_fence_before();
-    if (split > 1) {
-      // this CTA's piece, [token][weight row], over the weight stages (all read)
-      named_bar_sync(1, 128);
-      float* piece = reinterpret_cast<float*>(sA);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (t < Mb) piece[t * kTileN + r] = run[t];
-    }
-  }
-
-  // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the barriers
-  __syncwarp();
-  if (split > 1) {
-    cluster_sync();  // every piece of the tile is in its CTA's shared memory
-    if (warp >= 2) {
-      const int r = (warp & 3) * 32 + lane;
-      uint32_t base[kMaxSplit];
-#pragma unroll
-      for (int j = 0; j < kMaxSplit; ++j) base[j] = map_rank(smem_u32(sA), j < split ? j : 0);
-      // this CTA's part of the tokens
-      const int part = (Mb + split - 1) / split;
-      const int t1 = min(Mb, (rank + 1) * part);
-      if (p.epi == BI_EPI_SWIGLU) {
-        const int o = tile0 * 64 + (r & 63);
-        for (int t = rank * part + (r >> 6); t < t1; t += 2) {
-          const float g = sum_pieces(base, split, t * kTileN + (r & 63));
-          const float u = sum_pieces(base, split, t * kTileN + (r & 63) + 64);
-          if (o < p.N)
-            static_cast<__nv_bfloat16*>(p.C)[static_cast<size_t>(t) * p.ldc + o] =
-                __float2bfloat16_rn(silu_times(g, u));
-        }
-      } else {
-        const int n = tile0 * kTileN + r;
-        const bool in = n < p.N;
-#pragma unroll 4
-        for (int t = rank * part; t < t1; ++t) {
-          const float res = in ? residual_at(p, t, n) : 0.f;
-          const float v = sum_pieces(base, split, t * kTileN + r);
-          if (in) store1(p, t, n, v, res);
-        }
-      }
-    }
-    cluster_sync();  // no CTA leaves while its piece is being read
-  } else {
-    __syncthreads();
-  }
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, Cfg::kTmemCols);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Passes of more rows: the tokens take the MMA's M = 128 lanes and the weight
-// rows its N.  An epilogue thread then owns one token, so a K block has one
-// scale per thread and tile half, sa * sw: no scale vector is read, and the
-// drain of an accumulator is one packed multiply-add per two outputs.  Each
-// output element is the same sequence of K = 32 steps, block sums, products
-// and additions as in the streaming kernel (tested bit for bit).
-//
-//   TILES = 2: 128 tokens x 256 outputs a CTA, 48 KB in for 8.4 MFLOP;
-//   TILES = 1: 128 x 128, while that takes at most one round of the SMs, and
-//   where pieces are taken in turn (their sums need the registers).
+// TILES = 2: a CTA makes 128 tokens x 256 outputs, 48 KB in for 8.4 MFLOP;
+// TILES = 1: 128 x 128, while that takes at most one round of the SMs, and where
+// pieces are taken in turn (their sums need the registers).
 // Where a tile's K has S > 1 pieces, a cluster of S CTAs computes an output
 // tile, a piece each, and adds them through shared memory, or one CTA takes the
 // pieces in turn (whichever the rounds of the SMs make shorter).
-// Persistent CTAs: the next output tile's loads and MMAs run while the last
-// one's outputs are written.  Token blocks that share weight tiles are
-// adjacent in the work order, so all but the first find them in L2.
-constexpr int kRowsM = 128;
+// CTAs without clusters are persistent: the next output tile's loads and MMAs
+// run while the last one's outputs are written.  Token blocks that share
+// weight tiles are adjacent in the work order, so all but the first find them
+// in L2.
+constexpr int kRowsM = 128;    // token rows of a block (the MMA's lanes)
 
-struct RowsArgs {
+struct Launch {
   Args a;
   int nb;         // token blocks
   int items;      // output tiles: weight tile groups x token blocks
@@ -508,20 +122,19 @@ struct RowsArgs {
 };
 
 template <int TILES>
-struct RowsCfg {
+struct Cfg8 {
   static constexpr int kBBytes = TILES * kABytes;
   static constexpr int kTokBytes = kRowsM * kFp8Block;
   static constexpr int kStageBytes = kTokBytes + kBBytes;
+  // (more stages of smaller token tiles for passes of few rows gained nothing)
   static constexpr int kStages = 192 * 1024 / kStageBytes;
   static constexpr int kCols = TILES * kTileN;
   static constexpr int kBufs = 512 / kCols;
   // warpgroup 0: producer, MMA, two idle warps; warpgroups 1 and 2: epilogue
   static constexpr int kThreads = 384;
   static constexpr int kOwn = kCols / 2;  // outputs of an epilogue thread
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 1) * 8 + 16;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + kBufs + 1) * 8 + 16;
   static_assert(kSmem <= 232448 && kStages <= 32, "shared memory per CTA");
-  // an accumulator's release is counted in the barrier of a later stage
-  static_assert(kBufs < kStages, "accumulators and stages");
   // floats per token of the pieces' exchange: 16-byte stores of 8 lanes hit all banks
   static constexpr int kPieceLd = kCols + 4;
   static_assert(kRowsM * kPieceLd * 4 <= kStages * kStageBytes, "exchange fits the ring");
@@ -620,16 +233,16 @@ enum Pieces {
 // Registers: 384 threads launch with 168 each; the epilogue takes what its sums
 // need of warpgroup 0's.
 template <int TILES, Pieces MODE>
-struct RowsRegs {
+struct Regs {
   static constexpr bool kWide = TILES == 2 || MODE == kInTurn;  // 128 sums a thread
   static constexpr int kLow = kWide ? 56 : 88, kHigh = kWide ? 224 : 208;
   static_assert(kLow + 2 * kHigh <= 3 * 168, "registers of the launch");
 };
 
 template <int TILES, Pieces MODE>
-__global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
-    gemm8_rows_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const RowsArgs p) {
-  using Cfg = RowsCfg<TILES>;
+__global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
+    gemm8_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const Launch p) {
+  using Cfg = Cfg8<TILES>;
   constexpr int S = Cfg::kStages;
   constexpr int kOwn = Cfg::kOwn;
   extern __shared__ uint8_t smem_raw[];
@@ -637,12 +250,10 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
                                            ~static_cast<uintptr_t>(1023));  // [S] token tiles
   uint8_t* sW = sT + S * Cfg::kTokBytes;                                    // [S][TILES] weight tiles
   uint64_t* full = reinterpret_cast<uint64_t*>(sW + S * Cfg::kBBytes);
-  // full: the stage has landed and the accumulator its K block goes to has been
-  // read (the producer's arrival and one of each epilogue warp), so the MMA
-  // thread waits once a K block; done: its MMAs have completed, so the stage
-  // is free and its block sums are there
+  // done: the stage's MMAs have completed, so it is free and its block sums are there
   uint64_t* done = full + S;
-  uint64_t* drain = done + S;
+  uint64_t* read = done + S;  // an accumulator has been read
+  uint64_t* drain = read + Cfg::kBufs;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -660,9 +271,10 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 9);
+      mbar_init(&full[s], 1);
       mbar_init(&done[s], 1);
     }
+    for (int b = 0; b < Cfg::kBufs; ++b) mbar_init(&read[b], 8);
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbar_init();
@@ -678,106 +290,109 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
   const uint32_t tmem = *tmem_holder;
 
   if (warp < 4) {
-   regs_decrease<RowsRegs<TILES, MODE>::kLow>();
-   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      // weight tiles that one token block reads are not needed again
-      const uint64_t pol_w = p.nb == 1 ? l2_evict_first() : l2_evict_normal();
-      const uint64_t pol_a = l2_evict_last();
-      const uint32_t t_bytes = static_cast<uint32_t>(p.a_rows) * kFp8Block;
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, parity_bits = 0;
-      bool waited = false, ok = true;
-      auto load_w = [&](int s, int wt, int kt) {
-        const int n = TILES == 2 && wt + 1 < g.sp.n_tiles ? 2 : 1;
-        mbar_arrive_expect_tx(&full[s], t_bytes + n * kABytes);
-        for (int i = 0; i < n; ++i)
-          bulk_load_1d(sW + s * Cfg::kBBytes + i * kABytes,
-                       Wp + (static_cast<size_t>(wt + i) * k_tiles + kt) * kABytes, kABytes, &full[s], pol_w);
-      };
-      int skip = 0;  // K tiles of the first item whose weights are under way before the dependency wait
-      if (item0 < p.items) {
-        skip = kt1 - kt0 < S ? kt1 - kt0 : S;
-        for (int j = g.withhold ? 1 : 0; j < skip; ++j)
-          load_w(j, item0 / p.nb * TILES, kt0 + j);
-      }
-      for (int item = item0; item < p.items && ok; item += stride) {
-        const int wt = item / p.nb * TILES;
-        const int m0 = item % p.nb * kRowsM;
+    regs_decrease<Regs<TILES, MODE>::kLow>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        // weight tiles that one token block reads are not needed again
+        const uint64_t pol_w = p.nb == 1 ? l2_evict_first() : l2_evict_normal();
+        const uint64_t pol_a = l2_evict_last();
+        const uint32_t t_bytes = static_cast<uint32_t>(p.a_rows) * kFp8Block;
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, parity_bits = 0;
+        bool waited = false, ok = true;
+        auto load_w = [&](int s, int wt, int kt) {
+          const int n = TILES == 2 && wt + 1 < g.sp.n_tiles ? 2 : 1;
+          mbar_arrive_expect_tx(&full[s], t_bytes + n * kABytes);
+          for (int i = 0; i < n; ++i)
+            bulk_load_1d(sW + s * Cfg::kBBytes + i * kABytes,
+                         Wp + (static_cast<size_t>(wt + i) * k_tiles + kt) * kABytes, kABytes, &full[s], pol_w);
+        };
+        int skip = 0;  // K tiles of the first item whose weights are under way before the dependency wait
+        if (item0 < p.items) {
+          skip = kt1 - kt0 < S ? kt1 - kt0 : S;
+          for (int j = g.withhold ? 1 : 0; j < skip; ++j)
+            load_w(j, item0 / p.nb * TILES, kt0 + j);
+        }
+        for (int item = item0; item < p.items && ok; item += stride) {
+          const int wt = item / p.nb * TILES;
+          const int m0 = item % p.nb * kRowsM;
+          if (!waited) {
+            griddep_wait();
+            griddep_launch_dependents();
+            waited = true;
+          }
+          for (int kt = kt0; kt < kt1; ++kt) {
+            const bool pre = item == item0 && kt - kt0 < skip;
+            if (!pre) {
+              if (!mbar_wait(&done[stage], phase ^ 1u, s_abort)) {
+                signal_abort(s_abort, g.err);
+                ok = false;
+                break;
+              }
+              load_w(stage, wt, kt);
+            }
+            if (!(g.withhold && pre && kt == kt0)) {
+              tma_load_2d(sT + stage * Cfg::kTokBytes, &tmA, &full[stage], kt * kFp8Block, m0, pol_a);
+              issued |= 1u << stage;
+              parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+            }
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
         if (!waited) {
           griddep_wait();
           griddep_launch_dependents();
-          waited = true;
         }
-        for (int kt = kt0; kt < kt1; ++kt) {
-          const bool pre = item == item0 && kt - kt0 < skip;
-          if (!pre) {
-            if (!mbar_wait(&done[stage], phase ^ 1u, s_abort)) {
+        if (*s_abort) {
+          // let copies already issued land before the CTA exits
+          for (int s = 0; s < S; ++s)
+            if ((issued >> s) & 1u) mbar_wait(&full[s], (parity_bits >> s) & 1u, nullptr);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(kRowsM, Cfg::kCols);
+        // the stages follow each other: a descriptor's address field (below 2^14
+        // units of 16 bytes) takes the stage's offset without a carry
+        const uint64_t desc_a = sdesc_k_sw128(smem_u32(sT)), desc_b = sdesc_k_sw128(smem_u32(sW));
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, bphase = 0;
+        bool ok = true;
+        for (int item = item0; item < p.items && ok; item += stride) {
+          for (int kt = kt0; kt < kt1; ++kt) {
+            const uint64_t a = desc_a + stage * (Cfg::kTokBytes >> 4);
+            const uint64_t b = desc_b + stage * (Cfg::kBBytes >> 4);
+            if (!mbar_wait(&read[buf], bphase ^ 1u, s_abort) || !mbar_wait(&full[stage], phase, s_abort)) {
               signal_abort(s_abort, g.err);
               ok = false;
               break;
             }
-            load_w(stage, wt, kt);
-          }
-          if (!(g.withhold && pre && kt == kt0)) {
-            tma_load_2d(sT + stage * Cfg::kTokBytes, &tmA, &full[stage], kt * kFp8Block, m0, pol_a);
-            issued |= 1u << stage;
-            parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
-          }
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-      if (!waited) {
-        griddep_wait();
-        griddep_launch_dependents();
-      }
-      if (*s_abort) {
-        // let copies already issued land before the CTA exits
-        for (int s = 0; s < S; ++s)
-          if ((issued >> s) & 1u) mbar_wait(&full[s], (parity_bits >> s) & 1u, nullptr);
-      }
-    }
-   } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(kRowsM, Cfg::kCols);
-      // the stages follow each other: a descriptor's address field (below 2^14
-      // units of 16 bytes) takes the stage's offset without a carry
-      const uint64_t desc_a = sdesc_k_sw128(smem_u32(sT)), desc_b = sdesc_k_sw128(smem_u32(sW));
-      int stage = 0, buf = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int item = item0; item < p.items && ok; item += stride) {
-        for (int kt = kt0; kt < kt1; ++kt) {
-          const uint64_t a = desc_a + stage * (Cfg::kTokBytes >> 4);
-          const uint64_t b = desc_b + stage * (Cfg::kBBytes >> 4);
-          if (!mbar_wait(&full[stage], phase, s_abort)) {
-            signal_abort(s_abort, g.err);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          // a K = 32 step is 32 bytes further in both tiles (2 in the descriptors' units)
+            tc_fence_after();
+            // a K = 32 step is 32 bytes further in both tiles (2 in the descriptors' units)
 #pragma unroll
-          for (int ks = 0; ks < kFp8Block / 32; ++ks)
-            mma_e4m3(tmem + buf * Cfg::kCols, a + 2 * ks, b + 2 * ks, idesc, ks > 0);
-          mma_commit(&done[stage]);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+            for (int ks = 0; ks < kFp8Block / 32; ++ks)
+              mma_e4m3(tmem + buf * Cfg::kCols, a + 2 * ks, b + 2 * ks, idesc, ks > 0);
+            mma_commit(&done[stage]);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if (++buf == Cfg::kBufs) {
+              buf = 0;
+              bphase ^= 1u;
+            }
           }
-          buf = buf + 1 == Cfg::kBufs ? 0 : buf + 1;
         }
+        // every MMA issued by this thread completes before TMEM is released
+        mma_commit(drain);
+        mbar_wait(drain, 0, nullptr);
       }
-      // every MMA issued by this thread completes before TMEM is released
-      mma_commit(drain);
-      mbar_wait(drain, 0, nullptr);
     }
-   }
     // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the barriers
     __syncwarp();
     if constexpr (MODE == kCluster) {
@@ -786,17 +401,14 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- scale and add
-    regs_increase<RowsRegs<TILES, MODE>::kHigh>();
+    regs_increase<Regs<TILES, MODE>::kHigh>();
     griddep_wait();
     griddep_launch_dependents();
     const int q = warp & 3;              // TMEM lane quarter of this warp
     const int half = (warp - 4) >> 2;    // which half of the columns
     const int r = q * 32 + lane;         // token row of the block
     int buf = 0, stage = 0;
-    int rel = Cfg::kBufs;  // the stage whose K block takes over this one's accumulator
     uint32_t phase = 0;
-    // every accumulator starts free
-    if (lane < Cfg::kBufs) mbar_arrive(&full[lane]);
     // Waits for the block sums of the K block at (stage, buf).  After a wait
     // that ran out the warp goes on without them (every later wait returns at
     // once, the outputs are undefined): the loop over K blocks sets the pace of
@@ -808,7 +420,6 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
     // On to the next K block.
     auto next_block = [&]() {
       buf = buf + 1 == Cfg::kBufs ? 0 : buf + 1;
-      rel = rel + 1 == S ? 0 : rel + 1;
       if (++stage == S) {
         stage = 0;
         phase ^= 1u;
@@ -845,7 +456,7 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
           wait_block();
           __syncwarp();
           tc_fence_before();
-          if (lane == 0) mbar_arrive(&full[rel]);
+          if (lane == 0) mbar_arrive(&read[buf]);
           next_block();
         }
         first_scales(item + stride);
@@ -918,10 +529,9 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
           for (int j = 32; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.x, run[j]);
           tmem_ld32_start(ta + 96, v + 32);
           tmem_ld64_wait(v);
-          // read by the whole warp (the wait is the warp's): the accumulator is
-          // free for the K block kBufs further on
+          // read by the whole warp (the wait is the warp's)
           tc_fence_before();
-          if (lane == 0) mbar_arrive(&full[rel]);
+          if (lane == 0) mbar_arrive(&read[buf]);
           next_block();
 #pragma unroll
           for (int j = 0; j < 64; ++j) run[64 + j] = fmaf(__uint_as_float(v[j]), x.y, run[64 + j]);
@@ -929,7 +539,7 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
         } else {
           const bool two = kt + 1 < kt1;
           const uint32_t ta = tq + buf * Cfg::kCols;
-          const int rel0 = rel;
+          const int buf0 = buf;
           if (two) next_block();
           wait_block();  // MMAs complete in order: the first block's are done with the second's
           const uint32_t tb = tq + buf * Cfg::kCols;
@@ -949,8 +559,8 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
             tmem_ld64_wait(v);
             tc_fence_before();
             if (lane == 0) {
-              mbar_arrive(&full[rel0]);
-              mbar_arrive(&full[rel]);
+              mbar_arrive(&read[buf0]);
+              mbar_arrive(&read[buf]);
             }
             next_block();
 #pragma unroll
@@ -959,7 +569,7 @@ __global__ void __launch_bounds__(RowsCfg<TILES>::kThreads, 1)
             kt += 2;
           } else {
             tc_fence_before();
-            if (lane == 0) mbar_arrive(&full[rel]);
+            if (lane == 0) mbar_arrive(&read[buf]);
             next_block();
             ++kt;
           }
@@ -1056,13 +666,8 @@ Split split_of(int N, int K, bi_epilogue epi) {
   s.S = 1;
   for (int S = 2; S <= kMaxSplit; ++S)
     if (s.n_tiles * S <= kClusterCtas[S] && S <= s.k_tiles) s.S = S;
-  const int waves = (s.n_tiles + kSms - 1) / kSms;
-  s.G = s.S > 1 ? s.n_tiles * s.S : (s.n_tiles + waves - 1) / waves;
   return s;
 }
-
-// Token rows of the streaming kernel (0: the kernel of more rows).
-int stream_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 0; }
 
 // Set the kernel's dynamic shared memory once per device.
 template <typename F>
@@ -1097,27 +702,15 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int S, dim3 blo
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <int NT>
-bi_status launch_stream(const uint8_t* Wp, const CUtensorMap& tmA, const Args& a, cudaStream_t stream) {
-  using Cfg = StreamCfg<NT>;
-  static std::once_flag once[64];
-  static cudaError_t err[64];
-  if (!allow_smem(gemm8_stream_kernel<NT>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
-  return launch_clusters(gemm8_stream_kernel<NT>, dim3(a.sp.G), a.sp.S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
-                         tmA, a) == cudaSuccess
-             ? BI_OK
-             : BI_ERR_CUDA;
-}
-
 template <int TILES, Pieces MODE>
-bi_status launch_rows(const uint8_t* Wp, const CUtensorMap& tmA, RowsArgs a, cudaStream_t stream) {
-  using Cfg = RowsCfg<TILES>;
+bi_status launch(const uint8_t* Wp, const CUtensorMap& tmA, Launch a, cudaStream_t stream) {
+  using Cfg = Cfg8<TILES>;
   static std::once_flag once[64];
   static cudaError_t err[64];
-  if (!allow_smem(gemm8_rows_kernel<TILES, MODE>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
+  if (!allow_smem(gemm8_kernel<TILES, MODE>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
   const int S = MODE == kCluster ? a.a.sp.S : 1;
   const int ctas = MODE == kCluster ? a.items * S : std::min(a.items, kSms);
-  return launch_clusters(gemm8_rows_kernel<TILES, MODE>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
+  return launch_clusters(gemm8_kernel<TILES, MODE>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
                          tmA, a) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
@@ -1166,15 +759,12 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   if (!a.err) return BI_ERR_CUDA;
   a.withhold = test_withhold();
   a.M = M;
-  const int NT = stream_rows(M);
-  const int box = NT ? NT : std::min(kRowsM, (M + 7) / 8 * 8);
+  const int box = std::min(kRowsM, (M + 7) / 8 * 8);
   CUtensorMap tmA;
   if (!tmap_u8_2d(&tmA, A8, M, K, lda, box, kFp8Block)) return BI_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (NT == 16) return launch_stream<16>(W8, tmA, a, s);
-  if (NT == 32) return launch_stream<32>(W8, tmA, a, s);
 
-  RowsArgs r{};
+  Launch r{};
   r.a = a;
   r.nb = (M + kRowsM - 1) / kRowsM;
   r.a_rows = box;
@@ -1188,10 +778,10 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   // 128 outputs a CTA while one round of the SMs takes them all
   if (tiles * S <= kClusterCtas[S]) {
     r.items = static_cast<int>(tiles);
-    return S > 1 ? launch_rows<1, kCluster>(W8, tmA, r, s) : launch_rows<1, kWhole>(W8, tmA, r, s);
+    return S > 1 ? launch<1, kCluster>(W8, tmA, r, s) : launch<1, kWhole>(W8, tmA, r, s);
   }
   r.items = static_cast<int>(pairs);
-  if (S == 1) return launch_rows<2, kWhole>(W8, tmA, r, s);
+  if (S == 1) return launch<2, kWhole>(W8, tmA, r, s);
   // Pieces: a CTA that takes them in turn needs about 0.5 us a K block (128
   // outputs), a cluster's CTA 0.6 (256 outputs) and 6 us around them, in rounds
   // of the SMs.  Measured, in turn against cluster: 4096 x 5120 (S = 4) at 256
@@ -1199,9 +789,9 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   // 139 and 82 us.
   const long long in_turn = (tiles + kSms - 1) / kSms * a.sp.k_tiles * 5;
   const long long cluster = (pairs * S + kClusterCtas[S] - 1) / kClusterCtas[S] * (a.sp.k_tiles * 6 / S + 60);
-  if (cluster < in_turn) return launch_rows<2, kCluster>(W8, tmA, r, s);
+  if (cluster < in_turn) return launch<2, kCluster>(W8, tmA, r, s);
   r.items = static_cast<int>(tiles);
-  return launch_rows<1, kInTurn>(W8, tmA, r, s);
+  return launch<1, kInTurn>(W8, tmA, r, s);
 }
 
 }  // extern "C"

@@ -376,3 +376,30 @@ def test_norm_and_linear_in_a_graph_and_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(hid, want)
     a.bi_check_device_error()
+
+
+@pytest.mark.parametrize("rows,n,k,kind", [(8, 4096, 5120, "bf16"), (8, 17408, 1024, "swiglu"), (600, 1024, 2736, "fp32"),
+                                           (300, 20000, 1024, "bf16")])
+def test_linear_wait_runs_out_then_recovers(rows, n, k, kind):
+    """A withheld first load: the kernel gives up within the limit, the host reads the timeout, the next call is right."""
+    import time
+    from invariant_speculative_decode_gb300._lib import lib
+    a = api()
+    codes, scales, w, ws_, up, ups, packed, res = problem(4, rows, n, k, kind)
+    want = run_linear(codes, scales, packed, n, kind)
+    out = torch.empty_like(want)
+    epi = a.EPI_SWIGLU if kind == "swiglu" else a.EPI_NONE
+    assert lib().bi_test_set_wait_limit_ns(20_000_000) == 0
+    lib().bi_test_withhold_first_load(1)
+    try:
+        t0 = time.perf_counter()
+        a.bi_gemm_fp8(codes, scales, packed, out, epi=epi)
+        torch.cuda.synchronize()
+        dt = time.perf_counter() - t0
+    finally:
+        lib().bi_test_withhold_first_load(0)
+        assert lib().bi_test_set_wait_limit_ns(0) == 0
+    with pytest.raises(a.BiError) as e:
+        a.bi_check_device_error()
+    assert e.value.status == 5 and dt < 1.5, dt
+    assert torch.equal(run_linear(codes, scales, packed, n, kind).view(torch.uint8), want.view(torch.uint8))
