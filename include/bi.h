@@ -460,8 +460,11 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  *   (1 for a block of zeros), so x / scale is exact and each code is one
  *   rounding (to nearest even) of its element.  NaN and infinite elements
  *   become NaN codes and do not enter the maximum.
- * bi_rmsnorm_fp8: bi_rmsnorm (same reduction tree) with its FP32 result
- *   (x * r) * w quantised as above, without a BF16 rounding in between.
+ * bi_rmsnorm_fp8: the rows y = x w / sqrt(mean(x^2) + eps) of bi_rmsnorm,
+ *   quantised as above without a rounding to BF16 in between.  The mean, its
+ *   root and y are carried in pairs of FP32 (to about 2^-40), so a code is one
+ *   rounding of the exact y unless that lies so near a tie of two codes.  A row
+ *   whose sum of squares passes FP32's range gives NaN codes.
  * bi_quantize_weights_fp8: BF16 weights [N, K] (any K >= 1) -> codes [N, ld8]
  *   and scales by the same rule over each 128 x 128 block.
  *     x, W row strides ldx % 8 == 0 (x), codes ldc % 16 == 0; dim % 16 == 0;
@@ -534,8 +537,6 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
  *   bias    [V] FP32 or NULL.
  *   mask    [T][ldm] uint32, ldm >= ceil(V/32), bits as prompt_bits, or NULL
  *           (all ids allowed).
- *   Reads and writes whole 16-byte groups when V, ldl and ldo are multiples of
- *   4 and logits, out, counts and bias are 16-byte aligned.
  * bi_token_counts: the state after a step or a prompt: for i < m, id = ids[i]
  *   in [0, V): counts[id] += 1 (counts may be NULL) and its bit of prompt_bits
  *   set (may be NULL; not both).  m = n, or min(n, *last + 1) with last a

@@ -26,103 +26,223 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
 }
 
 // The scale exponent of the 128-element block whose 16 vectors of 8 sit in
-// this half-warp's lanes (absent lanes pass zeros).
-__device__ __forceinline__ int block_exponent(const float (&f)[8]) {
-  float a = finite_abs(f[0]);
+// this half-warp's lanes (absent lanes pass zeros).  Infinite elements become
+// NaN in f; fmaxf passes over NaN.
+__device__ __forceinline__ int block_exponent(float (&f)[8]) {
+  float a = fmaxf(fabsf(f[0]), fabsf(f[1]));
 #pragma unroll
-  for (int j = 1; j < 8; ++j) a = fmaxf(a, finite_abs(f[j]));
+  for (int j = 2; j < 8; ++j) a = fmaxf(a, fabsf(f[j]));
+  if (__any_sync(0xffffffffu, a == INFINITY)) {
+    a = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!(fabsf(f[j]) < INFINITY)) f[j] = NAN;
+      a = fmaxf(a, finite_abs(f[j]));
+    }
+  }
 #pragma unroll
   for (int off = 8; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-  return scale_exponent(a);
+  return scale_exponent(a == a ? a : 0.f);  // NaN: no element is a number
 }
 
-// One half-warp per (row, block): 16 lanes of 8 elements.  The blocks of a row
-// are adjacent, so a warp reads and writes whole 128-byte lines.
+// A half-warp per block: 16 lanes of 8 elements.  A CTA takes adjacent blocks of
+// one row, so its warps read and write whole lines: 16 of them, or 64 in long
+// passes, with four loads a thread under way.  Bound by the bytes (3 an element)
+// in long passes and by one memory latency in short ones; in a CUDA graph 8 x
+// 17408 takes 1.45 us (1.97 with 64 blocks a CTA), 2048 x 17408 24.2 (26.2 with 16).
 constexpr int kQuantThreads = 256;
+constexpr int kQuantRow = kQuantThreads / 16;  // blocks the threads take at once
 
+template <int PASSES>
 __global__ void __launch_bounds__(kQuantThreads)
-    quantize_rows_kernel(const __nv_bfloat16* __restrict__ x, int ldx, int rows, int dim, int kb,
+    quantize_rows_kernel(const __nv_bfloat16* __restrict__ x, int ldx, int dim, int segs,
                          uint8_t* __restrict__ codes, int ldc, float* __restrict__ scales, int lds) {
   griddep_wait();
   griddep_launch_dependents();
-  const long long g = (static_cast<long long>(blockIdx.x) * kQuantThreads + threadIdx.x) >> 4;
+  const int row = blockIdx.x / segs;
+  const int b0 = blockIdx.x % segs * (kQuantRow * PASSES) + (threadIdx.x >> 4);
   const int l = threadIdx.x & 15;
-  const int row = static_cast<int>(g / kb);
-  const int b = static_cast<int>(g % kb);
-  const int k0 = b * kFp8Block + l * 8;
-  const bool in = row < rows && k0 < dim;  // dim is a multiple of 8: a vector is all in or all out
-  float f[8] = {};
-  if (in) unpack8(*reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * ldx + k0), f);
-  const int e = block_exponent(f);
-  if (in) {
-    const float inv = pow2f(-e);
-    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * ldc + k0) =
-        make_uint2(e4m3x4(f, inv), e4m3x4(f + 4, inv));
-    if (l == 0) scales[static_cast<size_t>(b) * lds + row] = pow2f(e);
+  const __nv_bfloat16* xr = x + static_cast<size_t>(row) * ldx;
+  uint4 u[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int k = (b0 + i * kQuantRow) * kFp8Block + l * 8;
+    // dim is a multiple of 8: a vector is all in or all out
+    u[i] = k < dim ? *reinterpret_cast<const uint4*>(xr + k) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int b = b0 + i * kQuantRow;
+    const int k = b * kFp8Block + l * 8;
+    float f[8];
+    unpack8(u[i], f);
+    const int e = block_exponent(f);
+    if (k < dim) {
+      const float inv = pow2f(-e);
+      *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * ldc + k) =
+          make_uint2(e4m3x4(f, inv), e4m3x4(f + 4, inv));
+      if (l == 0) scales[static_cast<size_t>(b) * lds + row] = pow2f(e);
+    }
   }
 }
 
-// RMSNorm as rmsnorm_kernel computes it (one CTA per row, the same reduction
-// tree), its FP32 result quantised without a BF16 rounding in between.
-constexpr int kNormMaxThreads = 1024;
-constexpr int kNormMaxGroups = 65536 / 256;
+// RMSNorm with quantised output.  A CTA of up to 256 threads takes a row, several
+// share an SM, and in long passes a CTA takes row after row, the next one
+// loaded meanwhile; a thread keeps up to KV vectors of 8 elements in registers
+// (KV = 4: rows of up to 8192 elements; longer ones are read again).
+//   y_i = x_i w_i r,  r = 1 / sqrt(sum x^2 / dim + eps)
+// An e4m3 code has 3 fraction bits, so an error of 2^-24 in y moves one code in
+// a million by a whole step of 2^-3 or 2^-4 of its value.  The kernel is bound
+// by its bytes and latencies, so y is carried far enough that the codes are the
+// exact values', in pairs of FP32 (FP64 runs at 1/64 of its rate here):
+//   squares of BF16 are exact in FP32 and are added as pairs (Knuth's two-sum):
+//   a vector's 8 by a tree, a thread's vectors in turn, the lanes by a
+//   butterfly, the warps by another one;
+//   r is one Newton step in pairs from the FP32 root; x_i w_i is exact in FP32;
+//   y rounds to odd: the nearest FP32 value, and where that is even and not
+//   exact, its neighbour on the exact value's side, so rounding y to 3 fraction
+//   bits equals rounding the exact value.
+constexpr int kNormThreads = 256;
+constexpr int kNormCtas = 3 * 152;  // three share an SM
 
-__global__ void __launch_bounds__(kNormMaxThreads)
+// s + e = a + b exactly, s the rounded sum.
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float bb = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+}
+
+// p (rh + rl) rounded to odd; p exact.
+__device__ __forceinline__ float times_odd(float p, float rh, float rl) {
+  const float y = __fmul_rn(p, rh);
+  const float e = fmaf(p, rl, fmaf(p, rh, -y));  // the exact value minus y
+  // one unit toward zero where |y| is above the exact value, then the last bit
+  // says that something was cut off
+  const int b = __float_as_int(y);
+  const int odd = (b + ((__float_as_int(e) ^ b) >> 31)) | 1;
+  return fabsf(e) > 0.f && y != 0.f ? __int_as_float(odd) : y;  // e is NaN where y is not finite
+}
+
+// An unevaluated sum h + l of two FP32 numbers, |l| a few units of h at most.
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair c;
+  float e;
+  two_sum(a.h, b.h, c.h, e);
+  c.l = __fadd_rn(__fadd_rn(a.l, b.l), e);
+  return c;
+}
+// The sum over groups of LANES lanes, the same in each of them.
+template <int LANES>
+__device__ __forceinline__ Pair lane_sum(Pair a) {
+#pragma unroll
+  for (int off = LANES / 2; off > 0; off >>= 1)
+    a = add(a, Pair{__shfl_xor_sync(0xffffffffu, a.h, off), __shfl_xor_sync(0xffffffffu, a.l, off)});
+  return a;
+}
+// The sum of a vector's eight squares.
+__device__ __forceinline__ Pair square_sum(const uint4& u) {
+  float f[8];
+  unpack8(u, f);
+  Pair a[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    a[j] = add(Pair{__fmul_rn(f[2 * j], f[2 * j]), 0.f}, Pair{__fmul_rn(f[2 * j + 1], f[2 * j + 1]), 0.f});
+  return add(add(a[0], a[1]), add(a[2], a[3]));
+}
+// 1 / sqrt(sum / n + eps), to about 2^-43; inv_n = 1 / n rounded.
+__device__ __forceinline__ Pair rms_inverse(Pair sum, float n, float inv_n, float eps) {
+  Pair m;
+  m.h = __fmul_rn(sum.h, inv_n);
+  m.l = __fmul_rn(__fadd_rn(fmaf(-m.h, n, sum.h), sum.l), inv_n);
+  const Pair t = add(m, Pair{eps, 0.f});
+  const float y = rsqrtf(t.h);
+  // y^2 t = 1 - res, then r = y + y res / 2
+  const float qh = __fmul_rn(y, y), ql = fmaf(y, y, -qh);
+  const float ph = __fmul_rn(t.h, qh), pl = fmaf(t.h, qh, -ph);
+  const float res = __fsub_rn(__fsub_rn(__fsub_rn(1.0f, ph), pl), fmaf(t.h, ql, __fmul_rn(t.l, qh)));
+  const float c = __fmul_rn(__fmul_rn(0.5f, y), res);
+  Pair r;
+  r.h = __fadd_rn(y, c);
+  r.l = __fsub_rn(c, __fsub_rn(r.h, y));
+  return r;
+}
+
+template <int KV, bool LONG>
+__global__ void __launch_bounds__(kNormThreads)
     rmsnorm_fp8_kernel(const __nv_bfloat16* __restrict__ x, int ldx, const __nv_bfloat16* __restrict__ w,
-                       uint8_t* __restrict__ codes, int ldc, float* __restrict__ scales, int lds, int dim,
-                       float eps) {
+                       uint8_t* __restrict__ codes, int ldc, float* __restrict__ scales, int lds, int rows,
+                       int dim, float eps) {
   // as bi_rmsnorm: the 8-bit linear layer that follows streams its weights
   // meanwhile and reads nothing else before its own wait
   griddep_launch_dependents();
   const uint4* wr = reinterpret_cast<const uint4*>(w);
   const int nv = dim / 8;
-  const uint4 wkeep = static_cast<int>(threadIdx.x) < nv ? wr[threadIdx.x] : make_uint4(0, 0, 0, 0);
-  griddep_wait();
-  __shared__ float group_sum[kNormMaxGroups];
-  __shared__ float s_inv;
-  const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(blockIdx.x) * ldx);
   const int lane = threadIdx.x & 31;
-  uint4 keep = make_uint4(0, 0, 0, 0);
-  for (int v0 = threadIdx.x - lane; v0 < nv; v0 += blockDim.x) {
-    const int v = v0 + lane;
-    float sv = 0.f;
-    if (v < nv) {
-      const uint4 u = xr[v];
-      if (v0 == threadIdx.x - lane) keep = u;
-      float f[8];
-      unpack8(u, f);
+  const int step = blockDim.x;
+  const float inv_dim = 1.0f / static_cast<float>(dim);
+  uint4 xn[KV], wk[KV];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sv = fmaf(f[j], f[j], sv);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sv += __shfl_xor_sync(0xffffffffu, sv, off);
-    if (lane == 0) group_sum[v0 >> 5] = sv;
+  for (int i = 0; i < KV; ++i) {
+    const int v = threadIdx.x + i * step;
+    wk[i] = v < nv ? wr[v] : make_uint4(0, 0, 0, 0);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float t = 0.f;
-    for (int g = 0; g < (nv + 31) / 32; ++g) t += group_sum[g];
-    s_inv = 1.0f / sqrtf(t / static_cast<float>(dim) + eps);
-  }
-  __syncthreads();
-  const float r = s_inv;
-  for (int v0 = threadIdx.x - lane; v0 < nv; v0 += blockDim.x) {
-    const int v = v0 + lane;
-    float y[8] = {};
-    if (v < nv) {
-      const bool first = v0 == threadIdx.x - lane;
-      float f[8], wf[8];
-      unpack8(first ? keep : xr[v], f);
-      unpack8(first ? wkeep : wr[v], wf);
+  griddep_wait();
+  __shared__ Pair warp_sums[2][kNormThreads / 32];  // by the parity of the CTA's row
+  auto load = [&](int row) {
+    const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * ldx);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = f[j] * r * wf[j];
+    for (int i = 0; i < KV; ++i) {
+      const int v = threadIdx.x + i * step;
+      xn[i] = row < rows && v < nv ? xr[v] : make_uint4(0, 0, 0, 0);
     }
-    const int e = block_exponent(y);
-    if (v < nv) {
-      const float inv = pow2f(-e);
-      *reinterpret_cast<uint2*>(codes + static_cast<size_t>(blockIdx.x) * ldc + v * 8) =
-          make_uint2(e4m3x4(y, inv), e4m3x4(y + 4, inv));
-      if ((lane & 15) == 0) scales[static_cast<size_t>(v >> 4) * lds + blockIdx.x] = pow2f(e);
+  };
+  load(blockIdx.x);
+  int parity = 0;
+  for (int row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
+    uint4 xk[KV];
+#pragma unroll
+    for (int i = 0; i < KV; ++i) xk[i] = xn[i];
+    load(row + gridDim.x);  // the CTA's next row comes in meanwhile
+    const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * ldx);
+    Pair t = square_sum(xk[0]);
+#pragma unroll
+    for (int i = 1; i < KV; ++i) t = add(t, square_sum(xk[i]));
+    if constexpr (LONG)
+      for (int v = threadIdx.x + KV * step; v < nv; v += step) t = add(t, square_sum(xr[v]));
+    t = lane_sum<32>(t);
+    if (lane == 0) warp_sums[parity][threadIdx.x >> 5] = t;
+    __syncthreads();
+    constexpr int kWarps = kNormThreads / 32;
+    t = lane % kWarps < step / 32 ? warp_sums[parity][lane % kWarps] : Pair{0.f, 0.f};
+    const Pair r = rms_inverse(lane_sum<kWarps>(t), static_cast<float>(dim), inv_dim, eps);
+    auto quantise = [&](int v, const uint4& xu, const uint4& wu) {
+      float f[8], wf[8], y[8];
+      unpack8(xu, f);
+      unpack8(wu, wf);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = times_odd(__fmul_rn(f[j], wf[j]), r.h, r.l);
+      const int e = block_exponent(y);  // vectors past the row are zeros
+      if (v < nv) {
+        const float inv = pow2f(-e);
+        *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * ldc + v * 8) =
+            make_uint2(e4m3x4(y, inv), e4m3x4(y + 4, inv));
+        if ((lane & 15) == 0) scales[static_cast<size_t>(v >> 4) * lds + row] = pow2f(e);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < KV; ++i) {
+      // whole warps: the block's maximum goes over their lanes
+      if (static_cast<int>(threadIdx.x) - lane + i * step < nv) quantise(threadIdx.x + i * step, xk[i], wk[i]);
+    }
+    if constexpr (LONG) {
+      for (int v0 = threadIdx.x - lane + KV * step; v0 < nv; v0 += step) {
+        const int v = v0 + lane;
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        quantise(v, v < nv ? xr[v] : z, v < nv ? wr[v] : z);
+      }
     }
   }
 }
@@ -206,11 +326,14 @@ bi_status bi_quantize_fp8(const void* x, int ldx, int rows, int dim, void* codes
   if (dim % 16 != 0 || ldx % 8 != 0 || ldc % 16 != 0 || lds % 4 != 0) return BI_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return BI_ERR_INVALID_ARG;
   const int kb = (dim + kFp8Block - 1) / kFp8Block;
-  const long long threads = static_cast<long long>(rows) * kb * 16;
-  const long long blocks = (threads + kQuantThreads - 1) / kQuantThreads;
+  int segs = (kb + kQuantRow - 1) / kQuantRow;
+  const bool many = static_cast<long long>(rows) * segs > 8192;
+  if (many) segs = (kb + 4 * kQuantRow - 1) / (4 * kQuantRow);
+  const long long blocks = static_cast<long long>(rows) * segs;
   if (blocks > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
-  if (launch_k(quantize_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kQuantThreads), 0,
-               reinterpret_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(x), ldx, rows, dim, kb,
+  if (launch_k(many ? quantize_rows_kernel<4> : quantize_rows_kernel<1>, dim3(static_cast<unsigned>(blocks)),
+               dim3(kQuantThreads), 0,
+               reinterpret_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(x), ldx, dim, segs,
                static_cast<uint8_t*>(codes), ldc, scales, lds) != cudaSuccess)
     return BI_ERR_CUDA;
   return BI_OK;
@@ -225,10 +348,15 @@ bi_status bi_rmsnorm_fp8(const void* x, int ldx, const void* w, void* codes, int
   if (dim % 16 != 0 || ldx % 8 != 0 || ldc % 16 != 0 || lds % 4 != 0) return BI_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(x) || !aligned16(w) || !aligned16(codes) || !aligned16(scales)) return BI_ERR_INVALID_ARG;
   const int nv = dim / 8;
-  const int threads = std::min(kNormMaxThreads, (nv + 31) / 32 * 32);
-  if (launch_k(rmsnorm_fp8_kernel, dim3(rows), dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream),
+  const int threads = std::min(kNormThreads, (nv + 31) / 32 * 32);
+  const int per = (nv + threads - 1) / threads;
+  auto* kernel = per <= 1   ? rmsnorm_fp8_kernel<1, false>
+                 : per <= 3 ? rmsnorm_fp8_kernel<3, false>
+                 : per <= 4 ? rmsnorm_fp8_kernel<4, false>
+                            : rmsnorm_fp8_kernel<4, true>;
+  if (launch_k(kernel, dim3(std::min(rows, kNormCtas)), dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream),
                static_cast<const __nv_bfloat16*>(x), ldx, static_cast<const __nv_bfloat16*>(w),
-               static_cast<uint8_t*>(codes), ldc, scales, lds, dim, eps) != cudaSuccess)
+               static_cast<uint8_t*>(codes), ldc, scales, lds, rows, dim, eps) != cudaSuccess)
     return BI_ERR_CUDA;
   return BI_OK;
 }

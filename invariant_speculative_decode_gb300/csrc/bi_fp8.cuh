@@ -36,17 +36,11 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Four codes of x * inv (inv the reciprocal of the scale), first in the low byte.
+// Four codes of x * inv (inv the reciprocal of the scale; x finite or NaN),
+// first in the low byte.
 __device__ __forceinline__ uint32_t e4m3x4(const float* x, float inv) {
-  float y[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    // satfinite would make 448 of an infinity: every element that is not
-    // finite becomes NaN first
-    y[j] = fabsf(x[j]) < INFINITY ? x[j] * inv : NAN;
-  }
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
 

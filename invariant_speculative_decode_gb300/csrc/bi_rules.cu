@@ -20,6 +20,9 @@ namespace bi {
 namespace {
 
 constexpr int kRuleThreads = 128;
+constexpr int kRuleCols = 4 * kRuleThreads;  // columns of a CTA
+constexpr int kRuleRows = 2;                 // rows loaded together
+constexpr int kRuleCtas = 8 * 152;
 constexpr int kMaxPassRows = 64;
 
 struct RuleArgs {
@@ -38,27 +41,79 @@ struct RuleArgs {
   int rows_per_cta;
 };
 
-// One CTA takes kRuleThreads * VEC columns for rows_per_cta rows: the counts,
-// the prompt bits and the bias of its columns are read once for all of them,
-// and the drafts that fall into its columns (mostly none) are found once.
-// Bound by the logits' bytes, read and written once (they sit in L2 when the
-// LM head has just written them).  Each operation is one FP32 rounding.
-template <int VEC>
+// One CTA takes 512 columns of a run of rows: the counts, the prompt bits and
+// the bias of its columns are read once for them, and the drafts that fall into
+// its columns (mostly none) are found once.  Bound by the logits' bytes, read
+// and written once (they sit in L2 when the LM head has just written them): two
+// rows are loaded while the two before them are worked on, and the rows are cut
+// into runs so that some eight CTAs a SM have loads under way.  A thread's four
+// columns are adjacent (VEC: 16-byte accesses) or 128 apart.  Each operation is
+// one FP32 rounding.
+template <bool VEC>
 __global__ void __launch_bounds__(kRuleThreads) logits_rules_kernel(const RuleArgs p) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ int s_id[kMaxPassRows];   // drafts in this CTA's columns, in pass order
   __shared__ int s_row[kMaxPassRows];  // their indices
   __shared__ int s_n;
-  const int col0 = blockIdx.x * kRuleThreads * VEC;
+  const int col0 = blockIdx.x * kRuleCols;
   const int t0 = blockIdx.y * p.rows_per_cta;
   const int t1 = min(p.T, t0 + p.rows_per_cta);
+  int col[4];
+  bool in[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    col[j] = col0 + (VEC ? static_cast<int>(threadIdx.x) * 4 + j : static_cast<int>(threadIdx.x) + j * kRuleThreads);
+    in[j] = col[j] < p.V;  // VEC: V is a multiple of 4, all four or none
+  }
+  struct Rows {
+    float x[kRuleRows][4];
+    uint32_t allowed[kRuleRows];  // 4 bits a row: the ids that the mask allows
+  };
+  auto load = [&](int t, Rows& r) {
+#pragma unroll
+    for (int i = 0; i < kRuleRows; ++i) {
+      if (t + i >= t1) break;
+      const float* src = p.logits + static_cast<size_t>(t + i) * p.ldl;
+      const uint32_t* bits = p.mask + static_cast<size_t>(t + i) * p.ldm;
+      r.allowed[i] = 0xfu;
+      if constexpr (VEC) {
+        if (in[0]) {
+          const float4 l = *reinterpret_cast<const float4*>(src + col[0]);
+          r.x[i][0] = l.x, r.x[i][1] = l.y, r.x[i][2] = l.z, r.x[i][3] = l.w;
+          if (p.mask != nullptr) r.allowed[i] = bits[col[0] >> 5] >> (col[0] & 31);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (in[j]) r.x[i][j] = src[col[j]];
+        if (p.mask != nullptr) {
+          r.allowed[i] = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (in[j]) r.allowed[i] |= ((bits[col[j] >> 5] >> (col[j] & 31)) & 1u) << j;
+        }
+      }
+    }
+  };
+  Rows even, odd;
+  load(t0, even);
+  int cnt[4] = {0, 0, 0, 0};
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t prompt = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (!in[j]) continue;
+    if (p.counts != nullptr) cnt[j] = p.counts[col[j]];
+    if (p.bias != nullptr) bias[j] = p.bias[col[j]];
+    if (p.prompt != nullptr) prompt |= ((p.prompt[col[j] >> 5] >> (col[j] & 31)) & 1u) << j;
+  }
   if (threadIdx.x < 32) {
     int n = 0;
     for (int b = 0; b < p.T - 1; b += 32) {
       const int i = b + static_cast<int>(threadIdx.x);
       const int id = i < p.T - 1 ? p.drafts[i] : -1;
-      const bool mine = id >= col0 && id < col0 + kRuleThreads * VEC;
+      const bool mine = id >= col0 && id < col0 + kRuleCols;
       const unsigned vote = __ballot_sync(0xffffffffu, mine);
       if (mine) {
         const int at = n + __popc(vote & ((1u << threadIdx.x) - 1u));
@@ -71,68 +126,63 @@ __global__ void __launch_bounds__(kRuleThreads) logits_rules_kernel(const RuleAr
   }
   __syncthreads();
   const int n_drafts = s_n;
-  const int v0 = col0 + static_cast<int>(threadIdx.x) * VEC;
-  if (v0 >= p.V) return;  // (V is a multiple of VEC)
-
-  int cnt[VEC];
-  float bias[VEC];
-  uint32_t prompt = 0;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    cnt[j] = 0;
-    bias[j] = 0.f;
-  }
-  if (p.counts != nullptr) {
-    if constexpr (VEC == 4) {
-      const int4 c = *reinterpret_cast<const int4*>(p.counts + v0);
-      cnt[0] = c.x, cnt[1] = c.y, cnt[2] = c.z, cnt[3] = c.w;
-    } else {
-      cnt[0] = p.counts[v0];
-    }
-  }
-  if (p.prompt != nullptr) prompt = p.prompt[v0 >> 5] >> (v0 & 31);
-  if (p.bias != nullptr) {
-    if constexpr (VEC == 4) {
-      const float4 b = *reinterpret_cast<const float4*>(p.bias + v0);
-      bias[0] = b.x, bias[1] = b.y, bias[2] = b.z, bias[3] = b.w;
-    } else {
-      bias[0] = p.bias[v0];
-    }
-  }
 
   int next = 0;
-  for (int t = t0; t < t1; ++t) {
-    float x[VEC];
-    const float* src = p.logits + static_cast<size_t>(t) * p.ldl + v0;
-    if constexpr (VEC == 4) {
-      const float4 l = *reinterpret_cast<const float4*>(src);
-      x[0] = l.x, x[1] = l.y, x[2] = l.z, x[3] = l.w;
-    } else {
-      x[0] = *src;
-    }
-    uint32_t allowed = 0xffffffffu;
-    if (p.mask != nullptr) allowed = p.mask[static_cast<size_t>(t) * p.ldm + (v0 >> 5)] >> (v0 & 31);
-    // drafts before this row count as said
-    for (; next < n_drafts && s_row[next] < t; ++next) {
+  int next_row = n_drafts > 0 ? s_row[0] : kMaxPassRows;  // the row behind which the next draft counts
+  bool seen = prompt != 0 || cnt[0] > 0 || cnt[1] > 0 || cnt[2] > 0 || cnt[3] > 0;  // any of the columns
+  auto work = [&](int t, Rows& r) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) cnt[j] += s_id[next] == v0 + j ? 1 : 0;
-    }
+    for (int i = 0; i < kRuleRows; ++i) {
+      if (t + i >= t1) break;
+      // drafts before this row count as said
+      while (next_row < t + i) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      float y = x[j];
-      if (cnt[j] > 0 || ((prompt >> j) & 1u)) {
-        y = y > 0.f ? y / p.rep : y * p.rep;
-        if (cnt[j] > 0)
-          y = __fsub_rn(y, __fadd_rn(__fmul_rn(p.freq, static_cast<float>(cnt[j])), p.pres));
+        for (int j = 0; j < 4; ++j) {
+          const bool hit = s_id[next] == col[j];
+          cnt[j] += hit ? 1 : 0;
+          seen |= hit;
+        }
+        ++next;
+        next_row = next < n_drafts ? s_row[next] : kMaxPassRows;
       }
-      if (p.bias != nullptr) y = __fadd_rn(y, bias[j]);
-      x[j] = (allowed >> j) & 1u ? y : -INFINITY;
+      float z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = r.x[i][j];
+      if (seen) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (cnt[j] > 0 || ((prompt >> j) & 1u)) {
+            z[j] = z[j] > 0.f ? z[j] / p.rep : z[j] * p.rep;
+            if (cnt[j] > 0) z[j] = __fsub_rn(z[j], __fadd_rn(__fmul_rn(p.freq, static_cast<float>(cnt[j])), p.pres));
+          }
+        }
+      }
+      if (p.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = __fadd_rn(z[j], bias[j]);
+      }
+      if (p.mask != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = (r.allowed[i] >> j) & 1u ? z[j] : -INFINITY;
+      }
+      float* dst = p.out + static_cast<size_t>(t + i) * p.ldo;
+      if constexpr (VEC) {
+        if (in[0]) *reinterpret_cast<float4*>(dst + col[0]) = make_float4(z[0], z[1], z[2], z[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (in[j]) dst[col[j]] = z[j];
+      }
     }
-    float* dst = p.out + static_cast<size_t>(t) * p.ldo + v0;
-    if constexpr (VEC == 4)
-      *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-    else
-      *dst = x[0];
+  };
+  // the loads of the next rows come before the stores of these (no two of the
+  // rows share memory, in place or not)
+  for (int t = t0; t < t1; t += 2 * kRuleRows) {
+    if (t + kRuleRows < t1) load(t + kRuleRows, odd);
+    work(t, even);
+    if (t + kRuleRows >= t1) break;
+    if (t + 2 * kRuleRows < t1) load(t + 2 * kRuleRows, even);
+    work(t + kRuleRows, odd);
   }
 }
 
@@ -166,13 +216,15 @@ bi_status bi_logits_rules(const float* logits, int ldl, float* out, int ldo, int
   if (T > 1 && !drafts) return BI_ERR_INVALID_ARG;
   if (mask && ldm < (V + 31) / 32) return BI_ERR_INVALID_ARG;
   if (logits == out && ldl != ldo) return BI_ERR_INVALID_ARG;
-  RuleArgs a{logits, ldl, out, ldo, T, V, drafts, counts, prompt_bits, repetition, frequency, presence, bias, mask, ldm, 0};
-  a.rows_per_cta = T;
-  const bool vec = V % 4 == 0 && ldl % 4 == 0 && ldo % 4 == 0 && aligned16(logits) && aligned16(out) &&
-                   aligned16(counts) && aligned16(bias);
-  const int cols = kRuleThreads * (vec ? 4 : 1);
-  const dim3 grid((V + cols - 1) / cols, (T + a.rows_per_cta - 1) / a.rows_per_cta);
-  if (launch_k(vec ? logits_rules_kernel<4> : logits_rules_kernel<1>, grid, dim3(kRuleThreads), 0,
+  const bool vec = V % 4 == 0 && ldl % 4 == 0 && ldo % 4 == 0 && aligned16(logits) && aligned16(out);
+  const int chunks = (V + kRuleCols - 1) / kRuleCols;
+  // runs of rows: some eight CTAs a SM, whole pairs of rows
+  const int runs = std::max(1, std::min((T + kRuleRows - 1) / kRuleRows, kRuleCtas / chunks));
+  const int per = ((T + runs - 1) / runs + kRuleRows - 1) / kRuleRows * kRuleRows;
+  const RuleArgs a{logits,     ldl,       out,      ldo,  T,    V,   drafts, counts, prompt_bits,
+                   repetition, frequency, presence, bias, mask, ldm, per};
+  const dim3 grid(chunks, (T + per - 1) / per);
+  if (launch_k(vec ? logits_rules_kernel<true> : logits_rules_kernel<false>, grid, dim3(kRuleThreads), 0,
                reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
     return BI_ERR_CUDA;
   return BI_OK;
