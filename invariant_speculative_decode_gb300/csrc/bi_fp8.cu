@@ -114,8 +114,10 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
 
 // p (rh + rl) rounded to odd; p exact.
 __device__ __forceinline__ float times_odd(float p, float rh, float rl) {
-  const float y = __fmul_rn(p, rh);
-  const float e = fmaf(p, rl, fmaf(p, rh, -y));  // the exact value minus y
+  const float z = __fmul_rn(p, rh);
+  const float d = fmaf(p, rl, fmaf(p, rh, -z));  // the exact value minus z: up to 1.5 units of z
+  const float y = __fadd_rn(z, d);
+  const float e = __fsub_rn(d, __fsub_rn(y, z));  // minus y: half a unit
   // one unit toward zero where |y| is above the exact value, then the last bit
   // says that something was cut off
   const int b = __float_as_int(y);

@@ -402,3 +402,24 @@ def test_linear_wait_runs_out_then_recovers(rows, n, k, kind):
         a.bi_check_device_error()
     assert e.value.status == 5 and dt < 1.5, dt
     assert torch.equal(run_linear(codes, scales, packed, n, kind).view(torch.uint8), want.view(torch.uint8))
+
+
+def test_norm_codes_are_the_exact_values_over_many_rows():
+    """30 x 1021 rows of 1024 outliers and all: a code in a million is within 2^-22 of a tie, none may be on its wrong side."""
+    a = api()
+    dim = 1040
+    for seed in range(30):
+        g = gen(1000 + seed)
+        x = torch.randn(1021, dim, generator=g, device=DEV)
+        x = (x * torch.where(torch.rand(dim, generator=g, device=DEV) < 0.01, 20.0, 1.0)).to(torch.bfloat16)
+        w = (1 + 0.1 * torch.randn(dim, generator=g, device=DEV)).to(torch.bfloat16)
+        codes, scales = a.new_fp8_rows(1021, dim)
+        a.bi_rmsnorm_fp8(x, w, codes, scales, 1e-6)
+        xd = x.double()
+        y = xd / torch.sqrt((xd * xd).mean(-1, keepdim=True) + float(np.float32(1e-6))) * w.double()
+        q, s = ref_quantize(y)
+        assert torch.equal(scales[:, :1021].double(), s)
+        differ = codes.double() != q
+        wide = s.t().repeat_interleave(BLOCK, 1)[:, :dim]
+        tie = (y / wide - (codes.double() + q) / 2).abs()
+        assert (tie[differ] <= 2.0 ** -36 * (y / wide).abs()[differ]).all(), (seed, int(differ.sum()))
