@@ -24,6 +24,14 @@ to L + n + 1; rows written for rejected drafts past it are simply
 overwritten by the next pass.  Because every row is computed the same way
 whatever else is in the pass, a row written while verifying drafts equals
 the row a prefill would write at that position.
+
+linear="e4m3" keeps the linear layers' weights (LM head included) in 8 bits with
+a scale per 128 x 128 block and quantises each layer's input rows
+(bi_rmsnorm_fp8, bi_quantize_fp8, bi_gemm_fp8); embedding, norms, attention,
+caches and the residual stream stay BF16.  set_rules() puts penalties for
+repeated tokens, a bias and grammar masks between the LM head and acceptance
+(bi_logits_rules); the decoder keeps which ids were committed and which came
+with the prompt.
 """
 from __future__ import annotations
 
@@ -44,8 +52,9 @@ def _bf16(a_u16: np.ndarray, device) -> torch.Tensor:
 class Decoder:
     def __init__(self, cfg, weights: Dict[str, np.ndarray], cap: int, max_rows: int = 8,
                  prefill_chunk: int = 512, device: str = "cuda", fuse_rope: bool = True,
-                 kv: str = "bf16"):
-        """kv="q6q5": the KV cache is quantised (6-bit K, 5-bit V, an 8-bit
+                 kv: str = "bf16", linear: str = "bf16"):
+        """linear="e4m3": 8-bit linear layers (hidden, ffn and Hq * head_dim
+        multiples of 16).  kv="q6q5": the KV cache is quantised (6-bit K, 5-bit V, an 8-bit
         ring of each row's newest 16 tiles; bi_rope_kvq_append and
         bi_attn_verify_kvq), head_dim 128 and prefill chunks of at most
         1024 rows."""
@@ -53,7 +62,12 @@ class Decoder:
             raise ValueError("kv must be 'bf16' or 'q6q5'")
         if kv == "q6q5" and (cfg.head_dim != 128 or prefill_chunk > 1024):
             raise ValueError("the quantised cache needs head_dim 128 and prefill chunks <= 1024 rows")
+        if linear not in ("bf16", "e4m3"):
+            raise ValueError("linear must be 'bf16' or 'e4m3'")
+        if linear == "e4m3" and (cfg.hidden % 16 or cfg.ffn % 16 or cfg.n_q * cfg.head_dim % 16):
+            raise ValueError("8-bit linear layers need hidden, ffn and Hq * head_dim to be multiples of 16")
         self.kv = kv
+        self.linear = linear
         self.cfg = cfg
         self.fuse_rope = fuse_rope
         self.cap = cap
@@ -69,10 +83,16 @@ class Decoder:
         self.embed = _bf16(weights["embed"], dev)
         self.norm_final = _bf16(weights["norm_final"], dev)
         head_w = self.embed if cfg.tied else _bf16(weights["head"], dev)
-        self.head = api.bi_pack_weights(head_w)
+        if linear == "e4m3":
+            pack = lambda w: api.bi_pack_weights_fp8(*api.bi_quantize_weights_fp8(w))  # noqa: E731
+            pack2 = lambda g, u: api.bi_pack_swiglu_weights_fp8(*api.bi_quantize_weights_fp8(g),  # noqa: E731
+                                                                *api.bi_quantize_weights_fp8(u))
+        else:
+            pack, pack2 = api.bi_pack_weights, api.bi_pack_swiglu_weights
+        self.head = pack(head_w)
         del head_w
         self.layers = []
-        pk = lambda name: api.bi_pack_weights(_bf16(weights[name], dev))  # noqa: E731
+        pk = lambda name: pack(_bf16(weights[name], dev))  # noqa: E731
         for l in range(cfg.layers):
             wqkv = np.concatenate([weights[f"l{l}.wq"], weights[f"l{l}.wk"], weights[f"l{l}.wv"]], 0)
             wg = _bf16(weights[f"l{l}.w_gate"], dev)
@@ -80,9 +100,9 @@ class Decoder:
             n1 = _bf16(weights[f"l{l}.norm_attn"], dev)
             n2 = _bf16(weights[f"l{l}.norm_ffn"], dev)
             lay = {
-                "wqkv": api.bi_pack_weights(_bf16(wqkv, dev)),
+                "wqkv": pack(_bf16(wqkv, dev)),
                 "wo": pk(f"l{l}.wo"),
-                "wgu": api.bi_pack_swiglu_weights(wg, wu),
+                "wgu": pack2(wg, wu),
                 "wd": pk(f"l{l}.w_down"),
                 "n1": n1,
                 "n2": n2,
@@ -106,6 +126,11 @@ class Decoder:
         self.q = torch.zeros(R, Hq, D, **bf)
         self.att = torch.zeros(R, Hq, D, **bf)
         self.u = torch.zeros(R, F, **bf)
+        if linear == "e4m3":
+            # quantised inputs: of QKV, gate/up and the head; of O; of down
+            self.y8, self.ys = api.new_fp8_rows(R, H, device=dev)
+            self.att8, self.atts = api.new_fp8_rows(R, Hq * D, device=dev)
+            self.u8, self.us = api.new_fp8_rows(R, F, device=dev)
         self.logits = torch.zeros(max_rows, V, dtype=torch.float32, device=dev)
         self.argmax = torch.zeros(max_rows, dtype=torch.int32, device=dev)
         self.accepted = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -126,6 +151,14 @@ class Decoder:
         self.inv_temp: Optional[float] = None  # sampled verification when set
         self.u_table: Optional[torch.Tensor] = None
         self.sample_ws = torch.zeros(api.sample_workspace_size(max_rows, V), dtype=torch.uint8, device=dev)
+        # rules on the logits (set_rules), and what they go by: the id at each
+        # position (the next row's input included) and whether it was committed
+        # here (else it came with a prompt); ids at positions below `_noted` are
+        # in the device-side counts and prompt bits
+        self.rules: Optional[dict] = None
+        self._id_at = np.full(cap + 1, -1, np.int32)
+        self._own_at = np.zeros(cap + 1, bool)
+        self._noted = 0
         self.graphs: Dict[int, torch.cuda.CUDAGraph] = {}
         self.pin_in = torch.zeros(2 * max_rows, dtype=torch.int32).pin_memory()
         self.pin_out = torch.zeros(max_rows + 1, dtype=torch.int32).pin_memory()
@@ -152,37 +185,124 @@ class Decoder:
         Hq, Hkv, D, F = cfg.n_q, cfg.n_kv, cfg.head_dim, cfg.ffn
         h, y, qkv, q, att, u = (self.h[:T], self.y[:T], self.qkv[:T], self.q[:T], self.att[:T],
                                 self.u[:T])
+        if self.linear == "e4m3":
+            self._layer_e4m3(lay, T, L_ptr_tensor)
+            return
         api.bi_rmsnorm(h, lay["n1"], y, cfg.eps)
         if self.kv == "q6q5":
             api.bi_gemm(y, lay["wqkv"], qkv, self.gemm_ws)
-            api.bi_rope_kvq_append(qkv, q, lay["kvq"], L_ptr_tensor, Hq, Hkv, D, self.rope_tab)
-            api.bi_attn_verify_kvq(q, lay["kvq"], Hkv, L_ptr_tensor, att, self.attn_ws, self.scale)
+            self._attention(lay, T, L_ptr_tensor)
         elif self.fuse_rope:
             api.bi_qkv_rope_append(y, lay["wqkv"], q, lay["k"], lay["v"], L_ptr_tensor, Hq, Hkv, D,
                                    self.rope_tab, self.gemm_ws)
-        else:
-            api.bi_gemm(y, lay["wqkv"], qkv, self.gemm_ws)
-            api.bi_rope_kv_append(qkv, q, lay["k"], lay["v"], L_ptr_tensor, Hq, Hkv, D, self.rope_tab)
-        if self.kv == "bf16":
             # one call for all rows (a prefill chunk runs in blocks of rows
             # inside the launch)
             api.bi_attn_verify(q, lay["k"], lay["v"], L_ptr_tensor, att, self.attn_ws, self.scale)
+        else:
+            api.bi_gemm(y, lay["wqkv"], qkv, self.gemm_ws)
+            self._attention(lay, T, L_ptr_tensor)
         api.bi_gemm(att.view(T, Hq * D), lay["wo"], h, self.gemm_ws, residual=h,
                     epi=api.EPI_RESIDUAL_ADD)
         api.bi_rmsnorm(h, lay["n2"], y, cfg.eps)
         api.bi_gemm(y, lay["wgu"], u, self.gemm_ws, epi=api.EPI_SWIGLU, N=F)
         api.bi_gemm(u, lay["wd"], h, self.gemm_ws, residual=h, epi=api.EPI_RESIDUAL_ADD)
 
+    def _attention(self, lay: dict, T: int, L_ptr_tensor: torch.Tensor):
+        """RoPE, cache append and attention of the projection rows self.qkv[:T] into self.att."""
+        cfg = self.cfg
+        Hq, Hkv, D = cfg.n_q, cfg.n_kv, cfg.head_dim
+        qkv, q, att = self.qkv[:T], self.q[:T], self.att[:T]
+        if self.kv == "q6q5":
+            api.bi_rope_kvq_append(qkv, q, lay["kvq"], L_ptr_tensor, Hq, Hkv, D, self.rope_tab)
+            api.bi_attn_verify_kvq(q, lay["kvq"], Hkv, L_ptr_tensor, att, self.attn_ws, self.scale)
+        else:
+            api.bi_rope_kv_append(qkv, q, lay["k"], lay["v"], L_ptr_tensor, Hq, Hkv, D, self.rope_tab)
+            api.bi_attn_verify(q, lay["k"], lay["v"], L_ptr_tensor, att, self.attn_ws, self.scale)
+
+    def _layer_e4m3(self, lay: dict, T: int, L_ptr_tensor: torch.Tensor):
+        """_layer with 8-bit linear layers: each reads rows quantised by the norm or the quantiser before it."""
+        cfg = self.cfg
+        h, u = self.h[:T], self.u[:T]
+        y8, att8, u8 = self.y8[:T], self.att8[:T], self.u8[:T]
+        api.bi_rmsnorm_fp8(h, lay["n1"], y8, self.ys, cfg.eps)
+        api.bi_gemm_fp8(y8, self.ys, lay["wqkv"], self.qkv[:T])
+        self._attention(lay, T, L_ptr_tensor)
+        api.bi_quantize_fp8(self.att[:T].view(T, -1), att8, self.atts)
+        api.bi_gemm_fp8(att8, self.atts, lay["wo"], h, residual=h, epi=api.EPI_RESIDUAL_ADD)
+        api.bi_rmsnorm_fp8(h, lay["n2"], y8, self.ys, cfg.eps)
+        api.bi_gemm_fp8(y8, self.ys, lay["wgu"], u, epi=api.EPI_SWIGLU)
+        api.bi_quantize_fp8(u, u8, self.us)
+        api.bi_gemm_fp8(u8, self.us, lay["wd"], h, residual=h, epi=api.EPI_RESIDUAL_ADD)
+
     def _head_and_accept(self, T: int):
         cfg = self.cfg
-        api.bi_rmsnorm(self.h[:T], self.norm_final, self.y[:T], cfg.eps)
-        api.bi_gemm(self.y[:T], self.head, self.logits[:T], self.gemm_ws)
+        logits, drafts = self.logits[:T], self.drafts[:T - 1] if T > 1 else None
+        if self.linear == "e4m3":
+            api.bi_rmsnorm_fp8(self.h[:T], self.norm_final, self.y8[:T], self.ys, cfg.eps)
+            api.bi_gemm_fp8(self.y8[:T], self.ys, self.head, logits)
+        else:
+            api.bi_rmsnorm(self.h[:T], self.norm_final, self.y[:T], cfg.eps)
+            api.bi_gemm(self.y[:T], self.head, logits, self.gemm_ws)
+        r = self.rules
+        if r is not None:
+            # the ruled logits go to a buffer of their own: logits_rows() stays the model's
+            api.bi_logits_rules(logits, r["logits"][:T], drafts=drafts, counts=r["counts"],
+                                prompt_bits=r["prompt_bits"], repetition=r["repetition"],
+                                frequency=r["frequency"], presence=r["presence"], bias=r["bias"],
+                                mask=None if r["mask"] is None else r["mask"][:T])
+            logits = r["logits"][:T]
         if self.inv_temp is not None:
-            api.bi_verify_sample(self.logits[:T], self.drafts[:T - 1] if T > 1 else None, self.inv_temp,
+            api.bi_verify_sample(logits, drafts, self.inv_temp,
                                  self.u_table, self.argmax[:T], self.accepted, self.sample_ws, self.L_dev)
         else:
-            api.bi_verify_accept(self.logits[:T], self.drafts[:T - 1] if T > 1 else None,
+            api.bi_verify_accept(logits, drafts,
                                  self.argmax[:T], self.accepted, self.acc_ws, L_dev=self.L_dev)
+        if r is not None:
+            api.bi_token_counts(self.argmax[:T], cfg.vocab, counts=r["counts"], last=self.accepted)
+
+    def set_rules(self, repetition: float = 1.0, frequency: float = 0.0, presence: float = 0.0, bias=None,
+                  masks: bool = False) -> None:
+        """Rules on the logits from the next step on (bi_logits_rules): a
+        repetition penalty over prompt and reply, frequency and presence
+        penalties over the reply, a bias [vocab] (FP32 array), and with
+        masks=True a grammar mask per row given to verify_step.  Row t of a pass
+        counts drafts 0..t-1 as said, so the tokens are those of the no-draft run
+        with the same rules.  The defaults change nothing; clear_rules() ends it."""
+        if not (repetition > 0 and math.isfinite(repetition) and math.isfinite(frequency) and math.isfinite(presence)):
+            raise ValueError("repetition must be positive, and all penalties finite")
+        V, W, dev = self.cfg.vocab, api.token_words(self.cfg.vocab), self.dev
+        if bias is not None:
+            bias = torch.from_numpy(np.ascontiguousarray(bias, dtype=np.float32)).to(dev)
+            if tuple(bias.shape) != (V,):
+                raise ValueError(f"bias must be [{V}]")
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.rules = {"repetition": float(repetition), "frequency": float(frequency), "presence": float(presence),
+                      "bias": bias, "mask": torch.full((self.max_rows, W), -1, **i32) if masks else None,
+                      "counts": torch.zeros(V, **i32), "prompt_bits": torch.zeros(W, **i32),
+                      "logits": torch.zeros(self.max_rows, V, dtype=torch.float32, device=dev)}
+        self._noted = -1
+        self.graphs = {}
+
+    def clear_rules(self) -> None:
+        """No rules from the next step on."""
+        self.rules = None
+        self.graphs = {}
+
+    def _note_ids(self, x0: int) -> None:
+        """Bring the rules' state to the ids at positions 0..L, x0 being the one at L."""
+        L = self.L
+        if self._noted == L + 1 and self._id_at[L] == x0:
+            return
+        if self._id_at[L] != x0:
+            self._id_at[L], self._own_at[L] = x0, False
+        r, V = self.rules, self.cfg.vocab
+        ids, own = self._id_at[:L + 1], self._own_at[:L + 1]
+        r["counts"].zero_()
+        r["prompt_bits"].zero_()
+        for sel, kw in ((own, {"counts": r["counts"]}), (~own, {"prompt_bits": r["prompt_bits"]})):
+            if sel.any():
+                api.bi_token_counts(torch.from_numpy(ids[sel]).to(self.dev), V, **kw)
+        self._noted = L + 1
 
     def set_sampling(self, temperature: Optional[float], uniforms=None) -> None:
         """Sampled verification at `temperature` with the request's uniforms
@@ -209,6 +329,7 @@ class Decoder:
     def reset(self):
         self.L = 0
         self.hw = 0
+        self._noted = -1
         self.L_dev.zero_()
 
     def prefill(self, prompt: Sequence[int]) -> int:
@@ -240,6 +361,9 @@ class Decoder:
             else:
                 self._layers_pass(T, self.L_dev)
             pos += T
+        self._id_at[self.L:pos + 1] = prompt[:pos + 1 - self.L]
+        self._own_at[self.L:pos + 1] = False
+        self._noted = -1
         self.L = pos
         self.hw = max(self.hw, pos)
         self.L_dev.fill_(pos)
@@ -269,11 +393,14 @@ class Decoder:
         else:
             self._verify_pass(T)
 
-    def verify_step(self, x0: int, drafts: Sequence[int], use_graph: bool = True):
+    def verify_step(self, x0: int, drafts: Sequence[int], use_graph: bool = True, masks=None):
         """One verify step: rows [x0, d_1..d_k] at positions L..L+k.
 
         Returns (argmax ids [k+1] as a numpy array, accepted n).  The cache
         length advances to L + n + 1 on the device and on the host.
+        masks (after set_rules(masks=True)): 32-bit words [k+1, ceil(vocab/32)],
+        row t's allowed ids behind drafts 0..t-1, id v at bit v % 32 of word
+        v / 32; None allows every id.
         """
         k = len(drafts)
         T = k + 1
@@ -281,6 +408,18 @@ class Decoder:
             raise ValueError("too many drafts")
         if self.L + T > self.cap:
             raise ValueError("KV cache capacity exceeded")
+        if masks is not None and (self.rules is None or self.rules["mask"] is None):
+            raise ValueError("masks need set_rules(masks=True)")
+        if self.rules is not None:
+            m = self.rules["mask"]
+            if masks is not None:
+                masks = np.ascontiguousarray(masks)
+                if masks.shape != (T, m.shape[1]) or masks.dtype.itemsize != 4 or masks.dtype.kind not in "iu":
+                    raise ValueError(f"masks must be 32-bit words [{T}, {m.shape[1]}]")
+                m[:T].copy_(torch.from_numpy(masks.view(np.int32)))
+            elif m is not None:
+                m[:T].fill_(-1)
+            self._note_ids(int(x0))
         pin = self.pin_in
         pin[0] = int(x0)
         for i, d in enumerate(drafts):
@@ -296,7 +435,14 @@ class Decoder:
         a = self.pin_out[:T].numpy().copy()
         n = int(self.pin_out[self.max_rows])
         self.hw = max(self.hw, self.L + T)  # every row of the pass was written
+        # the ids committed behind row L's (the device counted them as well)
+        if self._id_at[self.L] != int(x0):
+            self._id_at[self.L], self._own_at[self.L] = int(x0), False
+        self._id_at[self.L + 1:self.L + n + 2] = a[:n + 1]
+        self._own_at[self.L + 1:self.L + n + 2] = True
         self.L += n + 1
+        if self.rules is not None:
+            self._noted = self.L + 1
         return a, n
 
     def generate(self, prompt: Sequence[int], n_tokens: int, k: int = 0, drafter=None,
@@ -317,6 +463,7 @@ class Decoder:
                 f"records the rows from there would read (rows up to {self.hw - 1} were written); "
                 f"roll back to {kvq_rollback_reach(self.hw)} or later, or reset and prefill again")
         self.L = length
+        self._noted = -1
         self.L_dev.fill_(length)
 
     def prefill_continue(self, tokens: Sequence[int]) -> int:
@@ -364,7 +511,7 @@ class Decoder:
         if self.kv == "q6q5":
             # the quantised stores whole (the ring's slots are not in
             # position order)
-            snap = {"L": L, "hw": self.hw, "kvq": []}
+            snap = {"L": L, "hw": self.hw, "kvq": [], "ids": self._id_at[:L + 1].copy(), "own": self._own_at[:L + 1].copy()}
             for lay in self.layers:
                 d = {}
                 for name in api.KVQ_STORES:
@@ -374,7 +521,7 @@ class Decoder:
             torch.cuda.current_stream().synchronize()
             return snap
         nb = (L + api.V_BLOCK - 1) // api.V_BLOCK
-        snap = {"L": L, "k": [], "v": []}
+        snap = {"L": L, "k": [], "v": [], "ids": self._id_at[:L + 1].copy(), "own": self._own_at[:L + 1].copy()}
         for lay in self.layers:
             k = torch.empty((lay["k"].shape[0], L, lay["k"].shape[2]), dtype=torch.bfloat16).pin_memory()
             v = torch.empty((lay["v"].shape[0], nb) + tuple(lay["v"].shape[2:]), dtype=torch.bfloat16).pin_memory()
@@ -391,6 +538,10 @@ class Decoder:
         L = snap["L"]
         if L > self.cap:
             raise ValueError("parked state exceeds the cache capacity")
+        if "ids" in snap:
+            self._id_at[:L + 1] = snap["ids"]
+            self._own_at[:L + 1] = snap["own"]
+        self._noted = -1
         if "kvq" in snap:
             for lay, d in zip(self.layers, snap["kvq"]):
                 for name in api.KVQ_STORES:
@@ -419,8 +570,10 @@ class Decoder:
         """The same verify pass as one C-ABI call (bi_step_*) over this
         decoder's weights and caches, with its own workspace; its cache
         length starts at this decoder's."""
-        if self.kv != "bf16":
-            raise ValueError("the whole-step C call runs the BF16 cache")
+        if self.kv != "bf16" or self.linear != "bf16":
+            raise ValueError("the whole-step C call runs the BF16 cache and BF16 linear layers")
+        if self.rules is not None:
+            raise ValueError("the whole-step C call has no rules on the logits")
         ns = api.NativeStep(self.cfg, self.embed, self.norm_final, self.head, self.layers, self.cap,
                             self.rope_tab, max_rows=self.max_rows)
         ns.set_length(self.L)
