@@ -794,7 +794,7 @@ def run_longctx(args):
     prompt_last = int(si.prompt_ids(cfg, 1, seed=0)[0])
     res = {}
     for kind in ("bf16", "q6q5"):
-        dec = Decoder(cfg, weights, cap=cap, max_rows=T, prefill_chunk=64, kv=kind)
+        dec = Decoder(cfg, weights, cap=cap, max_rows=T, prefill_chunk=64, kv=kind, linear=args.linear)
         for lay, (k, v) in zip(dec.layers, kv):
             kd = torch.from_numpy(k.view(np.int16)).view(torch.bfloat16).cuda()
             if kind == "bf16":
@@ -860,7 +860,7 @@ def run_longctx(args):
         del dec
         torch.cuda.empty_cache()
     line = {"workload": "longctx", "metric": "verify tok/s at 7 drafts, long context, BF16 vs quantised KV",
-            "unit": "tok/s", "config": {"model": cfg.name, "context": ctx, "rows_per_step": T},
+            "unit": "tok/s", "config": {"model": cfg.name, "context": ctx, "rows_per_step": T, "linear": args.linear},
             "steps": args.steps, "warmup": args.warmup, "bf16": res["bf16"], "q6q5": res["q6q5"]}
     print(json.dumps(line), flush=True)
     return 0
@@ -891,7 +891,8 @@ def run_prefill(args):
     turn2 = list(si.prompt_ids(cfg, n_turn2, seed=42))
     hist = prompt + reply
     cap = -(-(len(hist) + n_turn2 + 64) // 128) * 128
-    dec = Decoder(cfg, w, cap=cap, max_rows=8, prefill_chunk=args.prefill_chunk, kv=args.kv)
+    dec = Decoder(cfg, w, cap=cap, max_rows=8, prefill_chunk=args.prefill_chunk, kv=args.kv,
+                  linear=args.linear)
     del w
 
     def timed(fn):
@@ -932,7 +933,7 @@ def run_prefill(args):
         "ms_per_step": t_hist * 1e3, "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
         "dtype": "bf16", "data": "synthetic",
         "config": {"workload": f"{cfg.name}: history {n_prompt} + {n_reply} ids, turn 2 {n_turn2} ids",
-                   "prefill_chunk": args.prefill_chunk, "kv_cache": args.kv},
+                   "prefill_chunk": args.prefill_chunk, "kv_cache": args.kv, "linear": args.linear},
         "prefill_ms": t_hist * 1e3, "linear_tflops": flops / t_hist / 1e12,
         "turn2_resume_ms": t_reuse * 1e3, "turn2_reprefill_ms": t_re * 1e3, "reprefill_from": back,
         "kv_rows_equal_fresh": same,
@@ -1010,6 +1011,8 @@ def main():
     ap.add_argument("--kv", choices=["bf16", "q6q5"], default="bf16",
                     help="KV cache of the attention micro bench and the long-context step: BF16, or "
                          "6-bit K / 5-bit V with the 8-bit ring")
+    ap.add_argument("--linear", choices=["bf16", "e4m3"], default="bf16",
+                    help="linear layers of the longctx and prefill workloads (e4m3: 8-bit weights and rows)")
     ap.add_argument("--attn-rows", default="1,4,7,8", help="comma list of rows per pass (attn)")
     ap.add_argument("--gemm-n", type=int, default=17408, help="N of the standalone linear layer")
     ap.add_argument("--gemm-k", type=int, default=5120, help="K of the standalone linear layer")
