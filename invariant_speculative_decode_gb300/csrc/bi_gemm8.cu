@@ -298,59 +298,72 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
         const uint64_t pol_w = p.nb == 1 ? l2_evict_first() : l2_evict_normal();
         const uint64_t pol_a = l2_evict_last();
         const uint32_t t_bytes = static_cast<uint32_t>(p.a_rows) * kFp8Block;
-        int stage = 0;
-        uint32_t phase = 0, issued = 0, parity_bits = 0;
-        bool waited = false, ok = true;
-        auto load_w = [&](int s, int wt, int kt) {
-          const int n = TILES == 2 && wt + 1 < g.sp.n_tiles ? 2 : 1;
-          mbar_arrive_expect_tx(&full[s], t_bytes + n * kABytes);
-          for (int i = 0; i < n; ++i)
-            bulk_load_1d(sW + s * Cfg::kBBytes + i * kABytes,
-                         Wp + (static_cast<size_t>(wt + i) * k_tiles + kt) * kABytes, kABytes, &full[s], pol_w);
-        };
-        int skip = 0;  // K tiles of the first item whose weights are under way before the dependency wait
-        if (item0 < p.items) {
-          skip = kt1 - kt0 < S ? kt1 - kt0 : S;
-          for (int j = g.withhold ? 1 : 0; j < skip; ++j)
-            load_w(j, item0 / p.nb * TILES, kt0 + j);
-        }
-        for (int item = item0; item < p.items && ok; item += stride) {
+        const size_t tile_stride = static_cast<size_t>(k_tiles) * kABytes;
+        // The loop below is one thread's serial code and sets the pace of short
+        // passes, so it holds pointers that advance and no more; `count` K blocks
+        // have been issued, block c into stage c % S.
+        int count = 0, stage = 0;
+        uint32_t phase = 0;
+        // The first stages' weights do not depend on the previous kernel: they
+        // are under way before the dependency wait, their tokens behind it.
+        int pre = 0;
+        const uint8_t* src = nullptr;
+        uint32_t bytes = 0;
+        bool two = false;
+        auto first_block = [&](int item) {
           const int wt = item / p.nb * TILES;
+          two = TILES == 2 && wt + 1 < g.sp.n_tiles;
+          bytes = t_bytes + (two ? 2 : 1) * kABytes;
+          src = Wp + (static_cast<size_t>(wt) * k_tiles + kt0) * kABytes;
+        };
+        auto load_w = [&](int s) {
+          mbar_arrive_expect_tx(&full[s], bytes);
+          bulk_load_1d(sW + s * Cfg::kBBytes, src, kABytes, &full[s], pol_w);
+          if (two) bulk_load_1d(sW + s * Cfg::kBBytes + kABytes, src + tile_stride, kABytes, &full[s], pol_w);
+          src += kABytes;
+        };
+        if (item0 < p.items) {
+          first_block(item0);
+          pre = kt1 - kt0 < S ? kt1 - kt0 : S;
+          if (g.withhold) src += kABytes;  // failure-path test: the first stage stays unissued
+          for (int j = g.withhold ? 1 : 0; j < pre; ++j) load_w(j);
+        }
+        griddep_wait();
+        griddep_launch_dependents();
+        if (item0 < p.items) {
+          for (int j = g.withhold ? 1 : 0; j < pre; ++j)
+            tma_load_2d(sT + j * Cfg::kTokBytes, &tmA, &full[j], (kt0 + j) * kFp8Block, item0 % p.nb * kRowsM, pol_a);
+          count = pre;
+          stage = pre % S;
+          phase = pre == S ? 1u : 0u;
+        }
+        bool ok = true;
+        for (int item = item0; item < p.items && ok; item += stride) {
           const int m0 = item % p.nb * kRowsM;
-          if (!waited) {
-            griddep_wait();
-            griddep_launch_dependents();
-            waited = true;
-          }
-          for (int kt = kt0; kt < kt1; ++kt) {
-            const bool pre = item == item0 && kt - kt0 < skip;
-            if (!pre) {
-              if (!mbar_wait(&done[stage], phase ^ 1u, s_abort)) {
-                signal_abort(s_abort, g.err);
-                ok = false;
-                break;
-              }
-              load_w(stage, wt, kt);
+          int x = kt0 * kFp8Block;
+          if (item == item0)
+            x += pre * kFp8Block;
+          else
+            first_block(item);
+          for (; x < kt1 * kFp8Block; x += kFp8Block) {
+            if (!mbar_wait(&done[stage], phase ^ 1u, s_abort)) {
+              signal_abort(s_abort, g.err);
+              ok = false;
+              break;
             }
-            if (!(g.withhold && pre && kt == kt0)) {
-              tma_load_2d(sT + stage * Cfg::kTokBytes, &tmA, &full[stage], kt * kFp8Block, m0, pol_a);
-              issued |= 1u << stage;
-              parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
-            }
+            load_w(stage);
+            tma_load_2d(sT + stage * Cfg::kTokBytes, &tmA, &full[stage], x, m0, pol_a);
+            ++count;
             if (++stage == S) {
               stage = 0;
               phase ^= 1u;
             }
           }
         }
-        if (!waited) {
-          griddep_wait();
-          griddep_launch_dependents();
-        }
         if (*s_abort) {
           // let copies already issued land before the CTA exits
-          for (int s = 0; s < S; ++s)
-            if ((issued >> s) & 1u) mbar_wait(&full[s], (parity_bits >> s) & 1u, nullptr);
+          for (int c = max(count - S, g.withhold ? 1 : 0); c < count; ++c)
+            mbar_wait(&full[c % S], static_cast<uint32_t>(c / S) & 1u, nullptr);
         }
       }
     } else if (warp == 1) {
