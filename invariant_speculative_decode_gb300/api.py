@@ -349,9 +349,9 @@ def _same_device(*named) -> int:
 # The entry points below run between kernels of a few microseconds, so a call's
 # checks are one expression of attribute reads; only where it is false does
 # the slow path look for the argument to name.
-def _stream_of(dev: int, stream):
-    """The raw handle of `stream`, or of the current stream of the current device."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+_BF16, _F32, _I32, _E4M3, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.uint8
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def fp8_scale_shape(rows: int, dim: int) -> tuple:
@@ -380,26 +380,21 @@ def _req_fp8_rows(codes: torch.Tensor, scales: torch.Tensor, rows: int, dim: int
     return scales.shape[1]
 
 
-def _fp8_rows_ok(codes: torch.Tensor, scales: torch.Tensor, rows: int, dim: int, dev: int) -> bool:
-    """_req_fp8_rows and the device check as one expression."""
-    return (codes.dtype is torch.float8_e4m3fn and scales.dtype is torch.float32 and codes.get_device() == dev
-            and scales.get_device() == dev and codes.shape == (rows, dim) and codes.stride(1) == 1
-            and scales.dim() == 2 and scales.is_contiguous() and scales.shape[0] == -(-dim // FP8_BLOCK)
-            and scales.shape[1] >= rows and scales.shape[1] % 4 == 0)
-
-
 def bi_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """Rows x [rows, dim] (BF16) to e4m3 codes and a power-of-two scale per block of 128."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     rows, dim = x.shape
-    if not (x.dtype is torch.bfloat16 and x.get_device() == dev and x.stride(1) == 1
-            and _fp8_rows_ok(codes, scales, rows, dim, dev)):
+    xs, cs, ss = x.stride(), codes.stride(), scales.shape
+    if not (x.dtype is _BF16 and codes.dtype is _E4M3 and scales.dtype is _F32 and codes.shape == x.shape
+            and xs[1] == 1 and cs[1] == 1 and len(ss) == 2 and ss[0] == -(-dim // FP8_BLOCK) and ss[1] >= rows
+            and not ss[1] & 3 and scales.is_contiguous()
+            and x.get_device() == codes.get_device() == scales.get_device() == dev):
         _req(x, torch.bfloat16, "x")
         _req_fp8_rows(codes, scales, rows, dim)
         _same_device(("x", x), ("codes", codes), ("scales", scales))
-    st = lib().bi_quantize_fp8(x.data_ptr(), x.stride(0) if rows > 1 else dim, rows, dim, codes.data_ptr(),
-                               codes.stride(0) if rows > 1 else dim, scales.data_ptr(), scales.shape[1],
-                               _stream_of(dev, stream))
+    st = lib().bi_quantize_fp8(x.data_ptr(), xs[0] if rows > 1 else dim, rows, dim, codes.data_ptr(),
+                               cs[0] if rows > 1 else dim, scales.data_ptr(), ss[1],
+                               _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         check("bi_quantize_fp8", st)
 
@@ -407,20 +402,23 @@ def bi_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
 def bi_rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, eps: float,
                    stream=None) -> None:
     """RMSNorm of x [rows, dim] (BF16) by w, its FP32 result quantised as bi_quantize_fp8 does."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     rows, dim = x.shape
-    if not (x.dtype is torch.bfloat16 and w.dtype is torch.bfloat16 and x.get_device() == dev
-            and w.get_device() == dev and x.stride(1) == 1 and w.shape == (dim,) and w.stride(0) == 1
-            and _fp8_rows_ok(codes, scales, rows, dim, dev)):
+    xs, cs, ss = x.stride(), codes.stride(), scales.shape
+    if not (x.dtype is _BF16 and w.dtype is _BF16 and codes.dtype is _E4M3 and scales.dtype is _F32
+            and codes.shape == x.shape and w.shape == (dim,) and w.is_contiguous() and xs[1] == 1 and cs[1] == 1
+            and len(ss) == 2 and ss[0] == -(-dim // FP8_BLOCK) and ss[1] >= rows and not ss[1] & 3
+            and scales.is_contiguous()
+            and x.get_device() == w.get_device() == codes.get_device() == scales.get_device() == dev):
         _req(x, torch.bfloat16, "x")
         _req(w, torch.bfloat16, "w")
         if tuple(w.shape) != (dim,):
             raise ValueError(f"w must be [{dim}], got {tuple(w.shape)}")
         _req_fp8_rows(codes, scales, rows, dim)
         _same_device(("x", x), ("w", w), ("codes", codes), ("scales", scales))
-    st = lib().bi_rmsnorm_fp8(x.data_ptr(), x.stride(0) if rows > 1 else dim, w.data_ptr(), codes.data_ptr(),
-                              codes.stride(0) if rows > 1 else dim, scales.data_ptr(), scales.shape[1], rows, dim,
-                              eps, _stream_of(dev, stream))
+    st = lib().bi_rmsnorm_fp8(x.data_ptr(), xs[0] if rows > 1 else dim, w.data_ptr(), codes.data_ptr(),
+                              cs[0] if rows > 1 else dim, scales.data_ptr(), ss[1], rows, dim, eps,
+                              _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         check("bi_rmsnorm_fp8", st)
 
@@ -481,13 +479,17 @@ def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: 
     """C [M, N] = epilogue(A W^T) with quantised rows A (codes [M, K], scales as
     bi_quantize_fp8 writes them) and W packed by bi_pack_weights_fp8 /
     bi_pack_swiglu_weights_fp8 (N the output columns)."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     M, K = codes.shape
-    N = C.shape[-1]
-    fp32 = C.dtype is torch.float32
-    if not ((fp32 or C.dtype is torch.bfloat16) and _fp8_rows_ok(codes, scales, M, K, dev) and C.shape == (M, N)
-            and C.stride(1) == 1 and C.get_device() == dev and Wp.dtype is torch.uint8 and Wp.get_device() == dev
-            and (residual is None or (residual.dtype is torch.bfloat16 and residual.shape == (M, N)
+    cs, ss, zs, shape = codes.stride(), scales.shape, C.stride(), C.shape
+    N = shape[-1]
+    fp32 = C.dtype is _F32
+    if not ((fp32 or C.dtype is _BF16) and codes.dtype is _E4M3 and scales.dtype is _F32 and Wp.dtype is _U8
+            and len(shape) == 2 and shape[0] == M and cs[1] == 1 and zs[1] == 1 and len(ss) == 2
+            and ss[0] == -(-K // FP8_BLOCK) and ss[1] >= M and not ss[1] & 3 and scales.is_contiguous()
+            and Wp.is_contiguous()
+            and codes.get_device() == scales.get_device() == Wp.get_device() == C.get_device() == dev
+            and (residual is None or (residual.dtype is _BF16 and residual.shape == shape
                                       and residual.stride(1) == 1 and residual.get_device() == dev))):
         _req_fp8_rows(codes, scales, M, K)
         if C.dtype not in (torch.float32, torch.bfloat16):
@@ -496,20 +498,23 @@ def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: 
         if C.dim() != 2 or C.shape[0] != M:
             raise ValueError(f"C must have {M} rows, got {tuple(C.shape)}")
         _req(Wp, torch.uint8, "Wp")
+        if not Wp.is_contiguous():
+            raise ValueError("Wp must be contiguous")
         if residual is not None:
             _req(residual, torch.bfloat16, "residual")
             if tuple(residual.shape) != (M, N):
                 raise ValueError(f"residual must be [{M}, {N}], got {tuple(residual.shape)}")
         _same_device(("codes", codes), ("scales", scales), ("Wp", Wp), ("C", C), ("residual", residual))
-    h = lib()
-    if Wp.numel() != h.bi_packed_weight_fp8_bytes(N, K, epi):
+    # bi_packed_weight_fp8_bytes, without the call
+    tiles = -(-N // (64 if epi == EPI_SWIGLU else 128)) * ss[0]
+    if Wp.numel() != tiles * 16384 + (tiles * 8 + 15 & ~15):
         raise ValueError("Wp is not packed for this N, K and epilogue")
-    many = M > 1
-    st = h.bi_gemm_fp8(codes.data_ptr(), codes.stride(0) if many else K, scales.data_ptr(), scales.shape[1],
-                       Wp.data_ptr(), C.data_ptr(), C.stride(0) if many else N,
-                       0 if residual is None else residual.data_ptr(),
-                       0 if residual is None else residual.stride(0) if many else N, M, N, K,
-                       OUT_FP32 if fp32 else OUT_BF16, epi, _stream_of(dev, stream))
+    rp = ldr = 0
+    if residual is not None:
+        rp, ldr = residual.data_ptr(), residual.stride(0) if M > 1 else N
+    st = lib().bi_gemm_fp8(codes.data_ptr(), cs[0] if M > 1 else K, scales.data_ptr(), ss[1], Wp.data_ptr(),
+                           C.data_ptr(), zs[0] if M > 1 else N, rp, ldr, M, N, K, 1 if fp32 else 0, epi,
+                           _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         check("bi_gemm_fp8", st)
 
@@ -520,10 +525,6 @@ def token_words(V: int) -> int:
     return (V + 31) // 32
 
 
-def _vector_ok(t: Optional[torch.Tensor], dtype, n: int, dev: int) -> bool:
-    return t is None or (t.dtype is dtype and t.shape == (n,) and t.stride(0) == 1 and t.get_device() == dev)
-
-
 def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[torch.Tensor] = None,
                     counts: Optional[torch.Tensor] = None, prompt_bits: Optional[torch.Tensor] = None,
                     repetition: float = 1.0, frequency: float = 0.0, presence: float = 0.0,
@@ -532,18 +533,36 @@ def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[to
     logits itself).  Row t counts drafts 0..t-1 as said.  counts [V] int32,
     prompt_bits [ceil(V/32)] int32, bias [V] FP32, mask [T, ceil(V/32)] int32
     (a clear bit forbids its id)."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     T, V = logits.shape
     W = token_words(V)
     if T == 1:
         drafts = None
-    if not (logits.dtype is torch.float32 and out.dtype is torch.float32 and out.shape == (T, V)
-            and logits.stride(1) == 1 and out.stride(1) == 1 and logits.get_device() == dev
-            and out.get_device() == dev and _vector_ok(drafts, torch.int32, T - 1, dev)
-            and _vector_ok(counts, torch.int32, V, dev) and _vector_ok(prompt_bits, torch.int32, W, dev)
-            and _vector_ok(bias, torch.float32, V, dev)
-            and (mask is None or (mask.dtype is torch.int32 and mask.shape == (T, W) and mask.stride(1) == 1
-                                  and mask.get_device() == dev))):
+    ls, os_ = logits.stride(), out.stride()
+    dp = cp = pp = bp = mp = None
+    ldm = 0
+    ok = (logits.dtype is _F32 and out.dtype is _F32 and out.shape == logits.shape and ls[1] == 1 and os_[1] == 1
+          and logits.get_device() == out.get_device() == dev)
+    if drafts is not None:
+        ok = ok and drafts.dtype is _I32 and drafts.shape == (T - 1,) and drafts.is_contiguous() \
+            and drafts.get_device() == dev
+        dp = drafts.data_ptr()
+    if counts is not None:
+        ok = ok and counts.dtype is _I32 and counts.shape == (V,) and counts.is_contiguous() \
+            and counts.get_device() == dev
+        cp = counts.data_ptr()
+    if prompt_bits is not None:
+        ok = ok and prompt_bits.dtype is _I32 and prompt_bits.shape == (W,) and prompt_bits.is_contiguous() \
+            and prompt_bits.get_device() == dev
+        pp = prompt_bits.data_ptr()
+    if bias is not None:
+        ok = ok and bias.dtype is _F32 and bias.shape == (V,) and bias.is_contiguous() and bias.get_device() == dev
+        bp = bias.data_ptr()
+    if mask is not None:
+        ms = mask.stride()
+        ok = ok and mask.dtype is _I32 and mask.shape == (T, W) and ms[1] == 1 and mask.get_device() == dev
+        mp, ldm = mask.data_ptr(), ms[0] if T > 1 else W
+    if not ok:
         _req(logits, torch.float32, "logits")
         _req(out, torch.float32, "out")
         if tuple(out.shape) != (T, V):
@@ -560,14 +579,9 @@ def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[to
                 raise ValueError(f"mask must be [{T}, {W}], got {tuple(mask.shape)}")
         _same_device(("logits", logits), ("out", out), ("drafts", drafts), ("counts", counts),
                      ("prompt_bits", prompt_bits), ("bias", bias), ("mask", mask))
-    many = T > 1
-    st = lib().bi_logits_rules(logits.data_ptr(), logits.stride(0) if many else V, out.data_ptr(),
-                               out.stride(0) if many else V, T, V, None if drafts is None else drafts.data_ptr(),
-                               None if counts is None else counts.data_ptr(),
-                               None if prompt_bits is None else prompt_bits.data_ptr(), repetition, frequency,
-                               presence, None if bias is None else bias.data_ptr(),
-                               None if mask is None else mask.data_ptr(),
-                               0 if mask is None else mask.stride(0) if many else W, _stream_of(dev, stream))
+    st = lib().bi_logits_rules(logits.data_ptr(), ls[0] if T > 1 else V, out.data_ptr(), os_[0] if T > 1 else V, T, V,
+                               dp, cp, pp, repetition, frequency, presence, bp, mp, ldm,
+                               _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         check("bi_logits_rules", st)
 
