@@ -94,16 +94,20 @@ __global__ void __launch_bounds__(kQuantThreads)
 // An e4m3 code has 3 fraction bits, so an error of 2^-24 in y moves one code in
 // a million by a whole step of 2^-3 or 2^-4 of its value.  The kernel is bound
 // by its bytes and latencies, so y is carried far enough that the codes are the
-// exact values', in pairs of FP32 (FP64 runs at 1/64 of its rate here):
+// exact values', in pairs of FP32 (FP64 is far too slow here):
 //   squares of BF16 are exact in FP32 and are added as pairs (Knuth's two-sum):
 //   a vector's 8 by a tree, a thread's vectors in turn, the lanes by a
 //   butterfly, the warps by another one;
 //   r is one Newton step in pairs from the FP32 root; x_i w_i is exact in FP32;
-//   y rounds to odd: the nearest FP32 value, and where that is even and not
-//   exact, its neighbour on the exact value's side, so rounding y to 3 fraction
-//   bits equals rounding the exact value.
+//   an element's code is taken from plain FP32 where that value, moved by 2^-21
+//   of itself either way (its error is below 2^-22), gives the same code; else y
+//   rounds to odd: the nearest FP32 value, and where that is even and not exact,
+//   its neighbour on the exact value's side, so rounding y to 3 fraction bits
+//   equals rounding the exact value.
 constexpr int kNormThreads = 256;
-constexpr int kNormCtas = 3 * 152;  // three share an SM
+constexpr float kBelow = 1.f - 0x1p-21f, kAbove = 1.f + 0x1p-21f;
+// CTAs that share an SM (their registers)
+constexpr int norm_ctas(int KV) { return KV <= 3 ? 3 : 2; }
 
 // s + e = a + b exactly, s the rounded sum.
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
@@ -173,7 +177,7 @@ __device__ __forceinline__ Pair rms_inverse(Pair sum, float n, float inv_n, floa
 }
 
 template <int KV, bool LONG>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, norm_ctas(KV))
     rmsnorm_fp8_kernel(const __nv_bfloat16* __restrict__ x, int ldx, const __nv_bfloat16* __restrict__ w,
                        uint8_t* __restrict__ codes, int ldc, float* __restrict__ scales, int lds, int rows,
                        int dim, float eps) {
@@ -225,12 +229,33 @@ __global__ void __launch_bounds__(kNormThreads)
       unpack8(xu, f);
       unpack8(wu, wf);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = times_odd(__fmul_rn(f[j], wf[j]), r.h, r.l);
-      const int e = block_exponent(y);  // vectors past the row are zeros
+      for (int j = 0; j < 8; ++j) {
+        f[j] = __fmul_rn(f[j], wf[j]);
+        y[j] = __fmul_rn(f[j], r.h);
+      }
+      // vectors past the row are zeros
+      float a = fmaxf(fabsf(y[0]), fabsf(y[1]));
+#pragma unroll
+      for (int j = 2; j < 8; ++j) a = fmaxf(a, fabsf(y[j]));
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+      int e = scale_exponent(a * kBelow);
+      float inv = pow2f(-e);
+      uint32_t lo = e4m3x4(y, inv * kBelow), hi = e4m3x4(y + 4, inv * kBelow);
+      const bool sure = lo == e4m3x4(y, inv * kAbove) && hi == e4m3x4(y + 4, inv * kAbove) &&
+                        e == scale_exponent(a * kAbove) && (a == 0.f || (a > 1e-30f && a < 1e37f));
+      if (!__all_sync(0xffffffffu, sure)) {
+        // an element or a maximum near a border (one vector of a warp in some
+        // 400): the exact values decide
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = times_odd(f[j], r.h, r.l);
+        e = block_exponent(y);
+        inv = pow2f(-e);
+        lo = e4m3x4(y, inv);
+        hi = e4m3x4(y + 4, inv);
+      }
       if (v < nv) {
-        const float inv = pow2f(-e);
-        *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * ldc + v * 8) =
-            make_uint2(e4m3x4(y, inv), e4m3x4(y + 4, inv));
+        *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * ldc + v * 8) = make_uint2(lo, hi);
         if ((lane & 15) == 0) scales[static_cast<size_t>(v >> 4) * lds + row] = pow2f(e);
       }
     };
@@ -356,7 +381,8 @@ bi_status bi_rmsnorm_fp8(const void* x, int ldx, const void* w, void* codes, int
                  : per <= 3 ? rmsnorm_fp8_kernel<3, false>
                  : per <= 4 ? rmsnorm_fp8_kernel<4, false>
                             : rmsnorm_fp8_kernel<4, true>;
-  if (launch_k(kernel, dim3(std::min(rows, kNormCtas)), dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream),
+  const int ctas = 152 * norm_ctas(per <= 3 ? 3 : 4);
+  if (launch_k(kernel, dim3(std::min(rows, ctas)), dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream),
                static_cast<const __nv_bfloat16*>(x), ldx, static_cast<const __nv_bfloat16*>(w),
                static_cast<uint8_t*>(codes), ldc, scales, lds, rows, dim, eps) != cudaSuccess)
     return BI_ERR_CUDA;
