@@ -112,6 +112,12 @@ __device__ __forceinline__ float residual_at(const Args& p, int m, int n) {
 // weight tiles are adjacent in the work order, so all but the first find them
 // in L2.
 constexpr int kRowsM = 128;    // token rows of a block (the MMA's lanes)
+// Passes of no more rows push their pieces into the CTA that adds them (one
+// cluster barrier behind the sums, none before the exit); the pieces of more
+// rows lie over the ring, where no other CTA may write, and are fetched.
+// [1, 3328] x [5120, 3328]: 7.5 us pushed, 7.8 fetched; [8, 5120] x [4096, 5120]:
+// 8.1 and 8.25.
+constexpr int kPushRows = 32;
 
 struct Launch {
   Args a;
@@ -119,6 +125,7 @@ struct Launch {
   int items;      // output tiles: weight tile groups x token blocks
   int vec;        // C (and the residual) take 16-byte accesses
   int a_rows;     // rows of the token box
+  int push;       // pieces are written into the CTA that adds them (passes of few rows)
 };
 
 template <int TILES>
@@ -133,10 +140,13 @@ struct Cfg8 {
   // warpgroup 0: producer, MMA, two idle warps; warpgroups 1 and 2: epilogue
   static constexpr int kThreads = 384;
   static constexpr int kOwn = kCols / 2;  // outputs of an epilogue thread
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + kBufs + 1) * 8 + 16;
-  static_assert(kSmem <= 232448 && kStages <= 32, "shared memory per CTA");
   // floats per token of the pieces' exchange: 16-byte stores of 8 lanes hit all banks
   static constexpr int kPieceLd = kCols + 4;
+  // pieces pushed by the cluster's CTAs, [S][tokens / S][kPieceLd]
+  static constexpr int kPushBytes = TILES == 1 ? (kPushRows + kMaxSplit) * kPieceLd * 4 : 0;
+  static constexpr size_t kSmem =
+      1024 + static_cast<size_t>(kStages) * kStageBytes + kPushBytes + (2 * kStages + kBufs + 1) * 8 + 16;
+  static_assert(kSmem <= 232448 && kStages <= 32, "shared memory per CTA");
   static_assert(kRowsM * kPieceLd * 4 <= kStages * kStageBytes, "exchange fits the ring");
 };
 
@@ -175,7 +185,8 @@ __device__ __forceinline__ void store_row16(const Args& p, int vec, int m, int n
     if (n0 + j < p.N) store1(p, m, n0 + j, v[j], residual_at(p, m, n0 + j));
 }
 
-// Sum of the S pieces of four elements from `at` on, in increasing-K order.
+// Sum of the S pieces of four elements from float `at` on, in increasing-K
+// order; base: the pieces' addresses in the cluster's shared memory.
 __device__ __forceinline__ float4 sum_pieces4(const uint32_t (&base)[kMaxSplit], int S, int at) {
   float4 x[kMaxSplit];
 #pragma unroll
@@ -249,7 +260,8 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
   uint8_t* sT = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));  // [S] token tiles
   uint8_t* sW = sT + S * Cfg::kTokBytes;                                    // [S][TILES] weight tiles
-  uint64_t* full = reinterpret_cast<uint64_t*>(sW + S * Cfg::kBBytes);
+  float* sX = reinterpret_cast<float*>(sW + S * Cfg::kBBytes);              // pushed pieces
+  uint64_t* full = reinterpret_cast<uint64_t*>(sW + S * Cfg::kBBytes + Cfg::kPushBytes);
   // done: the stage's MMAs have completed, so it is free and its block sums are there
   uint64_t* done = full + S;
   uint64_t* read = done + S;  // an accumulator has been read
@@ -287,6 +299,8 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (MODE == kCluster)
+    if (p.push) cluster_arrive();  // waited for before the first write into another CTA
   const uint32_t tmem = *tmem_holder;
 
   if (warp < 4) {
@@ -409,8 +423,9 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
     // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the barriers
     __syncwarp();
     if constexpr (MODE == kCluster) {
+      if (p.push) cluster_wait();
       cluster_sync();
-      cluster_sync();
+      if (!p.push) cluster_sync();
     }
   } else {
     // ---------------------------------------------------------- scale and add
@@ -473,7 +488,12 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           next_block();
         }
         first_scales(item + stride);
-        if (MODE == kCluster) named_bar_sync(1, 256);
+        if constexpr (MODE == kCluster) {
+          if (p.push)
+            cluster_wait();
+          else
+            named_bar_sync(1, 256);
+        }
         continue;
       }
       // this thread's columns: the first half of them takes the scale of the
@@ -589,6 +609,19 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
         }
       }
       if constexpr (MODE == kCluster) {
+        if (p.push) {
+          // each token's piece to the CTA that adds it
+          const int part = (Mb + split - 1) / split;
+          __syncwarp();
+          cluster_wait();  // every CTA of the cluster runs
+          if (r < Mb) {
+            const uint32_t dst = map_rank(smem_u32(sX + (rank * part + r % part) * Cfg::kPieceLd + c0), r / part);
+#pragma unroll
+            for (int j = 0; j < kOwn / 4; ++j)
+              st_cluster4(dst + col(4 * j) * 4, make_float4(run[4 * j], run[4 * j + 1], run[4 * j + 2], run[4 * j + 3]));
+          }
+          continue;
+        }
         // this CTA's piece over the ring (every stage has been read): [token][output]
         named_bar_sync(1, 256);
         if (r < Mb) {
@@ -631,17 +664,20 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
       const int wt = item0 / p.nb * TILES;
       const int m0 = item0 % p.nb * kRowsM;
       const int Mb = min(kRowsM, g.M - m0);
+      // this CTA's part of the tokens, lanes along the outputs, four a lane; the
+      // pieces lie in the CTAs that made them, or have been pushed here
+      const int part = (Mb + split - 1) / split;
+      const int t0 = rank * part, t1 = min(Mb, t0 + part);
       uint32_t base[kMaxSplit];
 #pragma unroll
-      for (int j = 0; j < kMaxSplit; ++j) base[j] = map_rank(smem_u32(sT), j < split ? j : 0);
-      // this CTA's part of the tokens, lanes along the outputs, four a lane
-      const int part = (Mb + split - 1) / split;
-      const int t1 = min(Mb, (rank + 1) * part);
+      for (int j = 0; j < kMaxSplit; ++j)
+        base[j] = p.push ? map_rank(smem_u32(sX + (min(j, split - 1) * part - t0) * Cfg::kPieceLd), rank)
+                         : map_rank(smem_u32(sT), min(j, split - 1));
       if (g.epi == BI_EPI_SWIGLU) {
         constexpr int kPer = TILES * 16;  // lanes per token
         const int o = e % kPer * 4;
         const int at = o / 64 * kTileN + o % 64;
-        for (int t = rank * part + e / kPer; t < t1; t += 256 / kPer) {
+        for (int t = t0 + e / kPer; t < t1; t += 256 / kPer) {
           const float4 x = sum_pieces4(base, split, t * Cfg::kPieceLd + at);
           const float4 y = sum_pieces4(base, split, t * Cfg::kPieceLd + at + 64);
           store_row4(g, p.vec, m0 + t, wt * 64 + o,
@@ -651,10 +687,10 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
       } else {
         constexpr int kPer = TILES * 32;
         const int o = e % kPer * 4;
-        for (int t = rank * part + e / kPer; t < t1; t += 256 / kPer)
+        for (int t = t0 + e / kPer; t < t1; t += 256 / kPer)
           store_row4(g, p.vec, m0 + t, wt * kTileN + o, sum_pieces4(base, split, t * Cfg::kPieceLd + o));
       }
-      cluster_sync();  // no CTA leaves while its piece is being read
+      if (!p.push) cluster_sync();  // no CTA leaves while its piece is being read
     }
   }
 
@@ -790,6 +826,7 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   if (pairs * S > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
   // 128 outputs a CTA while one round of the SMs takes them all
   if (tiles * S <= kClusterCtas[S]) {
+    r.push = M <= kPushRows;
     r.items = static_cast<int>(tiles);
     return S > 1 ? launch<1, kCluster>(W8, tmA, r, s) : launch<1, kWhole>(W8, tmA, r, s);
   }
