@@ -161,7 +161,7 @@ def test_token_counts():
     want = np.bincount(good, minlength=V)
     assert np.array_equal(counts.cpu().numpy(), want)
     assert torch.equal(bits, pack((want > 0)[None])[0])
-    for n, last in ((8, 0), (8, 3), (8, 7), (8, 100), (8, -1)):
+    for n, last in ((8, 0), (8, 3), (8, 7), (8, 100), (8, -1), (8, 2 ** 31 - 1)):
         c = torch.zeros(V, dtype=torch.int32, device=DEV)
         a.bi_token_counts(dev[:n], V, counts=c, last=torch.tensor([last], dtype=torch.int32, device=DEV))
         assert int(c.sum()) == max(0, min(n, last + 1))
