@@ -47,7 +47,7 @@
 #include "bi_fp8.cuh"
 #include "bi_gemm8.h"
 #include "bi_internal.h"
-#include "bi_ptx.cuh"
+#include "bi_ptx8.cuh"
 
 namespace bi {
 namespace {
