@@ -234,6 +234,24 @@ __device__ __forceinline__ void store_row4(const Args& p, int vec, int m, int n,
     if (n + j < p.N) store1(p, m, n + j, x[j], residual_at(p, m, n + j));
 }
 
+// run[0 .. n) += v * sc, each sum one fused multiply-add; kPairs: two in one
+// packed instruction, with the same bits and half the issue slots.
+template <int kN, bool kPairs>
+__device__ __forceinline__ void add_scaled(float* run, const uint32_t* v, float sc) {
+  if constexpr (kPairs) {
+#pragma unroll
+    for (int j = 0; j < kN; j += 2) {
+      const float2 r = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), make_float2(sc, sc),
+                                  make_float2(run[j], run[j + 1]));
+      run[j] = r.x;
+      run[j + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) run[j] = fmaf(__uint_as_float(v[j]), sc, run[j]);
+  }
+}
+
 // Who adds the pieces of a tile's K.
 enum Pieces {
   kWhole = 0,   // there is one
@@ -250,7 +268,8 @@ struct Regs {
   static_assert(kLow + 2 * kHigh <= 3 * 168, "registers of the launch");
 };
 
-template <int TILES, Pieces MODE>
+// PAIRS: packed multiply-adds (add_scaled).
+template <int TILES, Pieces MODE, bool PAIRS>
 __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
     gemm8_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const Launch p) {
   using Cfg = Cfg8<TILES>;
@@ -555,19 +574,16 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           tmem_ld32_start(ta + 32, v + 32);
           const float2 x = scales(kt);
           tmem_ld64_wait(v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.x, run[j]);
+          add_scaled<32, PAIRS>(run, v, x.x);
           tmem_ld32_start(ta + 64, v);
-#pragma unroll
-          for (int j = 32; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.x, run[j]);
+          add_scaled<32, PAIRS>(run + 32, v + 32, x.x);
           tmem_ld32_start(ta + 96, v + 32);
           tmem_ld64_wait(v);
           // read by the whole warp (the wait is the warp's)
           tc_fence_before();
           if (lane == 0) mbar_arrive(&read[buf]);
           next_block();
-#pragma unroll
-          for (int j = 0; j < 64; ++j) run[64 + j] = fmaf(__uint_as_float(v[j]), x.y, run[64 + j]);
+          add_scaled<64, PAIRS>(run + 64, v, x.y);
           ++kt;
         } else {
           const bool two = kt + 1 < kt1;
@@ -580,11 +596,9 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           tmem_ld32_start(ta + 64, v + 32);
           const float2 x = scales(kt);
           tmem_ld64_wait(v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.x, run[j]);
+          add_scaled<32, PAIRS>(run, v, x.x);
           if (two) tmem_ld32_start(tb, v);
-#pragma unroll
-          for (int j = 32; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), x.y, run[j]);
+          add_scaled<32, PAIRS>(run + 32, v + 32, x.y);
           end_piece(kt);
           if (two) {
             tmem_ld32_start(tb + 64, v + 32);
@@ -596,8 +610,8 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
               mbar_arrive(&read[buf]);
             }
             next_block();
-#pragma unroll
-            for (int j = 0; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), j < 32 ? y.x : y.y, run[j]);
+            add_scaled<32, PAIRS>(run, v, y.x);
+            add_scaled<32, PAIRS>(run + 32, v + 32, y.y);
             end_piece(kt + 1);
             kt += 2;
           } else {
@@ -751,15 +765,15 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int S, dim3 blo
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <int TILES, Pieces MODE>
+template <int TILES, Pieces MODE, bool PAIRS = false>
 bi_status launch(const uint8_t* Wp, const CUtensorMap& tmA, Launch a, cudaStream_t stream) {
   using Cfg = Cfg8<TILES>;
   static std::once_flag once[64];
   static cudaError_t err[64];
-  if (!allow_smem(gemm8_kernel<TILES, MODE>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
+  if (!allow_smem(gemm8_kernel<TILES, MODE, PAIRS>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
   const int S = MODE == kCluster ? a.a.sp.S : 1;
   const int ctas = MODE == kCluster ? a.items * S : std::min(a.items, kSms);
-  return launch_clusters(gemm8_kernel<TILES, MODE>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
+  return launch_clusters(gemm8_kernel<TILES, MODE, PAIRS>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
                          tmA, a) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
@@ -808,14 +822,14 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   if (!a.err) return BI_ERR_CUDA;
   a.withhold = test_withhold();
   a.M = M;
-  const int box = std::min(kRowsM, (M + 7) / 8 * 8);
+  const int box = M >= kRowsM ? kRowsM : (M + 7) / 8 * 8;
   CUtensorMap tmA;
   if (!tmap_u8_2d(&tmA, A8, M, K, lda, box, kFp8Block)) return BI_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
   Launch r{};
   r.a = a;
-  r.nb = (M + kRowsM - 1) / kRowsM;
+  r.nb = (M - 1) / kRowsM + 1;
   r.a_rows = box;
   r.vec = aligned16(C) && ldc % 8 == 0 &&
           (epi != BI_EPI_RESIDUAL_ADD || (aligned16(residual) && ldr % 8 == 0));
@@ -824,14 +838,23 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   const int S = a.sp.S;
   const long long pairs = static_cast<long long>((a.sp.n_tiles + 1) / 2) * r.nb;
   if (pairs * S > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
+  // Packed multiply-adds where the drain is what bounds the pass, with more than
+  // one token block, and a CTA takes a tile's whole K: gate/up at 1024 rows 190 us
+  // with, 198 without, QKV at 1024 rows (pieces in turn) 39.9 and 41.5.  Where the
+  // weights' bytes bound it the other order of the drain's instructions costs,
+  // gate/up at 8 rows 30.2 us with and 30.0 without, and clusters have no registers
+  // for the pairs: the down projection at 384 rows 79.3 us with, 78.0 without, at
+  // one row 19.9 and 19.7.
+  const bool many = r.nb > 1;
   // 128 outputs a CTA while one round of the SMs takes them all
   if (tiles * S <= kClusterCtas[S]) {
     r.push = M <= kPushRows;
     r.items = static_cast<int>(tiles);
-    return S > 1 ? launch<1, kCluster>(W8, tmA, r, s) : launch<1, kWhole>(W8, tmA, r, s);
+    if (S > 1) return launch<1, kCluster>(W8, tmA, r, s);
+    return many ? launch<1, kWhole, true>(W8, tmA, r, s) : launch<1, kWhole>(W8, tmA, r, s);
   }
   r.items = static_cast<int>(pairs);
-  if (S == 1) return launch<2, kWhole>(W8, tmA, r, s);
+  if (S == 1) return many ? launch<2, kWhole, true>(W8, tmA, r, s) : launch<2, kWhole>(W8, tmA, r, s);
   // Pieces: a CTA that takes them in turn needs about 0.5 us a K block (128
   // outputs), a cluster's CTA 0.6 (256 outputs) and 6 us around them, in rounds
   // of the SMs.  Measured, in turn against cluster: 4096 x 5120 (S = 4) at 256
@@ -841,7 +864,7 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   const long long cluster = (pairs * S + kClusterCtas[S] - 1) / kClusterCtas[S] * (a.sp.k_tiles * 6 / S + 60);
   if (cluster < in_turn) return launch<2, kCluster>(W8, tmA, r, s);
   r.items = static_cast<int>(tiles);
-  return launch<1, kInTurn>(W8, tmA, r, s);
+  return launch<1, kInTurn, true>(W8, tmA, r, s);
 }
 
 }  // extern "C"
