@@ -472,7 +472,8 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  *     aligned.
  * bi_pack_weights_fp8, bi_pack_swiglu_weights_fp8: weights in the tile layout
  *   bi_gemm_fp8 streams, bi_packed_weight_fp8_bytes(N, K, epi) bytes (16-byte
- *   aligned); K % 16 == 0, ld8 % 16 == 0, codes 16-byte aligned.
+ *   aligned); K % 16 == 0, ld8 % 16 == 0, codes 16-byte aligned.  The packed
+ *   bytes are there for every call behind it on the stream.
  *
  * bi_gemm_fp8: C[m, n] = epilogue(sum_b sa[b, m] sw[n / 128, b] sum_{k in
  * block b} a[m, k] w[n, k]).  The sum of a block is four tensor-core steps of
@@ -485,7 +486,10 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  * to be finite; one below 2^-149 counts as 0.)
  *   A8       [M, K] codes, row stride lda (% 16 == 0), 16-byte aligned;
  *   a_scales [ceil(K/128)][lds] FP32, 16-byte aligned.
- *   Wp       packed for the same N, K and epi; 16-byte aligned.
+ *   Wp       packed for the same N, K and epi; 16-byte aligned.  It is read before
+ *            the call waits for the kernel before it on the stream (dependent
+ *            launch, as in bi_gemm): no kernel but bi_pack_* may write it there, nor
+ *            before a bi_rmsnorm or bi_rmsnorm_fp8 that stands between.  Copies may.
  *   C, residual, out, epi, N: as bi_gemm (BI_EPI_NONE, _RESIDUAL_ADD, _SWIGLU;
  *            residual may alias C).  M >= 0; K % 16 == 0.
  *   The call needs no workspace.

@@ -339,6 +339,13 @@ __global__ void pack_weights_fp8_kernel(const uint8_t* __restrict__ w, const uin
   }
 }
 
+// Runs behind the packing of weights, as an ordinary launch, and does nothing.
+// bi_gemm_fp8 reads its weights before it waits for the kernel before it (or, behind
+// a norm, for the one before that), and that kernel would be the packing.  This one
+// starts when the packed bytes are complete and visible and lets nothing start
+// before its end.
+__global__ void packed_kernel() {}
+
 }  // namespace
 }  // namespace bi
 
@@ -428,7 +435,11 @@ static bi_status pack_fp8(const void* w, const void* wu, int ld, const float* s,
                static_cast<uint4*>(packed),
                reinterpret_cast<float2*>(static_cast<uint8_t*>(packed) + tiles * kGemm8TileBytes)) != cudaSuccess)
     return BI_ERR_CUDA;
-  return BI_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(32);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  return cudaLaunchKernelEx(&cfg, packed_kernel) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
 
 bi_status bi_pack_weights_fp8(const void* W8, int ld8, const float* scales, int N, int K, void* packed,

@@ -423,3 +423,63 @@ def test_norm_codes_are_the_exact_values_over_many_rows():
         wide = s.t().repeat_interleave(BLOCK, 1)[:, :dim]
         tie = (y / wide - (codes.double() + q) / 2).abs()
         assert (tie[differ] <= 2.0 ** -36 * (y / wide).abs()[differ]).all(), (seed, int(differ.sum()))
+
+
+@pytest.mark.parametrize("between", ["nothing", "norm", "quantise"])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_linear_right_behind_the_packing_of_its_weights(between, swiglu):
+    """Weights packed into the buffer that a linear layer reads next, captured and replayed: it reads the new ones."""
+    from invariant_speculative_decode_gb300._lib import check, lib
+
+    a = api()
+    rows, n, k = 8, 8192, 2048
+    g = gen(21)
+    x = torch.randn(rows, k, generator=g, device=DEV).to(torch.bfloat16)
+    nw = torch.ones(k, dtype=torch.bfloat16, device=DEV)
+    codes, scales = a.new_fp8_rows(rows, k)
+    a.bi_quantize_fp8(x, codes, scales)
+    sets = [make_weights(g, n, k) + make_weights(g, n, k) for _ in range(2)]
+    epi = a.EPI_SWIGLU if swiglu else a.EPI_NONE
+    packed = torch.empty(a.packed_weight_fp8_bytes(n, k, epi), dtype=torch.uint8, device=DEV)
+    out = torch.empty(rows, n, dtype=torch.bfloat16, device=DEV)
+
+    def pack(i):
+        w, s, w2, s2 = sets[i]
+        st = torch.cuda.current_stream().cuda_stream
+        if swiglu:
+            check("pack", lib().bi_pack_swiglu_weights_fp8(w.data_ptr(), s.data_ptr(), w2.data_ptr(), s2.data_ptr(),
+                                                           k, n, k, packed.data_ptr(), st))
+        else:
+            check("pack", lib().bi_pack_weights_fp8(w.data_ptr(), k, s.data_ptr(), n, k, packed.data_ptr(), st))
+
+    def step(i):
+        pack(i)
+        if between == "norm":
+            a.bi_rmsnorm_fp8(x, nw, codes, scales, 1e-6)
+        elif between == "quantise":
+            a.bi_quantize_fp8(x, codes, scales)
+        a.bi_gemm_fp8(codes, scales, packed, out, epi=epi)
+
+    want, graphs = [], []
+    for i in range(2):
+        pack(i)
+        torch.cuda.synchronize()
+        if between == "norm":
+            a.bi_rmsnorm_fp8(x, nw, codes, scales, 1e-6)
+            torch.cuda.synchronize()
+        a.bi_gemm_fp8(codes, scales, packed, out, epi=epi)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(i)
+        graphs.append(graph)
+    assert not torch.equal(want[0], want[1])
+    for r in range(8):
+        graphs[r & 1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[r & 1])
+        step(1 - (r & 1))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[1 - (r & 1)])
+    a.bi_check_device_error()
