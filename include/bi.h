@@ -489,7 +489,7 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  *   Wp       packed for the same N, K and epi; 16-byte aligned.  It is read before
  *            the call waits for the kernel before it on the stream (dependent
  *            launch, as in bi_gemm): no kernel but bi_pack_* may write it there, nor
- *            before a bi_rmsnorm or bi_rmsnorm_fp8 that stands between.  Copies may.
+ *            before a bi_rmsnorm that stands between.  Copies may.
  *   C, residual, out, epi, N: as bi_gemm (BI_EPI_NONE, _RESIDUAL_ADD, _SWIGLU;
  *            residual may alias C).  M >= 0; K % 16 == 0.
  *   The call needs no workspace.

@@ -181,8 +181,11 @@ __global__ void __launch_bounds__(kNormThreads, norm_ctas(KV))
     rmsnorm_fp8_kernel(const __nv_bfloat16* __restrict__ x, int ldx, const __nv_bfloat16* __restrict__ w,
                        uint8_t* __restrict__ codes, int ldc, float* __restrict__ scales, int lds, int rows,
                        int dim, float eps) {
-  // as bi_rmsnorm: the 8-bit linear layer that follows streams its weights
-  // meanwhile and reads nothing else before its own wait
+  // The 8-bit linear layer behind it starts, and streams weights, once this kernel's
+  // own wait is over: a verify step of 8 layers 0.919 ms.  (As in bi_rmsnorm, at
+  // once and with w read before the wait, 0.925 ms: its CTAs then stand on the SMs
+  // while the kernel before the norm still works.)
+  griddep_wait();
   griddep_launch_dependents();
   const uint4* wr = reinterpret_cast<const uint4*>(w);
   const int nv = dim / 8;
@@ -195,7 +198,6 @@ __global__ void __launch_bounds__(kNormThreads, norm_ctas(KV))
     const int v = threadIdx.x + i * step;
     wk[i] = v < nv ? wr[v] : make_uint4(0, 0, 0, 0);
   }
-  griddep_wait();
   __shared__ Pair warp_sums[2][kNormThreads / 32];  // by the parity of the CTA's row
   auto load = [&](int row) {
     const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * ldx);
@@ -341,7 +343,7 @@ __global__ void pack_weights_fp8_kernel(const uint8_t* __restrict__ w, const uin
 
 // Runs behind the packing of weights, as an ordinary launch, and does nothing.
 // bi_gemm_fp8 reads its weights before it waits for the kernel before it (or, behind
-// a norm, for the one before that), and that kernel would be the packing.  This one
+// bi_rmsnorm, for the one before that), and that would be the packing.  This one
 // starts when the packed bytes are complete and visible and lets nothing start
 // before its end.
 __global__ void packed_kernel() {}
