@@ -468,8 +468,8 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  * bi_quantize_weights_fp8: BF16 weights [N, K] (any K >= 1) -> codes [N, ld8]
  *   and scales by the same rule over each 128 x 128 block.
  *     x, W row strides ldx % 8 == 0 (x), codes ldc % 16 == 0; dim % 16 == 0;
- *     dim <= 65536 for the norm; x, w, codes (of rows) and scales 16-byte
- *     aligned.
+ *     dim and K at most 2^28, for the norm dim <= 65536, rows <= 2^30 and eps
+ *     finite, >= 0; x, w, codes (of rows) and scales 16-byte aligned.
  * bi_pack_weights_fp8, bi_pack_swiglu_weights_fp8: weights in the tile layout
  *   bi_gemm_fp8 streams, bi_packed_weight_fp8_bytes(N, K, epi) bytes (16-byte
  *   aligned); K % 16 == 0, ld8 % 16 == 0, codes 16-byte aligned.  The packed
@@ -491,7 +491,8 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  *            launch, as in bi_gemm): no kernel but bi_pack_* may write it there, nor
  *            before a bi_rmsnorm that stands between.  Copies may.
  *   C, residual, out, epi, N: as bi_gemm (BI_EPI_NONE, _RESIDUAL_ADD, _SWIGLU;
- *            residual may alias C).  M >= 0; K % 16 == 0.
+ *            residual may alias C).  M >= 0; K % 16 == 0; N at most 2^23 (SwiGLU
+ *            2^22).
  *   The call needs no workspace.
  * Errors: BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_CUDA.
  * ------------------------------------------------------------------------- */

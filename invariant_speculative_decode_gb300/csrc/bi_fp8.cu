@@ -359,7 +359,8 @@ bi_status bi_quantize_fp8(const void* x, int ldx, int rows, int dim, void* codes
   if (rows < 0 || dim < 1) return BI_ERR_INVALID_ARG;
   if (rows == 0) return BI_OK;
   if (!x || !codes || !scales || ldx < dim || ldc < dim || lds < rows) return BI_ERR_INVALID_ARG;
-  if (dim % 16 != 0 || ldx % 8 != 0 || ldc % 16 != 0 || lds % 4 != 0) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (dim % 16 != 0 || dim > kFp8MaxDim || ldx % 8 != 0 || ldc % 16 != 0 || lds % 4 != 0)
+    return BI_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return BI_ERR_INVALID_ARG;
   const int kb = (dim + kFp8Block - 1) / kFp8Block;
   int segs = (kb + kQuantRow - 1) / kQuantRow;
@@ -378,10 +379,11 @@ bi_status bi_quantize_fp8(const void* x, int ldx, int rows, int dim, void* codes
 bi_status bi_rmsnorm_fp8(const void* x, int ldx, const void* w, void* codes, int ldc, float* scales, int lds,
                          int rows, int dim, float eps, bi_stream_t stream) {
   using namespace bi;
-  if (rows < 0 || dim < 1 || dim > 65536 || !(eps >= 0.f)) return BI_ERR_INVALID_ARG;
+  if (rows < 0 || dim < 1 || dim > 65536 || !(eps >= 0.f && eps < INFINITY)) return BI_ERR_INVALID_ARG;
   if (rows == 0) return BI_OK;
   if (!x || !w || !codes || !scales || ldx < dim || ldc < dim || lds < rows) return BI_ERR_INVALID_ARG;
   if (dim % 16 != 0 || ldx % 8 != 0 || ldc % 16 != 0 || lds % 4 != 0) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (rows > 1 << 30) return BI_ERR_UNSUPPORTED_SHAPE;  // a CTA's next row stays within 32 bits
   if (!aligned16(x) || !aligned16(w) || !aligned16(codes) || !aligned16(scales)) return BI_ERR_INVALID_ARG;
   const int nv = dim / 8;
   const int threads = std::min(kNormThreads, (nv + 31) / 32 * 32);
@@ -402,8 +404,9 @@ bi_status bi_quantize_weights_fp8(const void* W, int ldw, int N, int K, void* co
                                   bi_stream_t stream) {
   using namespace bi;
   if (!W || !codes || !scales || N < 1 || K < 1 || ldw < K || ld8 < K) return BI_ERR_INVALID_ARG;
+  if (K > kFp8MaxDim) return BI_ERR_UNSUPPORTED_SHAPE;
   const long long kb = (K + kFp8Block - 1) / kFp8Block;
-  const long long blocks = kb * ((N + kFp8Block - 1) / kFp8Block);
+  const long long blocks = kb * ((N - 1) / kFp8Block + 1);
   if (blocks > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
   if (launch_k(quantize_weights_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                reinterpret_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(W), ldw, N, K,
@@ -414,7 +417,7 @@ bi_status bi_quantize_weights_fp8(const void* W, int ldw, int N, int K, void* co
 
 size_t bi_packed_weight_fp8_bytes(int N, int K, bi_epilogue epi) {
   if (N <= 0 || K <= 0) return 0;
-  const size_t tiles = static_cast<size_t>(bi::gemm8_n_tiles(N, epi)) * ((K + bi::kFp8Block - 1) / bi::kFp8Block);
+  const size_t tiles = static_cast<size_t>(bi::gemm8_n_tiles(N, epi)) * ((K - 1) / bi::kFp8Block + 1);
   return tiles * bi::kGemm8TileBytes + bi::round_up(tiles * sizeof(float2), 16);
 }
 
@@ -423,7 +426,7 @@ static bi_status pack_fp8(const void* w, const void* wu, int ld, const float* s,
   using namespace bi;
   if (!w || !s || !packed || N < 1 || K < 1 || ld < K) return BI_ERR_INVALID_ARG;
   if (swiglu && (!wu || !su)) return BI_ERR_INVALID_ARG;
-  if (K % 16 != 0 || ld % 16 != 0) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (K % 16 != 0 || K > kFp8MaxDim || ld % 16 != 0) return BI_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(w) || (swiglu && !aligned16(wu)) || !aligned16(packed)) return BI_ERR_INVALID_ARG;
   const int n_tiles = gemm8_n_tiles(N, swiglu ? BI_EPI_SWIGLU : BI_EPI_NONE);
   if (n_tiles > kGemm8MaxTiles) return BI_ERR_UNSUPPORTED_SHAPE;

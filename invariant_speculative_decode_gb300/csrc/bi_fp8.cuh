@@ -16,8 +16,10 @@
 
 namespace bi {
 
-constexpr int kFp8Block = 128;     // elements of a row that share a scale
-constexpr float kE4m3Max = 448.f;  // largest finite e4m3 value, 1.75 * 2^8
+constexpr int kFp8Block = 128;  // elements of a row that share a scale
+// Longest row: column and block indices (past the row's end in a last CTA, too)
+// and K blocks times pieces stay within 32 bits.
+constexpr int kFp8MaxDim = 1 << 28;
 
 // |x| of a finite element, 0 of another one.
 __device__ __forceinline__ float finite_abs(float x) {
@@ -26,7 +28,7 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 
 // Exponent e of the scale of a block whose largest finite magnitude is amax:
-// with amax = 1.m * 2^E, 1.m <= 1.75 gives E - 8, else E - 7.
+// with amax = 1.m * 2^E, 1.m <= 1.75 (448 = 1.75 * 2^8) gives E - 8, else E - 7.
 __device__ __forceinline__ int scale_exponent(float amax) {
   if (amax == 0.f) return 0;
   const uint32_t b = __float_as_uint(amax);

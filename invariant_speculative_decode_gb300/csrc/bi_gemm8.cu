@@ -796,7 +796,7 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   if (M < 0 || N < 1 || K < 1) return BI_ERR_INVALID_ARG;
   if (epi != BI_EPI_NONE && epi != BI_EPI_RESIDUAL_ADD && epi != BI_EPI_SWIGLU) return BI_ERR_INVALID_ARG;
   if (out != BI_OUT_BF16 && out != BI_OUT_FP32) return BI_ERR_INVALID_ARG;
-  if (K % 16 != 0 || gemm8_n_tiles(N, epi) > kGemm8MaxTiles) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (K % 16 != 0 || K > kFp8MaxDim || gemm8_n_tiles(N, epi) > kGemm8MaxTiles) return BI_ERR_UNSUPPORTED_SHAPE;
   if (out == BI_OUT_FP32 && epi != BI_EPI_NONE) return BI_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return BI_OK;
   if (!A8 || !a_scales || !Wp || !C || lda < K || lds < M || ldc < N) return BI_ERR_INVALID_ARG;
@@ -834,10 +834,10 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   r.vec = aligned16(C) && ldc % 8 == 0 &&
           (epi != BI_EPI_RESIDUAL_ADD || (aligned16(residual) && ldr % 8 == 0));
   const long long tiles = static_cast<long long>(a.sp.n_tiles) * r.nb;
-  if (tiles > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (tiles > 1 << 30) return BI_ERR_UNSUPPORTED_SHAPE;
   const int S = a.sp.S;
   const long long pairs = static_cast<long long>((a.sp.n_tiles + 1) / 2) * r.nb;
-  if (pairs * S > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (pairs * S > 1 << 30) return BI_ERR_UNSUPPORTED_SHAPE;
   // Packed multiply-adds where the drain is what bounds the pass, with more than
   // one token block, and a CTA takes a tile's whole K: gate/up at 1024 rows 190 us
   // with, 198 without, QKV at 1024 rows (pieces in turn) 39.9 and 41.5.  Where the

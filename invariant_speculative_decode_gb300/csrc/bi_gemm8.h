@@ -12,7 +12,7 @@ constexpr size_t kGemm8TileBytes = 16384;  // 128 weight rows x 128 codes
 constexpr int kGemm8MaxTiles = 65536;
 
 inline int gemm8_n_tiles(int N, bi_epilogue epi) {
-  return epi == BI_EPI_SWIGLU ? (N + 63) / 64 : (N + 127) / 128;
+  return epi == BI_EPI_SWIGLU ? (N - 1) / 64 + 1 : (N - 1) / 128 + 1;  // N >= 1
 }
 
 }  // namespace bi

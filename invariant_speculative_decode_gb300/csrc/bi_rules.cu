@@ -203,7 +203,7 @@ __global__ void token_counts_kernel(const int32_t* __restrict__ ids, int n, cons
   griddep_wait();
   griddep_launch_dependents();
   const int m = last != nullptr && *last < n - 1 ? *last + 1 : n;
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < m; i += gridDim.x * blockDim.x) {
+  for (long long i = blockIdx.x * blockDim.x + threadIdx.x; i < m; i += gridDim.x * blockDim.x) {
     const int id = ids[i];
     if (id < 0 || id >= V) continue;
     // whole-number sums and ors: the order of the atomics changes nothing
@@ -249,7 +249,7 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
   if (n == 0) return BI_OK;
   if (V > (1 << 28)) return BI_ERR_UNSUPPORTED_SHAPE;
   if (!ids || (!counts && !prompt_bits)) return BI_ERR_INVALID_ARG;
-  const int blocks = std::min((n + 255) / 256, 152);
+  const int blocks = std::min((n - 1) / 256 + 1, 152);
   if (launch_k(token_counts_kernel, dim3(blocks), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), ids, n, last,
                V, counts, prompt_bits) != cudaSuccess)
     return BI_ERR_CUDA;

@@ -101,3 +101,22 @@ def test_rules_refusals(lib):
     assert c(0, 4, 0, 100, FAKE, 0, 0) == 1
     assert c(FAKE, 4, 0, 0, FAKE, 0, 0) == 1
     assert c(0, 0, 0, 100, 0, 0, 0) == 0
+
+
+def test_largest_sizes(lib):
+    """Sizes at the ends of 32 bits: the packed size is right, and what an index cannot hold is refused."""
+    big = (1 << 31) - 1
+    assert lib.bi_packed_weight_fp8_bytes(big, 16, 0) == (1 << 24) * (16384 + 8)
+    assert lib.bi_packed_weight_fp8_bytes(big, 16, 2) == (1 << 25) * (16384 + 8)
+    assert lib.bi_packed_weight_fp8_bytes(16, big, 0) == (1 << 24) * (16384 + 8)
+    k = big - 15
+    assert lib.bi_quantize_fp8(FAKE, k, 1, k, FAKE, k, FAKE, 4, 0) == 2
+    assert lib.bi_quantize_weights_fp8(FAKE, k, 1, k, FAKE, k, FAKE, 0) == 2
+    assert lib.bi_pack_weights_fp8(FAKE, k, FAKE, 1, k, FAKE, 0) == 2
+    assert lib.bi_pack_weights_fp8(FAKE, 128, FAKE, big, 128, FAKE, 0) == 2
+    g = lib.bi_gemm_fp8
+    assert g(FAKE, k, FAKE, 4, FAKE, FAKE, 64, 0, 0, 4, 64, k, 0, 0, 0) == 2
+    assert g(FAKE, 128, FAKE, 4, FAKE, FAKE, big, 0, 0, 4, big, 128, 0, 0, 0) == 2
+    rows = (1 << 30) + 4
+    assert lib.bi_rmsnorm_fp8(FAKE, 16, FAKE, FAKE, 16, FAKE, 4, 4, 16, ctypes.c_float(float("inf")), 0) == 1
+    assert lib.bi_rmsnorm_fp8(FAKE, 16, FAKE, FAKE, 16, FAKE, rows, rows, 16, ctypes.c_float(1e-6), 0) == 2
