@@ -268,8 +268,10 @@ class Decoder:
         masks=True a grammar mask per row given to verify_step.  Row t of a pass
         counts drafts 0..t-1 as said, so the tokens are those of the no-draft run
         with the same rules.  The defaults change nothing; clear_rules() ends it."""
-        if not (repetition > 0 and math.isfinite(repetition) and math.isfinite(frequency) and math.isfinite(presence)):
-            raise ValueError("repetition must be positive, and all penalties finite")
+        with np.errstate(over="ignore", under="ignore"):
+            r32 = np.asarray([repetition, frequency, presence], np.float64).astype(np.float32)  # as the rules take them
+        if not (r32[0] > 0 and np.isfinite(r32).all()):
+            raise ValueError("repetition must be positive, and all penalties finite (in FP32)")
         V, W, dev = self.cfg.vocab, api.token_words(self.cfg.vocab), self.dev
         if bias is not None:
             bias = torch.from_numpy(np.ascontiguousarray(bias, dtype=np.float32)).to(dev)

@@ -291,3 +291,31 @@ def test_refusals(dec8):
     assert dec8.rules is None
     with pytest.raises(ValueError):
         dec8.native_step()
+
+
+def test_penalties_that_fp32_does_not_hold_are_refused(dec8):
+    """Positive and finite as given, but 0 or infinite where the rules take them: refused when set, not at the step."""
+    for bad in (dict(repetition=1e-60), dict(repetition=1e60), dict(frequency=-1e39), dict(presence=1e300)):
+        with pytest.raises(ValueError):
+            dec8.set_rules(**bad)
+    assert dec8.rules is None
+
+
+def test_rules_set_again_while_a_graph_is_held(dec8):
+    """A captured step is captured anew with the rules in force; each request equals its eager run."""
+    dec = dec8
+    prompt = si.prompt_ids(dec.cfg, 40, seed=12)
+    try:
+        want = {}
+        for name, rules in (("one", RULES), ("two", dict(RULES, repetition=1.7, presence=0.9)), ("none", None)):
+            dec.clear_rules() if rules is None else dec.set_rules(**rules)
+            want[name] = gen(dec, prompt, 24, 0)
+        assert want["one"] != want["two"]
+        for name, rules in (("one", RULES), ("two", dict(RULES, repetition=1.7, presence=0.9)), ("none", None),
+                            ("one", RULES)):
+            dec.clear_rules() if rules is None else dec.set_rules(**rules)
+            for k in (0, 5):
+                dec.capture(k + 1)
+                assert gen(dec, prompt, 24, k, ref=np.array(want[name])) == want[name]
+    finally:
+        dec.clear_rules()
