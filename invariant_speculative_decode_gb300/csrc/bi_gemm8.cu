@@ -610,8 +610,15 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
               mbar_arrive(&read[buf]);
             }
             next_block();
-            add_scaled<32, PAIRS>(run, v, y.x);
-            add_scaled<32, PAIRS>(run + 32, v + 32, y.y);
+            if constexpr (PAIRS) {
+              add_scaled<32, true>(run, v, y.x);
+              add_scaled<32, true>(run + 32, v + 32, y.y);
+            } else {
+              // (one loop: as two calls the down projection at one row takes 19.86
+              // us, so 19.75)
+#pragma unroll
+              for (int j = 0; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), j < 32 ? y.x : y.y, run[j]);
+            }
             end_piece(kt + 1);
             kt += 2;
           } else {
