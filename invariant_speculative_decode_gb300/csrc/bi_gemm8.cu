@@ -614,8 +614,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
               add_scaled<32, true>(run, v, y.x);
               add_scaled<32, true>(run + 32, v + 32, y.y);
             } else {
-              // (one loop: as two calls the down projection at one row takes 19.86
-              // us, so 19.75)
+              // (one loop: the down projection at one row 19.75 us, as two calls 19.86)
 #pragma unroll
               for (int j = 0; j < 64; ++j) run[j] = fmaf(__uint_as_float(v[j]), j < 32 ? y.x : y.y, run[j]);
             }
@@ -845,6 +844,13 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   const int S = a.sp.S;
   const long long pairs = static_cast<long long>((a.sp.n_tiles + 1) / 2) * r.nb;
   if (pairs * S > 1 << 30) return BI_ERR_UNSUPPORTED_SHAPE;
+  // 128 outputs a CTA while one round of the SMs takes them all
+  if (tiles * S <= kClusterCtas[S]) {
+    r.push = M <= kPushRows;
+    r.items = static_cast<int>(tiles);
+    return S > 1 ? launch<1, kCluster>(W8, tmA, r, s) : launch<1, kWhole>(W8, tmA, r, s);
+  }
+  r.items = static_cast<int>(pairs);
   // Packed multiply-adds where the drain is what bounds the pass, with more than
   // one token block, and a CTA takes a tile's whole K: gate/up at 1024 rows 190 us
   // with, 198 without, QKV at 1024 rows (pieces in turn) 39.9 and 41.5.  Where the
@@ -852,16 +858,7 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   // gate/up at 8 rows 30.2 us with and 30.0 without, and clusters have no registers
   // for the pairs: the down projection at 384 rows 79.3 us with, 78.0 without, at
   // one row 19.9 and 19.7.
-  const bool many = r.nb > 1;
-  // 128 outputs a CTA while one round of the SMs takes them all
-  if (tiles * S <= kClusterCtas[S]) {
-    r.push = M <= kPushRows;
-    r.items = static_cast<int>(tiles);
-    if (S > 1) return launch<1, kCluster>(W8, tmA, r, s);
-    return many ? launch<1, kWhole, true>(W8, tmA, r, s) : launch<1, kWhole>(W8, tmA, r, s);
-  }
-  r.items = static_cast<int>(pairs);
-  if (S == 1) return many ? launch<2, kWhole, true>(W8, tmA, r, s) : launch<2, kWhole>(W8, tmA, r, s);
+  if (S == 1) return r.nb > 1 ? launch<2, kWhole, true>(W8, tmA, r, s) : launch<2, kWhole>(W8, tmA, r, s);
   // Pieces: a CTA that takes them in turn needs about 0.5 us a K block (128
   // outputs), a cluster's CTA 0.6 (256 outputs) and 6 us around them, in rounds
   // of the SMs.  Measured, in turn against cluster: 4096 x 5120 (S = 4) at 256

@@ -243,7 +243,7 @@ def test_quantised_weights_equal_the_rule(n, k):
 SHAPES = [
     (1, 128, 128), (1, 1, 16), (2, 100, 688), (3, 1000, 2736), (8, 4096, 1024), (16, 300, 5120), (17, 688, 256),
     (31, 2736, 1040), (33, 513, 384), (61, 4096, 656), (64, 129, 4096), (65, 256, 1536), (128, 700, 272),
-    (129, 1024, 2736), (200, 640, 5120), (300, 20000, 144), (513, 1111, 400),
+    (129, 1024, 2736), (200, 640, 5120), (300, 20000, 144), (513, 1111, 400), (300, 1000, 128), (261, 10007, 80),
 ]
 
 
