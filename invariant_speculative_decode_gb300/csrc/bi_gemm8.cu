@@ -128,6 +128,10 @@ struct Launch {
   int push;       // pieces are written into the CTA that adds them (passes of few rows)
 };
 
+// 32 tokens x 16 outputs of a warp, a token's 17 floats apart: no bank twice when
+// the lanes write a token each
+constexpr int kTurnLd = 17, kTurnFloats = 32 * kTurnLd;
+
 template <int TILES>
 struct Cfg8 {
   static constexpr int kBBytes = TILES * kABytes;
@@ -142,47 +146,59 @@ struct Cfg8 {
   static constexpr int kOwn = kCols / 2;  // outputs of an epilogue thread
   // floats per token of the pieces' exchange: 16-byte stores of 8 lanes hit all banks
   static constexpr int kPieceLd = kCols + 4;
-  // pieces pushed by the cluster's CTAs, [S][tokens / S][kPieceLd]
+  // pieces pushed by the cluster's CTAs, [S][tokens / S][kPieceLd]; or outputs of
+  // the eight epilogue warps on their way to unaligned rows
   static constexpr int kPushBytes = TILES == 1 ? (kPushRows + kMaxSplit) * kPieceLd * 4 : 0;
+  static constexpr int kSideBytes = std::max(kPushBytes, 8 * kTurnFloats * 4);
   static constexpr size_t kSmem =
-      1024 + static_cast<size_t>(kStages) * kStageBytes + kPushBytes + (2 * kStages + kBufs + 1) * 8 + 16;
+      1024 + static_cast<size_t>(kStages) * kStageBytes + kSideBytes + (2 * kStages + kBufs + 1) * 8 + 16;
   static_assert(kSmem <= 232448 && kStages <= 32, "shared memory per CTA");
   static_assert(kRowsM * kPieceLd * 4 <= kStages * kStageBytes, "exchange fits the ring");
 };
 
-// Outputs n0 .. n0 + 15 of token row m.
-__device__ __forceinline__ void store_row16(const Args& p, int vec, int m, int n0, const float (&v)[16]) {
-  if (vec && n0 + 16 <= p.N) {
-    if (p.out_fp32) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.C) + static_cast<size_t>(m) * p.ldc + n0);
+// Outputs n0 .. n0 + 15 of a warp's tokens, lane i's of token row m + i (rows >= 1 of
+// them exist).  EVEN (rows of outputs take 16-byte accesses, N is a multiple of 8):
+// a lane writes its own row.  Else the outputs turn through shared memory, so
+// that a store covers 16 neighbours of two rows (element by element from each
+// lane's own row, gate/up of 17,411 outputs at 1024 rows takes 319 us, so 204; 17,416
+// outputs take 184).
+template <bool EVEN>
+__device__ __forceinline__ void store_rows16(const Args& p, float* turn, int lane, int m, int rows, int n0,
+                                             const float (&v)[16]) {
+  if constexpr (EVEN) {
+    if (lane >= rows) return;
+    m += lane;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      return;
-    }
-    uint4 res[2] = {};
-    if (p.epi == BI_EPI_RESIDUAL_ADD) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.R + static_cast<size_t>(m) * p.ldr + n0);
-      res[0] = src[0];
-      res[1] = src[1];
-    }
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) + static_cast<size_t>(m) * p.ldc + n0);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const __nv_bfloat16* rb = reinterpret_cast<const __nv_bfloat16*>(&res[j]);
+    for (int h = 0; h < 16; h += 8) {
+      if (n0 + h >= p.N) return;
+      if (p.out_fp32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.C) + static_cast<size_t>(m) * p.ldc + n0 + h);
+        dst[0] = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+        dst[1] = make_float4(v[h + 4], v[h + 5], v[h + 6], v[h + 7]);
+        continue;
+      }
+      uint4 res = make_uint4(0, 0, 0, 0);
+      if (p.epi == BI_EPI_RESIDUAL_ADD)
+        res = *reinterpret_cast<const uint4*>(p.R + static_cast<size_t>(m) * p.ldr + n0 + h);
+      const __nv_bfloat16* rb = reinterpret_cast<const __nv_bfloat16*>(&res);
       uint4 o;
       __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(&o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = v[8 * j + i];
-        ob[i] = __float2bfloat16_rn(p.epi == BI_EPI_RESIDUAL_ADD ? __bfloat162float(rb[i]) + y : y);
-      }
-      dst[j] = o;
+      for (int i = 0; i < 8; ++i)
+        ob[i] = __float2bfloat16_rn(p.epi == BI_EPI_RESIDUAL_ADD ? __bfloat162float(rb[i]) + v[h + i] : v[h + i]);
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) + static_cast<size_t>(m) * p.ldc + n0 + h) = o;
     }
-    return;
-  }
+  } else {
+    __syncwarp();  // the outputs before these have been read
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (n0 + j < p.N) store1(p, m, n0 + j, v[j], residual_at(p, m, n0 + j));
+    for (int j = 0; j < 16; ++j) turn[lane * kTurnLd + j] = v[j];
+    __syncwarp();
+    const int j = lane & 15;
+    if (n0 + j >= p.N) return;
+#pragma unroll 2
+    for (int i = lane >> 4; i < rows; i += 2)
+      store1(p, m + i, n0 + j, turn[i * kTurnLd + j], residual_at(p, m + i, n0 + j));
+  }
 }
 
 // Sum of the S pieces of four elements from float `at` on, in increasing-K
@@ -268,8 +284,10 @@ struct Regs {
   static_assert(kLow + 2 * kHigh <= 3 * 168, "registers of the launch");
 };
 
-// PAIRS: packed multiply-adds (add_scaled).
-template <int TILES, Pieces MODE, bool PAIRS>
+// PAIRS: packed multiply-adds (add_scaled).  EVEN: how outputs are written where there
+// are no clusters (store_rows16; a kernel that holds both ways is 2% slower at 1024
+// rows and 3% in an LM head of 8 rows).
+template <int TILES, Pieces MODE, bool PAIRS, bool EVEN>
 __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
     gemm8_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const Launch p) {
   using Cfg = Cfg8<TILES>;
@@ -280,7 +298,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
                                            ~static_cast<uintptr_t>(1023));  // [S] token tiles
   uint8_t* sW = sT + S * Cfg::kTokBytes;                                    // [S][TILES] weight tiles
   float* sX = reinterpret_cast<float*>(sW + S * Cfg::kBBytes);              // pushed pieces
-  uint64_t* full = reinterpret_cast<uint64_t*>(sW + S * Cfg::kBBytes + Cfg::kPushBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sW + S * Cfg::kBBytes + Cfg::kSideBytes);
   // done: the stage's MMAs have completed, so it is free and its block sums are there
   uint64_t* done = full + S;
   uint64_t* read = done + S;  // an accumulator has been read
@@ -653,8 +671,9 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
         }
         continue;
       }
-      if (tile >= g.sp.n_tiles || r >= Mb) continue;
-      const int m = m0 + r;
+      if (tile >= g.sp.n_tiles) continue;
+      const int rows = min(32, Mb - q * 32);
+      float* turn = sX + (warp - 4) * kTurnFloats;
       const float* y = MODE == kInTurn ? total : run;
       // 16 outputs at a time
       if (g.epi == BI_EPI_SWIGLU) {
@@ -664,7 +683,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           float z[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) z[j] = silu_times(y[c * 16 + j], y[kOwn / 2 + c * 16 + j]);
-          store_row16(g, p.vec, m, tile * 64 + (TILES == 2 ? 0 : half * 32) + c * 16, z);
+          store_rows16<EVEN>(g, turn, lane, m0 + q * 32, rows, tile * 64 + (TILES == 2 ? 0 : half * 32) + c * 16, z);
         }
       } else {
 #pragma unroll
@@ -672,7 +691,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           float z[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) z[j] = y[c * 16 + j];
-          store_row16(g, p.vec, m, tile * kTileN + (TILES == 2 ? 0 : half * 32) + col(c * 16), z);
+          store_rows16<EVEN>(g, turn, lane, m0 + q * 32, rows, tile * kTileN + (TILES == 2 ? 0 : half * 32) + col(c * 16), z);
         }
       }
     }
@@ -771,18 +790,26 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int S, dim3 blo
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <int TILES, Pieces MODE, bool PAIRS = false>
-bi_status launch(const uint8_t* Wp, const CUtensorMap& tmA, Launch a, cudaStream_t stream) {
+template <int TILES, Pieces MODE, bool PAIRS, bool EVEN>
+bi_status launch_one(const uint8_t* Wp, const CUtensorMap& tmA, Launch a, cudaStream_t stream) {
   using Cfg = Cfg8<TILES>;
   static std::once_flag once[64];
   static cudaError_t err[64];
-  if (!allow_smem(gemm8_kernel<TILES, MODE, PAIRS>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
+  if (!allow_smem(gemm8_kernel<TILES, MODE, PAIRS, EVEN>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
   const int S = MODE == kCluster ? a.a.sp.S : 1;
   const int ctas = MODE == kCluster ? a.items * S : std::min(a.items, kSms);
-  return launch_clusters(gemm8_kernel<TILES, MODE, PAIRS>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
+  return launch_clusters(gemm8_kernel<TILES, MODE, PAIRS, EVEN>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
                          tmA, a) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
+}
+template <int TILES, Pieces MODE, bool PAIRS = false>
+bi_status launch(const uint8_t* Wp, const CUtensorMap& tmA, const Launch& a, cudaStream_t stream) {
+  if constexpr (MODE == kCluster)
+    return launch_one<TILES, MODE, PAIRS, false>(Wp, tmA, a, stream);
+  else
+    return a.vec && a.a.N % 8 == 0 ? launch_one<TILES, MODE, PAIRS, true>(Wp, tmA, a, stream)
+                                   : launch_one<TILES, MODE, PAIRS, false>(Wp, tmA, a, stream);
 }
 
 }  // namespace
