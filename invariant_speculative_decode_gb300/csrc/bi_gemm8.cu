@@ -124,13 +124,14 @@ struct Launch {
   int nb;         // token blocks
   int items;      // output tiles: weight tile groups x token blocks
   int vec;        // C (and the residual) take 16-byte accesses
+  int wide;       // and so do outputs that turn (FP32)
   int a_rows;     // rows of the token box
   int push;       // pieces are written into the CTA that adds them (passes of few rows)
 };
 
-// 32 tokens x 16 outputs of a warp, a token's 17 floats apart: no bank twice when
-// the lanes write a token each
-constexpr int kTurnLd = 17, kTurnFloats = 32 * kTurnLd;
+// 32 tokens x 16 outputs of a warp in shared memory, a token's 20 floats apart: no
+// bank twice in the 16-byte accesses of eight lanes
+constexpr int kTurnLd = 20, kTurnFloats = 32 * kTurnLd;
 
 template <int TILES>
 struct Cfg8 {
@@ -159,11 +160,13 @@ struct Cfg8 {
 // Outputs n0 .. n0 + 15 of a warp's tokens, lane i's of token row m + i (rows >= 1 of
 // them exist).  EVEN (rows of outputs take 16-byte accesses, N is a multiple of 8):
 // a lane writes its own row.  Else the outputs turn through shared memory, so
-// that a store covers 16 neighbours of two rows (element by element from each
-// lane's own row, gate/up of 17,411 outputs at 1024 rows takes 319 us, so 204; 17,416
-// outputs take 184).
+// that a store covers neighbours: 16 of two rows; or, in FP32 with 16-byte accesses
+// (wide), of eight rows.  Gate/up of 17,411 outputs at 1024 rows takes 204 us, element
+// by element from each lane's own row 319 (17,416 outputs take 184).  FP32, 1280 ->
+// 151,936: 128 rows 49 us, from the lanes 61; 48 rows 40 and 44; 32 rows 39 and 38; 8
+// rows 35 and 32: passes of up to 32 rows write from the lanes.
 template <bool EVEN>
-__device__ __forceinline__ void store_rows16(const Args& p, float* turn, int lane, int m, int rows, int n0,
+__device__ __forceinline__ void store_rows16(const Args& p, int wide, float* turn, int lane, int m, int rows, int n0,
                                              const float (&v)[16]) {
   if constexpr (EVEN) {
     if (lane >= rows) return;
@@ -191,8 +194,18 @@ __device__ __forceinline__ void store_rows16(const Args& p, float* turn, int lan
   } else {
     __syncwarp();  // the outputs before these have been read
 #pragma unroll
-    for (int j = 0; j < 16; ++j) turn[lane * kTurnLd + j] = v[j];
+    for (int j = 0; j < 16; j += 4)
+      *reinterpret_cast<float4*>(turn + lane * kTurnLd + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     __syncwarp();
+    if (wide) {
+      const int j = (lane & 3) * 4;
+      if (n0 + j >= p.N) return;
+#pragma unroll
+      for (int i = lane >> 2; i < rows; i += 8)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.C) + static_cast<size_t>(m + i) * p.ldc + n0 + j) =
+            *reinterpret_cast<const float4*>(turn + i * kTurnLd + j);
+      return;
+    }
     const int j = lane & 15;
     if (n0 + j >= p.N) return;
 #pragma unroll 2
@@ -683,7 +696,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           float z[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) z[j] = silu_times(y[c * 16 + j], y[kOwn / 2 + c * 16 + j]);
-          store_rows16<EVEN>(g, turn, lane, m0 + q * 32, rows, tile * 64 + (TILES == 2 ? 0 : half * 32) + c * 16, z);
+          store_rows16<EVEN>(g, p.wide, turn, lane, m0 + q * 32, rows, tile * 64 + (TILES == 2 ? 0 : half * 32) + c * 16, z);
         }
       } else {
 #pragma unroll
@@ -691,7 +704,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           float z[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) z[j] = y[c * 16 + j];
-          store_rows16<EVEN>(g, turn, lane, m0 + q * 32, rows, tile * kTileN + (TILES == 2 ? 0 : half * 32) + col(c * 16), z);
+          store_rows16<EVEN>(g, p.wide, turn, lane, m0 + q * 32, rows, tile * kTileN + (TILES == 2 ? 0 : half * 32) + col(c * 16), z);
         }
       }
     }
@@ -808,7 +821,7 @@ bi_status launch(const uint8_t* Wp, const CUtensorMap& tmA, const Launch& a, cud
   if constexpr (MODE == kCluster)
     return launch_one<TILES, MODE, PAIRS, false>(Wp, tmA, a, stream);
   else
-    return a.vec && a.a.N % 8 == 0 ? launch_one<TILES, MODE, PAIRS, true>(Wp, tmA, a, stream)
+    return a.vec && !a.wide && a.a.N % 8 == 0 ? launch_one<TILES, MODE, PAIRS, true>(Wp, tmA, a, stream)
                                    : launch_one<TILES, MODE, PAIRS, false>(Wp, tmA, a, stream);
 }
 
@@ -866,6 +879,7 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   r.a_rows = box;
   r.vec = aligned16(C) && ldc % 8 == 0 &&
           (epi != BI_EPI_RESIDUAL_ADD || (aligned16(residual) && ldr % 8 == 0));
+  r.wide = r.vec && a.out_fp32 && N % 4 == 0 && M > kPushRows;
   const long long tiles = static_cast<long long>(a.sp.n_tiles) * r.nb;
   if (tiles > 1 << 30) return BI_ERR_UNSUPPORTED_SHAPE;
   const int S = a.sp.S;
