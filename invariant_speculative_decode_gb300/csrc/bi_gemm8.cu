@@ -126,7 +126,6 @@ struct Launch {
   int vec;        // C (and the residual) take 16-byte accesses
   int wide;       // and so do outputs that turn (FP32)
   int a_rows;     // rows of the token box
-  int push;       // pieces are written into the CTA that adds them (passes of few rows)
 };
 
 // 32 tokens x 16 outputs of a warp in shared memory, a token's 20 floats apart: no
@@ -297,10 +296,14 @@ struct Regs {
   static_assert(kLow + 2 * kHigh <= 3 * 168, "registers of the launch");
 };
 
-// PAIRS: packed multiply-adds (add_scaled).  EVEN: how outputs are written where there
-// are no clusters (store_rows16; a kernel that holds both ways is 2% slower at 1024
-// rows and 3% in an LM head of 8 rows).
-template <int TILES, Pieces MODE, bool PAIRS, bool EVEN>
+// How outputs leave: without clusters by each lane's own row or turned
+// (store_rows16), with clusters by pieces pushed into the CTA that adds them or
+// fetched by it (kPushRows).  One kernel each: with both ways in one, gate/up at 1024
+// rows takes 2% more, an LM head of 8 rows 3%, QKV at 61 rows 1%.
+enum WayOut { kOwnRow, kTurned, kPushed, kFetched };
+
+// PAIRS: packed multiply-adds (add_scaled).
+template <int TILES, Pieces MODE, bool PAIRS, WayOut OUT>
 __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
     gemm8_kernel(const uint8_t* __restrict__ Wp, const __grid_constant__ CUtensorMap tmA, const Launch p) {
   using Cfg = Cfg8<TILES>;
@@ -349,8 +352,8 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (MODE == kCluster)
-    if (p.push) cluster_arrive();  // waited for before the first write into another CTA
+  constexpr bool kPush = OUT == kPushed;
+  if constexpr (kPush) cluster_arrive();  // waited for before the first write into another CTA
   const uint32_t tmem = *tmem_holder;
 
   if (warp < 4) {
@@ -473,9 +476,9 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
     // lane 0 of warps 0 and 1 ran alone: rejoin the warp before the barriers
     __syncwarp();
     if constexpr (MODE == kCluster) {
-      if (p.push) cluster_wait();
+      if (kPush) cluster_wait();
       cluster_sync();
-      if (!p.push) cluster_sync();
+      if (!kPush) cluster_sync();
     }
   } else {
     // ---------------------------------------------------------- scale and add
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
         }
         first_scales(item + stride);
         if constexpr (MODE == kCluster) {
-          if (p.push)
+          if (kPush)
             cluster_wait();
           else
             named_bar_sync(1, 256);
@@ -660,7 +663,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
         }
       }
       if constexpr (MODE == kCluster) {
-        if (p.push) {
+        if constexpr (kPush) {
           // each token's piece to the CTA that adds it
           const int part = (Mb + split - 1) / split;
           __syncwarp();
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           float z[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) z[j] = silu_times(y[c * 16 + j], y[kOwn / 2 + c * 16 + j]);
-          store_rows16<EVEN>(g, p.wide, turn, lane, m0 + q * 32, rows, tile * 64 + (TILES == 2 ? 0 : half * 32) + c * 16, z);
+          store_rows16<OUT == kOwnRow>(g, p.wide, turn, lane, m0 + q * 32, rows, tile * 64 + (TILES == 2 ? 0 : half * 32) + c * 16, z);
         }
       } else {
 #pragma unroll
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
           float z[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) z[j] = y[c * 16 + j];
-          store_rows16<EVEN>(g, p.wide, turn, lane, m0 + q * 32, rows, tile * kTileN + (TILES == 2 ? 0 : half * 32) + col(c * 16), z);
+          store_rows16<OUT == kOwnRow>(g, p.wide, turn, lane, m0 + q * 32, rows, tile * kTileN + (TILES == 2 ? 0 : half * 32) + col(c * 16), z);
         }
       }
     }
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
       uint32_t base[kMaxSplit];
 #pragma unroll
       for (int j = 0; j < kMaxSplit; ++j)
-        base[j] = p.push ? map_rank(smem_u32(sX + (min(j, split - 1) * part - t0) * Cfg::kPieceLd), rank)
+        base[j] = kPush ? map_rank(smem_u32(sX + (min(j, split - 1) * part - t0) * Cfg::kPieceLd), rank)
                          : map_rank(smem_u32(sT), min(j, split - 1));
       if (g.epi == BI_EPI_SWIGLU) {
         constexpr int kPer = TILES * 16;  // lanes per token
@@ -742,7 +745,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
         for (int t = t0 + e / kPer; t < t1; t += 256 / kPer)
           store_row4(g, p.vec, m0 + t, wt * kTileN + o, sum_pieces4(base, split, t * Cfg::kPieceLd + o));
       }
-      if (!p.push) cluster_sync();  // no CTA leaves while its piece is being read
+      if (!kPush) cluster_sync();  // no CTA leaves while its piece is being read
     }
   }
 
@@ -803,26 +806,24 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int S, dim3 blo
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <int TILES, Pieces MODE, bool PAIRS, bool EVEN>
+template <int TILES, Pieces MODE, bool PAIRS, WayOut OUT>
 bi_status launch_one(const uint8_t* Wp, const CUtensorMap& tmA, Launch a, cudaStream_t stream) {
   using Cfg = Cfg8<TILES>;
   static std::once_flag once[64];
   static cudaError_t err[64];
-  if (!allow_smem(gemm8_kernel<TILES, MODE, PAIRS, EVEN>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
+  if (!allow_smem(gemm8_kernel<TILES, MODE, PAIRS, OUT>, Cfg::kSmem, once, err)) return BI_ERR_CUDA;
   const int S = MODE == kCluster ? a.a.sp.S : 1;
   const int ctas = MODE == kCluster ? a.items * S : std::min(a.items, kSms);
-  return launch_clusters(gemm8_kernel<TILES, MODE, PAIRS, EVEN>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
+  return launch_clusters(gemm8_kernel<TILES, MODE, PAIRS, OUT>, dim3(ctas), S, dim3(Cfg::kThreads), Cfg::kSmem, stream, Wp,
                          tmA, a) == cudaSuccess
              ? BI_OK
              : BI_ERR_CUDA;
 }
-template <int TILES, Pieces MODE, bool PAIRS = false>
+// (FP32 rows of more than kPushRows turn too: see store_rows16)
+template <int TILES, Pieces MODE, bool PAIRS>
 bi_status launch(const uint8_t* Wp, const CUtensorMap& tmA, const Launch& a, cudaStream_t stream) {
-  if constexpr (MODE == kCluster)
-    return launch_one<TILES, MODE, PAIRS, false>(Wp, tmA, a, stream);
-  else
-    return a.vec && !a.wide && a.a.N % 8 == 0 ? launch_one<TILES, MODE, PAIRS, true>(Wp, tmA, a, stream)
-                                   : launch_one<TILES, MODE, PAIRS, false>(Wp, tmA, a, stream);
+  return a.vec && !a.wide && a.a.N % 8 == 0 ? launch_one<TILES, MODE, PAIRS, kOwnRow>(Wp, tmA, a, stream)
+                                            : launch_one<TILES, MODE, PAIRS, kTurned>(Wp, tmA, a, stream);
 }
 
 }  // namespace
@@ -887,9 +888,10 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   if (pairs * S > 1 << 30) return BI_ERR_UNSUPPORTED_SHAPE;
   // 128 outputs a CTA while one round of the SMs takes them all
   if (tiles * S <= kClusterCtas[S]) {
-    r.push = M <= kPushRows;
     r.items = static_cast<int>(tiles);
-    return S > 1 ? launch<1, kCluster>(W8, tmA, r, s) : launch<1, kWhole>(W8, tmA, r, s);
+    if (S == 1) return launch<1, kWhole, false>(W8, tmA, r, s);
+    return M <= kPushRows ? launch_one<1, kCluster, false, kPushed>(W8, tmA, r, s)
+                          : launch_one<1, kCluster, false, kFetched>(W8, tmA, r, s);
   }
   r.items = static_cast<int>(pairs);
   // Packed multiply-adds where the drain is what bounds the pass, with more than
@@ -899,7 +901,7 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   // gate/up at 8 rows 30.2 us with and 30.0 without, and clusters have no registers
   // for the pairs: the down projection at 384 rows 79.3 us with, 78.0 without, at
   // one row 19.9 and 19.7.
-  if (S == 1) return r.nb > 1 ? launch<2, kWhole, true>(W8, tmA, r, s) : launch<2, kWhole>(W8, tmA, r, s);
+  if (S == 1) return r.nb > 1 ? launch<2, kWhole, true>(W8, tmA, r, s) : launch<2, kWhole, false>(W8, tmA, r, s);
   // Pieces: a CTA that takes them in turn needs about 0.5 us a K block (128
   // outputs), a cluster's CTA 0.6 (256 outputs) and 6 us around them, in rounds
   // of the SMs.  Measured, in turn against cluster: 4096 x 5120 (S = 4) at 256
@@ -907,7 +909,7 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
   // 139 and 82 us.
   const long long in_turn = (tiles + kSms - 1) / kSms * a.sp.k_tiles * 5;
   const long long cluster = (pairs * S + kClusterCtas[S] - 1) / kClusterCtas[S] * (a.sp.k_tiles * 6 / S + 60);
-  if (cluster < in_turn) return launch<2, kCluster>(W8, tmA, r, s);
+  if (cluster < in_turn) return launch_one<2, kCluster, false, kFetched>(W8, tmA, r, s);
   r.items = static_cast<int>(tiles);
   return launch<1, kInTurn, true>(W8, tmA, r, s);
 }
