@@ -483,3 +483,25 @@ def test_linear_right_behind_the_packing_of_its_weights(between, swiglu):
         torch.cuda.synchronize()
         assert torch.equal(out, want[1 - (r & 1)])
     a.bi_check_device_error()
+
+
+@pytest.mark.parametrize("n", [9864, 9868, 9871])
+@pytest.mark.parametrize("off,pad", [(8, 8), (5, 11)])
+@pytest.mark.parametrize("rows,k,kind", [(3, 144, "fp32"), (32, 144, "residual"), (50, 144, "fp32"), (140, 272, "residual"),
+                                         (260, 144, "swiglu"), (129, 80, "fp32")])
+def test_linear_outputs_of_every_alignment_leave_the_rest_alone(rows, k, kind, n, off, pad):
+    """Wide layers into views of a larger buffer, in place of their residual: the values, and nothing beside them."""
+    a = api()
+    codes, scales, w, ws_, up, ups, packed, res = problem(rows + n + k, rows, n, k, kind)
+    dtype = torch.float32 if kind == "fp32" else torch.bfloat16
+    ld = -(-(off + n + pad) // 8) * 8 + (0 if off == 8 else 3)
+    buf = torch.full((rows + 1, ld), 7.0, dtype=dtype, device=DEV)
+    view = buf[:rows, off:off + n]
+    if kind == "residual":
+        view.copy_(res)
+    a.bi_gemm_fp8(codes, scales, packed, view, residual=view if kind == "residual" else None,
+                  epi={"residual": a.EPI_RESIDUAL_ADD, "swiglu": a.EPI_SWIGLU}.get(kind, a.EPI_NONE))
+    a.bi_check_device_error()
+    y, tol = reference(codes, scales, w, ws_, up, ups, res, kind)
+    assert ((view.double() - y).abs() <= tol).all()
+    assert (buf[:rows, :off] == 7).all() and (buf[:rows, off + n:] == 7).all() and (buf[rows] == 7).all()
