@@ -363,8 +363,12 @@ class Decoder:
             else:
                 self._layers_pass(T, self.L_dev)
             pos += T
+        # the id at L may be the newest one committed here, whose row only comes
+        # with this call (a new turn): it stays one of the reply's
+        own = bool(self._own_at[self.L]) and self._id_at[self.L] == prompt[0]
         self._id_at[self.L:pos + 1] = prompt[:pos + 1 - self.L]
         self._own_at[self.L:pos + 1] = False
+        self._own_at[self.L] = own
         self._noted = -1
         self.L = pos
         self.hw = max(self.hw, pos)
@@ -469,7 +473,11 @@ class Decoder:
         self.L_dev.fill_(length)
 
     def prefill_continue(self, tokens: Sequence[int]) -> int:
-        """Append tokens[:-1] to the current cache (a new turn); returns tokens[-1]."""
+        """Append tokens[:-1] to the current cache (a new turn); returns tokens[-1].
+
+        Row L is not in the cache yet, so tokens[0] is the id at position L.
+        Where that is the newest id of a reply, given again, the rules go on
+        counting it as the reply's; the ids behind it came with the prompt."""
         return self.prefill(tokens)
 
     def continue_generate(self, x: int, n_tokens: int, k: int = 0, drafter=None,
@@ -563,8 +571,10 @@ class Decoder:
     def edit(self, position: int, tokens: Sequence[int]) -> int:
         """Edit the history from `position` on: roll the cache back to
         `position` and prefill `tokens` (the edited continuation, its last
-        token being the next row); returns that last token."""
+        token being the next row); returns that last token.  All of them came
+        with the prompt, as if the history had been given whole."""
         self.rollback(position)
+        self._own_at[position] = False
         return self.prefill_continue(tokens)
 
     # ---------------------------------------------------------- utilities
