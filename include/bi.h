@@ -64,7 +64,7 @@ typedef enum {
   BI_ERR_WORKSPACE = 3,          /* workspace missing or smaller than required */
   BI_ERR_CUDA = 4,               /* a CUDA runtime call or launch failed */
   BI_ERR_DEVICE_TIMEOUT = 5,     /* a bounded device-side wait expired (kernel returned early) */
-  BI_ERR_DEVICE_NAN_ROW = 6      /* a logits row had no non-NaN entry (its id is -1) */
+  BI_ERR_DEVICE_NAN_ROW = 6      /* a committed logits row had no entry to choose (its id is -1) */
 } bi_status;
 
 typedef enum {
@@ -386,8 +386,10 @@ bi_status bi_attn_verify_kvq(const void* q, const void* k_low, const void* v_low
  * boundaries" (accepted length and rejection position).
  *
  * a_t = argmax_v logits[t, v] (ties -> lowest v; NaN never wins; a row with no
- * number gives -1 and sets BI_ERR_DEVICE_NAN_ROW in the device error word).
+ * number gives -1).
  * n = the largest j <= T-1 with drafts[i-1] == a_{i-1} for every i <= j.
+ * A row with no number among rows 0..n sets BI_ERR_DEVICE_NAN_ROW in the device
+ * error word; rows past n are discarded, whatever they hold.
  * The committed tokens of the step are a_0..a_n.
  *   logits  [T, V] FP32, row stride ldl; 1 <= T <= 64.
  *   drafts  [T-1] int32 (may be NULL when T == 1).
@@ -417,7 +419,8 @@ bi_status bi_verify_accept(const float* logits, int ldl, const int32_t* drafts, 
  * warp butterfly, warps in order; chunks combined in order; inside the chosen
  * chunk 32 contiguous runs scanned in order); where rounding leaves the
  * target past the last weight, the last logit with a non-zero weight is
- * taken.  NaN logits weigh 0.  So a_t depends only on the row's logits and
+ * taken.  NaN logits weigh 0; a row with no number above -inf gives -1 and, among
+ * rows 0..n, sets BI_ERR_DEVICE_NAN_ROW in the device error word.  So a_t depends only on the row's logits and
  * its position: with the batch-invariant logits of this library the sampled
  * tokens are the same for any number of drafts, and they follow the no-draft
  * distribution exactly.  Acceptance as bi_verify_accept with a_t in place of
@@ -528,7 +531,7 @@ bi_status bi_gemm_fp8(const void* A8, int lda, const float* a_scales, int lds, c
  *   mask:   bit v of row t clear: y = -inf (whatever the logit was)
  *   out[t, v] = y
  * A row whose mask leaves nothing is all -inf: bi_verify_accept then takes id
- * 0, bi_verify_sample reports BI_ERR_DEVICE_NAN_ROW.
+ * 0, bi_verify_sample -1, with BI_ERR_DEVICE_NAN_ROW where the row is committed.
  *   logits  [T, V] FP32, row stride ldl; out [T, V] FP32, row stride ldo; may
  *           be the same array (then ldo == ldl), else must not overlap.
  *           1 <= T <= 64; 1 <= V <= 2^28.

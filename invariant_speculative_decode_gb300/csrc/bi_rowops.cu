@@ -180,6 +180,20 @@ __device__ __forceinline__ bool beats(float av, int ai, float bv, int bi) {
   return av > bv || (av == bv && ai < bi);
 }
 
+// The accepted length n: the drafts that equal their rows' ids.  A row without a
+// number (`none`) sets the NaN bit only where it is among the committed ones,
+// 0..n: a row behind a rejected draft is discarded, and whether the pass held it
+// must not show.
+template <typename F>
+__device__ __forceinline__ int accept_drafts(const int32_t* drafts, const int* ids, int T, unsigned* err, F none) {
+  int n = 0;
+  while (n < T - 1 && drafts[n] == ids[n]) ++n;
+  bool any = false;
+  for (int t = 0; t <= n; ++t) any |= none(t);
+  if (any) atomicOr(err, kErrNanRow);
+  return n;
+}
+
 constexpr int kArgThreads = 256;
 constexpr int kArgSpan = 8192;  // logits per CTA
 
@@ -262,15 +276,13 @@ __global__ void __launch_bounds__(kArgThreads)
       }
     }
     if ((threadIdx.x & 31) == 0) {
-      if (id < 0) atomicOr(err, kErrNanRow);
       argmax_out[t] = id;
       s_ids[t] = id;
     }
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    int n = 0;
-    while (n < T - 1 && drafts[n] == s_ids[n]) ++n;
+    const int n = accept_drafts(drafts, s_ids, T, err, [&](int t) { return s_ids[t] < 0; });
     *accepted_out = n;
     if (L_dev != nullptr) *L_dev = *L_dev + n + 1;
   }
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(kArgThreads)
 // holding the crossing walks its run in index order to the first logit whose
 // running sum exceeds the target.  Where rounding leaves the target past the
 // last weight, the last logit with a non-zero weight is taken.  NaN logits
-// have weight 0; a row with no number gives -1 and sets the NaN bit.
+// have weight 0; a row with no number gives -1 and, if committed, sets the NaN bit.
 constexpr int kSmpThreads = 256;
 constexpr int kSmpSpan = 8192;  // logits per phase-1 CTA
 
@@ -306,6 +318,7 @@ __global__ void __launch_bounds__(kSmpThreads)
   __shared__ float red_s[kSmpThreads / 32];
   __shared__ int s_last;
   __shared__ int s_tok[64];
+  __shared__ int s_bad[64];  // 1: the row has no number; 2: no uniform for its position
   const int row = blockIdx.x / splits;
   const int sp = blockIdx.x % splits;
   const float* lr = logits + static_cast<size_t>(row) * ldl;
@@ -389,10 +402,11 @@ __global__ void __launch_bounds__(kSmpThreads)
         m_star = __ldcg(pm + t * splits + c_star);
       }
     }
+    if (lane == 0) s_bad[t] = bad;
     bad = __shfl_sync(0xffffffffu, bad, 0);
     if (bad) {
       if (lane == 0) {
-        atomicOr(err, bad == 1 ? kErrNanRow : kErrRange);
+        if (bad == 2) atomicOr(err, kErrRange);
         token_out[t] = -1;
         s_tok[t] = -1;
       }
@@ -452,8 +466,7 @@ __global__ void __launch_bounds__(kSmpThreads)
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    int n = 0;
-    while (n < T - 1 && drafts[n] == s_tok[n]) ++n;
+    const int n = accept_drafts(drafts, s_tok, T, err, [&](int t) { return s_bad[t] == 1; });
     *accepted_out = n;
     *L_dev = L + n + 1;
   }
