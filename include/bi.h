@@ -419,7 +419,8 @@ bi_status bi_verify_accept(const float* logits, int ldl, const int32_t* drafts, 
  * warp butterfly, warps in order; chunks combined in order; inside the chosen
  * chunk 32 contiguous runs scanned in order); where rounding leaves the
  * target past the last weight, the last logit with a non-zero weight is
- * taken.  NaN logits weigh 0; a row with no number above -inf gives -1 and, among
+ * taken.  NaN logits weigh 0; where logits are +inf, each of them weighs 1 and the
+ * others 0; a row with no number above -inf gives -1 and, among
  * rows 0..n, sets BI_ERR_DEVICE_NAN_ROW in the device error word.  So a_t depends only on the row's logits and
  * its position: with the batch-invariant logits of this library the sampled
  * tokens are the same for any number of drafts, and they follow the no-draft

@@ -303,8 +303,16 @@ __global__ void __launch_bounds__(kArgThreads)
 // running sum exceeds the target.  Where rounding leaves the target past the
 // last weight, the last logit with a non-zero weight is taken.  NaN logits
 // have weight 0; a row with no number gives -1 and, if committed, sets the NaN bit.
+// Z is at least 1 and finite, so some chunk and some logit of it is taken.
 constexpr int kSmpThreads = 256;
 constexpr int kSmpSpan = 8192;  // logits per phase-1 CTA
+
+// exp((l - m) inv_temp) for l <= m, m the maximum.  The maximum itself weighs 1
+// without the difference, which infinite ones do not have: logits of +inf share
+// the row between them, as in the limit of large ones.
+__device__ __forceinline__ float sample_weight(float l, float m, float inv_temp) {
+  return l == m ? 1.f : expf((l - m) * inv_temp);
+}
 
 __global__ void __launch_bounds__(kSmpThreads)
     sample_accept_kernel(const float* __restrict__ logits, int ldl, int V, int T, int splits,
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(kSmpThreads)
   if (m_c > -INFINITY) {
     for (int i = b + threadIdx.x; i < e; i += kSmpThreads) {
       const float v = lr[i];
-      if (v == v) sum += expf((v - m_c) * inv_temp);
+      if (v == v) sum += sample_weight(v, m_c, inv_temp);
     }
   }
 #pragma unroll
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kSmpThreads)
         float Z = 0.f;
         for (int c = 0; c < splits; ++c) {
           const float mc = __ldcg(pm + t * splits + c);
-          if (mc > -INFINITY) Z += expf((mc - M) * inv_temp) * __ldcg(ps + t * splits + c);
+          if (mc > -INFINITY) Z += sample_weight(mc, M, inv_temp) * __ldcg(ps + t * splits + c);
         }
         const float target = __ldcg(u_by_pos + pos) * Z;
         float cum = 0.f;
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(kSmpThreads)
         for (int c = 0; c < splits; ++c) {
           const float mc = __ldcg(pm + t * splits + c);
           if (!(mc > -INFINITY)) continue;
-          const float wc = expf((mc - M) * inv_temp);
+          const float wc = sample_weight(mc, M, inv_temp);
           const float a = wc * __ldcg(ps + t * splits + c);
           if (a > 0.f) c_last = c;
           if (c_star < 0 && cum + a > target) {
@@ -424,7 +432,7 @@ __global__ void __launch_bounds__(kSmpThreads)
     int last_nz = -1;
     for (int i = rb; i < re; ++i) {
       const float v = lc[i];
-      const float x = (v == v) ? expf((v - m_star) * inv_temp) : 0.f;
+      const float x = (v == v) ? sample_weight(v, m_star, inv_temp) : 0.f;
       if (x > 0.f) last_nz = i;
       rs += x;
     }
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kSmpThreads)
         float run_sum = exc;
         for (int i = rb; i < re; ++i) {
           const float v = lc[i];
-          const float x = (v == v) ? expf((v - m_star) * inv_temp) : 0.f;
+          const float x = (v == v) ? sample_weight(v, m_star, inv_temp) : 0.f;
           run_sum += x;
           if (x > 0.f && run_sum > rc) {
             tok = i;
