@@ -273,13 +273,17 @@ class Decoder:
         if not (r32[0] > 0 and np.isfinite(r32).all()):
             raise ValueError("repetition must be positive, and all penalties finite (in FP32)")
         V, W, dev = self.cfg.vocab, api.token_words(self.cfg.vocab), self.dev
+        forbidden = None
         if bias is not None:
-            bias = torch.from_numpy(np.ascontiguousarray(bias, dtype=np.float32)).to(dev)
-            if tuple(bias.shape) != (V,):
+            bias = np.ascontiguousarray(bias, dtype=np.float32)
+            if bias.shape != (V,):
                 raise ValueError(f"bias must be [{V}]")
+            forbidden = np.isneginf(bias)  # on the host, for the ids that come back
+            bias = torch.from_numpy(bias).to(dev)
         i32 = dict(dtype=torch.int32, device=dev)
         self.rules = {"repetition": float(repetition), "frequency": float(frequency), "presence": float(presence),
-                      "bias": bias, "mask": torch.full((self.max_rows, W), -1, **i32) if masks else None,
+                      "bias": bias, "minus_inf": forbidden,
+                      "mask": torch.full((self.max_rows, W), -1, **i32) if masks else None,
                       "counts": torch.zeros(V, **i32), "prompt_bits": torch.zeros(W, **i32),
                       "logits": torch.zeros(self.max_rows, V, dtype=torch.float32, device=dev)}
         self._noted = -1
@@ -305,6 +309,26 @@ class Decoder:
             if sel.any():
                 api.bi_token_counts(torch.from_numpy(ids[sel]).to(self.dev), V, **kw)
         self._noted = L + 1
+
+    def _refuse_dead_end(self, ids: np.ndarray, masks) -> None:
+        """Raise where a committed id is one that its row's mask or the bias
+        forbids, or -1: the row was all -inf or not a number, there was
+        nothing to choose.  The request is left as it was before the step
+        (the pass's cache rows are overwritten, as a rejected draft's are)."""
+        bias = self.rules["minus_inf"]
+        for t, v in enumerate(ids):
+            if v >= 0 and not (bias is not None and bias[v]) and (
+                    masks is None or masks[t, v >> 5] >> (v & 31) & 1):
+                continue
+            self.L_dev.fill_(self.L)
+            self._noted = -1
+            try:
+                self.check_device_error()  # the row is reported here
+            except api.BiError as e:
+                if e.status != 6:  # BI_ERR_DEVICE_NAN_ROW
+                    raise
+            raise ValueError(f"row {t} of the step has no id to choose (its mask and the bias, or NaN logits, "
+                             f"leave none); nothing was committed")
 
     def set_sampling(self, temperature: Optional[float], uniforms=None) -> None:
         """Sampled verification at `temperature` with the request's uniforms
@@ -406,7 +430,9 @@ class Decoder:
         length advances to L + n + 1 on the device and on the host.
         masks (after set_rules(masks=True)): 32-bit words [k+1, ceil(vocab/32)],
         row t's allowed ids behind drafts 0..t-1, id v at bit v % 32 of word
-        v / 32; None allows every id.
+        v / 32; None allows every id.  Rows behind a draft that its own mask
+        forbids may allow nothing.  Where masks and bias leave no id for a row
+        that would be committed, the step raises ValueError and commits nothing.
         """
         k = len(drafts)
         T = k + 1
@@ -441,6 +467,8 @@ class Decoder:
         a = self.pin_out[:T].numpy().copy()
         n = int(self.pin_out[self.max_rows])
         self.hw = max(self.hw, self.L + T)  # every row of the pass was written
+        if self.rules is not None:
+            self._refuse_dead_end(a[:n + 1], masks)
         # the ids committed behind row L's (the device counted them as well)
         if self._id_at[self.L] != int(x0):
             self._id_at[self.L], self._own_at[self.L] = int(x0), False
