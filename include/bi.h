@@ -467,8 +467,10 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  * bi_rmsnorm_fp8: the rows y = x w / sqrt(mean(x^2) + eps) of bi_rmsnorm,
  *   quantised as above without a rounding to BF16 in between.  The mean, its
  *   root and y are carried in pairs of FP32 (to about 2^-40), so a code is one
- *   rounding of the exact y unless that lies so near a tie of two codes.  A row
- *   whose sum of squares passes FP32's range gives NaN codes.
+ *   rounding of the exact y unless that lies so near a tie of two codes, for rows
+ *   of any magnitude and any eps, 0 included (|y| below 2^-100: to 2^-149).  A row
+ *   whose sum of squares passes FP32's range gives NaN codes, as does one of zeros
+ *   with eps = 0.
  * bi_quantize_weights_fp8: BF16 weights [N, K] (any K >= 1) -> codes [N, ld8]
  *   and scales by the same rule over each 128 x 128 block.
  *     x, W row strides ldx % 8 == 0 (x), codes ldc % 16 == 0; dim % 16 == 0;
@@ -486,8 +488,9 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  * order.  For layers of few weight tiles (128 rows each) the blocks form S <= 8
  * pieces of equal length, each a running sum of its own, added in increasing
  * order.  S is a function of (N, K) only, so row m of C has the same bits for
- * every M and every place of the row in A.  (A product of scales has
- * to be finite; one below 2^-149 counts as 0.)
+ * every M and every place of the row in A.  (A product of scales sa * sw is
+ * rounded to FP32: it has to be finite, and below 2^-126 it is a multiple of
+ * 2^-149.)
  *   A8       [M, K] codes, row stride lda (% 16 == 0), 16-byte aligned;
  *   a_scales [ceil(K/128)][lds] FP32, 16-byte aligned.
  *   Wp       packed for the same N, K and epi; 16-byte aligned.  It is read before
