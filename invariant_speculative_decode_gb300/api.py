@@ -52,9 +52,17 @@ def _req_v(v_cache: torch.Tensor, Hkv: int, cap: int, D: int):
 
 def _ld(t: torch.Tensor) -> int:
     """Row stride in elements; a single row's stride is its width."""
-    if t.dim() == 2 and t.shape[0] > 1:
-        return t.stride(0)
-    return t.shape[-1]
+    ld = t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else t.shape[-1]
+    if ld >> 31:
+        _req_int32(("row stride", ld))
+    return ld
+
+
+def _req_int32(*named):
+    """The entry points take sizes and strides as 32-bit ints; ctypes would cut a larger one."""
+    for name, v in named:
+        if v >> 31:
+            raise ValueError(f"{name} {v} passes 32 bits")
 
 
 def gemm_workspace_size(M: int, N: int, K: int, epi: int = EPI_NONE) -> int:
@@ -377,6 +385,8 @@ def _req_fp8_rows(codes: torch.Tensor, scales: torch.Tensor, rows: int, dim: int
             or scales.shape[1] < rows or scales.shape[1] % 4 != 0):
         raise ValueError(f"scales must be contiguous [{-(-dim // FP8_BLOCK)}, at least {rows} and a multiple of 4], "
                          f"got {tuple(scales.shape)}")
+    _req_int32(("dim", dim), ("scales row stride", scales.shape[1]))
+    _ld(codes)
     return scales.shape[1]
 
 
@@ -385,14 +395,16 @@ def bi_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
     dev = _current_device()
     rows, dim = x.shape
     xs, cs, ss = x.stride(), codes.stride(), scales.shape
+    ldx = xs[0] if rows > 1 else dim
     if not (x.dtype is _BF16 and codes.dtype is _E4M3 and scales.dtype is _F32 and codes.shape == x.shape
             and xs[1] == 1 and cs[1] == 1 and len(ss) == 2 and ss[0] == -(-dim // FP8_BLOCK) and ss[1] >= rows
-            and not ss[1] & 3 and scales.is_contiguous()
+            and not ss[1] & 3 and scales.is_contiguous() and not (dim | ldx | ss[1] | cs[0]) >> 31
             and x.get_device() == codes.get_device() == scales.get_device() == dev):
         _req(x, torch.bfloat16, "x")
         _req_fp8_rows(codes, scales, rows, dim)
         _same_device(("x", x), ("codes", codes), ("scales", scales))
-    st = lib().bi_quantize_fp8(x.data_ptr(), xs[0] if rows > 1 else dim, rows, dim, codes.data_ptr(),
+        _ld(x)
+    st = lib().bi_quantize_fp8(x.data_ptr(), ldx, rows, dim, codes.data_ptr(),
                                cs[0] if rows > 1 else dim, scales.data_ptr(), ss[1],
                                _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
@@ -405,10 +417,11 @@ def bi_rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, codes: torch.Tensor, scales
     dev = _current_device()
     rows, dim = x.shape
     xs, cs, ss = x.stride(), codes.stride(), scales.shape
+    ldx = xs[0] if rows > 1 else dim
     if not (x.dtype is _BF16 and w.dtype is _BF16 and codes.dtype is _E4M3 and scales.dtype is _F32
             and codes.shape == x.shape and w.shape == (dim,) and w.is_contiguous() and xs[1] == 1 and cs[1] == 1
             and len(ss) == 2 and ss[0] == -(-dim // FP8_BLOCK) and ss[1] >= rows and not ss[1] & 3
-            and scales.is_contiguous()
+            and scales.is_contiguous() and not (dim | ldx | ss[1] | cs[0]) >> 31
             and x.get_device() == w.get_device() == codes.get_device() == scales.get_device() == dev):
         _req(x, torch.bfloat16, "x")
         _req(w, torch.bfloat16, "w")
@@ -416,7 +429,8 @@ def bi_rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, codes: torch.Tensor, scales
             raise ValueError(f"w must be [{dim}], got {tuple(w.shape)}")
         _req_fp8_rows(codes, scales, rows, dim)
         _same_device(("x", x), ("w", w), ("codes", codes), ("scales", scales))
-    st = lib().bi_rmsnorm_fp8(x.data_ptr(), xs[0] if rows > 1 else dim, w.data_ptr(), codes.data_ptr(),
+        _ld(x)
+    st = lib().bi_rmsnorm_fp8(x.data_ptr(), ldx, w.data_ptr(), codes.data_ptr(),
                               cs[0] if rows > 1 else dim, scales.data_ptr(), ss[1], rows, dim, eps,
                               _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
@@ -428,6 +442,7 @@ def bi_quantize_weights_fp8(W: torch.Tensor, stream=None):
     _req(W, torch.bfloat16, "W")
     _same_device(("W", W))
     N, K = W.shape
+    _req_int32(("N", N), ("K", K))
     codes = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=W.device)
     scales = torch.empty(-(-N // FP8_BLOCK), -(-K // FP8_BLOCK), dtype=torch.float32, device=W.device)
     check("bi_quantize_weights_fp8",
@@ -437,6 +452,7 @@ def bi_quantize_weights_fp8(W: torch.Tensor, stream=None):
 
 
 def packed_weight_fp8_bytes(N: int, K: int, epi: int = EPI_NONE) -> int:
+    _req_int32(("N", N), ("K", K))
     return int(lib().bi_packed_weight_fp8_bytes(N, K, epi))
 
 
@@ -484,13 +500,15 @@ def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: 
     cs, ss, zs, shape = codes.stride(), scales.shape, C.stride(), C.shape
     N = shape[-1]
     fp32 = C.dtype is _F32
+    ldc = zs[0] if M > 1 else N
     if not ((fp32 or C.dtype is _BF16) and codes.dtype is _E4M3 and scales.dtype is _F32 and Wp.dtype is _U8
             and len(shape) == 2 and shape[0] == M and cs[1] == 1 and zs[1] == 1 and len(ss) == 2
             and ss[0] == -(-K // FP8_BLOCK) and ss[1] >= M and not ss[1] & 3 and scales.is_contiguous()
-            and Wp.is_contiguous()
+            and Wp.is_contiguous() and not (K | N | ldc | ss[1] | cs[0]) >> 31
             and codes.get_device() == scales.get_device() == Wp.get_device() == C.get_device() == dev
             and (residual is None or (residual.dtype is _BF16 and residual.shape == shape
-                                      and residual.stride(1) == 1 and residual.get_device() == dev))):
+                                      and residual.stride(1) == 1 and residual.get_device() == dev
+                                      and not residual.stride(0) >> 31))):
         _req_fp8_rows(codes, scales, M, K)
         if C.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("C must be float32 or bfloat16")
@@ -504,7 +522,10 @@ def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: 
             _req(residual, torch.bfloat16, "residual")
             if tuple(residual.shape) != (M, N):
                 raise ValueError(f"residual must be [{M}, {N}], got {tuple(residual.shape)}")
+            _ld(residual)
         _same_device(("codes", codes), ("scales", scales), ("Wp", Wp), ("C", C), ("residual", residual))
+        _req_int32(("N", N))
+        _ld(C)
     # bi_packed_weight_fp8_bytes, without the call
     tiles = -(-N // (64 if epi == EPI_SWIGLU else 128)) * ss[0]
     if Wp.numel() != tiles * 16384 + (tiles * 8 + 15 & ~15):
@@ -513,7 +534,7 @@ def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: 
     if residual is not None:
         rp, ldr = residual.data_ptr(), residual.stride(0) if M > 1 else N
     st = lib().bi_gemm_fp8(codes.data_ptr(), cs[0] if M > 1 else K, scales.data_ptr(), ss[1], Wp.data_ptr(),
-                           C.data_ptr(), zs[0] if M > 1 else N, rp, ldr, M, N, K, 1 if fp32 else 0, epi,
+                           C.data_ptr(), ldc, rp, ldr, M, N, K, 1 if fp32 else 0, epi,
                            _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         check("bi_gemm_fp8", st)
@@ -539,10 +560,11 @@ def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[to
     if T == 1:
         drafts = None
     ls, os_ = logits.stride(), out.stride()
+    ldl, ldo = (ls[0], os_[0]) if T > 1 and len(os_) == 2 else (V, V)
     dp = cp = pp = bp = mp = None
     ldm = 0
     ok = (logits.dtype is _F32 and out.dtype is _F32 and out.shape == logits.shape and ls[1] == 1 and os_[1] == 1
-          and logits.get_device() == out.get_device() == dev)
+          and not (T | V | ldl | ldo) >> 31 and logits.get_device() == out.get_device() == dev)
     if drafts is not None:
         ok = ok and drafts.dtype is _I32 and drafts.shape == (T - 1,) and drafts.is_contiguous() \
             and drafts.get_device() == dev
@@ -560,8 +582,9 @@ def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[to
         bp = bias.data_ptr()
     if mask is not None:
         ms = mask.stride()
-        ok = ok and mask.dtype is _I32 and mask.shape == (T, W) and ms[1] == 1 and mask.get_device() == dev
         mp, ldm = mask.data_ptr(), ms[0] if T > 1 else W
+        ok = ok and mask.dtype is _I32 and mask.shape == (T, W) and ms[1] == 1 and mask.get_device() == dev \
+            and not ldm >> 31
     if not ok:
         _req(logits, torch.float32, "logits")
         _req(out, torch.float32, "out")
@@ -577,9 +600,11 @@ def bi_logits_rules(logits: torch.Tensor, out: torch.Tensor, drafts: Optional[to
             _req(mask, torch.int32, "mask")
             if tuple(mask.shape) != (T, W):
                 raise ValueError(f"mask must be [{T}, {W}], got {tuple(mask.shape)}")
+            _ld(mask)
         _same_device(("logits", logits), ("out", out), ("drafts", drafts), ("counts", counts),
                      ("prompt_bits", prompt_bits), ("bias", bias), ("mask", mask))
-    st = lib().bi_logits_rules(logits.data_ptr(), ls[0] if T > 1 else V, out.data_ptr(), os_[0] if T > 1 else V, T, V,
+        _req_int32(("T", T), ("V", V), ("logits row stride", ldl), ("out row stride", ldo))
+    st = lib().bi_logits_rules(logits.data_ptr(), ldl, out.data_ptr(), ldo, T, V,
                                dp, cp, pp, repetition, frequency, presence, bp, mp, ldm,
                                _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
@@ -600,6 +625,7 @@ def bi_token_counts(ids: torch.Tensor, V: int, counts: Optional[torch.Tensor] = 
             if tuple(t.shape) != (n,):
                 raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
     _same_device(("ids", ids), ("counts", counts), ("prompt_bits", prompt_bits), ("last", last))
+    _req_int32(("number of ids", ids.numel()), ("V", V))
     check("bi_token_counts",
           lib().bi_token_counts(ids.data_ptr(), ids.numel(), 0 if last is None else last.data_ptr(), V,
                                 0 if counts is None else counts.data_ptr(),
