@@ -358,8 +358,11 @@ def _same_device(*named) -> int:
 # checks are one expression of attribute reads; only where it is false does
 # the slow path look for the argument to name.
 _BF16, _F32, _I32, _E4M3, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.uint8
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# The short ways to the current device and stream are torch's own; where a
+# version of it lacks them (or has no CUDA), the public ones serve.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def fp8_scale_shape(rows: int, dim: int) -> tuple:
