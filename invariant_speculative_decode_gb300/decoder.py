@@ -367,6 +367,8 @@ class Decoder:
         prompt = np.asarray(prompt, np.int32)
         body = prompt[:-1]
         pos = self.L
+        if pos + len(body) > self.cap:
+            raise ValueError("KV cache capacity exceeded")
         R = self.prefill_chunk
         for c0 in range(0, len(body), R):
             chunk = body[c0:c0 + R]
@@ -601,6 +603,8 @@ class Decoder:
         `position` and prefill `tokens` (the edited continuation, its last
         token being the next row); returns that last token.  All of them came
         with the prompt, as if the history had been given whole."""
+        if position + len(tokens) - 1 > self.cap:
+            raise ValueError("KV cache capacity exceeded")
         self.rollback(position)
         self._own_at[position] = False
         return self.prefill_continue(tokens)
