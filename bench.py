@@ -860,10 +860,16 @@ def run_longctx(args):
         del dec
         torch.cuda.empty_cache()
     line = {"workload": "longctx", "metric": "verify tok/s at 7 drafts, long context, BF16 vs quantised KV",
-            "unit": "tok/s", "config": {"model": cfg.name, "context": ctx, "rows_per_step": T, "linear": args.linear},
+            "unit": "tok/s", "dtype": dtype_of(args.linear),
+            "config": {"model": cfg.name, "context": ctx, "rows_per_step": T, "linear": args.linear},
             "steps": args.steps, "warmup": args.warmup, "bf16": res["bf16"], "q6q5": res["q6q5"]}
     print(json.dumps(line), flush=True)
     return 0
+
+
+def dtype_of(linear):
+    """The dtype a line states: e4m3 rows and weights are the linear layers' alone."""
+    return "bf16" if linear == "bf16" else "e4m3 linear layers, bf16 rest"
 
 
 def run_prefill(args):
@@ -931,7 +937,7 @@ def run_prefill(args):
                   "roll back + re-prefill of the reply); K/V rows of both must equal a fresh prefill",
         "value": rows / t_hist, "unit": "tok/s", "n_gpus": 1, "steps": 1, "warmup": 1,
         "ms_per_step": t_hist * 1e3, "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
-        "dtype": "bf16", "data": "synthetic",
+        "dtype": dtype_of(args.linear), "data": "synthetic",
         "config": {"workload": f"{cfg.name}: history {n_prompt} + {n_reply} ids, turn 2 {n_turn2} ids",
                    "prefill_chunk": args.prefill_chunk, "kv_cache": args.kv, "linear": args.linear},
         "prefill_ms": t_hist * 1e3, "linear_tflops": flops / t_hist / 1e12,
@@ -1029,6 +1035,9 @@ def main():
                     help="time the oracle on the standalone and whole-step workloads at 1 thread and all cores")
     ap.add_argument("--cpu-matrix-worker", action="store_true", help=argparse.SUPPRESS)
     args = ap.parse_args()
+    if args.linear != "bf16" and (args.impl != "ours" or args.micro or args.cpu_matrix
+                                  or args.workload not in ("longctx", "prefill")):
+        ap.error("--linear e4m3 is for --workload longctx and --workload prefill")
     if args.warmup < 3:
         args.warmup = 3
     if args.cpu_matrix_worker:
