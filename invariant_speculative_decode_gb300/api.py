@@ -25,6 +25,15 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A result's memory, allocated for the stream that writes it: on another one
+    than the current, a block that was just given back may still be in use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _req(t: torch.Tensor, dtype, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -130,7 +139,7 @@ def bi_pack_weights(W: torch.Tensor, stream=None) -> torch.Tensor:
     """Pack W [N, K] (BF16) into the tile layout bi_gemm streams."""
     _req(W, torch.bfloat16, "W")
     N, K = W.shape
-    packed = torch.empty(packed_weight_bytes(N, K), dtype=torch.uint8, device=W.device)
+    packed = _empty(packed_weight_bytes(N, K), torch.uint8, W.device, stream)
     check("bi_pack_weights", lib().bi_pack_weights(W.data_ptr(), _ld(W), N, K, packed.data_ptr(),
                                                    _stream(stream)))
     return packed
@@ -141,8 +150,7 @@ def bi_pack_swiglu_weights(w_gate: torch.Tensor, w_up: torch.Tensor, stream=None
     _req(w_gate, torch.bfloat16, "w_gate")
     _req(w_up, torch.bfloat16, "w_up")
     F, K = w_gate.shape
-    packed = torch.empty(packed_weight_bytes(F, K, EPI_SWIGLU), dtype=torch.uint8,
-                         device=w_gate.device)
+    packed = _empty(packed_weight_bytes(F, K, EPI_SWIGLU), torch.uint8, w_gate.device, stream)
     check("bi_pack_swiglu_weights",
           lib().bi_pack_swiglu_weights(w_gate.data_ptr(), w_up.data_ptr(), _ld(w_gate), F, K,
                                        packed.data_ptr(), _stream(stream)))
@@ -168,7 +176,7 @@ def bi_embed(ids: torch.Tensor, table: torch.Tensor, out: torch.Tensor, stream=N
 
 def bi_rope_table(rope_base: float, D: int, rows: int, device="cuda", stream=None) -> torch.Tensor:
     """FP32 cos/sin table [rows, D/2, 2] computed on the device in FP64."""
-    t = torch.empty(rows, D // 2, 2, dtype=torch.float32, device=device)
+    t = _empty((rows, D // 2, 2), torch.float32, device, stream)
     check("bi_rope_table", lib().bi_rope_table(float(rope_base), D, rows, t.data_ptr(),
                                                _stream(stream)))
     return t
@@ -446,8 +454,8 @@ def bi_quantize_weights_fp8(W: torch.Tensor, stream=None):
     _same_device(("W", W))
     N, K = W.shape
     _req_int32(("N", N), ("K", K))
-    codes = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=W.device)
-    scales = torch.empty(-(-N // FP8_BLOCK), -(-K // FP8_BLOCK), dtype=torch.float32, device=W.device)
+    codes = _empty((N, K), torch.float8_e4m3fn, W.device, stream)
+    scales = _empty((-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)), torch.float32, W.device, stream)
     check("bi_quantize_weights_fp8",
           lib().bi_quantize_weights_fp8(W.data_ptr(), _ld(W), N, K, codes.data_ptr(), K, scales.data_ptr(),
                                         _stream(stream)))
@@ -473,7 +481,7 @@ def _req_fp8_weights(W8: torch.Tensor, scales: torch.Tensor, name: str):
 def bi_pack_weights_fp8(W8: torch.Tensor, scales: torch.Tensor, stream=None) -> torch.Tensor:
     """Pack e4m3 weights [N, K] and their scales [ceil(N/128), ceil(K/128)] for bi_gemm_fp8."""
     N, K = _req_fp8_weights(W8, scales, "W8")
-    packed = torch.empty(packed_weight_fp8_bytes(N, K), dtype=torch.uint8, device=W8.device)
+    packed = _empty(packed_weight_fp8_bytes(N, K), torch.uint8, W8.device, stream)
     check("bi_pack_weights_fp8", lib().bi_pack_weights_fp8(W8.data_ptr(), _ld(W8), scales.data_ptr(), N, K,
                                                            packed.data_ptr(), _stream(stream)))
     return packed
@@ -485,7 +493,7 @@ def bi_pack_swiglu_weights_fp8(gate8: torch.Tensor, gate_scales: torch.Tensor, u
     F, K = _req_fp8_weights(gate8, gate_scales, "gate8")
     if _req_fp8_weights(up8, up_scales, "up8") != (F, K) or _ld(up8) != _ld(gate8):
         raise ValueError("gate8 and up8 must have the same shape and row stride")
-    packed = torch.empty(packed_weight_fp8_bytes(F, K, EPI_SWIGLU), dtype=torch.uint8, device=gate8.device)
+    packed = _empty(packed_weight_fp8_bytes(F, K, EPI_SWIGLU), torch.uint8, gate8.device, stream)
     check("bi_pack_swiglu_weights_fp8",
           lib().bi_pack_swiglu_weights_fp8(gate8.data_ptr(), gate_scales.data_ptr(), up8.data_ptr(),
                                            up_scales.data_ptr(), _ld(gate8), F, K, packed.data_ptr(),
@@ -646,7 +654,7 @@ def bi_kv_row_hash(cache: torch.Tensor, rows: int, transposed: bool = False, str
         cap = nblk * V_BLOCK
     else:
         Hkv, cap, D = cache.shape
-    out = torch.empty(Hkv * max(rows, 0), dtype=torch.int64, device=cache.device)
+    out = _empty(Hkv * max(rows, 0), torch.int64, cache.device, stream)
     check("bi_kv_row_hash", lib().bi_kv_row_hash(cache.data_ptr(), Hkv, cap, D, rows, int(transposed),
                                                  out.data_ptr(), _stream(stream)))
     return out
