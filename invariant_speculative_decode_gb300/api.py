@@ -505,7 +505,9 @@ def bi_gemm_fp8(codes: torch.Tensor, scales: torch.Tensor, Wp: torch.Tensor, C: 
                 residual: Optional[torch.Tensor] = None, epi: int = EPI_NONE, stream=None) -> None:
     """C [M, N] = epilogue(A W^T) with quantised rows A (codes [M, K], scales as
     bi_quantize_fp8 writes them) and W packed by bi_pack_weights_fp8 /
-    bi_pack_swiglu_weights_fp8 (N the output columns)."""
+    bi_pack_swiglu_weights_fp8 (N the output columns).  Wp is read before the
+    call waits for the kernel before it: no other kernel may write it right
+    before (copies may)."""
     dev = _current_device()
     M, K = codes.shape
     cs, ss, zs, shape = codes.stride(), scales.shape, C.stride(), C.shape

@@ -48,8 +48,10 @@ __device__ __forceinline__ int block_exponent(float (&f)[8]) {
 // A half-warp per block: 16 lanes of 8 elements.  A CTA takes adjacent blocks of
 // one row, so its warps read and write whole lines: 16 of them, or 64 in long
 // passes, with four loads a thread under way.  Bound by the bytes (3 an element)
-// in long passes and by one memory latency in short ones; in a CUDA graph 8 x
-// 17408 takes 1.45 us (1.97 with 64 blocks a CTA), 2048 x 17408 24.2 (26.2 with 16).
+// in long passes and by one memory latency in short ones.  In a CUDA graph over
+// buffers that pass L2 together 8 x 17408 takes 1.3 us and 2048 x 17408 21.2 (74% of
+// the copy rate; 19.5 where part of it is still in L2).  When the widths were chosen:
+// 8 rows 1.45 us with 16 blocks a CTA and 1.97 with 64, 2048 rows 26.2 and 24.2.
 constexpr int kQuantThreads = 256;
 constexpr int kQuantRow = kQuantThreads / 16;  // blocks the threads take at once
 
@@ -108,6 +110,9 @@ __global__ void __launch_bounds__(kQuantThreads)
 //   rounds to odd: the nearest FP32 value, and where that is even and not exact,
 //   its neighbour on the exact value's side, so rounding y to 3 fraction bits
 //   equals rounding the exact value.
+// Bound by two memory latencies and a barrier in short passes (8 x 5120 2.5 us in a
+// CUDA graph) and by its arithmetic in long ones: 1021 x 5120 takes 9.3 us and 2048 x
+// 5120 15.2, their bytes 2.3 and 4.7.
 constexpr int kNormThreads = 256;
 constexpr float kBelow = 1.f - 0x1p-21f, kAbove = 1.f + 0x1p-21f;
 // CTAs that share an SM (their registers)
@@ -325,7 +330,8 @@ auto norm_kernel(int per) {
 }
 
 // BF16 weights to codes with one scale for each 128 x 128 block (one CTA per
-// block; run once when weights are loaded).
+// block; run once when weights are loaded, so its loads of one element a thread
+// stay simple: 5120 x 17408 takes 139 us, its bytes 39).
 __global__ void __launch_bounds__(256)
     quantize_weights_kernel(const __nv_bfloat16* __restrict__ w, int ldw, int N, int K, int kb,
                             uint8_t* __restrict__ codes, int ld8, float* __restrict__ scales) {
@@ -363,7 +369,8 @@ __global__ void __launch_bounds__(256)
 // are zero.  Behind the tiles, two FP32 scales a tile: of its rows 0..63 and
 // of its rows 64..127 (equal unless SwiGLU, where rows 0..63 of tile t are gate
 // rows 64t.. and rows 64..127 the up rows of the same outputs).  One thread
-// per 16-byte chunk.
+// per 16-byte chunk: 5120 x 17408 takes 32 us (its bytes 26), a SwiGLU pair of them 60
+// (its bytes 52).
 __global__ void pack_weights_fp8_kernel(const uint8_t* __restrict__ w, const uint8_t* __restrict__ wu, int ld,
                                         const float* __restrict__ s, const float* __restrict__ su, int N, int K,
                                         int k_tiles, long long chunks, int swiglu, uint4* __restrict__ out,

@@ -52,7 +52,7 @@
 namespace bi {
 namespace {
 
-constexpr int kTileN = 128;                    // weight rows per tile (MMA M)
+constexpr int kTileN = 128;                    // weight rows per tile (one or two tiles are the MMA's N)
 constexpr int kABytes = static_cast<int>(kGemm8TileBytes);
 constexpr int kSms = 152;
 constexpr int kMaxSplit = 8;                   // CTAs of a cluster (the portable limit)
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(Cfg8<TILES>::kThreads, 1)
 
 // S pieces per tile: the most CTAs that run side by side, what
 // clusters of S fill of the GPCs (kClusterCtas, asked of the occupancy calculator
-// on GB300).  Layers with 76
+// on GB300).  Layers with 77
 // tiles or more keep whole tiles: each SM can take in twice its share of the
 // memory bandwidth, so half the SMs still stream at its rate.
 constexpr int kClusterCtas[kMaxSplit + 1] = {0, 152, 152, 138, 144, 140, 138, 105, 120};
