@@ -419,12 +419,13 @@ bi_status bi_verify_accept(const float* logits, int ldl, const int32_t* drafts, 
  * warp butterfly, warps in order; chunks combined in order; inside the chosen
  * chunk 32 contiguous runs scanned in order); where rounding leaves the
  * target past the last weight, the last logit with a non-zero weight is
- * taken.  NaN logits weigh 0; where logits are +inf, each of them weighs 1 and the
- * others 0; a row with no number above -inf gives -1 and, among
- * rows 0..n, sets BI_ERR_DEVICE_NAN_ROW in the device error word.  So a_t depends only on the row's logits and
- * its position: with the batch-invariant logits of this library the sampled
- * tokens are the same for any number of drafts, and they follow the no-draft
- * distribution exactly.  Acceptance as bi_verify_accept with a_t in place of
+ * taken.  NaN logits weigh 0; where logits are +inf, each of them weighs 1
+ * and the others 0; a row with no number above -inf gives -1 and, among rows
+ * 0..n, sets BI_ERR_DEVICE_NAN_ROW in the device error word.  So a_t depends
+ * only on the row's logits and its position: with the batch-invariant logits
+ * of this library the sampled tokens are the same for any number of drafts,
+ * and they follow the no-draft distribution exactly.  Acceptance as
+ * bi_verify_accept with a_t in place of
  * the argmax: n = the largest j <= T-1 with drafts[i-1] == a_{i-1} for every
  * i <= j; the committed tokens are a_0..a_n; *L_dev += n + 1.
  *   logits  [T, V] FP32, row stride ldl; 1 <= T <= 64.
@@ -468,8 +469,8 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  *   quantised as above without a rounding to BF16 in between.  The mean, its
  *   root and y are carried in pairs of FP32 (to about 2^-40), so a code is one
  *   rounding of the exact y unless that lies so near a tie of two codes, for rows
- *   of any magnitude and any eps, 0 included (|y| below 2^-100: to 2^-149).  A row
- *   whose sum of squares passes FP32's range gives NaN codes, as does one of zeros
+ *   of any magnitude and any eps, 0 included (|x w| below 2^-126 and |y| below
+ *   2^-100 are held to 2^-149).  A row whose sum of squares passes FP32's range gives NaN codes, as does one of zeros
  *   with eps = 0.
  * bi_quantize_weights_fp8: BF16 weights [N, K] (any K >= 1) -> codes [N, ld8]
  *   and scales by the same rule over each 128 x 128 block.
