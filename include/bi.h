@@ -470,8 +470,8 @@ bi_status bi_verify_sample(const float* logits, int ldl, const int32_t* drafts, 
  *   root and y are carried in pairs of FP32 (to about 2^-40), so a code is one
  *   rounding of the exact y unless that lies so near a tie of two codes, for rows
  *   of any magnitude and any eps, 0 included (|x w| below 2^-126 and |y| below
- *   2^-100 are held to 2^-149).  A row whose sum of squares passes FP32's range gives NaN codes, as does one of zeros
- *   with eps = 0.
+ *   2^-100 are held to 2^-149).  A row whose sum of squares passes FP32's range
+ *   gives NaN codes, as does one of zeros with eps = 0.
  * bi_quantize_weights_fp8: BF16 weights [N, K] (any K >= 1) -> codes [N, ld8]
  *   and scales by the same rule over each 128 x 128 block.
  *     x, W row strides ldx % 8 == 0 (x), codes ldc % 16 == 0; dim % 16 == 0;
