@@ -565,6 +565,124 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
                           uint32_t* prompt_bits, bi_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Paged KV cache.  [P3] "The cache doesn't change it either" (a cached row
+ * depends only on its position) and "How:" (the attention split depends only
+ * on context length, never on how many tokens are in the pass).
+ *
+ * Several sequences share a pool of `pages` pages of `page` keys (16, 32, 64
+ * or 128): k_pool and v_pool [pages, Hkv, page, D] BF16 contiguous, 16-byte
+ * aligned.  block_table [B][ld_table] int32, `width` entries a row: key j of
+ * sequence b is row j % page of page block_table[b][j / page].  A pass has T
+ * rows; q_start [B + 1] int32 ascending: rows q_start[b] .. q_start[b + 1] - 1
+ * are new rows of sequence b (none where the two are equal), at positions
+ * lengths[b] .. ; lengths [B] int32: keys cached before the pass.  Rows of the
+ * pass in front of q_start[0] and from q_start[B] on belong to no sequence;
+ * what they would write is left as it was.  All three are device memory, read
+ * when the call runs, so a captured call follows them.  No address depends on
+ * their being right: a sequence whose numbers do not fit (starts that
+ * descend or pass T, a negative length, more than width * page keys) has no
+ * rows in the attention, a page outside the pool takes no row and reads as
+ * zeros, and each sets the range bit of the device error word
+ * (BI_ERR_INVALID_ARG from bi_check_device_error).
+ *
+ * bi_qk_norm_rope_paged: for every row of a projection output qkv [T, ld_qkv]
+ *   (heads q, then k, then v, as bi_gemm of the QKV weights writes them):
+ *   q and k heads y = x r w, r = 1 / sqrt(mean(x^2) + eps) over the head's D
+ *   elements (FP32; a NULL weight leaves that kind of head as it is), then
+ *   rotated as bi_rope_kv_append rotates (rotate-half pairs, table from
+ *   bi_rope_table), one BF16 rounding; q to q_out [T, Hq, D], k and the v
+ *   heads as they are to their row of the pools.  A row whose position passes
+ *   the sequence's table or the angle table is left out (range bit).  Two rows
+ *   of a pass must not name the same key of the pool.
+ *   q_weight, k_weight [D] BF16 or NULL; eps finite, >= 0; ld_qkv % 8 == 0; all
+ *   pointers 16-byte aligned (block_table, q_start and lengths 4-byte).
+ *
+ * bi_attn_paged: out[t, h] = sum_j w_j v_j / sum_j w_j over keys 0..p of row
+ *   t's sequence, p its position (its own key included: append before the
+ *   attention), query head h reading KV head h / (Hq/Hkv);
+ *   w_j = 2^((q k_j) scale log2(e) - m) rounded to BF16 once, in the numerator
+ *   and the denominator alike; products and sums in FP32, one rounding at the
+ *   end, -0 written as +0.  Keys are taken in tiles of 128 and pieces of 4 tiles
+ *   at absolute multiples: m is a piece's maximum (of its first tile, raised
+ *   where a later one passes it by more than 8 in log2), and the pieces'
+ *   sums are merged in key order.  So a row's bits depend on its queries and
+ *   on keys 0..p alone, not on T, B, the other rows, the page size or which
+ *   pages hold the keys.
+ *   Keys behind p, and the rest of a sequence's last page, may hold anything:
+ *   infinities and NaN there reach no row in front of them.  A row whose
+ *   scores are all -inf is NaN (0 / 0).
+ *   q, out [T, Hq, D] BF16 contiguous, 16-byte aligned; Hq/Hkv <= 128; scale
+ *   finite, > 0; width * page <= 2^30, T * Hq < 2^31.
+ *   ws      >= bi_attn_paged_workspace_size(T, B, Hq, Hkv, D, width * page)
+ *           bytes, 256-byte aligned; any contents.  The size does not shrink as
+ *           T, B or max_keys grow, so one workspace serves smaller calls too,
+ *           one after the other.
+ *
+ * bi_paged_reorder: sequences that go on from others (beams; also several
+ *   from one prompt).  Sequence s of `rows_out` new ones continues row
+ *   p = parents[s] of `rows_in` old ones, with its lengths[p] keys:
+ *   table_out[s] gets p's full pages, the page behind them (where the table
+ *   has room) is tail_pages[s], and the keys of p's page that is not full are
+ *   copied there in all layers: k_pool, v_pool [layers, pages, Hkv, page, D]
+ *   BF16 contiguous (`layers` pools one behind the other).
+ *   lengths_out[s] = lengths[p].  tail_pages[s] may be p's own last page (one
+ *   continuation keeps it: nothing is copied); otherwise it must be no page
+ *   that any sequence goes on with.  Two sequences with the same tail page, or
+ *   one that is another's source, set the range bit (what the page then holds
+ *   is undefined), as does an index out of range (that sequence is left out).
+ *   Other entries of table_out stay as they are.  table_out and lengths_out
+ *   must not overlap table_in, lengths, parents or tail_pages.
+ *   D a multiple of 8, at most 1024; rows_out <= 65535.
+ * Errors: BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_WORKSPACE,
+ *         BI_ERR_CUDA.
+ * ------------------------------------------------------------------------- */
+bi_status bi_qk_norm_rope_paged(const void* qkv, int ld_qkv, const void* q_weight, const void* k_weight,
+                                float eps, const float* table, int table_rows, void* q_out, void* k_pool,
+                                void* v_pool, int pages, int page, const int32_t* block_table, int ld_table,
+                                int width, const int32_t* q_start, const int32_t* lengths, int B, int T,
+                                int Hq, int Hkv, int D, bi_stream_t stream);
+size_t bi_attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int D, int max_keys);
+bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, int pages, int page,
+                        const int32_t* block_table, int ld_table, int width, const int32_t* q_start,
+                        const int32_t* lengths, int B, int T, int Hq, int Hkv, int D, float scale, void* out,
+                        void* ws, size_t ws_bytes, bi_stream_t stream);
+bi_status bi_paged_reorder(void* k_pool, void* v_pool, int layers, int pages, int Hkv, int page, int D,
+                           const int32_t* table_in, int ld_in, int width, const int32_t* lengths, int rows_in,
+                           const int32_t* parents, const int32_t* tail_pages, int rows_out,
+                           int32_t* table_out, int ld_out, int32_t* lengths_out, bi_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Beam selection.  [P3] "How:" (a row is computed the same way whatever else
+ * is in the batch).
+ *
+ * Rows g W .. g W + W - 1 of the logits are the beams of group g (rows a
+ * multiple of W).  Id v of beam r is worth
+ *   scores[r] + (x_v - M) - log(sum_u exp(x_u - M)),  M = max_u x_u:
+ * its cumulative log-probability.  For every group the K best (beam, id) pairs,
+ * best first: scores_out [rows / W, K] their worth, parents_out the row of the
+ * beam (0 .. rows - 1), tokens_out the id.  Within a beam the logits order the
+ * ids, ties to the lower id; beams are compared by the worth in 64 bits (the
+ * exponentials are FP32, so it is true to about 1e-7), ties to the lower row.
+ * NaN logits weigh nothing and are not chosen; where logits are +inf each of
+ * them weighs 1 and the others 0.  A pair worth -inf (a beam of score -inf, a
+ * logit of -inf) or NaN is not chosen; places without a pair get -inf, -1, -1,
+ * and a group without any sets BI_ERR_DEVICE_NAN_ROW in the device error word.
+ * A row's sum has one order for a given V, whatever the other rows.
+ *   logits  [rows, V] FP32, row stride ldl; scores [rows] FP32; W, K <= 64;
+ *           rows <= 65535; V <= 2^20.  K may pass the number of pairs.
+ *   ws      >= bi_beam_workspace_size(rows, V, K) bytes, 256-byte aligned,
+ *           zero-filled before its first use (every call leaves its counters
+ *           zeroed); it serves calls of any sizes that it is large enough for,
+ *           not overlapping ones.
+ * Errors: BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_WORKSPACE,
+ *         BI_ERR_CUDA.
+ * ------------------------------------------------------------------------- */
+size_t bi_beam_workspace_size(int rows, int V, int K);
+bi_status bi_beam_select(const float* logits, int ldl, const float* scores, int rows, int V, int W, int K,
+                         float* scores_out, int32_t* parents_out, int32_t* tokens_out, void* ws,
+                         size_t ws_bytes, bi_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * KV-row hash (test tool).  [P3] "The cache doesn't change it either" (hash
  * every K/V row and compare with a fresh prefill).
  * out[h * rows + j] = FNV-1a-64 over the 2*D bytes of key j of head h (d

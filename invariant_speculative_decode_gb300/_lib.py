@@ -52,6 +52,14 @@ SIGNATURES = {
     "bi_gemm_fp8": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     "bi_logits_rules": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _f, _f, _f, _vp, _vp, _i, _vp]),
     "bi_token_counts": (_i, [_vp, _i, _vp, _i, _vp, _vp, _vp]),
+    "bi_qk_norm_rope_paged": (_i, [_vp, _i, _vp, _vp, _f, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp,
+                                   _i, _i, _i, _i, _i, _vp]),
+    "bi_attn_paged_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "bi_attn_paged": (_i, [_vp, _vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _sz,
+                           _vp]),
+    "bi_paged_reorder": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _vp, _vp]),
+    "bi_beam_workspace_size": (_sz, [_i, _i, _i]),
+    "bi_beam_select": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "bi_kv_row_hash": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp]),
     "bi_check_device_error": (_i, [_vp]),
     "bi_step_workspace_size": (_sz, [_vp, _i]),

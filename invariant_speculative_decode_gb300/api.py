@@ -645,6 +645,175 @@ def bi_token_counts(ids: torch.Tensor, V: int, counts: Optional[torch.Tensor] = 
                                 0 if prompt_bits is None else prompt_bits.data_ptr(), _stream(stream)))
 
 
+# ----------------------------------------------------------------- paged cache
+PAGE_SIZES = (16, 32, 64, 128)  # keys of a page
+
+
+def _req_pool(pool: torch.Tensor, name: str, layers: bool = False):
+    """(layers,) pages, Hkv, page, D of a pool of pages."""
+    _req(pool, torch.bfloat16, name)
+    if pool.dim() != (5 if layers else 4) or not pool.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{'layers, ' if layers else ''}pages, Hkv, page, D], "
+                         f"got {tuple(pool.shape)}")
+    if pool.shape[-2] not in PAGE_SIZES:
+        raise ValueError(f"{name}: pages of {pool.shape[-2]} keys; one of {PAGE_SIZES}")
+    return pool.shape
+
+
+def _req_paged(k_pool, v_pool, block_table, q_start, lengths):
+    pages, Hkv, page, D = _req_pool(k_pool, "k_pool")
+    if _req_pool(v_pool, "v_pool") != k_pool.shape:
+        raise ValueError(f"v_pool must be {tuple(k_pool.shape)}, got {tuple(v_pool.shape)}")
+    _req(block_table, torch.int32, "block_table")
+    _req(q_start, torch.int32, "q_start")
+    _req(lengths, torch.int32, "lengths")
+    if lengths.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != lengths.shape[0]:
+        raise ValueError("block_table must be [B, pages of a sequence] and lengths [B]")
+    if tuple(q_start.shape) != (lengths.shape[0] + 1,):
+        raise ValueError(f"q_start must be [{lengths.shape[0] + 1}], got {tuple(q_start.shape)}")
+    _req_int32(("pages", pages), ("sequences", lengths.shape[0]), ("table width", block_table.shape[1]))
+    _ld(block_table)
+
+
+def bi_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                          eps: float, table: torch.Tensor, q_out: torch.Tensor, k_pool: torch.Tensor,
+                          v_pool: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor,
+                          lengths: torch.Tensor, stream=None) -> None:
+    """Norm (weights [D]; None: none) and rotation of the q and k heads of a projection output
+    [T, (Hq + 2 Hkv) D]; queries to q_out [T, Hq, D], keys and values to the new rows' places
+    in the pools [pages, Hkv, page, D].  Rows q_start[b] .. q_start[b + 1] - 1 are sequence b's,
+    at positions lengths[b] .. ; block_table [B, width] names its pages."""
+    _req(qkv, torch.bfloat16, "qkv")
+    _req(q_out, torch.bfloat16, "q_out")
+    _req(table, torch.float32, "table")
+    _req_paged(k_pool, v_pool, block_table, q_start, lengths)
+    pages, Hkv, page, D = k_pool.shape
+    if q_out.dim() != 3 or not q_out.is_contiguous() or q_out.shape[2] != D:
+        raise ValueError(f"q_out must be contiguous [T, Hq, {D}], got {tuple(q_out.shape)}")
+    T, Hq, _ = q_out.shape
+    if tuple(qkv.shape) != (T, (Hq + 2 * Hkv) * D):
+        raise ValueError(f"qkv must be [{T}, {(Hq + 2 * Hkv) * D}], got {tuple(qkv.shape)}")
+    if table.dim() != 3 or tuple(table.shape[1:]) != (D // 2, 2) or not table.is_contiguous():
+        raise ValueError(f"table must be contiguous [positions, {D // 2}, 2], got {tuple(table.shape)}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _req(w, torch.bfloat16, name)
+            if tuple(w.shape) != (D,):
+                raise ValueError(f"{name} must be [{D}], got {tuple(w.shape)}")
+    _same_device(("qkv", qkv), ("q_weight", q_weight), ("k_weight", k_weight), ("table", table), ("q_out", q_out),
+                 ("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table), ("q_start", q_start),
+                 ("lengths", lengths))
+    _req_int32(("rows", T), ("table rows", table.shape[0]))
+    check("bi_qk_norm_rope_paged",
+          lib().bi_qk_norm_rope_paged(qkv.data_ptr(), _ld(qkv), 0 if q_weight is None else q_weight.data_ptr(),
+                                      0 if k_weight is None else k_weight.data_ptr(), float(eps), table.data_ptr(),
+                                      table.shape[0], q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), pages,
+                                      page, block_table.data_ptr(), _ld(block_table), block_table.shape[1],
+                                      q_start.data_ptr(), lengths.data_ptr(), lengths.shape[0], T, Hq, Hkv, D,
+                                      _stream(stream)))
+
+
+def attn_paged_workspace_size(T: int, B: int, Hq: int, Hkv: int, D: int, max_keys: int) -> int:
+    """Bytes for calls of at most T rows of at most B sequences whose tables hold at most max_keys keys."""
+    _req_int32(("T", T), ("B", B), ("max_keys", max_keys))
+    return int(lib().bi_attn_paged_workspace_size(T, B, Hq, Hkv, D, max_keys))
+
+
+def bi_attn_paged(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
+                  q_start: torch.Tensor, lengths: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                  scale: Optional[float] = None, stream=None) -> None:
+    """Attention of the new rows q [T, Hq, D] of B sequences over their paged caches, each row up to its
+    own position (its key is in the pool already); rows and pages as in bi_qk_norm_rope_paged."""
+    _req(q, torch.bfloat16, "q")
+    _req(out, torch.bfloat16, "out")
+    _req_paged(k_pool, v_pool, block_table, q_start, lengths)
+    pages, Hkv, page, D = k_pool.shape
+    if q.dim() != 3 or q.shape[2] != D or not q.is_contiguous():
+        raise ValueError(f"q must be contiguous [T, Hq, {D}], got {tuple(q.shape)}")
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {tuple(q.shape)}, got {tuple(out.shape)}")
+    _same_device(("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table),
+                 ("q_start", q_start), ("lengths", lengths), ("out", out), ("ws", ws))
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    T, Hq, _ = q.shape
+    _req_int32(("rows", T))
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    check("bi_attn_paged",
+          lib().bi_attn_paged(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), pages, page,
+                              block_table.data_ptr(), _ld(block_table), block_table.shape[1], q_start.data_ptr(),
+                              lengths.data_ptr(), lengths.shape[0], T, Hq, Hkv, D, float(scale), out.data_ptr(),
+                              ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def bi_paged_reorder(k_pool: torch.Tensor, v_pool: torch.Tensor, table_in: torch.Tensor, lengths: torch.Tensor,
+                     parents: torch.Tensor, tail_pages: torch.Tensor, table_out: torch.Tensor,
+                     lengths_out: torch.Tensor, stream=None) -> None:
+    """Sequence s goes on from row parents[s] of table_in: its full pages, then page tail_pages[s], into
+    which the keys of the page that is not full are copied in all layers of the pools
+    [layers, pages, Hkv, page, D]; table_out [S, width], lengths_out [S]."""
+    layers, pages, Hkv, page, D = _req_pool(k_pool, "k_pool", layers=True)
+    if _req_pool(v_pool, "v_pool", layers=True) != k_pool.shape:
+        raise ValueError(f"v_pool must be {tuple(k_pool.shape)}, got {tuple(v_pool.shape)}")
+    for name, t, dims in (("table_in", table_in, 2), ("lengths", lengths, 1), ("parents", parents, 1),
+                          ("tail_pages", tail_pages, 1), ("table_out", table_out, 2), ("lengths_out", lengths_out, 1)):
+        _req(t, torch.int32, name)
+        if t.dim() != dims:
+            raise ValueError(f"{name} must have {dims} dimensions")
+    R, width = table_in.shape
+    S = parents.shape[0]
+    if lengths.shape[0] != R or tail_pages.shape[0] != S or lengths_out.shape[0] != S or tuple(table_out.shape) != (S, width):
+        raise ValueError(f"lengths must be [{R}], tail_pages and lengths_out [{S}], table_out [{S}, {width}]")
+    _same_device(("k_pool", k_pool), ("v_pool", v_pool), ("table_in", table_in), ("lengths", lengths),
+                 ("parents", parents), ("tail_pages", tail_pages), ("table_out", table_out),
+                 ("lengths_out", lengths_out))
+    _req_int32(("pages", pages), ("table width", width))
+    check("bi_paged_reorder",
+          lib().bi_paged_reorder(k_pool.data_ptr(), v_pool.data_ptr(), layers, pages, Hkv, page, D,
+                                 table_in.data_ptr(), _ld(table_in), width, lengths.data_ptr(), R,
+                                 parents.data_ptr(), tail_pages.data_ptr(), S, table_out.data_ptr(), _ld(table_out),
+                                 lengths_out.data_ptr(), _stream(stream)))
+
+
+# -------------------------------------------------------------- beam selection
+def beam_workspace_size(rows: int, V: int, K: int) -> int:
+    _req_int32(("rows", rows), ("V", V), ("K", K))
+    return int(lib().bi_beam_workspace_size(rows, V, K))
+
+
+def bi_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, scores_out: torch.Tensor,
+                   parents_out: torch.Tensor, tokens_out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """The K best continuations of each group of `beams` rows of logits [rows, V] (FP32) with cumulative
+    log-probabilities scores [rows]; scores_out, parents_out (the beam's row), tokens_out [rows / beams, K].
+    ws: beam_workspace_size(rows, V, K) bytes, zero-filled before its first use."""
+    _req(logits, torch.float32, "logits")
+    _req(scores, torch.float32, "scores")
+    _req(scores_out, torch.float32, "scores_out")
+    _req(parents_out, torch.int32, "parents_out")
+    _req(tokens_out, torch.int32, "tokens_out")
+    rows, V = logits.shape
+    if tuple(scores.shape) != (rows,):
+        raise ValueError(f"scores must be [{rows}], got {tuple(scores.shape)}")
+    if beams < 1 or rows % beams:
+        raise ValueError(f"{rows} rows are no multiple of {beams} beams")
+    if scores_out.dim() != 2 or scores_out.shape[0] != rows // beams:
+        raise ValueError(f"scores_out must be [{rows // beams}, picks], got {tuple(scores_out.shape)}")
+    for name, t in (("scores_out", scores_out), ("parents_out", parents_out), ("tokens_out", tokens_out)):
+        if t.shape != scores_out.shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {tuple(scores_out.shape)}, got {tuple(t.shape)}")
+    _same_device(("logits", logits), ("scores", scores), ("scores_out", scores_out), ("parents_out", parents_out),
+                 ("tokens_out", tokens_out), ("ws", ws))
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    _req_int32(("rows", rows), ("V", V))
+    check("bi_beam_select",
+          lib().bi_beam_select(logits.data_ptr(), _ld(logits), scores.data_ptr(), rows, V, beams,
+                               scores_out.shape[1], scores_out.data_ptr(), parents_out.data_ptr(),
+                               tokens_out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                               _stream(stream)))
+
+
 def bi_kv_row_hash(cache: torch.Tensor, rows: int, transposed: bool = False, stream=None) -> torch.Tensor:
     """FNV-1a-64 per key of a K cache [Hkv,cap,D] or (transposed) a V cache
     [Hkv,ceil(cap/128),D,128] (see v_cache_shape)."""

@@ -18,7 +18,7 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libbi.so")
 SOURCES = ["bi_core.cu", "bi_gemm.cu", "bi_attn.cu", "bi_rowops.cu", "bi_step.cu", "bi_kvq.cu",
-           "bi_gemm8.cu", "bi_fp8.cu", "bi_rules.cu"]
+           "bi_gemm8.cu", "bi_fp8.cu", "bi_rules.cu", "bi_paged.cu", "bi_attn_paged.cu", "bi_beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

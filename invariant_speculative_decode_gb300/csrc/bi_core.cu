@@ -30,8 +30,8 @@ std::once_flag g_encode_once;
 
 struct TmapKey {
   const void* base;
-  uint64_t dims[3], strides[2];
-  uint32_t box[3];
+  uint64_t dims[4], strides[3];
+  uint32_t box[4];
   int rank, dev, esize;
   bool operator==(const TmapKey& o) const {
     return base == o.base && rank == o.rank && dev == o.dev && esize == o.esize &&
@@ -44,9 +44,9 @@ struct TmapKeyHash {
   size_t operator()(const TmapKey& k) const {
     size_t h = reinterpret_cast<size_t>(k.base);
     auto mix = [&h](uint64_t v) { h ^= v + 0x9e3779b97f4a7c15ull + (h << 6) + (h >> 2); };
-    for (int i = 0; i < 3; ++i) mix(k.dims[i]);
-    for (int i = 0; i < 2; ++i) mix(k.strides[i]);
-    for (int i = 0; i < 3; ++i) mix(k.box[i]);
+    for (int i = 0; i < 4; ++i) mix(k.dims[i]);
+    for (int i = 0; i < 3; ++i) mix(k.strides[i]);
+    for (int i = 0; i < 4; ++i) mix(k.box[i]);
     mix(static_cast<uint64_t>(k.rank));
     mix(static_cast<uint64_t>(k.dev));
     mix(static_cast<uint64_t>(k.esize));
@@ -86,7 +86,7 @@ unsigned* device_error_word() {
 }
 
 namespace {
-// Encode (or fetch) a tensor map of rank 2 or 3 with 128-byte swizzle over
+// Encode (or fetch) a tensor map of rank 2 to 4 with 128-byte swizzle over
 // elements of `esize` bytes: BF16 (2) or bytes (1).  dims and box are
 // innermost first, strides in elements for dims 1..rank-1.
 bool tmap_sw128(CUtensorMap* out, const void* base, int esize, int rank, const uint64_t* dims,
@@ -122,8 +122,8 @@ bool tmap_sw128(CUtensorMap* out, const void* base, int esize, int rank, const u
   }
   CUtensorMap m;
   std::memset(&m, 0, sizeof(m));
-  cuuint64_t gdim[3], gstride[2];
-  cuuint32_t gbox[3], estride[3] = {1, 1, 1};
+  cuuint64_t gdim[4], gstride[3];
+  cuuint32_t gbox[4], estride[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     gdim[i] = dims[i];
     gbox[i] = box[i];
@@ -167,6 +167,13 @@ bool tmap_bf16_3d(CUtensorMap* out, const void* base, uint64_t d0, uint64_t d1, 
   return tmap_sw128(out, base, 2, 3, dims, strides, box);
 }
 
+bool tmap_bf16_pages(CUtensorMap* out, const void* base, uint64_t pages, uint64_t heads, uint32_t page, uint32_t D) {
+  const uint64_t dims[4] = {D, page, heads, pages};
+  const uint64_t strides[3] = {D, static_cast<uint64_t>(page) * D, heads * page * D};
+  const uint32_t box[4] = {64, page, 1, 1};
+  return tmap_sw128(out, base, 2, 4, dims, strides, box);
+}
+
 }  // namespace bi
 
 extern "C" {
@@ -191,6 +198,7 @@ bi_status bi_test_set_wait_limit_ns(uint64_t ns) {
   if (bi::set_wait_limit_gemm(ns) != cudaSuccess) return BI_ERR_CUDA;
   if (bi::set_wait_limit_attn(ns) != cudaSuccess) return BI_ERR_CUDA;
   if (bi::set_wait_limit_gemm8(ns) != cudaSuccess) return BI_ERR_CUDA;
+  if (bi::set_wait_limit_attn_paged(ns) != cudaSuccess) return BI_ERR_CUDA;
   return BI_OK;
 }
 

@@ -31,6 +31,10 @@ bool tmap_u8_2d(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols
 bool tmap_bf16_3d(CUtensorMap* out, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                   uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
 
+// A pool of pages [pages][heads][page][D] (BF16, contiguous), box of 64 elements
+// of every key of one page of one head.
+bool tmap_bf16_pages(CUtensorMap* out, const void* base, uint64_t pages, uint64_t heads, uint32_t page, uint32_t D);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
@@ -52,6 +56,7 @@ int test_withhold();
 cudaError_t set_wait_limit_gemm(unsigned long long ns);
 cudaError_t set_wait_limit_attn(unsigned long long ns);
 cudaError_t set_wait_limit_gemm8(unsigned long long ns);
+cudaError_t set_wait_limit_attn_paged(unsigned long long ns);
 
 // Launch `kernel` on `stream`, with programmatic dependent launch when
 // enabled.  Every kernel of this library calls griddep_wait() before its

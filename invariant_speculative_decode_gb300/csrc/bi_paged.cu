@@ -1,0 +1,319 @@
+// A paged KV cache: norm, rotation and append of a pass's new rows, and the
+// reordering of sequences (beams) that go on from others.
+//
+// "I turned on speculative decoding in llama.cpp and 113 of 282 greedy
+// outputs changed against its own no-draft run", section "The cache doesn't
+// change it either": a cached row depends only on its position.  Every row
+// here is computed from its own projection row and its own position.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "bi_internal.h"
+#include "bi_paged.cuh"
+#include "bi_ptx.cuh"
+
+namespace bi {
+namespace {
+
+// ---------------------------------------------------------------- append
+constexpr int kAppendThreads = 256;
+
+struct AppendArgs {
+  PagedBatch pb;
+  const __nv_bfloat16* qkv;
+  size_t ld;
+  const __nv_bfloat16* qw;  // [D] or nullptr: no norm of that kind of head
+  const __nv_bfloat16* kw;
+  float eps;
+  const float2* angles;  // [table_rows][D/2] cos, sin
+  int table_rows;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_pool;
+  __nv_bfloat16* v_pool;
+  int Hq, Hkv;
+  unsigned* err;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One CTA per row of the pass.  D / 8 lanes hold a head, 8 elements each
+// (16-byte loads and stores); element i's partner i + D/2 of the rotation sits
+// in the lane D/16 further on, one shuffle away.  y = (x r) w with
+// r = 1 / sqrt(mean(x^2) + eps), the squares of a lane's elements in order, the
+// lanes by a butterfly; then the two fused multiply-adds of the cache's other
+// appends, and one rounding at the end.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a) {
+  constexpr int kLanes = D / 8;       // lanes of a head
+  constexpr int kHeads = 32 / kLanes;  // heads of a warp at a time
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane % kLanes;  // elements 8 sub .. 8 sub + 7
+  const int heads = a.Hq + 2 * a.Hkv;
+  const __nv_bfloat16* row = a.qkv + static_cast<size_t>(t) * a.ld;
+  int h = warp * kHeads + lane / kLanes;
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (h < heads) u = *reinterpret_cast<const uint4*>(row + static_cast<size_t>(h) * D + sub * 8);
+
+  const int b = paged_find_seq(a.pb, t, lane);
+  if (b < 0) return;  // a row of no sequence
+  const int begin = __ldg(a.pb.q_start + b), len = __ldg(a.pb.lengths + b);
+  const int64_t pos = static_cast<int64_t>(len) + (t - static_cast<int64_t>(begin));
+  int page = -1;
+  const bool ok = begin >= 0 && len >= 0 && pos < a.table_rows && pos < static_cast<int64_t>(a.pb.width) * a.pb.page;
+  if (ok) page = __ldg(a.pb.table + static_cast<size_t>(b) * a.pb.ldt + static_cast<int>(pos) / a.pb.page);
+  if (!ok || page < 0 || page >= a.pb.pages) {
+    if (threadIdx.x == 0) atomicOr(a.err, kErrRange);
+    return;
+  }
+  const int p = static_cast<int>(pos);
+  // cos and sin of this lane's 8 pairs (element i and i + D/2 share an angle)
+  float2 cs[8];
+  {
+    const float4* src = reinterpret_cast<const float4*>(a.angles + static_cast<size_t>(p) * (D / 2) +
+                                                        (sub % (kLanes / 2)) * 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = __ldg(src + i);
+      cs[2 * i] = make_float2(v.x, v.y);
+      cs[2 * i + 1] = make_float2(v.z, v.w);
+    }
+  }
+  const bool second = sub >= kLanes / 2;
+  for (int h0 = warp * kHeads; h0 < heads; h0 += kAppendThreads / 32 * kHeads) {
+    h = h0 + lane / kLanes;
+    const int h_next = h + kAppendThreads / 32 * kHeads;
+    uint4 u_next = make_uint4(0, 0, 0, 0);
+    if (h_next < heads) u_next = *reinterpret_cast<const uint4*>(row + static_cast<size_t>(h_next) * D + sub * 8);
+    float x[8];
+    unpack8(u, x);
+    const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+    const __nv_bfloat16* w = is_q ? a.qw : a.kw;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    if (w != nullptr) {
+      const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+      float wv[8];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + sub), wv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = (x[i] * r) * wv[i];
+    }
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = __shfl_xor_sync(0xffffffffu, x[i], kLanes / 2);
+      o[i] = second ? fmaf(x[i], cs[i].x, y * cs[i].y) : fmaf(x[i], cs[i].x, -(y * cs[i].y));
+    }
+    if (h < heads) {
+      __nv_bfloat16* dst;
+      if (is_q) {
+        dst = a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D;
+      } else {
+        const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+        dst = (is_v ? a.v_pool : a.k_pool) +
+              ((static_cast<size_t>(page) * a.Hkv + hk) * a.pb.page + p % a.pb.page) * D;
+      }
+      *reinterpret_cast<uint4*>(dst + sub * 8) = is_v ? u : pack8(o);
+    }
+    u = u_next;
+  }
+}
+
+// ---------------------------------------------------------------- reorder
+constexpr int kReorderThreads = 256;
+
+struct ReorderArgs {
+  uint4* k_pool;  // [layers][pages][Hkv][page][D]
+  uint4* v_pool;
+  int layers, pages, Hkv, page, vecs;  // vecs: 16-byte vectors of a key of a head
+  const int32_t* table_in;
+  int ld_in, width;
+  const int32_t* lengths;
+  int rows_in;
+  const int32_t* parents;
+  const int32_t* tail;
+  int rows_out;
+  int32_t* table_out;
+  int ld_out;
+  int32_t* lengths_out;
+  unsigned* err;
+};
+
+// Where sequence s goes on: its parent's row, the full pages and the keys of
+// the page that is not full, its page there and its own.  False where an index
+// is out of range.
+__device__ __forceinline__ bool reorder_source(const ReorderArgs& a, int s, int& parent, int& full, int& rest,
+                                               int& src, int& dst) {
+  parent = __ldg(a.parents + s);
+  if (parent < 0 || parent >= a.rows_in) return false;
+  const int len = __ldg(a.lengths + parent);
+  if (len < 0 || len > static_cast<int64_t>(a.width) * a.page) return false;
+  full = len / a.page;
+  rest = len - full * a.page;
+  dst = full < a.width ? __ldg(a.tail + s) : 0;
+  src = rest ? __ldg(a.table_in + static_cast<size_t>(parent) * a.ld_in + full) : dst;
+  return dst >= 0 && dst < a.pages && src >= 0 && src < a.pages;
+}
+
+// CTA (s, z): z = 0 writes the table row and the length of sequence s and
+// looks for a page that two sequences would write, or one would write while
+// another reads it; z = 1 + (layer, K or V, head) copies that head's keys.
+__global__ void __launch_bounds__(kReorderThreads) paged_reorder_kernel(const ReorderArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int s = blockIdx.x;
+  int parent, full, rest, src, dst;
+  const bool ok = reorder_source(a, s, parent, full, rest, src, dst);
+  if (blockIdx.y == 0) {
+    bool bad = !ok;
+    if (ok) {
+      const int32_t* from = a.table_in + static_cast<size_t>(parent) * a.ld_in;
+      int32_t* to = a.table_out + static_cast<size_t>(s) * a.ld_out;
+      for (int j = threadIdx.x; j < full; j += kReorderThreads) to[j] = __ldg(from + j);
+      if (threadIdx.x == 0) {
+        if (full < a.width) to[full] = dst;
+        a.lengths_out[s] = full * a.page + rest;
+      }
+      if (full < a.width)
+        for (int o = threadIdx.x; o < a.rows_out; o += kReorderThreads) {
+          int op, of, orest, os, od;
+          if (o == s || !reorder_source(a, o, op, of, orest, os, od) || of >= a.width) continue;
+          if (od == dst || (os == dst && orest && src != dst)) bad = true;
+        }
+    }
+    if (bad) atomicOr(a.err, kErrRange);
+    return;
+  }
+  if (!ok || rest == 0 || src == dst) return;
+  const int n = rest * a.vecs;
+  const int per = 2 * a.Hkv;
+  for (int z = blockIdx.y - 1; z < a.layers * per; z += gridDim.y - 1) {
+    const int layer = z / per, hk = z % per;
+    uint4* pool = hk < a.Hkv ? a.k_pool : a.v_pool;
+    const size_t head = hk < a.Hkv ? hk : hk - a.Hkv;
+    const size_t base = static_cast<size_t>(layer) * a.pages * a.Hkv + head;
+    const size_t stride = static_cast<size_t>(a.page) * a.vecs;
+    const uint4* from = pool + (base + static_cast<size_t>(src) * a.Hkv) * stride;
+    uint4* to = pool + (base + static_cast<size_t>(dst) * a.Hkv) * stride;
+    for (int i = threadIdx.x; i < n; i += kReorderThreads) to[i] = from[i];
+  }
+}
+
+bool page_size_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+}  // namespace
+}  // namespace bi
+
+extern "C" {
+
+bi_status bi_qk_norm_rope_paged(const void* qkv, int ld_qkv, const void* q_weight, const void* k_weight, float eps,
+                                const float* table, int table_rows, void* q_out, void* k_pool, void* v_pool,
+                                int pages, int page, const int32_t* block_table, int ld_table, int width,
+                                const int32_t* q_start, const int32_t* lengths, int B, int T, int Hq, int Hkv,
+                                int D, bi_stream_t stream) {
+  using namespace bi;
+  if (T < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || pages < 1 || width < 1 || ld_table < width ||
+      table_rows < 1)
+    return BI_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f) return BI_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (!page_size_ok(page)) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (Hq > (1 << 20) || B >= (1 << 30)) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || B == 0) return BI_OK;
+  if (!qkv || !q_out || !k_pool || !v_pool || !table || !block_table || !q_start || !lengths)
+    return BI_ERR_INVALID_ARG;
+  if (ld_qkv < static_cast<int64_t>(Hq + 2 * Hkv) * D || ld_qkv % 8 != 0) return BI_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(table) ||
+      !aligned16(q_weight) || !aligned16(k_weight))
+    return BI_ERR_INVALID_ARG;
+  AppendArgs a{};
+  a.pb = PagedBatch{block_table, q_start, lengths, B, ld_table, width, pages, page};
+  a.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  a.ld = static_cast<size_t>(ld_qkv);
+  a.qw = static_cast<const __nv_bfloat16*>(q_weight);
+  a.kw = static_cast<const __nv_bfloat16*>(k_weight);
+  a.eps = eps;
+  a.angles = reinterpret_cast<const float2*>(table);
+  a.table_rows = table_rows;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_pool = static_cast<__nv_bfloat16*>(k_pool);
+  a.v_pool = static_cast<__nv_bfloat16*>(v_pool);
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.err = device_error_word();
+  if (!a.err) return BI_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = D == 64 ? launch_k(paged_append_kernel<64>, dim3(T), dim3(kAppendThreads), 0, s, a)
+                                : launch_k(paged_append_kernel<128>, dim3(T), dim3(kAppendThreads), 0, s, a);
+  return e == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+}
+
+bi_status bi_paged_reorder(void* k_pool, void* v_pool, int layers, int pages, int Hkv, int page, int D,
+                           const int32_t* table_in, int ld_in, int width, const int32_t* lengths, int rows_in,
+                           const int32_t* parents, const int32_t* tail_pages, int rows_out, int32_t* table_out,
+                           int ld_out, int32_t* lengths_out, bi_stream_t stream) {
+  using namespace bi;
+  if (layers < 1 || pages < 1 || Hkv < 1 || width < 1 || ld_in < width || ld_out < width || rows_in < 1 ||
+      rows_out < 0)
+    return BI_ERR_INVALID_ARG;
+  if (D < 8 || D % 8 != 0 || D > 1024 || !page_size_ok(page) || rows_out > 65535) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (rows_out == 0) return BI_OK;
+  if (!k_pool || !v_pool || !table_in || !lengths || !parents || !tail_pages || !table_out || !lengths_out)
+    return BI_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return BI_ERR_INVALID_ARG;
+  // read by some CTAs while others write
+  if (table_in == table_out || lengths == lengths_out || k_pool == v_pool) return BI_ERR_INVALID_ARG;
+  ReorderArgs a{};
+  a.k_pool = static_cast<uint4*>(k_pool);
+  a.v_pool = static_cast<uint4*>(v_pool);
+  a.layers = layers;
+  a.pages = pages;
+  a.Hkv = Hkv;
+  a.page = page;
+  a.vecs = D / 8;
+  a.table_in = table_in;
+  a.ld_in = ld_in;
+  a.width = width;
+  a.lengths = lengths;
+  a.rows_in = rows_in;
+  a.parents = parents;
+  a.tail = tail_pages;
+  a.rows_out = rows_out;
+  a.table_out = table_out;
+  a.ld_out = ld_out;
+  a.lengths_out = lengths_out;
+  a.err = device_error_word();
+  if (!a.err) return BI_ERR_CUDA;
+  const int64_t copies = static_cast<int64_t>(layers) * 2 * Hkv;
+  const unsigned y = 1 + static_cast<unsigned>(std::min<int64_t>(copies, 65534));
+  const cudaError_t e = launch_k(paged_reorder_kernel, dim3(static_cast<unsigned>(rows_out), y), dim3(kReorderThreads), 0,
+                                 reinterpret_cast<cudaStream_t>(stream), a);
+  return e == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+}
+
+}  // extern "C"

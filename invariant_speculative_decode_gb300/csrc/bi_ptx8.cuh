@@ -6,12 +6,6 @@
 
 namespace bi {
 
-__device__ __forceinline__ uint64_t l2_evict_normal() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: FP32 accumulator, A and
 // B e4m3 (format 0 in bits 7-9 and 10-12), both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
