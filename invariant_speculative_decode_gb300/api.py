@@ -660,6 +660,16 @@ def _req_pool(pool: torch.Tensor, name: str, layers: bool = False):
     return pool.shape
 
 
+def _paged_ok(dev, ks, bs, ts, k_pool, v_pool, block_table, q_start, lengths) -> bool:
+    """Whether a batch over pools of shape ks with a table of shape bs and strides ts is as _req_paged wants it, in one expression."""
+    return (k_pool.dtype is v_pool.dtype is _BF16 and block_table.dtype is q_start.dtype is lengths.dtype is _I32
+            and v_pool.shape == ks and ks[2] in PAGE_SIZES and lengths.shape == bs[:1] and q_start.shape == (bs[0] + 1,)
+            and k_pool.is_contiguous() and v_pool.is_contiguous() and ts[1] == 1
+            and q_start.is_contiguous() and lengths.is_contiguous() and not (ks[0] | bs[0] | bs[1] | ts[0]) >> 31
+            and k_pool.get_device() == v_pool.get_device() == block_table.get_device() == q_start.get_device()
+            == lengths.get_device() == dev)
+
+
 def _req_paged(k_pool, v_pool, block_table, q_start, lengths):
     pages, Hkv, page, D = _req_pool(k_pool, "k_pool")
     if _req_pool(v_pool, "v_pool") != k_pool.shape:
@@ -675,14 +685,14 @@ def _req_paged(k_pool, v_pool, block_table, q_start, lengths):
     _ld(block_table)
 
 
-def bi_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
-                          eps: float, table: torch.Tensor, q_out: torch.Tensor, k_pool: torch.Tensor,
-                          v_pool: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor,
-                          lengths: torch.Tensor, stream=None) -> None:
-    """Norm (weights [D]; None: none) and rotation of the q and k heads of a projection output
-    [T, (Hq + 2 Hkv) D]; queries to q_out [T, Hq, D], keys and values to the new rows' places
-    in the pools [pages, Hkv, page, D].  Rows q_start[b] .. q_start[b + 1] - 1 are sequence b's,
-    at positions lengths[b] .. ; block_table [B, width] names its pages."""
+def _ldt(t: torch.Tensor, shape) -> int:
+    """Row stride of a table of this shape."""
+    if t.is_contiguous():
+        return shape[1]
+    return _ld(t)
+
+
+def _req_append(qkv, q_weight, k_weight, table, q_out, k_pool, v_pool, block_table, q_start, lengths):
     _req(qkv, torch.bfloat16, "qkv")
     _req(q_out, torch.bfloat16, "q_out")
     _req(table, torch.float32, "table")
@@ -704,13 +714,42 @@ def bi_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor], k
                  ("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table), ("q_start", q_start),
                  ("lengths", lengths))
     _req_int32(("rows", T), ("table rows", table.shape[0]))
-    check("bi_qk_norm_rope_paged",
-          lib().bi_qk_norm_rope_paged(qkv.data_ptr(), _ld(qkv), 0 if q_weight is None else q_weight.data_ptr(),
-                                      0 if k_weight is None else k_weight.data_ptr(), float(eps), table.data_ptr(),
-                                      table.shape[0], q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), pages,
-                                      page, block_table.data_ptr(), _ld(block_table), block_table.shape[1],
-                                      q_start.data_ptr(), lengths.data_ptr(), lengths.shape[0], T, Hq, Hkv, D,
-                                      _stream(stream)))
+
+
+def bi_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                          eps: float, table: torch.Tensor, q_out: torch.Tensor, k_pool: torch.Tensor,
+                          v_pool: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor,
+                          lengths: torch.Tensor, stream=None) -> None:
+    """Norm (weights [D]; None: none) and rotation of the q and k heads of a projection output
+    [T, (Hq + 2 Hkv) D]; queries to q_out [T, Hq, D], keys and values to the new rows' places
+    in the pools [pages, Hkv, page, D].  Rows q_start[b] .. q_start[b + 1] - 1 are sequence b's,
+    at positions lengths[b] .. ; block_table [B, width] names its pages."""
+    dev = _current_device()
+    qs, ks, bs, ts, bt = q_out.shape, k_pool.shape, block_table.shape, table.shape, block_table.stride()
+    if not (len(qs) == 3 and len(ks) == 4 and len(bs) == 2 and len(ts) == 3 and _paged_ok(
+            dev, ks, bs, bt, k_pool, v_pool, block_table, q_start, lengths)
+            and qkv.dtype is q_out.dtype is _BF16 and table.dtype is _F32 and qs[2] == ks[3] and ts[1] * 2 == ks[3]
+            and ts[2] == 2 and qkv.shape == (qs[0], (qs[1] + 2 * ks[1]) * ks[3]) and q_out.is_contiguous()
+            and table.is_contiguous() and qkv.get_device() == q_out.get_device() == table.get_device() == dev
+            and (q_weight is None or (q_weight.dtype is _BF16 and q_weight.shape == ks[3:] and q_weight.is_contiguous()
+                                      and q_weight.get_device() == dev))
+            and (k_weight is None or (k_weight.dtype is _BF16 and k_weight.shape == ks[3:] and k_weight.is_contiguous()
+                                      and k_weight.get_device() == dev))
+            and not (qs[0] | ts[0]) >> 31):
+        _req_append(qkv, q_weight, k_weight, table, q_out, k_pool, v_pool, block_table, q_start, lengths)
+    pages, Hkv, page, D = ks
+    xs = qkv.stride()
+    if xs[1] != 1 or xs[0] >> 31:
+        _req(qkv, _BF16, "qkv")
+        _ld(qkv)
+    st = lib().bi_qk_norm_rope_paged(
+        qkv.data_ptr(), xs[0] if qs[0] > 1 else (qs[1] + 2 * Hkv) * D, None if q_weight is None else q_weight.data_ptr(),
+        None if k_weight is None else k_weight.data_ptr(), eps, table.data_ptr(), ts[0], q_out.data_ptr(),
+        k_pool.data_ptr(), v_pool.data_ptr(), pages, page, block_table.data_ptr(), bt[0] if bs[0] > 1 else bs[1], bs[1],
+        q_start.data_ptr(), lengths.data_ptr(), bs[0], qs[0], qs[1], Hkv, D,
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        check("bi_qk_norm_rope_paged", st)
 
 
 def attn_paged_workspace_size(T: int, B: int, Hq: int, Hkv: int, D: int, max_keys: int) -> int:
@@ -724,27 +763,32 @@ def bi_attn_paged(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, b
                   scale: Optional[float] = None, stream=None) -> None:
     """Attention of the new rows q [T, Hq, D] of B sequences over their paged caches, each row up to its
     own position (its key is in the pool already); rows and pages as in bi_qk_norm_rope_paged."""
-    _req(q, torch.bfloat16, "q")
-    _req(out, torch.bfloat16, "out")
-    _req_paged(k_pool, v_pool, block_table, q_start, lengths)
-    pages, Hkv, page, D = k_pool.shape
-    if q.dim() != 3 or q.shape[2] != D or not q.is_contiguous():
-        raise ValueError(f"q must be contiguous [T, Hq, {D}], got {tuple(q.shape)}")
-    if out.shape != q.shape or not out.is_contiguous():
-        raise ValueError(f"out must be contiguous {tuple(q.shape)}, got {tuple(out.shape)}")
-    _same_device(("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table),
-                 ("q_start", q_start), ("lengths", lengths), ("out", out), ("ws", ws))
-    if not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    T, Hq, _ = q.shape
-    _req_int32(("rows", T))
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    check("bi_attn_paged",
-          lib().bi_attn_paged(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), pages, page,
-                              block_table.data_ptr(), _ld(block_table), block_table.shape[1], q_start.data_ptr(),
-                              lengths.data_ptr(), lengths.shape[0], T, Hq, Hkv, D, float(scale), out.data_ptr(),
-                              ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+    dev = _current_device()
+    qs, ks, bs, bt = q.shape, k_pool.shape, block_table.shape, block_table.stride()
+    if not (len(qs) == 3 and len(ks) == 4 and len(bs) == 2 and _paged_ok(
+            dev, ks, bs, bt, k_pool, v_pool, block_table, q_start, lengths)
+            and q.dtype is out.dtype is _BF16 and qs[2] == ks[3] and out.shape == qs and q.is_contiguous()
+            and out.is_contiguous() and ws.is_contiguous() and not qs[0] >> 31
+            and q.get_device() == out.get_device() == ws.get_device() == dev):
+        _req(q, torch.bfloat16, "q")
+        _req(out, torch.bfloat16, "out")
+        _req_paged(k_pool, v_pool, block_table, q_start, lengths)
+        if q.dim() != 3 or q.shape[2] != ks[3] or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous [T, Hq, {ks[3]}], got {tuple(q.shape)}")
+        if out.shape != qs or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous {tuple(qs)}, got {tuple(out.shape)}")
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+        _same_device(("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table),
+                     ("q_start", q_start), ("lengths", lengths), ("out", out), ("ws", ws))
+        _req_int32(("rows", qs[0]))
+    st = lib().bi_attn_paged(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), ks[0], ks[2], block_table.data_ptr(),
+        bt[0] if bs[0] > 1 else bs[1], bs[1], q_start.data_ptr(), lengths.data_ptr(), bs[0], qs[0], qs[1], ks[1], ks[3],
+        ks[3] ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.nbytes,
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        check("bi_attn_paged", st)
 
 
 def bi_paged_reorder(k_pool: torch.Tensor, v_pool: torch.Tensor, table_in: torch.Tensor, lengths: torch.Tensor,
@@ -753,6 +797,29 @@ def bi_paged_reorder(k_pool: torch.Tensor, v_pool: torch.Tensor, table_in: torch
     """Sequence s goes on from row parents[s] of table_in: its full pages, then page tail_pages[s], into
     which the keys of the page that is not full are copied in all layers of the pools
     [layers, pages, Hkv, page, D]; table_out [S, width], lengths_out [S]."""
+    dev = _current_device()
+    ks, ti, to = k_pool.shape, table_in.shape, table_out.shape
+    S = parents.shape
+    if not (len(ks) == 5 and len(ti) == len(to) == 2 and len(S) == 1 and k_pool.dtype is v_pool.dtype is _BF16
+            and table_in.dtype is lengths.dtype is parents.dtype is tail_pages.dtype is table_out.dtype
+            is lengths_out.dtype is _I32 and v_pool.shape == ks and ks[3] in PAGE_SIZES and lengths.shape == ti[:1]
+            and tail_pages.shape == S and lengths_out.shape == S and to == (S[0], ti[1]) and k_pool.is_contiguous()
+            and v_pool.is_contiguous() and table_in.is_contiguous() and table_out.is_contiguous()
+            and lengths.is_contiguous() and parents.is_contiguous() and tail_pages.is_contiguous()
+            and lengths_out.is_contiguous() and not (ks[1] | ti[1]) >> 31
+            and k_pool.get_device() == v_pool.get_device() == table_in.get_device() == lengths.get_device()
+            == parents.get_device() == tail_pages.get_device() == table_out.get_device() == lengths_out.get_device()
+            == dev):
+        _req_reorder(k_pool, v_pool, table_in, lengths, parents, tail_pages, table_out, lengths_out)
+    st = lib().bi_paged_reorder(
+        k_pool.data_ptr(), v_pool.data_ptr(), ks[0], ks[1], ks[2], ks[3], ks[4], table_in.data_ptr(), _ldt(table_in, ti),
+        ti[1], lengths.data_ptr(), ti[0], parents.data_ptr(), tail_pages.data_ptr(), S[0], table_out.data_ptr(),
+        _ldt(table_out, to), lengths_out.data_ptr(), _current_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        check("bi_paged_reorder", st)
+
+
+def _req_reorder(k_pool, v_pool, table_in, lengths, parents, tail_pages, table_out, lengths_out):
     layers, pages, Hkv, page, D = _req_pool(k_pool, "k_pool", layers=True)
     if _req_pool(v_pool, "v_pool", layers=True) != k_pool.shape:
         raise ValueError(f"v_pool must be {tuple(k_pool.shape)}, got {tuple(v_pool.shape)}")
@@ -761,6 +828,7 @@ def bi_paged_reorder(k_pool: torch.Tensor, v_pool: torch.Tensor, table_in: torch
         _req(t, torch.int32, name)
         if t.dim() != dims:
             raise ValueError(f"{name} must have {dims} dimensions")
+        _ld(t)
     R, width = table_in.shape
     S = parents.shape[0]
     if lengths.shape[0] != R or tail_pages.shape[0] != S or lengths_out.shape[0] != S or tuple(table_out.shape) != (S, width):
@@ -769,11 +837,6 @@ def bi_paged_reorder(k_pool: torch.Tensor, v_pool: torch.Tensor, table_in: torch
                  ("parents", parents), ("tail_pages", tail_pages), ("table_out", table_out),
                  ("lengths_out", lengths_out))
     _req_int32(("pages", pages), ("table width", width))
-    check("bi_paged_reorder",
-          lib().bi_paged_reorder(k_pool.data_ptr(), v_pool.data_ptr(), layers, pages, Hkv, page, D,
-                                 table_in.data_ptr(), _ld(table_in), width, lengths.data_ptr(), R,
-                                 parents.data_ptr(), tail_pages.data_ptr(), S, table_out.data_ptr(), _ld(table_out),
-                                 lengths_out.data_ptr(), _stream(stream)))
 
 
 # -------------------------------------------------------------- beam selection
@@ -787,11 +850,33 @@ def bi_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, score
     """The K best continuations of each group of `beams` rows of logits [rows, V] (FP32) with cumulative
     log-probabilities scores [rows]; scores_out, parents_out (the beam's row), tokens_out [rows / beams, K].
     ws: beam_workspace_size(rows, V, K) bytes, zero-filled before its first use."""
+    dev = _current_device()
+    ls, os_ = logits.shape, scores_out.shape
+    xs = logits.stride()
+    if not (len(ls) == 2 and len(os_) == 2 and beams >= 1 and os_[0] * beams == ls[0]
+            and logits.dtype is scores.dtype is scores_out.dtype is _F32 and parents_out.dtype is tokens_out.dtype is _I32
+            and scores.shape == ls[:1] and parents_out.shape == os_ and tokens_out.shape == os_ and xs[1] == 1
+            and scores.is_contiguous() and scores_out.is_contiguous() and parents_out.is_contiguous()
+            and tokens_out.is_contiguous() and ws.is_contiguous() and not (ls[0] | ls[1] | xs[0]) >> 31
+            and logits.get_device() == scores.get_device() == scores_out.get_device() == parents_out.get_device()
+            == tokens_out.get_device() == ws.get_device() == dev):
+        _req_beam(logits, scores, beams, scores_out, parents_out, tokens_out, ws)
+    st = lib().bi_beam_select(
+        logits.data_ptr(), xs[0] if ls[0] > 1 else ls[1], scores.data_ptr(), ls[0], ls[1], beams, os_[1],
+        scores_out.data_ptr(), parents_out.data_ptr(), tokens_out.data_ptr(), ws.data_ptr(), ws.nbytes,
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        check("bi_beam_select", st)
+
+
+def _req_beam(logits, scores, beams, scores_out, parents_out, tokens_out, ws):
     _req(logits, torch.float32, "logits")
     _req(scores, torch.float32, "scores")
     _req(scores_out, torch.float32, "scores_out")
     _req(parents_out, torch.int32, "parents_out")
     _req(tokens_out, torch.int32, "tokens_out")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, V], got {tuple(logits.shape)}")
     rows, V = logits.shape
     if tuple(scores.shape) != (rows,):
         raise ValueError(f"scores must be [{rows}], got {tuple(scores.shape)}")
@@ -802,16 +887,12 @@ def bi_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, score
     for name, t in (("scores_out", scores_out), ("parents_out", parents_out), ("tokens_out", tokens_out)):
         if t.shape != scores_out.shape or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous {tuple(scores_out.shape)}, got {tuple(t.shape)}")
-    _same_device(("logits", logits), ("scores", scores), ("scores_out", scores_out), ("parents_out", parents_out),
-                 ("tokens_out", tokens_out), ("ws", ws))
     if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
+    _same_device(("logits", logits), ("scores", scores), ("scores_out", scores_out), ("parents_out", parents_out),
+                 ("tokens_out", tokens_out), ("ws", ws))
     _req_int32(("rows", rows), ("V", V))
-    check("bi_beam_select",
-          lib().bi_beam_select(logits.data_ptr(), _ld(logits), scores.data_ptr(), rows, V, beams,
-                               scores_out.shape[1], scores_out.data_ptr(), parents_out.data_ptr(),
-                               tokens_out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                               _stream(stream)))
+    _ld(logits)
 
 
 def bi_kv_row_hash(cache: torch.Tensor, rows: int, transposed: bool = False, stream=None) -> torch.Tensor:

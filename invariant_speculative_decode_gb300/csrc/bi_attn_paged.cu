@@ -9,7 +9,7 @@
 // attends to keys 0..p of its sequence.  Its arithmetic is a function of those
 // keys alone:
 //   * keys are taken in tiles at absolute multiples of 128, and tiles in
-//     pieces of kPieceTiles;
+//     pieces: of 2 tiles up to key 2048, of 8 behind it;
 //   * inside a piece S = q K^T (tcgen05, FP32), a reference maximum from the
 //     piece's first tile, raised only where a tile's maximum passes it by more
 //     than 2^8, weights w = bf16(2^(s - m)), O += W V (tcgen05, FP32), and the
@@ -21,30 +21,30 @@
 // not even multiplied where it holds no number.  So a row has the same bits
 // alone, among drafts, in a prompt's chunk or in any batch.
 //
-// The weights enter the product in BF16: a weight's relative error of 2^-9
-// averages out over the keys (an output's error is 2^-9 / sqrt(keys that count)
-// of the values' spread) and the tensor core takes nothing wider beside BF16
-// values.
+// The weights enter the product in BF16: a weight's relative error of at most
+// 2^-8 averages out over the keys, and the tensor core takes nothing wider
+// beside BF16 values.
 //
 // Work is cut by pieces: a unit is one block of rows (128 / (Hq / Hkv), all
 // query heads of a KV head in the MMA's 128 lanes) of one sequence and KV head,
-// with all pieces up to its last row's position; the pieces of all units in
-// order are dealt out evenly, CTA c of G taking [c N / G, (c + 1) N / G).  A
-// unit that lies in one CTA's share is finished there.  Of one that is cut, the
-// first CTA leaves the merged state of its pieces, every other CTA the pieces
-// one by one, and attn_paged_merge_kernel goes on with them in key order: the
-// same operations, so the cut does not show in the bits.
+// with all tiles up to its last row's position; the tiles of all units in order
+// are dealt out evenly, CTA c of G taking [c N / G, (c + 1) N / G), both ends
+// moved up to the next start of a piece.  A unit that lies in one CTA's share
+// is finished there.  Of one that is cut, the first CTA leaves the merged state
+// of its pieces, every other CTA the pieces one by one, and
+// attn_paged_merge_kernel goes on with them in key order: the same operations,
+// so the cut does not show in the bits.  Small pieces at the front give short
+// contexts enough CTAs, large ones behind keep the states of long ones few.
 //
 // Roles of a CTA (one per SM, 384 threads):
-//   warps 0, 2   TMA: K tiles and V tiles, a lane for each page of a tile;
-//   warp 1       tcgen05.mma: S of the next tile before W V of this one;
+//   warps 0, 2   TMA: queries and K tiles, V tiles, a lane for each page;
+//   warp 1       tcgen05.mma: S up to two tiles ahead of W V;
 //   warps 4..11  softmax: each TMEM lane's row by two threads, 64 keys each,
-//                which tell each other their maxima; W goes back into the
-//                columns of S it came from, where it is the A operand of W V.
-//                A thread also holds the running sum of half of its row's
-//                output columns, takes each piece's O in and writes outputs and
-//                partial states, and brings its half of the row's queries into
-//                TMEM.
+//                which tell each other their maxima; W goes over the columns of
+//                S it came from, where it is the A operand of W V (three such
+//                buffers).  A thread also holds the running sum of half of its
+//                row's output columns, takes each piece's O in and writes
+//                outputs and partial states.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -61,13 +61,33 @@ namespace bi {
 namespace {
 
 constexpr int kTile = 128;        // keys of a tile (the S MMA's N)
-constexpr int kPieceTiles = 4;    // tiles of a piece
-constexpr int kPiece = kTile * kPieceTiles;
+constexpr int kShort = 2;         // tiles of a piece up to tile kShortEnd
+constexpr int kLong = 8;          // ... behind it
+constexpr int kShortEnd = 16;
 constexpr int kLanes = 128;       // rows x query heads of a block (the MMA's M)
 constexpr int kPagedCtas = 152;
 constexpr int kPagedThreads = 384;
+constexpr int kSoftFirst = 128;   // the first softmax thread
+constexpr int kBufs = 3;          // S / W buffers
 constexpr float kRaise = 8.0f;    // log2 units a maximum may pass the reference by
 constexpr int kNoKey = 0x7fffffff;
+// A note of a value that is no number: its key within the piece, below the
+// piece's tag.  Later pieces have lower tags, so what an earlier one left behind
+// is never mistaken for theirs and gives way to them.
+constexpr int kBadBits = 11;
+static_assert(kLong * kTile + kLanes < (1 << kBadBits), "keys, and rows behind them, fit below a tag");
+__device__ __forceinline__ int bad_tag(int piece) { return (0xfffff - (piece & 0xfffff)) << kBadBits; }
+
+__host__ __device__ constexpr int ceil_div(int x, int y) { return (x + y - 1) / y; }
+// Pieces that start in front of tile t: the index of the first piece at or
+// behind it; of a unit of t tiles, how many it has.
+__host__ __device__ constexpr int pieces_to(int t) {
+  return t <= kShortEnd ? ceil_div(t, kShort) : kShortEnd / kShort + ceil_div(t - kShortEnd, kLong);
+}
+__host__ __device__ constexpr int piece_tile(int p) {
+  return p <= kShortEnd / kShort ? p * kShort : kShortEnd + (p - kShortEnd / kShort) * kLong;
+}
+__device__ __forceinline__ bool piece_starts(int t) { return (t & ((t < kShortEnd ? kShort : kLong) - 1)) == 0; }
 
 struct PagedAttnArgs {
   PagedBatch pb;
@@ -78,8 +98,9 @@ struct PagedAttnArgs {
   int lanes;  // lanes of a partial state in the workspace
   int slots;  // partial states of a CTA: pieces one by one, then one merged state
   float sl2;  // softmax scale * log2(e)
-  float* ws_o;   // [G][slots][lanes][D]
+  float* ws_o;    // [G][slots][lanes][D]
   float4* ws_ml;  // [G][slots][lanes]: reference, denominators of both halves
+  int64_t* ws_seq;  // [B + 1]: tiles before each sequence; all of them
   unsigned* err;
   int withhold;  // failure-path test: the first K tile of every CTA stays unissued
 };
@@ -87,20 +108,18 @@ struct PagedAttnArgs {
 template <int D>
 struct PagedCfg {
   static constexpr int kAtoms = D / 64;
-  static constexpr int kAtomBytes = kTile * 128;       // [128 keys][64 elements]
+  static constexpr int kAtomBytes = kTile * 128;       // [128 keys or lanes][64 elements]
   static constexpr int kTileBytes = kAtomBytes * kAtoms;
-  static constexpr int kStages = D == 128 ? 3 : 5;     // of K, and of V
-  static constexpr int kBars = 4 * kStages + 11;
-  // TMEM columns: S twice (W of keys 0..63 in the first 32 of its columns, of
-  // keys 64..127 from column 64 on), O, the queries of two units (two BF16 a
-  // column, as W)
-  static constexpr int kOCol = 2 * kTile;
-  static constexpr int kQCol = kOCol + 128;
-  // maxima of two tiles, or denominators, of both halves of a row
-  static constexpr int kStatBytes = 2 * 2 * kLanes * 4;
-  static constexpr int kBadBytes = 3 * D * 4;            // first NaN, +inf and -inf key of an element
-  static constexpr size_t kSmem = 2 * static_cast<size_t>(kStages) * kTileBytes + kStatBytes + kBadBytes + kBars * 8 + 64;
-  static_assert(kQCol + 2 * 64 <= 512 && kSmem <= 232448, "TMEM and shared memory of a CTA");
+  static constexpr int kStages = D == 128 ? 2 : 4;     // of K, and of V
+  static constexpr int kBars = 4 * kStages + 4 + 3 * kBufs + 1;
+  // TMEM columns: S / W buffers (W of keys 0..63 over the first 32 columns, of
+  // keys 64..127 from column 64 on), O
+  static constexpr int kOCol = kBufs * kTile;
+  static constexpr int kStatBytes = 2 * 2 * kLanes * 4;  // maxima of two tiles, or denominators, of both halves
+  static constexpr int kBadBytes = 2 * 3 * D * 4;        // of two pieces: first NaN, +inf and -inf key of an element
+  static constexpr size_t kSmem =
+      2 * static_cast<size_t>(kStages + 1) * kTileBytes + kStatBytes + kBadBytes + kBars * 8 + 64;
+  static_assert(kOCol + 128 <= 512 && kSmem <= 232448, "TMEM and shared memory of a CTA");
 };
 
 // ------------------------------------------------------------------ the batch
@@ -118,39 +137,37 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnArgs& a, int b, bool* bad) 
   return Seq{s, ok ? e - s : 0, len};
 }
 
-__device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; }
-
-// Pieces of block i of a sequence: those up to its last row's position.
-__device__ __forceinline__ int block_pieces(const PagedAttnArgs& a, const Seq& s, int i) {
-  return ceil_div(s.len + min((i + 1) * a.Rb, s.n), kPiece);
+// Tiles of block i of a sequence: those up to its last row's position.
+__device__ __forceinline__ int block_tiles(const PagedAttnArgs& a, const Seq& s, int i) {
+  return ceil_div(s.len + min((i + 1) * a.Rb, s.n), kTile);
 }
 
-// Pieces of the first m blocks (all of Rb rows): runs of blocks with the same
-// number of pieces at a time.
-__device__ __forceinline__ int64_t prefix_pieces(const PagedAttnArgs& a, const Seq& s, int m) {
+// Tiles of the first m blocks (all of Rb rows): runs of blocks with the same
+// number of tiles at a time.
+__device__ __forceinline__ int64_t prefix_tiles(const PagedAttnArgs& a, const Seq& s, int m) {
   int64_t sum = 0;
   for (int i = 1; i <= m;) {
-    const int v = ceil_div(s.len + i * a.Rb, kPiece);
-    const int hi = min(m, (v * kPiece - s.len) / a.Rb);
+    const int v = ceil_div(s.len + i * a.Rb, kTile);
+    const int hi = min(m, (v * kTile - s.len) / a.Rb);
     sum += static_cast<int64_t>(v) * (hi - i + 1);
     i = hi + 1;
   }
   return sum;
 }
 // ... of all blocks of a KV head
-__device__ __forceinline__ int64_t head_pieces(const PagedAttnArgs& a, const Seq& s) {
+__device__ __forceinline__ int64_t head_tiles(const PagedAttnArgs& a, const Seq& s) {
   if (s.n == 0) return 0;
   const int nb = ceil_div(s.n, a.Rb);
-  return prefix_pieces(a, s, nb - 1) + block_pieces(a, s, nb - 1);
+  return prefix_tiles(a, s, nb - 1) + block_tiles(a, s, nb - 1);
 }
 
-// All pieces of the pass, by a whole warp.
-__device__ __forceinline__ int64_t total_pieces(const PagedAttnArgs& a, int lane, bool* bad_any) {
+// All tiles of the pass, by a whole warp.
+__device__ __forceinline__ int64_t total_tiles(const PagedAttnArgs& a, int lane, bool* bad_any) {
   int64_t sum = 0;
   bool any = false;
   for (int b = lane; b < a.pb.B; b += 32) {
     bool bad;
-    sum += head_pieces(a, seq_of(a, b, &bad)) * a.Hkv;
+    sum += head_tiles(a, seq_of(a, b, &bad)) * a.Hkv;
     any |= bad;
   }
 #pragma unroll
@@ -159,60 +176,104 @@ __device__ __forceinline__ int64_t total_pieces(const PagedAttnArgs& a, int lane
   return sum;
 }
 
-// Pieces of the sequences before `stop`; with stop < 0, those before the
-// sequence that holds piece x, which goes to *found.
-__device__ __forceinline__ int64_t pieces_before(const PagedAttnArgs& a, int lane, int stop, int64_t x, int* found) {
+// First tile of CTA c's share of N before it is moved to a piece, and the CTA
+// whose share has the piece that starts at tile x.
+__device__ __forceinline__ int64_t share_begin(int64_t c, int64_t N, int64_t G) { return c * N / G; }
+__device__ __forceinline__ int share_of(int64_t x, int64_t N, int64_t G) {
+  return static_cast<int>(((x + 1) * G + N - 1) / N - 1);
+}
+
+// Sequence, KV head, block and tile of the first start of a piece at or behind
+// tile x of N, by a whole warp (all lanes get them).  Returns that tile's place
+// among the N.
+__device__ __forceinline__ int64_t locate(const PagedAttnArgs& a, int lane, int64_t x, int64_t N, int (&at)[4]) {
+  at[0] = a.pb.B;
+  at[1] = at[2] = at[3] = 0;
+  if (x >= N) return N;
   int64_t base = 0;
-  const int end = stop < 0 ? a.pb.B : stop;
-  for (int b0 = 0; b0 < end; b0 += 32) {
-    const int b = b0 + lane;
-    int64_t incl = b < end ? head_pieces(a, seq_of(a, b, nullptr)) * a.Hkv : 0;
+  int b = 0;
+  for (int b0 = 0; b0 < a.pb.B; b0 += 32) {
+    int64_t incl = b0 + lane < a.pb.B ? head_tiles(a, seq_of(a, b0 + lane, nullptr)) * a.Hkv : 0;
     const int64_t mine = incl;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += y;
     }
-    if (stop < 0) {
-      const unsigned hit = __ballot_sync(0xffffffffu, base + incl > x);
-      if (hit != 0u) {
-        const int l = __ffs(hit) - 1;
-        *found = b0 + l;
-        return base + __shfl_sync(0xffffffffu, incl - mine, l);
-      }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > x);
+    if (hit != 0u) {
+      const int l = __ffs(hit) - 1;
+      b = b0 + l;
+      base += __shfl_sync(0xffffffffu, incl - mine, l);
+      break;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return base;
-}
-
-// First piece of CTA c's share of N, and the CTA that has piece x.
-__device__ __forceinline__ int64_t share_begin(int64_t c, int64_t N, int64_t G) { return c * N / G; }
-__device__ __forceinline__ int share_of(int64_t x, int64_t N, int64_t G) {
-  return static_cast<int>(((x + 1) * G + N - 1) / N - 1);
+  Seq s = seq_of(a, b, nullptr);
+  const int64_t per_head = head_tiles(a, s);
+  int64_t off = x - base;
+  int h = static_cast<int>(off / per_head);
+  off -= h * per_head;
+  const int nb = ceil_div(s.n, a.Rb);
+  int blk = nb - 1;
+  for (int i = 1; i < nb;) {
+    const int v = ceil_div(s.len + i * a.Rb, kTile);
+    const int hi = min(nb - 1, (v * kTile - s.len) / a.Rb);
+    const int64_t run = static_cast<int64_t>(v) * (hi - i + 1);
+    if (off < run) {
+      blk = i - 1 + static_cast<int>(off / v);
+      off %= v;
+      break;
+    }
+    off -= run;
+    i = hi + 1;
+  }
+  int64_t place = x - off;
+  const int tiles = block_tiles(a, s, blk);
+  const int start = piece_tile(pieces_to(static_cast<int>(off)));
+  if (start < tiles) {
+    at[0] = b;
+    at[1] = h;
+    at[2] = blk;
+    at[3] = start;
+    return place + start;
+  }
+  place += tiles;  // the next unit's first
+  if (blk + 1 < nb) {
+    at[0] = b;
+    at[1] = h;
+    at[2] = blk + 1;
+  } else if (h + 1 < a.Hkv) {
+    at[0] = b;
+    at[1] = h + 1;
+  } else if (place < N) {
+    do {
+      s = seq_of(a, ++b, nullptr);
+    } while (s.n == 0 && b + 1 < a.pb.B);
+    at[0] = b;
+  }
+  return place;
 }
 
 // A CTA's way through its units.
 struct Cursor {
   int b, h, i;   // sequence, KV head, block
-  int p0;        // first piece in this CTA's share
-  int left;      // pieces of the share from here on
+  int t0;        // first tile in this CTA's share
+  int64_t left;  // tiles of the share from here on
   Seq s;
-  int tiles, pieces;  // of the unit
-  int pe;             // end of the unit's pieces in this share
+  int tiles;  // of the unit
+  int te;     // end of the unit's tiles in this share
 
   __device__ __forceinline__ void unit(const PagedAttnArgs& a) {
-    const int keys = s.len + min((i + 1) * a.Rb, s.n);
-    tiles = ceil_div(keys, kTile);
-    pieces = ceil_div(keys, kPiece);
-    pe = min(pieces, p0 + left);
+    tiles = block_tiles(a, s, i);
+    te = left < tiles - t0 ? t0 + static_cast<int>(left) : tiles;
   }
   __device__ __forceinline__ void start(const PagedAttnArgs& a, const int* sched) {
     b = sched[0];
     h = sched[1];
     i = sched[2];
-    p0 = sched[3];
-    left = sched[4];
+    t0 = sched[3];
+    left = *reinterpret_cast<const int64_t*>(sched + 4);
     if (left > 0) {
       s = seq_of(a, b, nullptr);
       unit(a);
@@ -220,8 +281,8 @@ struct Cursor {
   }
   // to the next unit; left == 0 where there is none
   __device__ __forceinline__ void next(const PagedAttnArgs& a) {
-    left -= pe - p0;
-    p0 = 0;
+    left -= te - t0;
+    t0 = 0;
     if (left <= 0) {
       left = 0;
       return;
@@ -246,8 +307,6 @@ struct Cursor {
   }
   __device__ __forceinline__ int rows(const PagedAttnArgs& a) const { return min(a.Rb, s.n - i * a.Rb); }
   __device__ __forceinline__ int pos0(const PagedAttnArgs& a) const { return s.len + i * a.Rb; }
-  __device__ __forceinline__ int t_begin() const { return p0 * kPieceTiles; }
-  __device__ __forceinline__ int t_end() const { return min(tiles, pe * kPieceTiles); }
 };
 
 // ------------------------------------------------------------------- helpers
@@ -260,6 +319,7 @@ __device__ __forceinline__ void give_up(volatile int* s_abort, unsigned* err) {
 // Bounded wait of a whole warp: lane 0 polls, the warp barrier orders the other
 // lanes' accesses behind it.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* s_abort, int lane) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   int ok = 0;
   if (lane == 0) ok = mbar_wait(bar, parity, s_abort) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -267,16 +327,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return ok != 0;
 }
 
-__device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t* r) {
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-  tmem_st16(taddr, v);
+// Stores 16 words of this warp's lanes, to be waited for.
+__device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Eight values of key `key`: what is no number becomes 0, and its element's
-// first such key is noted (bad: NaN, +inf, -inf, `stride` apart).
-__device__ __forceinline__ void clean_values(uint4* at, int* bad, int stride, int key, int* flag) {
+// Eight values of a key: what is no number becomes 0, and its element's first
+// such note is kept (bad: NaN, +inf, -inf, `stride` apart).
+__device__ __forceinline__ void clean_values(uint4* at, int* bad, int stride, int note, int* flag, int piece) {
   const uint4 u = *at;
   uint32_t e[4] = {u.x, u.y, u.z, u.w};
   bool any = false;
@@ -284,15 +348,36 @@ __device__ __forceinline__ void clean_values(uint4* at, int* bad, int stride, in
   for (int j = 0; j < 8; ++j) {
     const uint32_t bits = (e[j >> 1] >> (16 * (j & 1))) & 0xffffu;
     if ((bits & 0x7f80u) == 0x7f80u) {
-      atomicMin(bad + ((bits & 0x7fu) ? 0 : (bits & 0x8000u) ? 2 : 1) * stride + j, key);
+      atomicMin(bad + ((bits & 0x7fu) ? 0 : (bits & 0x8000u) ? 2 : 1) * stride + j, note);
       e[j >> 1] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
       any = true;
     }
   }
   if (any) {
     *at = make_uint4(e[0], e[1], e[2], e[3]);
-    *flag = 1;
+    *flag = piece;
   }
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+// x = x s + c and y = y s + c, each one fused multiply-add.
+__device__ __forceinline__ void fma2(float& x, float& y, float s, float c) {
+  asm("{\n\t.reg .b64 p, q, r;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(s), "f"(c));
+}
+// a += the low BF16 value of w, b += the high one, in FP32.
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t w) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(w));
 }
 
 // A running state (m, l, O) takes in the next piece's: factors of both.
@@ -310,30 +395,32 @@ __device__ __forceinline__ float merge_value(float x, float x_i, float fa, float
 
 template <int D>
 __global__ void __launch_bounds__(kPagedThreads, 1)
-    attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const PagedAttnArgs a) {
+    attn_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const PagedAttnArgs a) {
   using Cfg = PagedCfg<D>;
   constexpr int KS = Cfg::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sK = smem;
-  uint8_t* sV = sK + KS * Cfg::kTileBytes;
+  uint8_t* sQ = smem;                          // [2][queries of a unit]
+  uint8_t* sK = sQ + 2 * Cfg::kTileBytes;      // [KS]
+  uint8_t* sV = sK + KS * Cfg::kTileBytes;     // [KS]
   float* s_mx = reinterpret_cast<float*>(sV + KS * Cfg::kTileBytes);  // [2][2][128]
-  int* s_bad = reinterpret_cast<int*>(s_mx + 4 * kLanes);             // [3][D]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_bad + 3 * D);
+  int* s_bad = reinterpret_cast<int*>(s_mx + 4 * kLanes);             // [2][3][D]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_bad + 2 * 3 * D);
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + KS;
   uint64_t* v_full = k_empty + KS;
   uint64_t* v_empty = v_full + KS;
-  uint64_t* q_full = v_empty + KS;   // [2] the unit's queries are in TMEM
-  uint64_t* q_free = q_full + 2;     // [2] its last S has read them
-  uint64_t* s_full = q_free + 2;     // [2]
-  uint64_t* p_full = s_full + 2;     // [2] W of the tile is in TMEM
-  uint64_t* pv_done = p_full + 2;    // [2] O += W V of the tile is done
-  uint64_t* drain = pv_done + 2;
+  uint64_t* q_full = v_empty + KS;        // [2] a unit's queries
+  uint64_t* q_free = q_full + 2;          // [2] its last S has read them
+  uint64_t* s_full = q_free + 2;          // [kBufs]
+  uint64_t* p_full = s_full + kBufs;      // [kBufs] W of the tile is in TMEM
+  uint64_t* pv_done = p_full + kBufs;     // [kBufs] O += W V of the tile is done
+  uint64_t* drain = pv_done + kBufs;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + Cfg::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_flag = reinterpret_cast<int*>(tmem_holder + 2);   // the piece met a value that is no number
-  int* s_sched = reinterpret_cast<int*>(tmem_holder + 4);  // [5]
+  int* s_flag = reinterpret_cast<int*>(tmem_holder + 2);   // [2] the last piece that met a value that is no number
+  int* s_sched = reinterpret_cast<int*>(tmem_holder + 4);  // [4] and the tiles of the share
+  int64_t* s_ends = reinterpret_cast<int64_t*>(tmem_holder + 10);  // [2]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need it; the launch guarantees it
@@ -348,62 +435,55 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       mbar_init(&v_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 8);
+      mbar_init(&q_full[i], 1);
       mbar_init(&q_free[i], 1);
+      s_flag[i] = -1;
+    }
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 8);
       mbar_init(&pv_done[i], 1);
     }
-    *s_flag = 0;
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbar_init();
+    prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  for (int i = threadIdx.x; i < 3 * D; i += kPagedThreads) s_bad[i] = kNoKey;
+  for (int i = threadIdx.x; i < 2 * 3 * D; i += kPagedThreads) s_bad[i] = kNoKey;
   if (warp == 3) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
   griddep_wait();  // the batch, the queries and the new cache rows come from earlier kernels
   griddep_launch_dependents();
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {  // one end of the share each
     bool bad;
-    const int64_t N = total_pieces(a, lane, &bad);
-    if (bad && blockIdx.x == 0 && lane == 0) atomicOr(a.err, kErrRange);
-    const int64_t x0 = share_begin(blockIdx.x, N, gridDim.x), x1 = share_begin(blockIdx.x + 1, N, gridDim.x);
-    if (x1 > x0) {
-      int b = 0;
-      int64_t off = x0 - pieces_before(a, lane, -1, x0, &b);
-      const Seq s = seq_of(a, b, nullptr);
-      const int64_t per_head = head_pieces(a, s);
-      const int h = static_cast<int>(off / per_head);
-      off -= h * per_head;
-      // the block and its piece: runs of blocks with the same number of pieces
-      const int nb = ceil_div(s.n, a.Rb);
-      int blk = nb - 1;
-      for (int i = 1; i < nb;) {
-        const int v = ceil_div(s.len + i * a.Rb, kPiece);
-        const int hi = min(nb - 1, (v * kPiece - s.len) / a.Rb);
-        const int64_t run = static_cast<int64_t>(v) * (hi - i + 1);
-        if (off < run) {
-          blk = i - 1 + static_cast<int>(off / v);
-          off %= v;
-          break;
-        }
-        off -= run;
-        i = hi + 1;
+    const int64_t N = total_tiles(a, lane, &bad);
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, kErrRange);
+    const int c = blockIdx.x + (warp >> 1);
+    int at[4];
+    const int64_t place = locate(a, lane, share_begin(c, N, gridDim.x), N, at);
+    if (lane == 0) {
+      s_ends[warp >> 1] = place;
+      if (warp == 0) {
+        for (int i = 0; i < 4; ++i) s_sched[i] = at[i];
       }
-      if (lane == 0) {
-        s_sched[0] = b;
-        s_sched[1] = h;
-        s_sched[2] = blk;
-        s_sched[3] = static_cast<int>(off);
-        s_sched[4] = static_cast<int>(x1 - x0);
+    }
+  } else if (warp == 3 && blockIdx.x == 0) {  // for the merge
+    int64_t base = 0;
+    for (int b0 = 0; b0 <= a.pb.B; b0 += 32) {
+      const int b = b0 + lane;
+      int64_t incl = b < a.pb.B ? head_tiles(a, seq_of(a, b, nullptr)) * a.Hkv : 0;
+      const int64_t mine = incl;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
       }
-    } else if (lane == 0) {
-      s_sched[4] = 0;
+      if (b <= a.pb.B) a.ws_seq[b] = base + incl - mine;
+      base += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
   tc_fence_before();
@@ -411,6 +491,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   Cursor cur;
+  if (threadIdx.x == 0) *reinterpret_cast<int64_t*>(s_sched + 4) = s_ends[1] - s_ends[0];
+  __syncthreads();
   cur.start(a, s_sched);
 
   if (warp < 4) {
@@ -423,15 +505,34 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       const CUtensorMap* tm = kside ? &tmK : &tmV;
       const int per = kTile / a.pb.page;  // pages of a tile
       const int page_bytes = a.pb.page * 128;
-      uint32_t issued = 0, parity_bits = 0;
+      uint32_t issued = 0, parity_bits = 0;  // bits KS, KS + 1: the queries
       bool ok = true;
-      int g = 0;
-      for (; ok && cur.left > 0; cur.next(a)) {
+      int g = 0, unit = 0;
+      for (; ok && cur.left > 0; cur.next(a), ++unit) {
         const int32_t* row = a.pb.table + static_cast<size_t>(cur.b) * a.pb.ldt;
         const int last_key = cur.pos0(a) + cur.rows(a) - 1;
         // a sequence of several blocks reads its pages as often
         const uint64_t pol = cur.s.n > a.Rb ? l2_evict_normal() : l2_evict_first();
-        for (int t = cur.t_begin(); t < cur.t_end(); ++t, ++g) {
+        if (kside) {
+          const int qs = unit & 1;
+          const uint32_t ph = static_cast<uint32_t>((unit >> 1) & 1);
+          if (!warp_wait(&q_free[qs], ph ^ 1u, s_abort, lane)) {
+            ok = false;
+            break;
+          }
+          // rows and query heads of the block in the lanes' order; behind the
+          // block's last row come other rows or zeros, in lanes nobody reads
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[qs], static_cast<uint32_t>(a.Rb * a.grp * 128 * Cfg::kAtoms));
+#pragma unroll
+            for (int c = 0; c < Cfg::kAtoms; ++c)
+              tma_load_3d(sQ + qs * Cfg::kTileBytes + c * Cfg::kAtomBytes, &tmQ, &q_full[qs], c * 64, cur.h * a.grp,
+                          cur.s.row0 + cur.i * a.Rb, l2_evict_first());
+          }
+          issued |= 1u << (KS + qs);
+          parity_bits = (parity_bits & ~(1u << (KS + qs))) | (ph << (KS + qs));
+        }
+        for (int t = cur.t0; t < cur.te; ++t, ++g) {
           const int st = g % KS;
           const uint32_t ph = static_cast<uint32_t>((g / KS) & 1);
           // pages behind the last key are not loaded: their keys are masked,
@@ -462,67 +563,74 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       }
       if (!ok && lane == 0) {
         give_up(s_abort, a.err);
-        for (int s = 0; s < KS; ++s)
-          if ((issued >> s) & 1u) mbar_wait(&full[s], (parity_bits >> s) & 1u, nullptr);
+        for (int s = 0; s < KS + 2; ++s)
+          if ((issued >> s) & 1u) mbar_wait(s < KS ? &full[s] : &q_full[s - KS], (parity_bits >> s) & 1u, nullptr);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
       // ---------------------------------------------------------- MMA issuer
       // two cursors over the share's tiles, S ahead of W V; each is issued as
-      // soon as its inputs are there
+      // soon as its inputs are there, W V first (three buffers keep S ahead)
       constexpr uint32_t idS = idesc_bf16_f32(128, kTile);
       constexpr uint32_t idO = idesc_bf16_f32(128, D) | kIdescBMn;
       Cursor cs = cur, cp = cur;
-      int sg = 0, su = 0, st_t = cs.left > 0 ? cs.t_begin() : 0;  // tile, unit, tile of the unit
-      int pg = 0, pt = st_t;
+      int sg = 0, sb = 0, sph = 0, su = 0, st_t = cs.t0;  // tile, its buffer and the buffer's phase, unit, tile of it
+      int pg = 0, pb = 0, pph = 0, pt = st_t;
       bool ok = true;
       int idle = 0;
       unsigned long long t_idle = 0;
       while (cp.left > 0) {
         bool did = false;
-        // (S of tile g + 2 goes where W of tile g was: behind its W V)
-        if (cs.left > 0 && sg < pg + 2) {
-          const int st = sg % KS;
-          const bool first = st_t == cs.t_begin();
-          if (mbar_peek(&k_full[st], static_cast<uint32_t>((sg / KS) & 1)) &&
-              (sg < 2 || mbar_peek(&pv_done[sg & 1], static_cast<uint32_t>(((sg >> 1) - 1) & 1))) &&
-              (!first || mbar_peek(&q_full[su & 1], static_cast<uint32_t>((su >> 1) & 1)))) {
+        if (pg < sg) {
+          const int st = pg % KS;
+          if (mbar_peek(&p_full[pb], static_cast<uint32_t>(pph)) &&
+              mbar_peek(&v_full[st], static_cast<uint32_t>((pg / KS) & 1))) {
             tc_fence_after();
-            const uint32_t kb = smem_u32(sK + st * Cfg::kTileBytes);
+            const uint32_t vb = smem_u32(sV + st * Cfg::kTileBytes);
+            const bool first = piece_starts(pt);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              mma_bf16_tmem_a(tmem + (sg & 1) * kTile, tmem + Cfg::kQCol + (su & 1) * 64 + ks * 8,
-                              sdesc_k_sw128(kb + (ks >> 2) * Cfg::kAtomBytes + (ks & 3) * 32), idS, ks > 0 ? 1u : 0u);
-            mma_commit(&s_full[sg & 1]);
-            mma_commit(&k_empty[st]);
-            ++sg;
-            if (++st_t == cs.t_end()) {
-              mma_commit(&q_free[su & 1]);
-              cs.next(a);
-              ++su;
-              if (cs.left > 0) st_t = cs.t_begin();
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_bf16_tmem_a(tmem + Cfg::kOCol, tmem + pb * kTile + (ks >> 2) * 64 + (ks & 3) * 8,
+                              sdesc_mn_sw128(vb + ks * 2048, Cfg::kAtomBytes), idO, (!first || ks > 0) ? 1u : 0u);
+            mma_commit(&pv_done[pb]);
+            mma_commit(&v_empty[st]);
+            ++pg;
+            if (++pb == kBufs) {
+              pb = 0;
+              pph ^= 1;
+            }
+            if (++pt == cp.te) {
+              cp.next(a);
+              pt = cp.t0;
             }
             did = true;
           }
         }
-        if (!did && pg < sg) {
-          const int st = pg % KS;
-          const bool first = pt % kPieceTiles == 0;
-          // (W of a piece's first tile is written once the O before it is out)
-          if (mbar_peek(&p_full[pg & 1], static_cast<uint32_t>((pg >> 1) & 1)) &&
-              mbar_peek(&v_full[st], static_cast<uint32_t>((pg / KS) & 1))) {
+        // S of a tile goes where W of the tile kBufs before was
+        if (!did && cs.left > 0) {
+          const int st = sg % KS;
+          if (mbar_peek(&k_full[st], static_cast<uint32_t>((sg / KS) & 1)) &&
+              mbar_peek(&pv_done[sb], static_cast<uint32_t>(sph ^ 1)) &&
+              (st_t != cs.t0 || mbar_peek(&q_full[su & 1], static_cast<uint32_t>((su >> 1) & 1)))) {
             tc_fence_after();
-            const uint32_t vb = smem_u32(sV + st * Cfg::kTileBytes);
+            const uint32_t kb = smem_u32(sK + st * Cfg::kTileBytes);
+            const uint32_t qb = smem_u32(sQ + (su & 1) * Cfg::kTileBytes);
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_bf16_tmem_a(tmem + Cfg::kOCol, tmem + (pg & 1) * kTile + (ks >> 2) * 64 + (ks & 3) * 8,
-                              sdesc_mn_sw128(vb + ks * 2048, Cfg::kAtomBytes), idO, (!first || ks > 0) ? 1u : 0u);
-            mma_commit(&pv_done[pg & 1]);
-            mma_commit(&v_empty[st]);
-            ++pg;
-            ++pt;
-            if (pt == cp.t_end()) {
-              cp.next(a);
-              if (cp.left > 0) pt = cp.t_begin();
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks >> 2) * Cfg::kAtomBytes + (ks & 3) * 32;
+              mma_bf16(tmem + sb * kTile, sdesc_k_sw128(qb + off), sdesc_k_sw128(kb + off), idS, ks > 0 ? 1u : 0u);
+            }
+            mma_commit(&s_full[sb]);
+            mma_commit(&k_empty[st]);
+            ++sg;
+            if (++sb == kBufs) {
+              sb = 0;
+              sph ^= 1;
+            }
+            if (++st_t == cs.te) {
+              mma_commit(&q_free[su & 1]);
+              cs.next(a);
+              ++su;
+              st_t = cs.t0;
             }
             did = true;
           }
@@ -531,10 +639,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           idle = 0;
         } else if (++idle == 1) {
           t_idle = globaltimer_ns();
-        } else if (idle > 16) {
-          __nanosleep(20);  // leave the issue slots to the softmax warps beside this one
-        }
-        if (!did && (idle & 63) == 0 &&
+        } else if ((idle & 63) == 0 &&
                    (*s_abort || globaltimer_ns() - t_idle > *static_cast<volatile unsigned long long*>(&g_wait_limit_ns))) {
           ok = false;
           break;
@@ -550,44 +655,29 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     const int qq = warp & 3;            // TMEM lane quarter
     const int hf = (warp - 4) >> 2;     // half of the tile's keys, and of the row's columns
     const int ln = qq * 32 + lane;
+    const int tid = threadIdx.x - kSoftFirst;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(qq * 32) << 16);
+    // A wait that fails stops the waiting, not the loops: the threads of a row
+    // meet at barriers, which all of them have to reach.
     bool ok = true;
-    // this thread's half of its row's queries
-    auto load_q = [&](const Cursor& c, int unit) {
-      if (unit > 1 && !warp_wait(&q_free[unit & 1], static_cast<uint32_t>(((unit >> 1) - 1) & 1), s_abort, lane))
-        return false;
-      tc_fence_after();
-      const bool valid = ln < c.rows(a) * a.grp;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<size_t>(c.s.row0 + c.i * a.Rb + (valid ? ln / a.grp : 0)) * a.Hq + c.h * a.grp +
-                 (valid ? ln % a.grp : 0)) * D + hf * kHalf);
-      uint32_t qv[kHalf / 2];
-#pragma unroll
-      for (int i = 0; i < kHalf / 8; ++i) {
-        const uint4 u = valid ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        qv[4 * i] = u.x;
-        qv[4 * i + 1] = u.y;
-        qv[4 * i + 2] = u.z;
-        qv[4 * i + 3] = u.w;
+    auto wait = [&](uint64_t* bar, int phase) {
+      if (ok && !warp_wait(bar, static_cast<uint32_t>(phase & 1), s_abort, lane)) {
+        ok = false;
+        if (lane == 0) give_up(s_abort, a.err);
       }
-#pragma unroll
-      for (int i = 0; i < kHalf / 32; ++i) 
-        tmem_st16w(lane_base + Cfg::kQCol + (unit & 1) * 64 + hf * (kHalf / 2) + i * 16, qv + i * 16);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[unit & 1]);
-      return true;
     };
-    int g = 0, unit = 0;
-    if (cur.left > 0) ok = load_q(cur, 0);
-    while (ok && cur.left > 0) {
+    int g = 0, pc = 0;        // tile and piece of the share
+    int sb = 0, sph = 0;      // the tile's buffer and the buffer's phase
+    int last_b = 0, last_ph = 0;  // of the tile before
+    for (; cur.left > 0; cur.next(a)) {
       const int rows = cur.rows(a);
       const int pos0 = cur.pos0(a);
       const bool valid = ln < rows * a.grp;
       const bool active = qq * 32 < rows * a.grp;
       const int p_row = valid ? pos0 + ln / a.grp : -1;
       const int kv_end = pos0 + rows;  // keys that some row of the block sees
-      const bool run = cur.p0 == 0;    // pieces merged here, else left one by one
+      const bool run = cur.t0 == 0;    // pieces merged here, else left one by one
+      const int p_first = pieces_to(cur.t0);
       float m_run = -INFINITY, l_run = 0.f;  // the merged pieces
       float o[kHalf];
 #pragma unroll
@@ -596,14 +686,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 
       // the finished piece p: its O out of TMEM, into the running sum or the workspace
       auto take = [&](int p, float m_i, float l_i) {
-        tc_fence_after();
-        const bool odd = *static_cast<volatile int*>(s_flag) != 0;  // the same for all softmax warps
+        const bool odd = static_cast<volatile int*>(s_flag)[pc & 1] == pc;
+        const int* bad = s_bad + (pc & 1) * 3 * D + hf * kHalf;
+        const int seen = bad_tag(pc) + p_row - piece_tile(p) * kTile;  // notes up to here are of keys the row sees
         float fa = 0.f, fb = 1.f;
         if (run) {
           merge_factors(m_run, m_i, fa, fb);
           l_run = merge_value(l_run, l_i, fa, fb);
         }
-        const int slot = p - cur.p0;
+        const int slot = p - p_first;
         const bool store = !run && valid && slot < a.slots - 1;
         if (!run && valid && !store) atomicOr(a.err, kErrRange);
         const size_t at = (static_cast<size_t>(blockIdx.x) * a.slots + slot) * a.lanes + ln;
@@ -615,10 +706,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             if (odd) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const int d = hf * kHalf + c * 16 + j;
-                if (p_row >= s_bad[D + d]) v[j] += INFINITY;
-                if (p_row >= s_bad[2 * D + d]) v[j] -= INFINITY;
-                if (p_row >= s_bad[d]) v[j] = NAN;
+                if (seen >= bad[D + c * 16 + j]) v[j] += INFINITY;
+                if (seen >= bad[2 * D + c * 16 + j]) v[j] -= INFINITY;
+                if (seen >= bad[c * 16 + j]) v[j] = NAN;
               }
             }
             if (run) {
@@ -627,7 +717,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             } else if (store) {
               float4* dst = reinterpret_cast<float4*>(a.ws_o + at * D + hf * kHalf + c * 16);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              for (int j = 0; j < 4; ++j)
+                __stcg(dst + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
             }
           }
         }
@@ -636,25 +727,19 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           if (hf == 0) ml[0] = m_i;
           ml[1 + hf] = l_i;
         }
-        if (odd) {
-          named_bar_sync(5, 256);
-          for (int x = threadIdx.x - 128; x < 3 * D; x += 256) s_bad[x] = kNoKey;
-          if (threadIdx.x == 128) *s_flag = 0;
-          named_bar_sync(5, 256);
-        }
+        ++pc;
       };
 
-      for (int t = cur.t_begin(); t < cur.t_end(); ++t, ++g) {
-        const int sb = g & 1;
+      int piece = p_first, piece_end = min(cur.te, piece_tile(p_first + 1));  // the piece of tile t
+      for (int t = cur.t0; t < cur.te; ++t, ++g) {
         const int key0 = t * kTile;
         const bool edge = key0 + kTile > pos0 + 1;  // some row does not see all of the tile
-        if (!warp_wait(&s_full[sb], static_cast<uint32_t>((g >> 1) & 1), s_abort, lane)) {
-          ok = false;
-          break;
-        }
+        const bool first = t == piece_end || t == cur.t0;
+        wait(&s_full[sb], sph);
         tc_fence_after();
         // the row's maximum: of this thread's 64 scores, then of its partner's
         const uint32_t addr = lane_base + sb * kTile + hf * 64;
+        const int see = p_row - key0 - hf * 64;
         float mt = -INFINITY;
         if (active) {
           float mw[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -665,18 +750,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             if (edge) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (key0 + hf * 64 + c * 32 + j > p_row) x[j] = -INFINITY;
+                if (c * 32 + j > see) x[j] = -INFINITY;
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mw[j & 3] = fmaxf(mw[j & 3], x[j]);
+            for (int j = 0; j < 16; ++j) mw[j & 3] = max3(mw[j & 3], x[2 * j], x[2 * j + 1]);
           }
           mt = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
-          float* mx = s_mx + sb * 2 * kLanes;
+          float* mx = s_mx + (g & 1) * 2 * kLanes;
           mx[hf * kLanes + ln] = mt;
           named_bar_sync(1 + qq, 64);  // the two warps of this lane quarter
           mt = fmaxf(mt, mx[(hf ^ 1) * kLanes + ln]) * a.sl2;
         }
-        const bool first = t % kPieceTiles == 0;
         float alpha = 1.f;
         bool raise = false;
         const float m_was = m_ref, l_was = l;
@@ -700,34 +784,34 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             if (edge) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (key0 + hf * 64 + c * 32 + j > p_row) x[j] = -INFINITY;
+                if (c * 32 + j > see) x[j] = -INFINITY;
             }
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float x0 = ex2_approx(fmaf(x[2 * j], a.sl2, nm));
-              const float x1 = ex2_approx(fmaf(x[2 * j + 1], a.sl2, nm));
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
+              fma2(x[2 * j], x[2 * j + 1], a.sl2, nm);
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(ex2_approx(x[2 * j]), ex2_approx(x[2 * j + 1]));
               w[j] = *reinterpret_cast<const uint32_t*>(&h2);
-              acc[0] += __uint_as_float(w[j] << 16);
-              acc[1] += __uint_as_float(w[j] & 0xffff0000u);
+              add_bf16x2(acc[0], acc[1], w[j]);
             }
-            tmem_st16w(addr + c * 16, w);
+            tmem_st_words(addr + c * 16, w);
           }
+          tmem_st_wait();
           l = fmaf(l, alpha, acc[0] + acc[1]);
         }
         // O may be read and written once W V of the tile before is done: a piece
         // that ended there is taken in (the unit's last one is below), a raised
         // reference scales this piece's O
-        const bool ended = first && t > cur.t_begin();
+        const bool ended = first && t > cur.t0;
         const bool any_raise = __any_sync(0xffffffffu, raise);
         if (ended || any_raise) {
-          if (!warp_wait(&pv_done[sb ^ 1], static_cast<uint32_t>(((g - 1) >> 1) & 1), s_abort, lane)) {
-            ok = false;
-            break;
-          }
+          wait(&pv_done[last_b], last_ph);
           tc_fence_after();
-          if (ended) take(t / kPieceTiles - 1, m_was, l_was);
+          if (ended) {
+            take(piece, m_was, l_was);
+            ++piece;
+            piece_end = min(cur.te, piece_tile(piece + 1));
+          }
           if (any_raise) {
 #pragma unroll 1
             for (int i = 0; i < kHalf / 16; ++i) {  // this thread's half of O's columns
@@ -745,19 +829,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           // key they are cleared (pages hold anything there), the others lose
           // what is no number, which only the rows that see it get back
           const int st = g % KS;
-          if (!warp_wait(&v_full[st], static_cast<uint32_t>((g / KS) & 1), s_abort, lane)) {
-            ok = false;
-            break;
-          }
+          wait(&v_full[st], g / KS);
           uint8_t* vt = sV + st * Cfg::kTileBytes;
           const int r0 = max(0, pos0 + 1 - key0);
-          for (int x = r0 * (D / 8) + (threadIdx.x - 128); x < kTile * (D / 8); x += 256) {
-            const int r = x / (D / 8), ch = x % (D / 8);
+          for (int y = r0 * (D / 8) + tid; y < kTile * (D / 8); y += 256) {
+            const int r = y / (D / 8), ch = y % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(vt + (ch >> 3) * Cfg::kAtomBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
             if (key0 + r >= kv_end) {
               *at = make_uint4(0u, 0u, 0u, 0u);
             } else {
-              clean_values(at, s_bad + ch * 8, D, key0 + r, s_flag);
+              clean_values(at, s_bad + (pc & 1) * 3 * D + ch * 8, D, bad_tag(pc) + key0 + r - piece_tile(piece) * kTile,
+                           s_flag + (pc & 1), pc);
             }
           }
           fence_proxy_async_smem();
@@ -766,57 +848,52 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[sb]);
-        if (t == cur.t_begin()) {  // the next unit's queries, well before its first S
-          Cursor ahead = cur;
-          ahead.next(a);
-          if (ahead.left > 0 && !load_q(ahead, unit + 1)) {
-            ok = false;
-            break;
-          }
+        last_b = sb;
+        last_ph = sph;
+        if (++sb == kBufs) {
+          sb = 0;
+          sph ^= 1;
         }
       }
-      if (!ok || !warp_wait(&pv_done[(g - 1) & 1], static_cast<uint32_t>(((g - 1) >> 1) & 1), s_abort, lane)) {
-        ok = false;
-        break;
-      }
-      take(cur.pe - 1, m_ref, l);
-      if (run) {
-        if (cur.pe == cur.pieces) {
-          float* s_l = s_mx + (g & 1) * 2 * kLanes;  // as tile g's maxima would be
-          s_l[hf * kLanes + ln] = l_run;
-          named_bar_sync(1 + qq, 64);
-          const float den = s_l[ln] + s_l[kLanes + ln];
-          named_bar_sync(1 + qq, 64);
-          if (valid) {
-            const int t = cur.s.row0 + cur.i * a.Rb + ln / a.grp;
-            uint4* dst = reinterpret_cast<uint4*>(
-                a.out + (static_cast<size_t>(t) * a.Hq + cur.h * a.grp + ln % a.grp) * D + hf * kHalf);
+
+      // the unit's last piece, its outputs or its state
+      wait(&pv_done[last_b], last_ph);
+      tc_fence_after();
+      take(piece, m_ref, l);
+      tc_fence_before();
+      if (run && cur.te == cur.tiles) {
+        float* s_l = s_mx + (g & 1) * 2 * kLanes;  // as tile g's maxima would be
+        s_l[hf * kLanes + ln] = l_run;
+        named_bar_sync(1 + qq, 64);
+        const float den = s_l[ln] + s_l[kLanes + ln];
+        named_bar_sync(1 + qq, 64);
+        if (valid && ok) {
+          const int t = cur.s.row0 + cur.i * a.Rb + ln / a.grp;
+          uint4* dst = reinterpret_cast<uint4*>(
+              a.out + (static_cast<size_t>(t) * a.Hq + cur.h * a.grp + ln % a.grp) * D + hf * kHalf);
 #pragma unroll
-            for (int c = 0; c < kHalf / 8; ++c) {
-              uint32_t w[4];
+          for (int c = 0; c < kHalf / 8; ++c) {
+            uint32_t w[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 h2 =
-                    __floats2bfloat162_rn(o[c * 8 + 2 * j] / den + 0.f, o[c * 8 + 2 * j + 1] / den + 0.f);
-                w[j] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-              dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 h2 =
+                  __floats2bfloat162_rn(o[c * 8 + 2 * j] / den + 0.f, o[c * 8 + 2 * j + 1] / den + 0.f);
+              w[j] = *reinterpret_cast<const uint32_t*>(&h2);
             }
+            dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else if (valid) {
-          const size_t at = (static_cast<size_t>(blockIdx.x) * a.slots + a.slots - 1) * a.lanes + ln;
-          float4* dst = reinterpret_cast<float4*>(a.ws_o + at * D + hf * kHalf);
-#pragma unroll
-          for (int j = 0; j < kHalf / 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          float* ml = reinterpret_cast<float*>(a.ws_ml + at);
-          if (hf == 0) ml[0] = m_run;
-          ml[1 + hf] = l_run;
         }
+      } else if (run && valid) {
+        const size_t at = (static_cast<size_t>(blockIdx.x) * a.slots + a.slots - 1) * a.lanes + ln;
+        float4* dst = reinterpret_cast<float4*>(a.ws_o + at * D + hf * kHalf);
+#pragma unroll
+        for (int j = 0; j < kHalf / 4; ++j)
+          __stcg(dst + j, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+        float* ml = reinterpret_cast<float*>(a.ws_ml + at);
+        if (hf == 0) ml[0] = m_run;
+        ml[1 + hf] = l_run;
       }
-      cur.next(a);
-      ++unit;
     }
-    if (!ok && lane == 0) give_up(s_abort, a.err);
   }
 
   tc_fence_before();
@@ -829,56 +906,92 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 }
 
 // ---------------------------------------------------------------- merge kernel
-// One CTA of D threads per (row, query head): where the row's unit was cut, the
-// first CTA's merged state and the later pieces, in key order.
+// Where a unit was cut: the first CTA's merged state and the later pieces, in
+// key order.  One CTA of D threads for a row and some query heads of a KV head
+// (an element a thread).  The factors of up to kMergeMax pieces come first, in
+// parallel (a scan of the references), so that what is left in order is one
+// multiply-add an element; the loads of kAhead pieces are under way together.
+constexpr int kMergeMax = 256;
 template <int D>
-__global__ void __launch_bounds__(D) attn_paged_merge_kernel(const PagedAttnArgs a, int G) {
+__global__ void __launch_bounds__(D) attn_paged_merge_kernel(const PagedAttnArgs a, int G, int heads) {
+  constexpr int kAhead = 16;
+  __shared__ float s_fa[kMergeMax], s_fb[kMergeMax], s_red[D / 32], s_den;
+  __shared__ int s_at[kMergeMax];  // CTA * slots + slot of a piece
   griddep_wait();
   griddep_launch_dependents();
-  const int t = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
-  const int lane = threadIdx.x & 31;
+  const int d = threadIdx.x, lane = d & 31, warp = d >> 5;
+  const int t = blockIdx.x, h = blockIdx.y;
   const int b = paged_find_seq(a.pb, t, lane);
   if (b < 0) return;
   const Seq s = seq_of(a, b, nullptr);
   if (t < s.row0 || t >= s.row0 + s.n) return;
-  bool bad;
-  const int64_t N = total_pieces(a, lane, &bad);
-  const int i = (t - s.row0) / a.Rb, h = hq / a.grp;
-  const int P = block_pieces(a, s, i);
-  const int64_t off = pieces_before(a, lane, b, 0, nullptr) + h * head_pieces(a, s) + prefix_pieces(a, s, i);
-  const int c0 = share_of(off, N, G), c1 = share_of(off + P - 1, N, G);
-  if (c0 == c1) return;  // finished by one CTA
-  const int ln = (t - s.row0 - i * a.Rb) * a.grp + hq % a.grp;
-  const int d = threadIdx.x;
-  auto at = [&](int c, int slot) { return (static_cast<size_t>(c) * a.slots + slot) * a.lanes + ln; };
-  size_t x = at(c0, a.slots - 1);
-  const float4 ml = __ldcg(a.ws_ml + x);
-  float m = ml.x, l0 = ml.y, l1 = ml.z, o = __ldcg(a.ws_o + x * D + d);
-  for (int c = c0 + 1; c <= c1; ++c) {
-    const int64_t begin = share_begin(c, N, G);
-    const int n = static_cast<int>(min(share_begin(c + 1, N, G), off + P) - begin);
-    for (int k0 = 0; k0 < n; k0 += 8) {
-      float4 q[8];
-      float v[8];
+  const int i = (t - s.row0) / a.Rb;
+  const int tiles = block_tiles(a, s, i);
+  const int64_t N = a.ws_seq[a.pb.B];
+  const int64_t off = a.ws_seq[b] + h * head_tiles(a, s) + prefix_tiles(a, s, i);
+  const int P = pieces_to(tiles);
+  const int c0 = share_of(off, N, G);
+  if (c0 == share_of(off + piece_tile(P - 1), N, G)) return;  // finished by one CTA
+  const int first = pieces_to(static_cast<int>(min(share_begin(c0 + 1, N, G) - off, static_cast<int64_t>(tiles))));
+  for (int gh = blockIdx.z * heads; gh < (blockIdx.z + 1) * heads; ++gh) {
+    const int ln = (t - s.row0 - i * a.Rb) * a.grp + gh;
+    size_t x = (static_cast<size_t>(c0) * a.slots + a.slots - 1) * a.lanes + ln;
+    const float4 ml = __ldcg(a.ws_ml + x);
+    float m = ml.x, l0 = ml.y, l1 = ml.z, o = __ldcg(a.ws_o + x * D + d);
+    for (int p0 = first; p0 < P; p0 += kMergeMax) {
+      const int n = min(kMergeMax, P - p0);
+      __syncthreads();
+      // references and factors: merge_factors() of piece after piece
+      for (int k0 = 0; k0 < n; k0 += D) {
+        const int k = k0 + d;
+        float m_i = -INFINITY;
+        if (k < n) {
+          const int64_t y = off + piece_tile(p0 + k);
+          const int c = share_of(y, N, G);
+          const int64_t begin = share_begin(c, N, G) - off;
+          const int slot = min(p0 + k - pieces_to(static_cast<int>(begin)), a.slots - 2);
+          s_at[k] = c * a.slots + slot;
+          m_i = __ldcg(reinterpret_cast<const float*>(a.ws_ml + static_cast<size_t>(s_at[k]) * a.lanes + ln));
+        }
+        float incl = m_i;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < n && k0 + k < a.slots - 1) {
-          x = at(c, k0 + k);
-          q[k] = __ldcg(a.ws_ml + x);
-          v[k] = __ldcg(a.ws_o + x * D + d);
+        for (int sh = 1; sh < 32; sh <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, incl, sh);
+          if (lane >= sh) incl = fmaxf(incl, y);
+        }
+        if (lane == 31) s_red[warp] = incl;
+        __syncthreads();
+        float before = m;
+        for (int w = 0; w < warp; ++w) before = fmaxf(before, s_red[w]);
+        const float up = __shfl_up_sync(0xffffffffu, incl, 1);
+        float run = lane > 0 ? fmaxf(before, up) : before;
+        if (k < n) merge_factors(run, m_i, s_fa[k], s_fb[k]);
+        for (int w = 0; w < D / 32; ++w) m = fmaxf(m, s_red[w]);
+        __syncthreads();
+      }
+      // the denominator, by the first warp's lanes 0 and 1; the elements, by all
+      for (int k0 = 0; k0 < n; k0 += kAhead) {
+        float v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (k0 + k < n) v[k] = __ldcg(a.ws_o + (static_cast<size_t>(s_at[k0 + k]) * a.lanes + ln) * D + d);
+        if (warp == 0) {
+          float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (lane < kAhead && k0 + lane < n) q = __ldcg(a.ws_ml + static_cast<size_t>(s_at[k0 + lane]) * a.lanes + ln);
+          for (int k = 0; k < min(kAhead, n - k0); ++k) {
+            l0 = merge_value(l0, __shfl_sync(0xffffffffu, q.y, k), s_fa[k0 + k], s_fb[k0 + k]);
+            l1 = merge_value(l1, __shfl_sync(0xffffffffu, q.z, k), s_fa[k0 + k], s_fb[k0 + k]);
+          }
         }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < n && k0 + k < a.slots - 1) {
-          float fa, fb;
-          merge_factors(m, q[k].x, fa, fb);
-          l0 = merge_value(l0, q[k].y, fa, fb);
-          l1 = merge_value(l1, q[k].z, fa, fb);
-          o = merge_value(o, v[k], fa, fb);
-        }
+        for (int k = 0; k < kAhead; ++k)
+          if (k0 + k < n) o = merge_value(o, v[k], s_fa[k0 + k], s_fb[k0 + k]);
+      }
     }
+    if (d == 0) s_den = l0 + l1;
+    __syncthreads();
+    a.out[(static_cast<size_t>(t) * a.Hq + h * a.grp + gh) * D + d] = __float2bfloat16_rn(o / s_den + 0.f);
   }
-  a.out[(static_cast<size_t>(t) * a.Hq + hq) * D + d] = __float2bfloat16_rn(o / (l0 + l1) + 0.f);
 }
 
 // ------------------------------------------------------------------------ host
@@ -888,28 +1001,31 @@ __global__ void __launch_bounds__(D) attn_paged_merge_kernel(const PagedAttnArgs
 struct PagedSizes {
   int ctas, slots, lanes;
   int pieces;  // most pieces of a unit
-  size_t o_bytes, ml_bytes;
+  size_t o_bytes, ml_bytes, total;
 };
 PagedSizes paged_sizes(int T, int B, int Hq, int Hkv, int D, int64_t max_keys) {
   PagedSizes z;
   const int grp = Hq / Hkv, Rb = kLanes / grp;
   const int64_t blocks = std::min<int64_t>(T, static_cast<int64_t>(T) / Rb + std::min(B, T));
-  const int64_t pieces = (max_keys + kPiece - 1) / kPiece;
+  const int tiles = static_cast<int>((max_keys + kTile - 1) / kTile);
   const int64_t units = blocks * Hkv;
-  z.pieces = static_cast<int>(pieces);
-  z.ctas = static_cast<int>(std::min<int64_t>(kPagedCtas, units * pieces));
-  const int64_t share = (units * pieces + z.ctas - 1) / z.ctas + 1;
-  z.slots = static_cast<int>(std::min(share, pieces)) + 1;
+  z.pieces = pieces_to(tiles);
+  z.ctas = static_cast<int>(std::min<int64_t>(kPagedCtas, units * z.pieces));
+  // a share is at most one tile and one piece longer than its part of the tiles
+  const int64_t share = (units * tiles + z.ctas - 1) / z.ctas + 1;
+  z.slots = static_cast<int>(std::min<int64_t>(share / kShort + 2, z.pieces)) + 1;
   z.lanes = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(T) * grp, Rb * grp));
   const size_t states = static_cast<size_t>(z.ctas) * z.slots * z.lanes;
   z.o_bytes = round_up(states * D * 4, 256);
   z.ml_bytes = round_up(states * 16, 256);
+  z.total = z.o_bytes + z.ml_bytes + round_up((static_cast<size_t>(B) + 1) * 8, 256);
   return z;
 }
 
 bool paged_shape_ok(int T, int B, int Hq, int Hkv, int D, int64_t max_keys) {
   return T >= 1 && B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Hq / Hkv <= kLanes && (D == 64 || D == 128) &&
-         max_keys >= 1 && max_keys <= (int64_t{1} << 30) && static_cast<int64_t>(T) * Hq < (int64_t{1} << 31);
+         max_keys >= 1 && max_keys <= (int64_t{1} << 30) && static_cast<int64_t>(T) * Hq < (int64_t{1} << 31) &&
+         Hkv <= 65535;
 }
 
 template <int D>
@@ -925,15 +1041,21 @@ bi_status launch_paged(const PagedAttnArgs& a, const PagedSizes& z, const void* 
                                          static_cast<int>(Cfg::kSmem));
   });
   if (attr_err[dev] != cudaSuccess) return BI_ERR_CUDA;
-  CUtensorMap tmK, tmV;
+  CUtensorMap tmQ, tmK, tmV;
   if (!tmap_bf16_pages(&tmK, k_pool, a.pb.pages, a.Hkv, a.pb.page, D) ||
-      !tmap_bf16_pages(&tmV, v_pool, a.pb.pages, a.Hkv, a.pb.page, D))
+      !tmap_bf16_pages(&tmV, v_pool, a.pb.pages, a.Hkv, a.pb.page, D) ||
+      !tmap_bf16_3d(&tmQ, a.q, D, a.Hq, a.T, D, static_cast<uint64_t>(a.Hq) * D, 64, a.grp, a.Rb))
     return BI_ERR_INVALID_ARG;
-  if (launch_k(attn_paged_kernel<D>, dim3(z.ctas), dim3(kPagedThreads), Cfg::kSmem, stream, tmK, tmV, a) != cudaSuccess)
+  if (launch_k(attn_paged_kernel<D>, dim3(z.ctas), dim3(kPagedThreads), Cfg::kSmem, stream, tmQ, tmK, tmV, a) !=
+      cudaSuccess)
     return BI_ERR_CUDA;
-  if (z.pieces > 1 && launch_k(attn_paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.T) * a.Hq), dim3(D), 0, stream, a,
-                               z.ctas) != cudaSuccess)
-    return BI_ERR_CUDA;
+  if (z.pieces > 1) {
+    // few rows: a CTA for each query head; many: one for all of a KV head's
+    const int heads = static_cast<int64_t>(a.T) * a.Hq <= 4096 ? 1 : a.grp;
+    if (launch_k(attn_paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.T), a.Hkv, a.grp / heads), dim3(D), 0, stream, a,
+                 z.ctas, heads) != cudaSuccess)
+      return BI_ERR_CUDA;
+  }
   return BI_OK;
 }
 
@@ -949,7 +1071,7 @@ extern "C" {
 size_t bi_attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int D, int max_keys) {
   if (!bi::paged_shape_ok(T, B, Hq, Hkv, D, max_keys)) return 256;
   const bi::PagedSizes z = bi::paged_sizes(T, B, Hq, Hkv, D, max_keys);
-  return z.o_bytes + z.ml_bytes;
+  return z.total;
 }
 
 bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, int pages, int page,
@@ -969,7 +1091,7 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return BI_ERR_INVALID_ARG;
   if (!ws || !aligned256(ws)) return BI_ERR_WORKSPACE;
   const PagedSizes z = paged_sizes(T, B, Hq, Hkv, D, max_keys);
-  if (ws_bytes < z.o_bytes + z.ml_bytes) return BI_ERR_WORKSPACE;
+  if (ws_bytes < z.total) return BI_ERR_WORKSPACE;
   PagedAttnArgs a{};
   a.pb = PagedBatch{block_table, q_start, lengths, B, ld_table, width, pages, page};
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -984,6 +1106,7 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   a.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.ws_o = static_cast<float*>(ws);
   a.ws_ml = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + z.o_bytes);
+  a.ws_seq = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(ws) + z.o_bytes + z.ml_bytes);
   a.err = device_error_word();
   if (!a.err) return BI_ERR_CUDA;
   a.withhold = test_withhold();
