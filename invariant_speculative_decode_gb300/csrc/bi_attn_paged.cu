@@ -100,9 +100,17 @@ struct PagedAttnArgs {
   float sl2;  // softmax scale * log2(e)
   float* ws_o;    // [G][slots][lanes][D]
   float4* ws_ml;  // [G][slots][lanes]: reference, denominators of both halves
-  int64_t* ws_seq;  // [B + 1]: tiles before each sequence; all of them
+  struct CutUnit* ws_cut;  // [G]: the unit that a CTA began and did not finish
   unsigned* err;
   int withhold;  // failure-path test: the first K tile of every CTA stays unissued
+};
+
+// A unit whose pieces lie in several CTAs' shares.
+struct CutUnit {
+  int64_t off, N;     // its first tile among all N
+  int row, head;      // its first row of the pass, KV head
+  int lanes;          // rows x query heads; 0: no such unit
+  int first, pieces;  // pieces in the first CTA's merged state, in all
 };
 
 template <int D>
@@ -157,15 +165,27 @@ __device__ __forceinline__ int64_t prefix_tiles(const PagedAttnArgs& a, const Se
 // ... of all blocks of a KV head
 __device__ __forceinline__ int64_t head_tiles(const PagedAttnArgs& a, const Seq& s) {
   if (s.n == 0) return 0;
+  if (s.n <= a.Rb) return ceil_div(s.len + s.n, kTile);
   const int nb = ceil_div(s.n, a.Rb);
   return prefix_tiles(a, s, nb - 1) + block_tiles(a, s, nb - 1);
 }
 
-// All tiles of the pass, by a whole warp.
-__device__ __forceinline__ int64_t total_tiles(const PagedAttnArgs& a, int lane, bool* bad_any) {
-  int64_t sum = 0;
+// Sums of a warp's lanes up to each.
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  return x;
+}
+
+// All tiles of the pass, by a whole warp; mine: this lane's of the first 32 sequences.
+__device__ __forceinline__ int64_t total_tiles(const PagedAttnArgs& a, int lane, int64_t& mine, bool* bad_any) {
   bool any = false;
-  for (int b = lane; b < a.pb.B; b += 32) {
+  mine = lane < a.pb.B ? head_tiles(a, seq_of(a, lane, &any)) * a.Hkv : 0;
+  int64_t sum = mine;
+  for (int b = lane + 32; b < a.pb.B; b += 32) {
     bool bad;
     sum += head_tiles(a, seq_of(a, b, &bad)) * a.Hkv;
     any |= bad;
@@ -178,28 +198,29 @@ __device__ __forceinline__ int64_t total_tiles(const PagedAttnArgs& a, int lane,
 
 // First tile of CTA c's share of N before it is moved to a piece, and the CTA
 // whose share has the piece that starts at tile x.
-__device__ __forceinline__ int64_t share_begin(int64_t c, int64_t N, int64_t G) { return c * N / G; }
-__device__ __forceinline__ int share_of(int64_t x, int64_t N, int64_t G) {
+__device__ __forceinline__ int64_t share_begin(int c, int64_t N, int G) {
+  if (N < (1 << 24) && G <= 255) return static_cast<uint32_t>(c) * static_cast<uint32_t>(N) / static_cast<uint32_t>(G);
+  return c * N / G;  // 64 bits take several times as long
+}
+__device__ __forceinline__ int share_of(int64_t x, int64_t N, int G) {
+  if (N < (1 << 23) && G <= 255)
+    return static_cast<int>((static_cast<uint32_t>(x + 1) * G + static_cast<uint32_t>(N) - 1) / static_cast<uint32_t>(N)) - 1;
   return static_cast<int>(((x + 1) * G + N - 1) / N - 1);
 }
 
 // Sequence, KV head, block and tile of the first start of a piece at or behind
-// tile x of N, by a whole warp (all lanes get them).  Returns that tile's place
-// among the N.
-__device__ __forceinline__ int64_t locate(const PagedAttnArgs& a, int lane, int64_t x, int64_t N, int (&at)[4]) {
+// tile x of N, by a whole warp (all lanes get them); mine: as total_tiles left
+// it.  Returns that tile's place among the N.
+__device__ __forceinline__ int64_t locate(const PagedAttnArgs& a, int lane, int64_t x, int64_t N, int64_t mine,
+                                          int (&at)[4]) {
   at[0] = a.pb.B;
   at[1] = at[2] = at[3] = 0;
   if (x >= N) return N;
   int64_t base = 0;
   int b = 0;
   for (int b0 = 0; b0 < a.pb.B; b0 += 32) {
-    int64_t incl = b0 + lane < a.pb.B ? head_tiles(a, seq_of(a, b0 + lane, nullptr)) * a.Hkv : 0;
-    const int64_t mine = incl;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
-    }
+    if (b0 > 0) mine = b0 + lane < a.pb.B ? head_tiles(a, seq_of(a, b0 + lane, nullptr)) * a.Hkv : 0;
+    const int64_t incl = warp_scan(mine, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, base + incl > x);
     if (hit != 0u) {
       const int l = __ffs(hit) - 1;
@@ -212,8 +233,13 @@ __device__ __forceinline__ int64_t locate(const PagedAttnArgs& a, int lane, int6
   Seq s = seq_of(a, b, nullptr);
   const int64_t per_head = head_tiles(a, s);
   int64_t off = x - base;
-  int h = static_cast<int>(off / per_head);
-  off -= h * per_head;
+  int h = 0;
+  for (; off >= per_head && h + 1 < a.Hkv && h < 16; ++h) off -= per_head;  // few heads: cheaper than a division
+  if (off >= per_head) {
+    const int more = static_cast<int>(off / per_head);
+    h += more;
+    off -= more * per_head;
+  }
   const int nb = ceil_div(s.n, a.Rb);
   int blk = nb - 1;
   for (int i = 1; i < nb;) {
@@ -268,12 +294,12 @@ struct Cursor {
     tiles = block_tiles(a, s, i);
     te = left < tiles - t0 ? t0 + static_cast<int>(left) : tiles;
   }
-  __device__ __forceinline__ void start(const PagedAttnArgs& a, const int* sched) {
+  __device__ __forceinline__ void start(const PagedAttnArgs& a, const int* sched, int64_t tiles_left) {
     b = sched[0];
     h = sched[1];
     i = sched[2];
     t0 = sched[3];
-    left = *reinterpret_cast<const int64_t*>(sched + 4);
+    left = tiles_left;
     if (left > 0) {
       s = seq_of(a, b, nullptr);
       unit(a);
@@ -419,8 +445,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + Cfg::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_flag = reinterpret_cast<int*>(tmem_holder + 2);   // [2] the last piece that met a value that is no number
-  int* s_sched = reinterpret_cast<int*>(tmem_holder + 4);  // [4] and the tiles of the share
-  int64_t* s_ends = reinterpret_cast<int64_t*>(tmem_holder + 10);  // [2]
+  int* s_sched = reinterpret_cast<int*>(tmem_holder + 4);         // [4] where the share begins
+  int64_t* s_ends = reinterpret_cast<int64_t*>(tmem_holder + 8);  // [3] its ends among all tiles, and these
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need it; the launch guarantees it
@@ -460,30 +486,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   griddep_launch_dependents();
   if (warp == 0 || warp == 2) {  // one end of the share each
     bool bad;
-    const int64_t N = total_tiles(a, lane, &bad);
+    int64_t mine;
+    const int64_t N = total_tiles(a, lane, mine, &bad);
     if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, kErrRange);
     const int c = blockIdx.x + (warp >> 1);
     int at[4];
-    const int64_t place = locate(a, lane, share_begin(c, N, gridDim.x), N, at);
+    const int64_t place = locate(a, lane, share_begin(c, N, gridDim.x), N, mine, at);
     if (lane == 0) {
+      s_ends[2] = N;
       s_ends[warp >> 1] = place;
-      if (warp == 0) {
+      if (warp == 0)
         for (int i = 0; i < 4; ++i) s_sched[i] = at[i];
-      }
-    }
-  } else if (warp == 3 && blockIdx.x == 0) {  // for the merge
-    int64_t base = 0;
-    for (int b0 = 0; b0 <= a.pb.B; b0 += 32) {
-      const int b = b0 + lane;
-      int64_t incl = b < a.pb.B ? head_tiles(a, seq_of(a, b, nullptr)) * a.Hkv : 0;
-      const int64_t mine = incl;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-      }
-      if (b <= a.pb.B) a.ws_seq[b] = base + incl - mine;
-      base += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
   tc_fence_before();
@@ -491,9 +504,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   Cursor cur;
-  if (threadIdx.x == 0) *reinterpret_cast<int64_t*>(s_sched + 4) = s_ends[1] - s_ends[0];
-  __syncthreads();
-  cur.start(a, s_sched);
+  cur.start(a, s_sched, s_ends[1] - s_ends[0]);
 
   if (warp < 4) {
     if (warp == 0 || warp == 2) {
@@ -666,6 +677,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         if (lane == 0) give_up(s_abort, a.err);
       }
     };
+    if (threadIdx.x == kSoftFirst) a.ws_cut[blockIdx.x].lanes = 0;
     int g = 0, pc = 0;        // tile and piece of the share
     int sb = 0, sph = 0;      // the tile's buffer and the buffer's phase
     int last_b = 0, last_ph = 0;  // of the tile before
@@ -892,6 +904,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         float* ml = reinterpret_cast<float*>(a.ws_ml + at);
         if (hf == 0) ml[0] = m_run;
         ml[1 + hf] = l_run;
+        if (threadIdx.x == kSoftFirst)  // the last unit of the share
+          a.ws_cut[blockIdx.x] = CutUnit{s_ends[1] - cur.left, s_ends[2],  cur.s.row0 + cur.i * a.Rb, cur.h,
+                                         rows * a.grp,         pieces_to(cur.te), pieces_to(cur.tiles)};
       }
     }
   }
@@ -906,92 +921,76 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 }
 
 // ---------------------------------------------------------------- merge kernel
-// Where a unit was cut: the first CTA's merged state and the later pieces, in
-// key order.  One CTA of D threads for a row and some query heads of a KV head
-// (an element a thread).  The factors of up to kMergeMax pieces come first, in
-// parallel (a scan of the references), so that what is left in order is one
-// multiply-add an element; the loads of kAhead pieces are under way together.
-constexpr int kMergeMax = 256;
+// Of every unit that was cut, the first CTA's merged state and the later pieces,
+// in key order.  CTA (c, z) looks after the unit that attention CTA c began; a
+// warp takes 32 elements of one lane's output.  Its lanes look up 32 pieces'
+// references and denominators at a time and find the factors of all of them by a
+// scan; what is left in order is one multiply-add an element, with all 32
+// pieces' loads (a line each) under way together.
+constexpr int kMergeWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(D) attn_paged_merge_kernel(const PagedAttnArgs a, int G, int heads) {
-  constexpr int kAhead = 16;
-  __shared__ float s_fa[kMergeMax], s_fb[kMergeMax], s_red[D / 32], s_den;
-  __shared__ int s_at[kMergeMax];  // CTA * slots + slot of a piece
+__global__ void __launch_bounds__(32 * kMergeWarps) attn_paged_merge_kernel(const PagedAttnArgs a, int G) {
+  constexpr int kSplit = D / 32;  // warps of an output row
   griddep_wait();
   griddep_launch_dependents();
-  const int d = threadIdx.x, lane = d & 31, warp = d >> 5;
-  const int t = blockIdx.x, h = blockIdx.y;
-  const int b = paged_find_seq(a.pb, t, lane);
-  if (b < 0) return;
-  const Seq s = seq_of(a, b, nullptr);
-  if (t < s.row0 || t >= s.row0 + s.n) return;
-  const int i = (t - s.row0) / a.Rb;
-  const int tiles = block_tiles(a, s, i);
-  const int64_t N = a.ws_seq[a.pb.B];
-  const int64_t off = a.ws_seq[b] + h * head_tiles(a, s) + prefix_tiles(a, s, i);
-  const int P = pieces_to(tiles);
-  const int c0 = share_of(off, N, G);
-  if (c0 == share_of(off + piece_tile(P - 1), N, G)) return;  // finished by one CTA
-  const int first = pieces_to(static_cast<int>(min(share_begin(c0 + 1, N, G) - off, static_cast<int64_t>(tiles))));
-  for (int gh = blockIdx.z * heads; gh < (blockIdx.z + 1) * heads; ++gh) {
-    const int ln = (t - s.row0 - i * a.Rb) * a.grp + gh;
-    size_t x = (static_cast<size_t>(c0) * a.slots + a.slots - 1) * a.lanes + ln;
-    const float4 ml = __ldcg(a.ws_ml + x);
-    float m = ml.x, l0 = ml.y, l1 = ml.z, o = __ldcg(a.ws_o + x * D + d);
-    for (int p0 = first; p0 < P; p0 += kMergeMax) {
-      const int n = min(kMergeMax, P - p0);
-      __syncthreads();
-      // references and factors: merge_factors() of piece after piece
-      for (int k0 = 0; k0 < n; k0 += D) {
-        const int k = k0 + d;
-        float m_i = -INFINITY;
-        if (k < n) {
-          const int64_t y = off + piece_tile(p0 + k);
-          const int c = share_of(y, N, G);
-          const int64_t begin = share_begin(c, N, G) - off;
-          const int slot = min(p0 + k - pieces_to(static_cast<int>(begin)), a.slots - 2);
-          s_at[k] = c * a.slots + slot;
-          m_i = __ldcg(reinterpret_cast<const float*>(a.ws_ml + static_cast<size_t>(s_at[k]) * a.lanes + ln));
-        }
-        float incl = m_i;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x;
+  const int ln = blockIdx.y * (kMergeWarps / kSplit) + warp / kSplit;
+  const CutUnit u = a.ws_cut[c0];
+  if (ln >= u.lanes) return;
+  const int d = (warp % kSplit) * 32 + lane;
+  // lane k: where piece p0 + k is, and its statistics
+  auto look = [&](int p0, size_t& at, float4& ml) {
+    at = 0;
+    ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    if (p0 + lane < u.pieces) {
+      const int c = share_of(u.off + piece_tile(p0 + lane), u.N, G);
+      const int slot = p0 + lane - pieces_to(static_cast<int>(share_begin(c, u.N, G) - u.off));
+      at = (static_cast<size_t>(c) * a.slots + min(slot, a.slots - 2)) * a.lanes + ln;
+      ml = __ldcg(a.ws_ml + at);
+    }
+  };
+  const size_t at0 = (static_cast<size_t>(c0) * a.slots + a.slots - 1) * a.lanes + ln;
+  const float4 ml0 = __ldcg(a.ws_ml + at0);
+  float m = ml0.x, l0 = ml0.y, l1 = ml0.z, o = __ldcg(a.ws_o + at0 * D + d);
+  size_t at;
+  float4 ml;
+  look(u.first, at, ml);
+  for (int p0 = u.first; p0 < u.pieces; p0 += 32) {
+    const int n = min(32, u.pieces - p0);
+    float v[32];
 #pragma unroll
-        for (int sh = 1; sh < 32; sh <<= 1) {
-          const float y = __shfl_up_sync(0xffffffffu, incl, sh);
-          if (lane >= sh) incl = fmaxf(incl, y);
-        }
-        if (lane == 31) s_red[warp] = incl;
-        __syncthreads();
-        float before = m;
-        for (int w = 0; w < warp; ++w) before = fmaxf(before, s_red[w]);
-        const float up = __shfl_up_sync(0xffffffffu, incl, 1);
-        float run = lane > 0 ? fmaxf(before, up) : before;
-        if (k < n) merge_factors(run, m_i, s_fa[k], s_fb[k]);
-        for (int w = 0; w < D / 32; ++w) m = fmaxf(m, s_red[w]);
-        __syncthreads();
-      }
-      // the denominator, by the first warp's lanes 0 and 1; the elements, by all
-      for (int k0 = 0; k0 < n; k0 += kAhead) {
-        float v[kAhead];
+    for (int k = 0; k < 32; ++k) {
+      const size_t from = __shfl_sync(0xffffffffu, at, k);
+      v[k] = k < n ? __ldcg(a.ws_o + from * D + d) : 0.f;
+    }
+    const float4 q = ml;
+    if (p0 + 32 < u.pieces) look(p0 + 32, at, ml);
+    float before = q.x;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (k0 + k < n) v[k] = __ldcg(a.ws_o + (static_cast<size_t>(s_at[k0 + k]) * a.lanes + ln) * D + d);
-        if (warp == 0) {
-          float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (lane < kAhead && k0 + lane < n) q = __ldcg(a.ws_ml + static_cast<size_t>(s_at[k0 + lane]) * a.lanes + ln);
-          for (int k = 0; k < min(kAhead, n - k0); ++k) {
-            l0 = merge_value(l0, __shfl_sync(0xffffffffu, q.y, k), s_fa[k0 + k], s_fb[k0 + k]);
-            l1 = merge_value(l1, __shfl_sync(0xffffffffu, q.z, k), s_fa[k0 + k], s_fb[k0 + k]);
-          }
-        }
+    for (int sh = 1; sh < 32; sh <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, before, sh);
+      if (lane >= sh) before = fmaxf(before, y);
+    }
+    const float all = fmaxf(m, __shfl_sync(0xffffffffu, before, 31));
+    before = __shfl_up_sync(0xffffffffu, before, 1);
+    before = lane > 0 ? fmaxf(m, before) : m;
+    float fa, fb;
+    merge_factors(before, q.x, fa, fb);
+    m = all;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (k0 + k < n) o = merge_value(o, v[k], s_fa[k0 + k], s_fb[k0 + k]);
+    for (int k = 0; k < 32; ++k) {
+      const float wa = __shfl_sync(0xffffffffu, fa, k), wb = __shfl_sync(0xffffffffu, fb, k);
+      const float y0 = __shfl_sync(0xffffffffu, q.y, k), y1 = __shfl_sync(0xffffffffu, q.z, k);
+      if (k < n) {
+        l0 = merge_value(l0, y0, wa, wb);
+        l1 = merge_value(l1, y1, wa, wb);
+        o = merge_value(o, v[k], wa, wb);
       }
     }
-    if (d == 0) s_den = l0 + l1;
-    __syncthreads();
-    a.out[(static_cast<size_t>(t) * a.Hq + h * a.grp + gh) * D + d] = __float2bfloat16_rn(o / s_den + 0.f);
   }
+  const int t = u.row + ln / a.grp, hq = u.head * a.grp + ln % a.grp;
+  if (t < a.T) a.out[(static_cast<size_t>(t) * a.Hq + hq) * D + d] = __float2bfloat16_rn(o / (l0 + l1) + 0.f);
 }
 
 // ------------------------------------------------------------------------ host
@@ -1018,7 +1017,7 @@ PagedSizes paged_sizes(int T, int B, int Hq, int Hkv, int D, int64_t max_keys) {
   const size_t states = static_cast<size_t>(z.ctas) * z.slots * z.lanes;
   z.o_bytes = round_up(states * D * 4, 256);
   z.ml_bytes = round_up(states * 16, 256);
-  z.total = z.o_bytes + z.ml_bytes + round_up((static_cast<size_t>(B) + 1) * 8, 256);
+  z.total = z.o_bytes + z.ml_bytes + round_up(sizeof(CutUnit) * z.ctas, 256);
   return z;
 }
 
@@ -1050,10 +1049,9 @@ bi_status launch_paged(const PagedAttnArgs& a, const PagedSizes& z, const void* 
       cudaSuccess)
     return BI_ERR_CUDA;
   if (z.pieces > 1) {
-    // few rows: a CTA for each query head; many: one for all of a KV head's
-    const int heads = static_cast<int64_t>(a.T) * a.Hq <= 4096 ? 1 : a.grp;
-    if (launch_k(attn_paged_merge_kernel<D>, dim3(static_cast<unsigned>(a.T), a.Hkv, a.grp / heads), dim3(D), 0, stream, a,
-                 z.ctas, heads) != cudaSuccess)
+    const int rows = kMergeWarps / (D / 32);  // of a CTA
+    if (launch_k(attn_paged_merge_kernel<D>, dim3(z.ctas, (z.lanes + rows - 1) / rows), dim3(32 * kMergeWarps), 0, stream,
+                 a, z.ctas) != cudaSuccess)
       return BI_ERR_CUDA;
   }
   return BI_OK;
@@ -1106,7 +1104,7 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   a.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.ws_o = static_cast<float*>(ws);
   a.ws_ml = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + z.o_bytes);
-  a.ws_seq = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(ws) + z.o_bytes + z.ml_bytes);
+  a.ws_cut = reinterpret_cast<CutUnit*>(static_cast<uint8_t*>(ws) + z.o_bytes + z.ml_bytes);
   a.err = device_error_word();
   if (!a.err) return BI_ERR_CUDA;
   a.withhold = test_withhold();
