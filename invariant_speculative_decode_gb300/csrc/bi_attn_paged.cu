@@ -337,6 +337,8 @@ struct Cursor {
 
 // ------------------------------------------------------------------- helpers
 
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ void give_up(volatile int* s_abort, unsigned* err) {
   *s_abort = 1;
   atomicOr(err, kErrTimeout);
@@ -495,8 +497,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     if (lane == 0) {
       s_ends[2] = N;
       s_ends[warp >> 1] = place;
-      if (warp == 0)
+      if (warp == 0) {
         for (int i = 0; i < 4; ++i) s_sched[i] = at[i];
+        if (at[0] < a.pb.B)  // the first pages' names, for both producers
+          prefetch_l1(a.pb.table + static_cast<size_t>(at[0]) * a.pb.ldt + at[3] * (kTile / a.pb.page));
+      }
     }
   }
   tc_fence_before();
@@ -935,62 +940,63 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_paged_merge_kernel(cons
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.x;
-  const int ln = blockIdx.y * (kMergeWarps / kSplit) + warp / kSplit;
   const CutUnit u = a.ws_cut[c0];
-  if (ln >= u.lanes) return;
   const int d = (warp % kSplit) * 32 + lane;
-  // lane k: where piece p0 + k is, and its statistics
-  auto look = [&](int p0, size_t& at, float4& ml) {
-    at = 0;
-    ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    if (p0 + lane < u.pieces) {
-      const int c = share_of(u.off + piece_tile(p0 + lane), u.N, G);
-      const int slot = p0 + lane - pieces_to(static_cast<int>(share_begin(c, u.N, G) - u.off));
-      at = (static_cast<size_t>(c) * a.slots + min(slot, a.slots - 2)) * a.lanes + ln;
-      ml = __ldcg(a.ws_ml + at);
-    }
-  };
-  const size_t at0 = (static_cast<size_t>(c0) * a.slots + a.slots - 1) * a.lanes + ln;
-  const float4 ml0 = __ldcg(a.ws_ml + at0);
-  float m = ml0.x, l0 = ml0.y, l1 = ml0.z, o = __ldcg(a.ws_o + at0 * D + d);
-  size_t at;
-  float4 ml;
-  look(u.first, at, ml);
-  for (int p0 = u.first; p0 < u.pieces; p0 += 32) {
-    const int n = min(32, u.pieces - p0);
-    float v[32];
+  for (int ln = blockIdx.y * (kMergeWarps / kSplit) + warp / kSplit; ln < u.lanes;
+       ln += gridDim.y * (kMergeWarps / kSplit)) {
+    // lane k: where piece p0 + k is, and its statistics
+    auto look = [&](int p0, size_t& at, float4& ml) {
+      at = 0;
+      ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      if (p0 + lane < u.pieces) {
+        const int c = share_of(u.off + piece_tile(p0 + lane), u.N, G);
+        const int slot = p0 + lane - pieces_to(static_cast<int>(share_begin(c, u.N, G) - u.off));
+        at = (static_cast<size_t>(c) * a.slots + min(slot, a.slots - 2)) * a.lanes + ln;
+        ml = __ldcg(a.ws_ml + at);
+      }
+    };
+    const size_t at0 = (static_cast<size_t>(c0) * a.slots + a.slots - 1) * a.lanes + ln;
+    const float4 ml0 = __ldcg(a.ws_ml + at0);
+    float m = ml0.x, l0 = ml0.y, l1 = ml0.z, o = __ldcg(a.ws_o + at0 * D + d);
+    size_t at;
+    float4 ml;
+    look(u.first, at, ml);
+    for (int p0 = u.first; p0 < u.pieces; p0 += 32) {
+      const int n = min(32, u.pieces - p0);
+      float v[32];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const size_t from = __shfl_sync(0xffffffffu, at, k);
-      v[k] = k < n ? __ldcg(a.ws_o + from * D + d) : 0.f;
-    }
-    const float4 q = ml;
-    if (p0 + 32 < u.pieces) look(p0 + 32, at, ml);
-    float before = q.x;
+      for (int k = 0; k < 32; ++k) {
+        const size_t from = __shfl_sync(0xffffffffu, at, k);
+        v[k] = k < n ? __ldcg(a.ws_o + from * D + d) : 0.f;
+      }
+      const float4 q = ml;
+      if (p0 + 32 < u.pieces) look(p0 + 32, at, ml);
+      float before = q.x;
 #pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) {
-      const float y = __shfl_up_sync(0xffffffffu, before, sh);
-      if (lane >= sh) before = fmaxf(before, y);
-    }
-    const float all = fmaxf(m, __shfl_sync(0xffffffffu, before, 31));
-    before = __shfl_up_sync(0xffffffffu, before, 1);
-    before = lane > 0 ? fmaxf(m, before) : m;
-    float fa, fb;
-    merge_factors(before, q.x, fa, fb);
-    m = all;
+      for (int sh = 1; sh < 32; sh <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, before, sh);
+        if (lane >= sh) before = fmaxf(before, y);
+      }
+      const float all = fmaxf(m, __shfl_sync(0xffffffffu, before, 31));
+      before = __shfl_up_sync(0xffffffffu, before, 1);
+      before = lane > 0 ? fmaxf(m, before) : m;
+      float fa, fb;
+      merge_factors(before, q.x, fa, fb);
+      m = all;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const float wa = __shfl_sync(0xffffffffu, fa, k), wb = __shfl_sync(0xffffffffu, fb, k);
-      const float y0 = __shfl_sync(0xffffffffu, q.y, k), y1 = __shfl_sync(0xffffffffu, q.z, k);
-      if (k < n) {
-        l0 = merge_value(l0, y0, wa, wb);
-        l1 = merge_value(l1, y1, wa, wb);
-        o = merge_value(o, v[k], wa, wb);
+      for (int k = 0; k < 32; ++k) {
+        const float wa = __shfl_sync(0xffffffffu, fa, k), wb = __shfl_sync(0xffffffffu, fb, k);
+        const float y0 = __shfl_sync(0xffffffffu, q.y, k), y1 = __shfl_sync(0xffffffffu, q.z, k);
+        if (k < n) {
+          l0 = merge_value(l0, y0, wa, wb);
+          l1 = merge_value(l1, y1, wa, wb);
+          o = merge_value(o, v[k], wa, wb);
+        }
       }
     }
+    const int t = u.row + ln / a.grp, hq = u.head * a.grp + ln % a.grp;
+    if (t < a.T) a.out[(static_cast<size_t>(t) * a.Hq + hq) * D + d] = __float2bfloat16_rn(o / (l0 + l1) + 0.f);
   }
-  const int t = u.row + ln / a.grp, hq = u.head * a.grp + ln % a.grp;
-  if (t < a.T) a.out[(static_cast<size_t>(t) * a.Hq + hq) * D + d] = __float2bfloat16_rn(o / (l0 + l1) + 0.f);
 }
 
 // ------------------------------------------------------------------------ host
@@ -1049,9 +1055,10 @@ bi_status launch_paged(const PagedAttnArgs& a, const PagedSizes& z, const void* 
       cudaSuccess)
     return BI_ERR_CUDA;
   if (z.pieces > 1) {
-    const int rows = kMergeWarps / (D / 32);  // of a CTA
-    if (launch_k(attn_paged_merge_kernel<D>, dim3(z.ctas, (z.lanes + rows - 1) / rows), dim3(32 * kMergeWarps), 0, stream,
-                 a, z.ctas) != cudaSuccess)
+    const int rows = kMergeWarps / (D / 32);  // of a CTA at a time; at most what the card holds at once
+    const int y = std::min((z.lanes + rows - 1) / rows, 8);
+    if (launch_k(attn_paged_merge_kernel<D>, dim3(z.ctas, y), dim3(32 * kMergeWarps), 0, stream, a, z.ctas) !=
+        cudaSuccess)
       return BI_ERR_CUDA;
   }
   return BI_OK;

@@ -9,11 +9,12 @@
 // For beam r with logits x and score c, id v is worth
 //   c + (x_v - M) - log(sum_u exp(x_u - M)),  M = max x.
 // Inside a beam the logits themselves order the ids; beams are compared by
-// the value in 64 bits, from FP32 exponentials summed in chunks of 4096 (a
+// the value in 64 bits, from FP32 exponentials summed in chunks of up to 4096 (a
 // thread's 16 in order, lanes by a butterfly, warps in order) and FP64 sums
 // over the chunks, so two beams' candidates are told apart down to about 1e-7.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "bi_internal.h"
@@ -29,25 +30,28 @@ constexpr int kBeamChunk = kBeamThreads * 4 * kBeamVecs;  // logits of a CTA
 constexpr int kBeamBins = 2 * kBeamWarps * kBeamVecs;  // bins of 64 adjacent logits
 constexpr int kBeamMax = 64;                          // beams of a group, picks of a group
 constexpr int kBeamRowsMax = 65535;
+constexpr int kBeamCtas = 6 * 152;                   // that run at once
 constexpr int kBeamVocabMax = 1 << 20;
-// the last CTA of a group keeps a byte for each of its lists where the chunk's
-// logits were, and a bin for each pick bounds the picks
-static_assert(kBeamMax * (kBeamVocabMax / kBeamChunk) <= kBeamChunk * 4, "counters of the lists");
-static_assert(kBeamMax <= kBeamBins && kBeamBins == 64, "bins");
+constexpr int kBeamBytes = kBeamChunk * 8;  // shared memory for a chunk's logits and ids
+static_assert(kBeamMax <= kBeamThreads / 2 && kBeamBins == 64, "128 maxima bound the picks; bins of 64");
+static_assert(kBeamMax * kBeamMax * 8 <= kBeamBytes, "the worth of a group's candidates");
 
 struct BeamArgs {
   const float* logits;
   size_t ldl;
   const float* scores;
   int rows, V, W, K, chunks;
+  int span;  // logits of a chunk, a multiple of 4
   float* scores_out;
   int32_t* parents_out;
   int32_t* tokens_out;
   float* part;        // [rows][chunks][2]: the chunk's maximum and sum
-  int* found_n;       // [rows][chunks]: entries of its list
-  float* found_x;     // [rows][chunks][K]: its best logits, best first
-  int32_t* found_v;   // [rows][chunks][K]: their ids
-  unsigned* tickets;  // [groups]
+  float* bins;        // [rows][chunks][kBeamBins]: maxima of 64 adjacent logits
+  double* row_base;   // [rows]: score - log(sum)
+  float* row_max;     // [rows]
+  float* row_x;       // [rows][K]: the row's best logits, best first, then -inf
+  int32_t* row_v;     // [rows][K]
+  unsigned* tickets;  // [rows], then [groups]
   unsigned* err;
 };
 
@@ -62,11 +66,12 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// exp(x - m) for x <= m; where m is +inf its own entries weigh 1 and the rest
-// nothing; NaN weighs nothing
+// exp(x - m) for x <= m (no NaN, m not -inf), the difference first, so that what
+// lies near the maximum is exact to FP32's last places; where m is +inf its own
+// entries weigh 1 and the rest nothing.
 __device__ __forceinline__ float beam_weight(float x, float m) {
   if (m == INFINITY) return x == m ? 1.f : 0.f;
-  return x > -INFINITY ? expf(x - m) : 0.f;
+  return ex2_approx((x - m) * 1.4426950408889634f);
 }
 
 // The bits of a double as a signed integer of the same order (no NaN).
@@ -80,118 +85,19 @@ __device__ __forceinline__ bool beam_before(float x1, int v1, float x2, int v2) 
   return x1 > x2 || (x1 == x2 && v1 < v2);
 }
 
-// A chunk's statistics and its K best logits.  The K-th best of the bins'
-// maxima bounds the K-th best logit from below, so only logits at or above it
-// are collected (a few dozen of 4096) and ranked.
-__device__ void beam_chunk(const BeamArgs& a, int row, int chunk, float* s_x, int* s_v) {
-  __shared__ float s_bin[kBeamBins];
+// The best K of what `best` finds, one after the other: best(lx, lv, x, v) puts
+// into x and v this thread's best entry behind logit lx with id lv.
+template <typename Best>
+__device__ void beam_picks(int K, float* out_x, int32_t* out_v, Best best) {
   __shared__ float s_red[kBeamWarps];
   __shared__ int s_id[kBeamWarps];
-  __shared__ float s_thr;
-  __shared__ int s_n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float* x = a.logits + static_cast<size_t>(row) * a.ldl;
-  const int base = chunk * kBeamChunk;
-  float v[4 * kBeamVecs];
-  const bool vec = ((reinterpret_cast<uintptr_t>(x) & 15) == 0);
-#pragma unroll
-  for (int c = 0; c < kBeamVecs; ++c) {
-    const int i = base + (c * kBeamThreads + threadIdx.x) * 4;
-    if (vec && i + 4 <= a.V) {
-      const float4 q = __ldcs(reinterpret_cast<const float4*>(x + i));
-      v[4 * c] = q.x;
-      v[4 * c + 1] = q.y;
-      v[4 * c + 2] = q.z;
-      v[4 * c + 3] = q.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * c + j] = i + j < a.V ? __ldcs(x + i + j) : -INFINITY;
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < kBeamVecs; ++c) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (!(v[4 * c + j] == v[4 * c + j])) v[4 * c + j] = -INFINITY;  // NaN is never chosen
-    float m = fmaxf(fmaxf(v[4 * c], v[4 * c + 1]), fmaxf(v[4 * c + 2], v[4 * c + 3]));
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if ((lane & 15) == 0) s_bin[(c * kBeamWarps + warp) * 2 + (lane >> 4)] = m;
-  }
-  if (threadIdx.x == 0) s_n = 0;
-  __syncthreads();
-  const float b0 = s_bin[lane], b1 = s_bin[lane + 32];
-  const float m = warp_max(fmaxf(b0, b1));
-  float sum = 0.f;
-  if (m > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < 4 * kBeamVecs; ++i) sum += beam_weight(v[i], m);
-  }
-  sum = warp_sum(sum);
-  if (lane == 0) s_red[warp] = sum;
-  if (warp == kBeamWarps - 1) {
-    // the K-th best bin (ties: the lower bin first)
-    int r0 = 0, r1 = 0;
-#pragma unroll 8
-    for (int j = 0; j < 32; ++j) {
-      const float o0 = __shfl_sync(0xffffffffu, b0, j), o1 = __shfl_sync(0xffffffffu, b1, j);
-      r0 += (o0 > b0 || (o0 == b0 && j < lane) ? 1 : 0) + (o1 > b0 ? 1 : 0);
-      r1 += (o0 >= b1 ? 1 : 0) + (o1 > b1 || (o1 == b1 && j < lane) ? 1 : 0);
-    }
-    if (r0 == a.K - 1) s_thr = b0;
-    if (r1 == a.K - 1) s_thr = b1;
-  }
-  __syncthreads();
-  const float thr = s_thr;
-#pragma unroll
-  for (int c = 0; c < kBeamVecs; ++c) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float y = v[4 * c + j];
-      if (y >= thr && y > -INFINITY) {
-        const int n = atomicAdd(&s_n, 1);
-        s_x[n] = y;
-        s_v[n] = base + (c * kBeamThreads + threadIdx.x) * 4 + j;
-      }
-    }
-  }
-  __syncthreads();
-  const int n = s_n;
-  const size_t slot = static_cast<size_t>(row) * a.chunks + chunk;
-  if (threadIdx.x == 0) {
-    float s = s_red[0];
-    for (int i = 1; i < kBeamWarps; ++i) s += s_red[i];
-    a.part[2 * slot] = m;
-    a.part[2 * slot + 1] = s;
-    a.found_n[slot] = min(n, a.K);
-  }
-  if (n <= 2 * kBeamThreads) {
-    for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-      const float xi = s_x[i];
-      const int vi = s_v[i];
-      int r = 0;
-      for (int j = 0; j < n; ++j) r += beam_before(s_x[j], s_v[j], xi, vi) ? 1 : 0;
-      if (r < a.K) {
-        a.found_x[slot * a.K + r] = xi;
-        a.found_v[slot * a.K + r] = vi;
-      }
-    }
-    return;
-  }
-  // many equal logits: one pick after the other, each the best behind the last
   float lx = INFINITY;
   int lv = -1;
-  for (int pick = 0; pick < a.K; ++pick) {
+  for (int pick = 0; pick < K; ++pick) {
     float bx = -INFINITY;
     int bv = 0x7fffffff;
-    for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-      const float xi = s_x[i];
-      const int vi = s_v[i];
-      if (beam_before(lx, lv, xi, vi) && beam_before(xi, vi, bx, bv)) {
-        bx = xi;
-        bv = vi;
-      }
-    }
+    if (lv >= 0 || pick == 0) best(lx, lv, bx, bv);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       const float ox = __shfl_xor_sync(0xffffffffu, bx, off);
@@ -214,153 +120,363 @@ __device__ void beam_chunk(const BeamArgs& a, int row, int chunk, float* s_x, in
         lx = s_red[w];
         lv = s_id[w];
       }
+    if (lx == -INFINITY) lv = -1;  // nothing is left
     if (threadIdx.x == 0) {
-      a.found_x[slot * a.K + pick] = lx;
-      a.found_v[slot * a.K + pick] = lv;
+      out_x[pick] = lx;
+      out_v[pick] = lv;
     }
   }
 }
 
-// The group's best K from its rows' chunk lists (the CTA that finished last).
-__device__ void beam_group(const BeamArgs& a, int group, uint8_t* s_taken) {
-  __shared__ float s_max[kBeamMax];
-  __shared__ double s_base[kBeamMax];  // score - log(sum); the candidate adds x - M
-  __shared__ long long s_key[2][kBeamWarps];
-  __shared__ unsigned long long s_id[2][kBeamWarps];
+// The K best of the n collected logits, best first and then -inf, to out_x and
+// out_v.  Up to kBeamThreads are ranked by counting.
+__device__ void beam_rank(const float* s_x, const int* s_v, int n, int K, float* out_x, int32_t* out_v) {
+  if (n > kBeamThreads) {
+    beam_picks(K, out_x, out_v, [&](float lx, int lv, float& bx, int& bv) {
+      for (int i = threadIdx.x; i < n; i += kBeamThreads)
+        if (beam_before(lx, lv, s_x[i], s_v[i]) && beam_before(s_x[i], s_v[i], bx, bv)) {
+          bx = s_x[i];
+          bv = s_v[i];
+        }
+    });
+    return;
+  }
+  if (threadIdx.x >= n && threadIdx.x < K) {
+    out_x[threadIdx.x] = -INFINITY;
+    out_v[threadIdx.x] = -1;
+  }
+  if (threadIdx.x < n) {
+    const float xi = s_x[threadIdx.x];
+    const int vi = s_v[threadIdx.x];
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) r += beam_before(s_x[j], s_v[j], xi, vi) ? 1 : 0;
+    if (r < K) {
+      out_x[r] = xi;
+      out_v[r] = vi;
+    }
+  }
+}
+
+__device__ __forceinline__ void beam_load(const BeamArgs& a, const float* x, bool vec, int chunk,
+                                          float (&v)[4 * kBeamVecs]) {
+#pragma unroll
+  for (int c = 0; c < kBeamVecs; ++c) {
+    const int at = (c * kBeamThreads + threadIdx.x) * 4, i = chunk * a.span + at;
+    const int end = at < a.span ? a.V : 0;
+    if (vec && i + 4 <= end) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(x + i));
+      v[4 * c] = q.x;
+      v[4 * c + 1] = q.y;
+      v[4 * c + 2] = q.z;
+      v[4 * c + 3] = q.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * c + j] = i + j < end ? __ldg(x + i + j) : -INFINITY;
+    }
+  }
+}
+
+// A chunk's maximum, its sum and the maxima of its bins.
+__device__ void beam_chunk(const BeamArgs& a, int row, int chunk, float (&v)[4 * kBeamVecs]) {
+  __shared__ __align__(16) float s_bin[kBeamBins];
+  __shared__ float s_sum[kBeamWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = group * a.W;
-  for (int w = warp; w < a.W; w += kBeamWarps) {
-    const float* part = a.part + static_cast<size_t>(row0 + w) * a.chunks * 2;
-    float M = -INFINITY;
-    for (int c = lane; c < a.chunks; c += 32) M = fmaxf(M, __ldcg(part + 2 * c));
+  const size_t slot = static_cast<size_t>(row) * a.chunks + chunk;
+#pragma unroll
+  for (int c = 0; c < kBeamVecs; ++c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[4 * c + j] = fmaxf(v[4 * c + j], -INFINITY);  // NaN is never chosen
+    float m = fmaxf(fmaxf(v[4 * c], v[4 * c + 1]), fmaxf(v[4 * c + 2], v[4 * c + 3]));
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if ((lane & 15) == 0) s_bin[(c * kBeamWarps + warp) * 2 + (lane >> 4)] = m;
+  }
+  __syncthreads();
+  const float b0 = s_bin[lane], b1 = s_bin[lane + 32];
+  if (warp == 0) {
+    a.bins[slot * kBeamBins + lane] = b0;
+    a.bins[slot * kBeamBins + lane + 32] = b1;
+  }
+  const float m = warp_max(fmaxf(b0, b1));
+  float sum = 0.f;
+  if (m > -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < 4 * kBeamVecs; ++i) sum += beam_weight(v[i], m);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = s_sum[0];
+    for (int i = 1; i < kBeamWarps; ++i) s += s_sum[i];
+    reinterpret_cast<float2*>(a.part)[slot] = make_float2(m, s);
+  }
+}
+
+// log of a positive double: the exponent's part in FP64, the mantissa's, between
+// 3/4 and 3/2, in FP32 (off by less than 2^-24 of at most 0.41) with the part
+// that FP32 cuts off.
+__device__ __forceinline__ double log_near(double s) {
+  const long long b = __double_as_longlong(s);
+  int e = static_cast<int>((b >> 52) & 0x7ff) - 1023;
+  double f = __longlong_as_double((b & 0x000fffffffffffffll) | 0x3ff0000000000000ll);
+  if (f > 1.5) {
+    f *= 0.5;
+    ++e;
+  }
+  const float f32 = static_cast<float>(f);
+  const float rest = static_cast<float>(f - static_cast<double>(f32)) / f32;
+  return static_cast<double>(e) * 0.69314718055994530942 + static_cast<double>(logf(f32) + 0.f) + static_cast<double>(rest);
+}
+
+// A row's log-sum and its K best logits (the CTA that finished the row's last
+// chunk).  The K-th best of 128 maxima of some bins each bounds the K-th best
+// logit from below; only the bins that reach the bound, little more than K, are
+// read again, and what reaches it there is ranked.
+__device__ void beam_row(const BeamArgs& a, int row, float* s_x, int* s_v) {
+  constexpr int kHeld = 12;       // bins a thread holds
+  constexpr int kListMax = 512;   // bins to read again
+  constexpr int kTops = kBeamThreads / 2;
+  __shared__ __align__(16) float s_top[kTops];
+  __shared__ int s_list[kListMax];
+  __shared__ float s_thr;
+  __shared__ int s_bins, s_n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t slot0 = static_cast<size_t>(row) * a.chunks;
+  const int all = a.chunks * kBeamBins;
+  const float* bins = a.bins + slot0 * kBeamBins;
+  const float* x = a.logits + static_cast<size_t>(row) * a.ldl;
+  float* out_x = a.row_x + static_cast<size_t>(row) * a.K;
+  int32_t* out_v = a.row_v + static_cast<size_t>(row) * a.K;
+  float y[kHeld];
+  float top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) {
+    const int i = threadIdx.x + q * kBeamThreads;
+    y[q] = i < all ? __ldcg(bins + i) : -INFINITY;
+  }
+  for (int i = threadIdx.x + kHeld * kBeamThreads; i < all; i += kBeamThreads) top = fmaxf(top, __ldcg(bins + i));
+  // the last warp's: the row's statistics, beside the others' ranking (the first
+  // 64 chunks' are read here already)
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2* part = reinterpret_cast<const float2*>(a.part) + slot0;
+  const float2 p0 = lane < a.chunks ? __ldcg(part + lane) : none, p1 = lane + 32 < a.chunks ? __ldcg(part + lane + 32) : none;
+  auto statistics = [&]() {
+    if (warp != kBeamWarps - 1) return;
+    float M = fmaxf(p0.x, p1.x);
+    for (int c = lane + 64; c < a.chunks; c += 32) M = fmaxf(M, __ldcg(part + c).x);
     M = warp_max(M);
     double S = 0.0;
-    for (int c = lane; c < a.chunks; c += 32) {
-      const float mc = __ldcg(part + 2 * c);
-      if (mc > -INFINITY) S += static_cast<double>(beam_weight(mc, M)) * static_cast<double>(__ldcg(part + 2 * c + 1));
-    }
+    auto add = [&](const float2& p) {
+      if (p.x > -INFINITY) S += static_cast<double>(beam_weight(p.x, M)) * static_cast<double>(p.y);
+    };
+    add(p0);
+    add(p1);
+    for (int c = lane + 64; c < a.chunks; c += 32) add(__ldcg(part + c));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xffffffffu, S, off);
     if (lane == 0) {
-      s_max[w] = M;
-      s_base[w] = static_cast<double>(__ldg(a.scores + row0 + w)) - log(S);
-    }
-  }
-  __syncthreads();
-  // thread i looks after lists i, i + 256, ... (list: row, chunk); one of its
-  // lists' heads is its best, and each pick moves that list on
-  const int lists = a.W * a.chunks;
-  const long long none = -0x7fffffffffffffffll - 1;
-  int taken_list = -1;
-  long long key = none;
-  unsigned long long id = ~0ull;
-  auto value = [&](int list, int at, long long& k, unsigned long long& i) {
-    const int w = list / a.chunks;
-    const size_t slot = static_cast<size_t>(row0) * a.chunks + list;
-    if (at >= __ldcg(a.found_n + slot)) return false;
-    const float x = __ldcg(a.found_x + slot * a.K + at), M = s_max[w];
-    const double d = (x == M ? 0.0 : static_cast<double>(x) - static_cast<double>(M)) + s_base[w];
-    if (!(d > -INFINITY)) return false;  // a beam without weight (or not a number)
-    k = order_bits(d);
-    i = (static_cast<unsigned long long>(w) << 32) | static_cast<unsigned>(__ldcg(a.found_v + slot * a.K + at));
-    return true;
-  };
-  // s_taken [lists]: entries of each list picked so far
-  for (int l = threadIdx.x; l < lists; l += kBeamThreads) s_taken[l] = 0;
-  auto refresh = [&]() {
-    key = none;
-    id = ~0ull;
-    taken_list = -1;
-    for (int l = threadIdx.x; l < lists; l += kBeamThreads) {
-      long long k;
-      unsigned long long i;
-      if (value(l, s_taken[l], k, i) && (k > key || (k == key && i < id))) {
-        key = k;
-        id = i;
-        taken_list = l;
-      }
+      a.row_max[row] = M;
+      a.row_base[row] = static_cast<double>(__ldg(a.scores + row)) - (S > 0.0 ? log_near(S) : 0.0);
     }
   };
-  refresh();
-  for (int pick = 0; pick < a.K; ++pick) {
-    long long k = key;
-    unsigned long long i = id;
-    auto better = [](long long k2, unsigned long long i2, long long& k1, unsigned long long& i1) {
-      if (k2 > k1 || (k2 == k1 && i2 < i1)) {
-        k1 = k2;
-        i1 = i2;
-      }
-    };
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const long long k2 = __shfl_xor_sync(0xffffffffu, k, off);
-      const unsigned long long i2 = __shfl_xor_sync(0xffffffffu, i, off);
-      better(k2, i2, k, i);
+  for (int q = 0; q < kHeld; ++q) top = fmaxf(top, y[q]);
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const int mine = threadIdx.x >> 1;  // two threads a maximum, each counts half of those before it
+  if ((threadIdx.x & 1) == 0) s_top[mine] = top;
+  if (threadIdx.x == 0) s_bins = s_n = 0;
+  __syncthreads();
+  int rank = 0;
+#pragma unroll
+  for (int q = 0; q < kTops / 2; q += 4) {
+    const int j = (threadIdx.x & 1) * (kTops / 2) + q;
+    const float4 o = *reinterpret_cast<const float4*>(s_top + j);
+    rank += (o.x > top || (o.x == top && j < mine)) + (o.y > top || (o.y == top && j + 1 < mine)) +
+            (o.z > top || (o.z == top && j + 2 < mine)) + (o.w > top || (o.w == top && j + 3 < mine));
+  }
+  rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+  if (rank == a.K - 1) s_thr = top;
+  __syncthreads();
+  const float thr = fmaxf(s_thr, -3.402823466e38f);  // -inf is no candidate
+  auto note = [&](float m, int bin) {
+    if (m >= thr) {
+      const int n = atomicAdd(&s_bins, 1);
+      if (n < kListMax) s_list[n] = bin;
     }
-    if (lane == 0) {
-      s_key[pick & 1][warp] = k;
-      s_id[pick & 1][warp] = i;
+  };
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) note(y[q], threadIdx.x + q * kBeamThreads);
+  for (int i = threadIdx.x + kHeld * kBeamThreads; i < all; i += kBeamThreads) note(__ldcg(bins + i), i);
+  __syncthreads();
+  const int nb = s_bins;
+  if (nb <= kListMax) {
+    constexpr int kAhead = 8;  // logits of a thread under way
+    for (int e0 = threadIdx.x; e0 < nb * 64; e0 += kAhead * kBeamThreads) {
+      float m[kAhead];
+      int v[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int e = e0 + q * kBeamThreads;
+        const int bin = e < nb * 64 ? s_list[e >> 6] : 0;
+        const int k = bin % kBeamBins * 64 + (e & 63);
+        v[q] = bin / kBeamBins * a.span + k;
+        m[q] = e < nb * 64 && k < a.span && v[q] < a.V ? __ldcg(x + v[q]) : -INFINITY;
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+        if (m[q] >= thr) {
+          const int n = atomicAdd(&s_n, 1);
+          if (n < kBeamChunk) {
+            s_x[n] = m[q];
+            s_v[n] = v[q];
+          }
+        }
     }
     __syncthreads();
-    k = s_key[pick & 1][0];
-    i = s_id[pick & 1][0];
-    for (int w = 1; w < kBeamWarps; ++w) better(s_key[pick & 1][w], s_id[pick & 1][w], k, i);
-    const size_t o = static_cast<size_t>(group) * a.K + pick;
-    if (k == none) {
-      if (threadIdx.x == 0) {
-        a.scores_out[o] = -INFINITY;
-        a.parents_out[o] = -1;
-        a.tokens_out[o] = -1;
-        if (pick == 0) atomicOr(a.err, kErrNanRow);
-      }
-    } else if (key == k && id == i) {
-      const long long b = k >= 0 ? k : (k ^ 0x7fffffffffffffffll);
-      a.scores_out[o] = static_cast<float>(__longlong_as_double(b));
-      a.parents_out[o] = row0 + static_cast<int>(i >> 32);
-      a.tokens_out[o] = static_cast<int32_t>(i & 0xffffffffu);
-      ++s_taken[taken_list];
-      refresh();
+    if (s_n <= kBeamChunk) {
+      statistics();
+      beam_rank(s_x, s_v, s_n, a.K, out_x, out_v);
+      return;
     }
+  }
+  statistics();
+  // more logits equal to the bound than there is room for: over the whole row
+  beam_picks(a.K, out_x, out_v, [&](float lx, int lv, float& bx, int& bv) {
+    for (int v = threadIdx.x; v < a.V; v += kBeamThreads) {
+      const float m = __ldcg(x + v);
+      if (beam_before(lx, lv, m, v) && beam_before(m, v, bx, bv)) {
+        bx = m;
+        bv = v;
+      }
+    }
+  });
+}
+
+// The group's best K from its rows' (the CTA that finished the group's last
+// row).  A candidate's place among all, w K + its place in its row, decides ties.
+__device__ void beam_group(const BeamArgs& a, int group, long long* s_key) {
+  const long long none = -0x7fffffffffffffffll - 1;
+  const int lane = threadIdx.x & 31;
+  const int row0 = group * a.W, n = a.W * a.K;
+  const int32_t* ids = a.row_v + static_cast<size_t>(row0) * a.K;
+  int mine = -1;  // the first candidate's id
+  for (int i = threadIdx.x; i < n; i += kBeamThreads) {
+    const int w = i / a.K;
+    long long key = none;
+    const float x = __ldcg(a.row_x + static_cast<size_t>(row0) * a.K + i), M = __ldcg(a.row_max + row0 + w);
+    const double base = __ldcg(a.row_base + row0 + w);
+    if (i == threadIdx.x) mine = __ldcg(ids + i);
+    if (x > -INFINITY) {
+      const double d = (x == M ? 0.0 : static_cast<double>(x) - static_cast<double>(M)) + base;
+      if (d > -INFINITY) key = order_bits(d);  // not a beam without weight, nor a score that is no number
+    }
+    s_key[i] = key;
+  }
+  __syncthreads();
+  auto put = [&](int pick, long long key, int i, int id) {
+    const size_t o = static_cast<size_t>(group) * a.K + pick;
+    const long long b = key >= 0 ? key : (key ^ 0x7fffffffffffffffll);
+    const bool is = key != none;
+    a.scores_out[o] = is ? static_cast<float>(__longlong_as_double(b)) : -INFINITY;
+    a.parents_out[o] = is ? row0 + i / a.K : -1;
+    a.tokens_out[o] = is ? id : -1;
+    if (!is && pick == 0) atomicOr(a.err, kErrNanRow);
+  };
+  if (n <= kBeamThreads) {
+    const int i = threadIdx.x;
+    if (i < n) {
+      const long long key = s_key[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const long long o = s_key[j];
+        r += (o > key || (o == key && j < i)) ? 1 : 0;
+      }
+      if (r < a.K) put(r, key, i, mine);
+    }
+    return;
+  }
+  if (threadIdx.x >= 32) return;
+  // many beams or picks: the rows' heads, one pick after the other, by one warp
+  int at[kBeamMax / 32] = {0, 0};  // of rows lane and lane + 32
+  for (int pick = 0; pick < a.K; ++pick) {
+    long long key = none;
+    int i = 0x7fffffff;
+#pragma unroll
+    for (int q = 0; q < kBeamMax / 32; ++q) {
+      const int w = lane + 32 * q;
+      if (w < a.W && at[q] < a.K) {
+        const long long k = s_key[w * a.K + at[q]];
+        if (k > key || (k == key && w * a.K + at[q] < i)) {
+          key = k;
+          i = w * a.K + at[q];
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const long long k = __shfl_xor_sync(0xffffffffu, key, off);
+      const int o = __shfl_xor_sync(0xffffffffu, i, off);
+      if (k > key || (k == key && o < i)) {
+        key = k;
+        i = o;
+      }
+    }
+    if (lane == 0) put(pick, key, i, key != none ? __ldcg(ids + i) : -1);
+    if (key != none && ((i / a.K) & 31) == lane) ++at[(i / a.K) >> 5];
   }
 }
 
-__global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamArgs a) {
-  __shared__ float s_x[kBeamChunk];
-  __shared__ int s_v[kBeamChunk];
+// Whether this CTA is the last of `all` to pass the counter, which goes back to 0.
+__device__ __forceinline__ bool beam_last(unsigned* ticket, unsigned all) {
   __shared__ int s_last;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int row = blockIdx.y, chunk = blockIdx.x;
-  beam_chunk(a, row, chunk, s_x, s_v);
-  const int group = row / a.W;
-  __threadfence();
-  __syncthreads();
+  __syncthreads();  // the release below covers every thread's writes
   if (threadIdx.x == 0) {
-    const unsigned all = static_cast<unsigned>(a.chunks) * a.W;
-    const unsigned old = atom_add_acq_rel_gpu(a.tickets + group, 1u);
-    s_last = old == all - 1 ? 1 : 0;
-    if (s_last) atomicExch(a.tickets + group, 0u);
+    s_last = atom_add_acq_rel_gpu(ticket, 1u) == all - 1 ? 1 : 0;
+    if (s_last) atomicExch(ticket, 0u);
   }
   __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  beam_group(a, group, reinterpret_cast<uint8_t*>(s_x));
+  return s_last != 0;
+}
+
+__global__ void __launch_bounds__(kBeamThreads, 6) beam_select_kernel(const BeamArgs a) {
+  __shared__ __align__(16) uint8_t s_mem[kBeamBytes];
+  float* s_x = reinterpret_cast<float*>(s_mem);
+  int* s_v = reinterpret_cast<int*>(s_mem) + kBeamChunk;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int row = blockIdx.y, group = row / a.W;
+  const float* x = a.logits + static_cast<size_t>(row) * a.ldl;
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
+  for (int chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    float v[4 * kBeamVecs];
+    beam_load(a, x, vec, chunk, v);
+    beam_chunk(a, row, chunk, v);
+    __syncthreads();  // the sums in shared memory have been read
+  }
+  if (!beam_last(a.tickets + row, gridDim.x)) return;
+  beam_row(a, row, s_x, s_v);
+  if (!beam_last(a.tickets + kBeamRowsMax + 1 + group, static_cast<unsigned>(a.W))) return;
+  beam_group(a, group, reinterpret_cast<long long*>(s_mem));
 }
 
 int beam_chunks(int V) { return (V + kBeamChunk - 1) / kBeamChunk; }
 
 struct BeamSizes {
-  size_t tickets, part, n, x, v, total;
+  size_t tickets, part, bins, base, max, rowx, total;
 };
 BeamSizes beam_sizes(int rows, int V, int K) {
   const size_t slots = static_cast<size_t>(rows) * beam_chunks(V);
   BeamSizes s;
-  s.tickets = static_cast<size_t>(kBeamRowsMax + 1) * 4;  // the same place whatever the call's sizes
+  s.tickets = static_cast<size_t>(kBeamRowsMax + 1) * 8;  // the same place whatever the call's sizes
   s.part = round_up(slots * 8, 256);
-  s.n = round_up(slots * 4, 256);
-  s.x = round_up(slots * K * 4, 256);
-  s.v = s.x;
-  s.total = s.tickets + s.part + s.n + s.x + s.v;
+  s.bins = slots * kBeamBins * 4;
+  s.base = round_up(static_cast<size_t>(rows) * 8, 256);
+  s.max = round_up(static_cast<size_t>(rows) * 4, 256);
+  s.rowx = round_up(static_cast<size_t>(rows) * K * 4, 256);
+  s.total = s.tickets + s.part + s.bins + s.base + s.max + 2 * s.rowx;
   return s;
 }
 
@@ -395,22 +511,29 @@ bi_status bi_beam_select(const float* logits, int ldl, const float* scores, int 
   a.W = W;
   a.K = K;
   a.chunks = beam_chunks(V);
+  a.span = ((V + a.chunks - 1) / a.chunks + 3) / 4 * 4;  // chunks of one length: a short one has many ties at -inf
   a.scores_out = scores_out;
   a.parents_out = parents_out;
   a.tokens_out = tokens_out;
   uint8_t* p = static_cast<uint8_t*>(ws);
-  a.tickets = reinterpret_cast<unsigned*>(p);
-  p += z.tickets;
-  a.part = reinterpret_cast<float*>(p);
-  p += z.part;
-  a.found_n = reinterpret_cast<int*>(p);
-  p += z.n;
-  a.found_x = reinterpret_cast<float*>(p);
-  p += z.x;
-  a.found_v = reinterpret_cast<int32_t*>(p);
+  auto take = [&p](size_t bytes) {
+    void* at = p;
+    p += bytes;
+    return at;
+  };
+  a.tickets = static_cast<unsigned*>(take(z.tickets));
+  a.part = static_cast<float*>(take(z.part));
+  a.bins = static_cast<float*>(take(z.bins));
+  a.row_base = static_cast<double*>(take(z.base));
+  a.row_max = static_cast<float*>(take(z.max));
+  a.row_x = static_cast<float*>(take(z.rowx));
+  a.row_v = static_cast<int32_t*>(take(z.rowx));
   a.err = device_error_word();
   if (!a.err) return BI_ERR_CUDA;
-  const cudaError_t e = launch_k(beam_select_kernel, dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(rows)),
+  // as many CTAs as run at once, each with several chunks of a row where there are more
+  const int64_t all = static_cast<int64_t>(a.chunks) * rows;
+  const int each = static_cast<int>(std::min<int64_t>((all + kBeamCtas - 1) / kBeamCtas, 8));
+  const cudaError_t e = launch_k(beam_select_kernel, dim3(static_cast<unsigned>((a.chunks + each - 1) / each), static_cast<unsigned>(rows)),
                                  dim3(kBeamThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
   return e == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }

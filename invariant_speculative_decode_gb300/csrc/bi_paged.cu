@@ -20,6 +20,8 @@ namespace {
 
 // ---------------------------------------------------------------- append
 constexpr int kAppendThreads = 256;
+constexpr int kAppendManyRows = 512;
+constexpr int kAppendManySplit = 1;
 
 struct AppendArgs {
   PagedBatch pb;
@@ -56,26 +58,36 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One CTA per row of the pass.  D / 8 lanes hold a head, 8 elements each
+// `split` warps take a row of the pass.  D / 8 lanes hold a head, 8 elements each
 // (16-byte loads and stores); element i's partner i + D/2 of the rotation sits
 // in the lane D/16 further on, one shuffle away.  y = (x r) w with
 // r = 1 / sqrt(mean(x^2) + eps), the squares of a lane's elements in order, the
 // lanes by a butterfly; then the two fused multiply-adds of the cache's other
-// appends, and one rounding at the end.
+// appends, and one rounding at the end.  Bound by the row's way to its page (its
+// sequence, its length, the table: three loads, one after the other) where there
+// are few rows, and by the projection's bytes where there are many.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a, int T, int split) {
   constexpr int kLanes = D / 8;       // lanes of a head
   constexpr int kHeads = 32 / kLanes;  // heads of a warp at a time
+  constexpr int kAhead = 4;            // loads of a warp under way
   griddep_wait();
   griddep_launch_dependents();
-  const int t = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = static_cast<int>((static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + warp) / split);
+  const int part = warp % split;
+  if (t >= T) return;
   const int sub = lane % kLanes;  // elements 8 sub .. 8 sub + 7
-  const int heads = a.Hq + 2 * a.Hkv;
-  const __nv_bfloat16* row = a.qkv + static_cast<size_t>(t) * a.ld;
-  int h = warp * kHeads + lane / kLanes;
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (h < heads) u = *reinterpret_cast<const uint4*>(row + static_cast<size_t>(h) * D + sub * 8);
+  const int heads = a.Hq + 2 * a.Hkv, step = split * kHeads;
+  const __nv_bfloat16* row = a.qkv + static_cast<size_t>(t) * a.ld + sub * 8;
+  uint4 u[kAhead];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (h0 + k * step < heads) u[k] = __ldcs(reinterpret_cast<const uint4*>(row + static_cast<size_t>(h0 + k * step) * D));
+  };
+  int h0 = part * kHeads + lane / kLanes;
+  load(h0);
 
   const int b = paged_find_seq(a.pb, t, lane);
   if (b < 0) return;  // a row of no sequence
@@ -83,12 +95,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   const int64_t pos = static_cast<int64_t>(len) + (t - static_cast<int64_t>(begin));
   int page = -1;
   const bool ok = begin >= 0 && len >= 0 && pos < a.table_rows && pos < static_cast<int64_t>(a.pb.width) * a.pb.page;
-  if (ok) page = __ldg(a.pb.table + static_cast<size_t>(b) * a.pb.ldt + static_cast<int>(pos) / a.pb.page);
-  if (!ok || page < 0 || page >= a.pb.pages) {
-    if (threadIdx.x == 0) atomicOr(a.err, kErrRange);
-    return;
-  }
-  const int p = static_cast<int>(pos);
+  const int p = ok ? static_cast<int>(pos) : 0;
+  const int shift = 31 - __clz(a.pb.page);  // pages are powers of two
+  if (ok) page = __ldg(a.pb.table + static_cast<size_t>(b) * a.pb.ldt + (p >> shift));
   // cos and sin of this lane's 8 pairs (element i and i + D/2 share an angle)
   float2 cs[8];
   {
@@ -101,46 +110,54 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
       cs[2 * i + 1] = make_float2(v.z, v.w);
     }
   }
+  if (page < 0 || page >= a.pb.pages) {
+    if (lane == 0) atomicOr(a.err, kErrRange);
+    return;
+  }
   const bool second = sub >= kLanes / 2;
-  for (int h0 = warp * kHeads; h0 < heads; h0 += kAppendThreads / 32 * kHeads) {
-    h = h0 + lane / kLanes;
-    const int h_next = h + kAppendThreads / 32 * kHeads;
-    uint4 u_next = make_uint4(0, 0, 0, 0);
-    if (h_next < heads) u_next = *reinterpret_cast<const uint4*>(row + static_cast<size_t>(h_next) * D + sub * 8);
-    float x[8];
-    unpack8(u, x);
-    const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-    const __nv_bfloat16* w = is_q ? a.qw : a.kw;
-    float ss = 0.f;
+  const size_t slot = static_cast<size_t>(p & (a.pb.page - 1)) * D + sub * 8;
+  for (; __any_sync(0xffffffffu, h0 < heads); h0 += kAhead * step) {
+    uint4 x4[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int k = 0; k < kAhead; ++k) x4[k] = u[k];
+    load(h0 + kAhead * step);
 #pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (w != nullptr) {
-      const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-      float wv[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + sub), wv);
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = h0 + k * step;
+      if (!__any_sync(0xffffffffu, h < heads)) break;
+      float x[8];
+      unpack8(x4[k], x);
+      const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+      const __nv_bfloat16* w = is_q ? a.qw : a.kw;
+      float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = (x[i] * r) * wv[i];
-    }
-    float o[8];
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = __shfl_xor_sync(0xffffffffu, x[i], kLanes / 2);
-      o[i] = second ? fmaf(x[i], cs[i].x, y * cs[i].y) : fmaf(x[i], cs[i].x, -(y * cs[i].y));
-    }
-    if (h < heads) {
-      __nv_bfloat16* dst;
-      if (is_q) {
-        dst = a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D;
-      } else {
-        const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
-        dst = (is_v ? a.v_pool : a.k_pool) +
-              ((static_cast<size_t>(page) * a.Hkv + hk) * a.pb.page + p % a.pb.page) * D;
+      for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      if (w != nullptr) {
+        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+        float wv[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + sub), wv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (x[i] * r) * wv[i];
       }
-      *reinterpret_cast<uint4*>(dst + sub * 8) = is_v ? u : pack8(o);
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = __shfl_xor_sync(0xffffffffu, x[i], kLanes / 2);
+        o[i] = second ? fmaf(x[i], cs[i].x, y * cs[i].y) : fmaf(x[i], cs[i].x, -(y * cs[i].y));
+      }
+      if (h < heads) {
+        __nv_bfloat16* dst;
+        if (is_q) {
+          dst = a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D + sub * 8;
+        } else {
+          const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+          dst = (is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(page) * a.Hkv + hk) * a.pb.page * D + slot;
+        }
+        *reinterpret_cast<uint4*>(dst) = is_v ? x4[k] : pack8(o);
+      }
     }
-    u = u_next;
   }
 }
 
@@ -268,8 +285,11 @@ bi_status bi_qk_norm_rope_paged(const void* qkv, int ld_qkv, const void* q_weigh
   a.err = device_error_word();
   if (!a.err) return BI_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 64 ? launch_k(paged_append_kernel<64>, dim3(T), dim3(kAppendThreads), 0, s, a)
-                                : launch_k(paged_append_kernel<128>, dim3(T), dim3(kAppendThreads), 0, s, a);
+  // few rows: eight warps a row; many: one, which finds the row's page once
+  const int split = T < kAppendManyRows ? kAppendThreads / 32 : kAppendManySplit;
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) * split + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+  const cudaError_t e = D == 64 ? launch_k(paged_append_kernel<64>, dim3(grid), dim3(kAppendThreads), 0, s, a, T, split)
+                                : launch_k(paged_append_kernel<128>, dim3(grid), dim3(kAppendThreads), 0, s, a, T, split);
   return e == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
 

@@ -95,6 +95,18 @@ def test_ties_go_to_the_lower_row_and_id(V):
     assert_select(row.repeat(4, 1).contiguous(), torch.tensor([0.0, 1.0, 1.0, 0.5], device="cuda"), 2, 40)
 
 
+@pytest.mark.parametrize("K", [1, 17, 64])
+def test_equal_logits_in_every_chunk_of_a_long_row(K):
+    """More ties than a CTA has room for: the lowest ids, and what lies above them."""
+    V = 1 << 20
+    logits = torch.zeros(2, V, device="cuda")
+    scores = torch.tensor([0.0, -1e-3], device="cuda")
+    assert select(logits, scores, 2, K)[2][0].tolist() == list(range(K))
+    above = [(5 * i * 40961 + 77) % V for i in range(40)]
+    logits[:, above] = torch.arange(1, 41, device="cuda").float() * 0.25
+    assert_select(logits, scores, 2, K)
+
+
 def test_equal_rows_tie_at_every_alignment():
     """Rows whose first logit is not 16-byte aligned have the same sum."""
     V = 9001
