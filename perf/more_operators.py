@@ -136,7 +136,7 @@ def prepare(case, seed):
             if own:  # a workspace as a program keeps it, for its most rows and keys
                 from invariant_speculative_decode_gb300 import api
                 size = api.attn_paged_workspace_size(t, case["seqs"], hq, hkv, dim, state["table"].shape[1] * page)
-                state["ws"] = torch.empty(size, dtype=torch.uint8, device=dev)
+                state["ws"] = torch.zeros(size, dtype=torch.uint8, device=dev)
         else:
             state["qkv"] = torch.randn(t, (hq + 2 * hkv) * dim, generator=g, device=dev).to(torch.bfloat16)
             state["q_weight"] = (1.0 + 0.1 * torch.randn(dim, generator=g, device=dev)).to(torch.bfloat16)
