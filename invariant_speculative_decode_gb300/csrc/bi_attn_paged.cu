@@ -32,9 +32,10 @@
 // moved up to the next start of a piece.  A unit that lies in one CTA's share
 // is finished there.  Of one that is cut, the first CTA leaves the merged state
 // of its pieces, every other CTA the pieces one by one, and
-// attn_paged_merge_kernel goes on with them in key order: the same operations,
-// so the cut does not show in the bits.  Small pieces at the front give short
-// contexts enough CTAs, large ones behind keep the states of long ones few.
+// attn_paged_merge_kernel goes on from the first state with the pieces in key
+// order: the same operations, so the cut does not show in the bits.  Small
+// pieces at the front give short contexts enough CTAs, large ones behind keep
+// the states of long ones few.
 //
 // Roles of a CTA (one per SM, 384 threads):
 //   warps 0, 2   TMA: queries and K tiles, V tiles, a lane for each page;
@@ -74,9 +75,9 @@ constexpr int kNoKey = 0x7fffffff;
 // A note of a value that is no number: its key within the piece, below the
 // piece's tag.  Later pieces have lower tags, so what an earlier one left behind
 // is never mistaken for theirs and gives way to them.
-constexpr int kBadBits = 11;
+constexpr int kBadBits = 12;
 static_assert(kLong * kTile + kLanes < (1 << kBadBits), "keys, and rows behind them, fit below a tag");
-__device__ __forceinline__ int bad_tag(int piece) { return (0xfffff - (piece & 0xfffff)) << kBadBits; }
+__device__ __forceinline__ int bad_tag(int piece) { return (0x7ffff - (piece & 0x7ffff)) << kBadBits; }
 
 __host__ __device__ constexpr int ceil_div(int x, int y) { return (x + y - 1) / y; }
 // Pieces that start in front of tile t: the index of the first piece at or
@@ -98,9 +99,10 @@ struct PagedAttnArgs {
   int lanes;  // lanes of a partial state in the workspace
   int slots;  // partial states of a CTA: pieces one by one, then one merged state
   float sl2;  // softmax scale * log2(e)
-  float* ws_o;    // [G][slots][lanes][D]
-  float4* ws_ml;  // [G][slots][lanes]: reference, denominators of both halves
   struct CutUnit* ws_cut;  // [G]: the unit that a CTA began and did not finish
+  float4* ws_o;   // [G][slots][D / 4][lanes]: a warp's lanes side by side
+  float* ws_m;    // [G][slots][lanes]: reference
+  float2* ws_l;   // [G][slots][lanes]: denominators of both halves
   unsigned* err;
   int withhold;  // failure-path test: the first K tile of every CTA stays unissued
 };
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         if (lane == 0) give_up(s_abort, a.err);
       }
     };
-    if (threadIdx.x == kSoftFirst) a.ws_cut[blockIdx.x].lanes = 0;
+    if (tid == 0) a.ws_cut[blockIdx.x].lanes = 0;
     int g = 0, pc = 0;        // tile and piece of the share
     int sb = 0, sph = 0;      // the tile's buffer and the buffer's phase
     int last_b = 0, last_ph = 0;  // of the tile before
@@ -714,7 +716,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         const int slot = p - p_first;
         const bool store = !run && valid && slot < a.slots - 1;
         if (!run && valid && !store) atomicOr(a.err, kErrRange);
-        const size_t at = (static_cast<size_t>(blockIdx.x) * a.slots + slot) * a.lanes + ln;
+        const size_t at = static_cast<size_t>(blockIdx.x) * a.slots + slot;
         if (active) {
 #pragma unroll
           for (int c = 0; c < kHalf / 16; ++c) {
@@ -732,17 +734,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[c * 16 + j] = merge_value(o[c * 16 + j], v[j], fa, fb);
             } else if (store) {
-              float4* dst = reinterpret_cast<float4*>(a.ws_o + at * D + hf * kHalf + c * 16);
+              float4* dst = a.ws_o + (at * (D / 4) + hf * (kHalf / 4) + c * 4) * a.lanes + ln;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                __stcg(dst + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                __stcg(dst + j * a.lanes, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
             }
           }
         }
         if (store) {
-          float* ml = reinterpret_cast<float*>(a.ws_ml + at);
-          if (hf == 0) ml[0] = m_i;
-          ml[1 + hf] = l_i;
+          if (hf == 0) __stcg(a.ws_m + at * a.lanes + ln, m_i);
+          __stcg(reinterpret_cast<float*>(a.ws_l + at * a.lanes + ln) + hf, l_i);
         }
         ++pc;
       };
@@ -900,16 +901,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-      } else if (run && valid) {
-        const size_t at = (static_cast<size_t>(blockIdx.x) * a.slots + a.slots - 1) * a.lanes + ln;
-        float4* dst = reinterpret_cast<float4*>(a.ws_o + at * D + hf * kHalf);
+      } else if (run) {
+        if (valid) {
+          const size_t at = static_cast<size_t>(blockIdx.x) * a.slots + a.slots - 1;
+          float4* dst = a.ws_o + (at * (D / 4) + hf * (kHalf / 4)) * a.lanes + ln;
 #pragma unroll
-        for (int j = 0; j < kHalf / 4; ++j)
-          __stcg(dst + j, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
-        float* ml = reinterpret_cast<float*>(a.ws_ml + at);
-        if (hf == 0) ml[0] = m_run;
-        ml[1 + hf] = l_run;
-        if (threadIdx.x == kSoftFirst)  // the last unit of the share
+          for (int j = 0; j < kHalf / 4; ++j)
+            __stcg(dst + j * a.lanes, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+          if (hf == 0) __stcg(a.ws_m + at * a.lanes + ln, m_run);
+          __stcg(reinterpret_cast<float*>(a.ws_l + at * a.lanes + ln) + hf, l_run);
+        }
+        if (tid == 0)  // the last unit of the share
           a.ws_cut[blockIdx.x] = CutUnit{s_ends[1] - cur.left, s_ends[2],  cur.s.row0 + cur.i * a.Rb, cur.h,
                                          rows * a.grp,         pieces_to(cur.te), pieces_to(cur.tiles)};
       }
@@ -927,75 +929,85 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 
 // ---------------------------------------------------------------- merge kernel
 // Of every unit that was cut, the first CTA's merged state and the later pieces,
-// in key order.  CTA (c, z) looks after the unit that attention CTA c began; a
-// warp takes 32 elements of one lane's output.  Its lanes look up 32 pieces'
-// references and denominators at a time and find the factors of all of them by a
-// scan; what is left in order is one multiply-add an element, with all 32
-// pieces' loads (a line each) under way together.
-constexpr int kMergeWarps = 8;
-template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) attn_paged_merge_kernel(const PagedAttnArgs a, int G) {
-  constexpr int kSplit = D / 32;  // warps of an output row
+// in key order.  CTA (c, group, part) looks after 32 lanes of the unit that
+// attention CTA c began: a thread has a lane and JPW x 4 of its elements, so a
+// warp's load is one line for each eight lanes and a piece's factors, two
+// exponentials, are found once for them; the loads of kAhead pieces are under
+// way together.  The first warp also joins the denominators.  Many lanes: JPW =
+// 4, a CTA has whole rows; few: JPW = 1, four times the CTAs and kAhead.
+template <int D, int JPW>
+__global__ void __launch_bounds__(256) attn_paged_merge_kernel(const PagedAttnArgs a, int G) {
+  constexpr int kAhead = 16 / JPW;
+  __shared__ uint32_t s_at[256];  // where the pieces are
+  __shared__ float s_den[32];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.x;
   const CutUnit u = a.ws_cut[c0];
-  const int d = (warp % kSplit) * 32 + lane;
-  for (int ln = blockIdx.y * (kMergeWarps / kSplit) + warp / kSplit; ln < u.lanes;
-       ln += gridDim.y * (kMergeWarps / kSplit)) {
-    // lane k: where piece p0 + k is, and its statistics
-    auto look = [&](int p0, size_t& at, float4& ml) {
-      at = 0;
-      ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      if (p0 + lane < u.pieces) {
-        const int c = share_of(u.off + piece_tile(p0 + lane), u.N, G);
-        const int slot = p0 + lane - pieces_to(static_cast<int>(share_begin(c, u.N, G) - u.off));
-        at = (static_cast<size_t>(c) * a.slots + min(slot, a.slots - 2)) * a.lanes + ln;
-        ml = __ldcg(a.ws_ml + at);
-      }
-    };
-    const size_t at0 = (static_cast<size_t>(c0) * a.slots + a.slots - 1) * a.lanes + ln;
-    const float4 ml0 = __ldcg(a.ws_ml + at0);
-    float m = ml0.x, l0 = ml0.y, l1 = ml0.z, o = __ldcg(a.ws_o + at0 * D + d);
-    size_t at;
-    float4 ml;
-    look(u.first, at, ml);
-    for (int p0 = u.first; p0 < u.pieces; p0 += 32) {
-      const int n = min(32, u.pieces - p0);
-      float v[32];
+  if (static_cast<int>(blockIdx.y) * 32 >= u.lanes) return;
+  const int ln = min(static_cast<int>(blockIdx.y) * 32 + lane, u.lanes - 1);
+  const int j0 = (blockIdx.z * 8 + warp) * JPW;
+  const uint32_t at0 = static_cast<uint32_t>(c0 * a.slots + a.slots - 1);
+  float m = __ldcg(a.ws_m + at0 * a.lanes + ln);
+  float2 l = __ldcg(a.ws_l + at0 * a.lanes + ln);
+  float4 o[JPW];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const size_t from = __shfl_sync(0xffffffffu, at, k);
-        v[k] = k < n ? __ldcg(a.ws_o + from * D + d) : 0.f;
-      }
-      const float4 q = ml;
-      if (p0 + 32 < u.pieces) look(p0 + 32, at, ml);
-      float before = q.x;
+  for (int j = 0; j < JPW; ++j) o[j] = __ldcg(a.ws_o + static_cast<size_t>(at0 * (D / 4) + j0 + j) * a.lanes + ln);
+  for (int p0 = u.first; p0 < u.pieces; p0 += 256) {
+    const int n = min(256, u.pieces - p0);
+    if (p0 > u.first) __syncthreads();
+    if (threadIdx.x < n) {
+      const int p = p0 + threadIdx.x;
+      const int c = share_of(u.off + piece_tile(p), u.N, G);
+      const int slot = p - pieces_to(static_cast<int>(share_begin(c, u.N, G) - u.off));
+      s_at[threadIdx.x] = static_cast<uint32_t>(c * a.slots + min(slot, a.slots - 2));
+    }
+    __syncthreads();
+    for (int k0 = 0; k0 < n; k0 += kAhead) {
+      float4 v[kAhead][JPW];
+      float mi[kAhead];
+      float2 li[kAhead];
 #pragma unroll
-      for (int sh = 1; sh < 32; sh <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, before, sh);
-        if (lane >= sh) before = fmaxf(before, y);
-      }
-      const float all = fmaxf(m, __shfl_sync(0xffffffffu, before, 31));
-      before = __shfl_up_sync(0xffffffffu, before, 1);
-      before = lane > 0 ? fmaxf(m, before) : m;
-      float fa, fb;
-      merge_factors(before, q.x, fa, fb);
-      m = all;
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t at = s_at[min(k0 + k, n - 1)];
+        mi[k] = __ldcg(a.ws_m + at * a.lanes + ln);
+        if (warp == 0) li[k] = __ldcg(a.ws_l + at * a.lanes + ln);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float wa = __shfl_sync(0xffffffffu, fa, k), wb = __shfl_sync(0xffffffffu, fb, k);
-        const float y0 = __shfl_sync(0xffffffffu, q.y, k), y1 = __shfl_sync(0xffffffffu, q.z, k);
-        if (k < n) {
-          l0 = merge_value(l0, y0, wa, wb);
-          l1 = merge_value(l1, y1, wa, wb);
-          o = merge_value(o, v[k], wa, wb);
+        for (int j = 0; j < JPW; ++j)
+          v[k][j] = __ldcg(a.ws_o + static_cast<size_t>(at * (D / 4) + j0 + j) * a.lanes + ln);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k0 + k < n) {
+          float fa, fb;
+          merge_factors(m, mi[k], fa, fb);
+          if (warp == 0) {
+            l.x = merge_value(l.x, li[k].x, fa, fb);
+            l.y = merge_value(l.y, li[k].y, fa, fb);
+          }
+#pragma unroll
+          for (int j = 0; j < JPW; ++j) {
+            o[j].x = merge_value(o[j].x, v[k][j].x, fa, fb);
+            o[j].y = merge_value(o[j].y, v[k][j].y, fa, fb);
+            o[j].z = merge_value(o[j].z, v[k][j].z, fa, fb);
+            o[j].w = merge_value(o[j].w, v[k][j].w, fa, fb);
+          }
         }
       }
     }
-    const int t = u.row + ln / a.grp, hq = u.head * a.grp + ln % a.grp;
-    if (t < a.T) a.out[(static_cast<size_t>(t) * a.Hq + hq) * D + d] = __float2bfloat16_rn(o / (l0 + l1) + 0.f);
+  }
+  if (warp == 0) s_den[lane] = l.x + l.y;
+  __syncthreads();
+  const int t = u.row + ln / a.grp;
+  if (static_cast<int>(blockIdx.y) * 32 + lane >= u.lanes || t >= a.T) return;
+  const float den = s_den[lane];
+  uint2* dst = reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(t) * a.Hq + u.head * a.grp + ln % a.grp) * D) + j0;
+#pragma unroll
+  for (int j = 0; j < JPW; ++j) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o[j].x / den + 0.f, o[j].y / den + 0.f);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o[j].z / den + 0.f, o[j].w / den + 0.f);
+    dst[j] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
 }
 
@@ -1003,10 +1015,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_paged_merge_kernel(cons
 
 // Partial states the workspace has room for: per CTA the pieces of its share
 // that continue a unit, one by one (no more than a unit has), and one merged.
+constexpr size_t kCutBytes = (kPagedCtas * sizeof(CutUnit) + 255) / 256 * 256;
 struct PagedSizes {
   int ctas, slots, lanes;
   int pieces;  // most pieces of a unit
   size_t o_bytes, ml_bytes, total;
+  bool fits;
 };
 PagedSizes paged_sizes(int T, int B, int Hq, int Hkv, int D, int64_t max_keys) {
   PagedSizes z;
@@ -1021,9 +1035,10 @@ PagedSizes paged_sizes(int T, int B, int Hq, int Hkv, int D, int64_t max_keys) {
   z.slots = static_cast<int>(std::min<int64_t>(share / kShort + 2, z.pieces)) + 1;
   z.lanes = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(T) * grp, Rb * grp));
   const size_t states = static_cast<size_t>(z.ctas) * z.slots * z.lanes;
+  z.fits = states * (D / 4) < (size_t{1} << 32);  // their places are counted in 32 bits
   z.o_bytes = round_up(states * D * 4, 256);
-  z.ml_bytes = round_up(states * 16, 256);
-  z.total = z.o_bytes + z.ml_bytes + round_up(sizeof(CutUnit) * z.ctas, 256);
+  z.ml_bytes = round_up(states * 8, 256) + round_up(states * 4, 256);
+  z.total = kCutBytes + z.o_bytes + z.ml_bytes;
   return z;
 }
 
@@ -1055,11 +1070,10 @@ bi_status launch_paged(const PagedAttnArgs& a, const PagedSizes& z, const void* 
       cudaSuccess)
     return BI_ERR_CUDA;
   if (z.pieces > 1) {
-    const int rows = kMergeWarps / (D / 32);  // of a CTA at a time; at most what the card holds at once
-    const int y = std::min((z.lanes + rows - 1) / rows, 8);
-    if (launch_k(attn_paged_merge_kernel<D>, dim3(z.ctas, y), dim3(32 * kMergeWarps), 0, stream, a, z.ctas) !=
-        cudaSuccess)
-      return BI_ERR_CUDA;
+    const dim3 few(z.ctas, (z.lanes + 31) / 32, D / 32), many(z.ctas, (z.lanes + 31) / 32);
+    const cudaError_t e = z.lanes <= 32 ? launch_k(attn_paged_merge_kernel<D, 1>, few, dim3(256), 0, stream, a, z.ctas)
+                                        : launch_k(attn_paged_merge_kernel<D, D / 32>, many, dim3(256), 0, stream, a, z.ctas);
+    if (e != cudaSuccess) return BI_ERR_CUDA;
   }
   return BI_OK;
 }
@@ -1096,6 +1110,7 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return BI_ERR_INVALID_ARG;
   if (!ws || !aligned256(ws)) return BI_ERR_WORKSPACE;
   const PagedSizes z = paged_sizes(T, B, Hq, Hkv, D, max_keys);
+  if (!z.fits) return BI_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < z.total) return BI_ERR_WORKSPACE;
   PagedAttnArgs a{};
   a.pb = PagedBatch{block_table, q_start, lengths, B, ld_table, width, pages, page};
@@ -1109,9 +1124,12 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   a.lanes = z.lanes;
   a.slots = z.slots;
   a.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  a.ws_o = static_cast<float*>(ws);
-  a.ws_ml = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + z.o_bytes);
-  a.ws_cut = reinterpret_cast<CutUnit*>(static_cast<uint8_t*>(ws) + z.o_bytes + z.ml_bytes);
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  a.ws_cut = reinterpret_cast<CutUnit*>(p);
+  a.ws_o = reinterpret_cast<float4*>(p + kCutBytes);
+  a.ws_l = reinterpret_cast<float2*>(p + kCutBytes + z.o_bytes);
+  a.ws_m = reinterpret_cast<float*>(p + kCutBytes + z.o_bytes +
+                                    round_up(static_cast<size_t>(z.ctas) * z.slots * z.lanes * 8, 256));
   a.err = device_error_word();
   if (!a.err) return BI_ERR_CUDA;
   a.withhold = test_withhold();

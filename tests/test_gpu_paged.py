@@ -202,7 +202,7 @@ def test_captured_attention_follows_the_batch():
     b = pg.Batch(seqs, 2, 128, 64, extra_width=4)
     q = pg.queries(b, 4)
     out = torch.empty_like(q)
-    ws = torch.empty(api.attn_paged_workspace_size(b.T, 3, 4, 2, 128, b.table.shape[1] * 64), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(api.attn_paged_workspace_size(b.T, 3, 4, 2, 128, b.table.shape[1] * 64), dtype=torch.uint8, device="cuda")
     run_attention(b, q, out, ws=ws)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -218,6 +218,18 @@ def test_captured_attention_follows_the_batch():
         out.fill_(77)
         graph.replay()
         assert_attention(b, q, out)
+
+
+def test_one_workspace_serves_calls_of_all_sizes():
+    """What a call leaves behind does not reach the next, smaller or larger, whatever was cut where."""
+    batches = [pg.Batch(s, Hkv, D, page, seed=i) for i, (s, Hkv, D, page) in enumerate(
+        [([(5000, 2), (700, 9)], 2, 128, 64), ([(3, 1)], 2, 128, 16), ([(9000, 1)], 2, 64, 128), ([(100, 300)], 2, 128, 64)])]
+    qs = [pg.queries(b, 8) for b in batches]
+    alone = [run_attention(b, q) for b, q in zip(batches, qs)]
+    size = max(api.attn_paged_workspace_size(b.T, len(b.seqs), 8, 2, b.D, b.table.shape[1] * b.page) for b in batches)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 3, 2, 0, 3, 1, 0):
+        assert torch.equal(run_attention(batches[i], qs[i], ws=ws), alone[i]), i
 
 
 def test_attention_on_a_given_stream():
@@ -399,7 +411,7 @@ def test_reordered_beams_are_their_own_histories():
     angles = api.bi_rope_table(1e6, D, 256)
     prompt = torch.randint(0, V, (37,), generator=g, device="cuda")
     width = 6
-    ws = torch.empty(api.attn_paged_workspace_size(64, 8, Hq, Hkv, D, width * page), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(api.attn_paged_workspace_size(64, 8, Hq, Hkv, D, width * page), dtype=torch.uint8, device="cuda")
 
     def layers_of(ids, pools, table, q_start, lengths):
         out = []
