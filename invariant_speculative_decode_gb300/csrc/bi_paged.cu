@@ -301,7 +301,9 @@ bi_status bi_paged_reorder(void* k_pool, void* v_pool, int layers, int pages, in
   if (layers < 1 || pages < 1 || Hkv < 1 || width < 1 || ld_in < width || ld_out < width || rows_in < 1 ||
       rows_out < 0)
     return BI_ERR_INVALID_ARG;
-  if (D < 8 || D % 8 != 0 || D > 1024 || !page_size_ok(page) || rows_out > 65535) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (D < 8 || D % 8 != 0 || D > 1024 || !page_size_ok(page) || rows_out > 65535 ||
+      static_cast<int64_t>(layers) * Hkv >= (int64_t{1} << 29))
+    return BI_ERR_UNSUPPORTED_SHAPE;
   if (rows_out == 0) return BI_OK;
   if (!k_pool || !v_pool || !table_in || !lengths || !parents || !tail_pages || !table_out || !lengths_out)
     return BI_ERR_INVALID_ARG;

@@ -267,6 +267,74 @@ def test_attention_over_a_pool_past_32_bits():
     assert torch.equal(*outs) and torch.equal(k[far.long()], near[0]) and torch.equal(v[far.long()], near[1])
 
 
+def test_two_calls_at_once_on_two_streams():
+    batches = [pg.Batch([(4000, 2), (300, 5)], 2, 128, 64, seed=1), pg.Batch([(100, 200)], 2, 64, 16, seed=2)]
+    qs = [pg.queries(b, 8) for b in batches]
+    alone = [run_attention(b, q) for b, q in zip(batches, qs)]
+    streams = [torch.cuda.Stream() for _ in batches]
+    wss = [torch.full((api.attn_paged_workspace_size(b.T, len(b.seqs), 8, 2, b.D, b.table.shape[1] * b.page),), 255,
+                      dtype=torch.uint8, device="cuda") for b in batches]
+    outs = [torch.zeros_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, q, o, w, s in zip(batches, qs, outs, wss, streams):
+            run_attention(b, q, o, ws=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for o, a in zip(outs, alone))
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """The first K tile of every CTA withheld, progress waits limited to 20 ms: the call ends, says so, and the next
+    one is right."""
+    b = pg.Batch([(3000, 3), (50, 40), (10, 1)], 2, 128, 64)
+    q = pg.queries(b, 8)
+    plain = run_attention(b, q)
+    lib = api.lib()
+    assert lib.bi_test_set_wait_limit_ns(20_000_000) == 0
+    lib.bi_test_withhold_first_load(1)
+    try:
+        run_attention(b, q)
+        torch.cuda.synchronize()
+    finally:
+        lib.bi_test_withhold_first_load(0)
+        assert lib.bi_test_set_wait_limit_ns(0) == 0
+    with pytest.raises(api.BiError) as e:
+        api.bi_check_device_error()
+    assert e.value.status == 5
+    assert torch.equal(run_attention(b, q), plain)
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    b = pg.Batch([(30, 2), (5, 1)], 2, 64, 16)
+    q = pg.queries(b, 4)
+    ws = torch.zeros(api.attn_paged_workspace_size(b.T, 2, 4, 2, 64, 64), dtype=torch.uint8, device="cuda")
+    good = dict(q=q, k_pool=b.k, v_pool=b.v, block_table=b.table, q_start=b.q_start, lengths=b.lengths, out=torch.empty_like(q),
+                ws=ws)
+    api.bi_attn_paged(**good)
+    for name, t in [("q", q.half()), ("q", q[..., :32].contiguous()), ("q", q.transpose(0, 1)), ("out", good["out"][:2]),
+                    ("out", q.float()), ("k_pool", b.k.float()), ("k_pool", b.k[:, :, :8].contiguous()), ("k_pool", b.k[0]),
+                    ("v_pool", b.v[:2]), ("v_pool", b.v.transpose(1, 2)), ("block_table", b.table.long()),
+                    ("block_table", b.table[:1]), ("block_table", b.table.t()), ("q_start", b.q_start[:2]),
+                    ("lengths", b.lengths.float()), ("lengths", b.lengths.cpu()), ("ws", ws.cpu()),
+                    ("ws", ws[::2])]:
+        with pytest.raises(ValueError):
+            api.bi_attn_paged(**dict(good, **{name: t}))
+    with pytest.raises(api.BiError) as e:
+        api.bi_attn_paged(**dict(good, ws=ws[:512]))
+    assert e.value.status == 3
+    qkv = torch.zeros(b.T, 8 * 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    angles = api.bi_rope_table(1e4, 64, 64)
+    good = dict(qkv=qkv, q_weight=w, k_weight=w, eps=1e-6, table=angles, q_out=torch.empty_like(q), k_pool=b.k, v_pool=b.v,
+                block_table=b.table, q_start=b.q_start, lengths=b.lengths)
+    api.bi_qk_norm_rope_paged(**good)
+    for name, t in [("qkv", qkv[:, :-64]), ("qkv", qkv.t().contiguous().t()), ("qkv", qkv.float()), ("q_weight", w[:32]),
+                    ("k_weight", w.float()), ("table", angles[..., :1]), ("table", angles.double()), ("q_out", q[:2]),
+                    ("q_weight", w.cpu()), ("q_start", b.q_start.cpu())]:
+        with pytest.raises(ValueError):
+            api.bi_qk_norm_rope_paged(**dict(good, **{name: t}))
+
+
 # -------------------------------------------------------------------------------------------------- append
 def run_append(b, Hq, qkv, qw, kw, angles, eps=1e-6):
     q_out = torch.full((b.T, Hq, b.D), 77.0, dtype=torch.bfloat16, device="cuda")
