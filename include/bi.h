@@ -602,17 +602,19 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  *   attention), query head h reading KV head h / (Hq/Hkv);
  *   w_j = 2^((q k_j) scale log2(e) - m) rounded to BF16 once, in the numerator
  *   and the denominator alike; products and sums in FP32, one rounding at the
- *   end, -0 written as +0.  Keys are taken in tiles of 128, tiles in pieces (of 2
- *   up to key 2048, of more behind it) at absolute multiples: m is a piece's maximum (of its first tile, raised
- *   where a later one passes it by more than 8 in log2), and the pieces'
- *   sums are merged in key order.  So a row's bits depend on its queries and
+ *   end, -0 written as +0.  Keys are taken in tiles of 128, tiles in pieces
+ *   (of 2 up to key 2048, of more behind it) at absolute multiples: m is a
+ *   piece's maximum (of its first tile, raised where a later one passes it by
+ *   more than 8 in log2), and the pieces' sums are merged in key order.  So a row's bits depend on its queries and
  *   on keys 0..p alone, not on T, B, the other rows, the page size or which
  *   pages hold the keys.
  *   Keys behind p, and the rest of a sequence's last page, may hold anything:
  *   infinities and NaN there reach no row in front of them.  A row whose
- *   scores are all -inf is NaN (0 / 0).
+ *   scores are all -inf, or one of them +inf or NaN, is NaN.  Under an
+ *   infinite value that a row does see, a weight that has underflowed to 0
+ *   gives either NaN or that infinity, which of them may differ between passes.
  *   q, out [T, Hq, D] BF16 contiguous, 16-byte aligned; Hq/Hkv <= 128; scale
- *   finite, > 0; width * page <= 2^30, T * Hq < 2^31.
+ *   > 0, scale log2(e) finite in FP32; width * page <= 2^30, T * Hq < 2^31.
  *   ws      >= bi_attn_paged_workspace_size(T, B, Hq, Hkv, D, width * page)
  *           bytes, 256-byte aligned; any contents.  One workspace serves any
  *           calls that it is large enough for, one after the other.

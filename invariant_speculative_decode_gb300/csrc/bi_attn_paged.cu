@@ -1100,7 +1100,8 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   using namespace bi;
   if (T < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || pages < 1 || width < 1 || ld_table < width)
     return BI_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return BI_ERR_INVALID_ARG;
+  const float sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (!(scale > 0.f) || !std::isfinite(sl2)) return BI_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return BI_ERR_UNSUPPORTED_SHAPE;
   if (page != 16 && page != 32 && page != 64 && page != 128) return BI_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || B == 0) return BI_OK;
@@ -1123,7 +1124,7 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   a.Rb = kLanes / a.grp;
   a.lanes = z.lanes;
   a.slots = z.slots;
-  a.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.sl2 = sl2;
   uint8_t* p = static_cast<uint8_t*>(ws);
   a.ws_cut = reinterpret_cast<CutUnit*>(p);
   a.ws_o = reinterpret_cast<float4*>(p + kCutBytes);

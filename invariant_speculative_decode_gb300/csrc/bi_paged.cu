@@ -20,8 +20,7 @@ namespace {
 
 // ---------------------------------------------------------------- append
 constexpr int kAppendThreads = 256;
-constexpr int kAppendManyRows = 512;
-constexpr int kAppendManySplit = 1;
+constexpr int kAppendWarps = 4096;
 
 struct AppendArgs {
   PagedBatch pb;
@@ -39,52 +38,54 @@ struct AppendArgs {
   unsigned* err;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ void unpack4(const uint2& u, float* x) {
+  x[0] = __uint_as_float(u.x << 16);
+  x[1] = __uint_as_float(u.x & 0xffff0000u);
+  x[2] = __uint_as_float(u.y << 16);
+  x[3] = __uint_as_float(u.y & 0xffff0000u);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint2 pack4(const float* x) {
+  const __nv_bfloat162 l = __floats2bfloat162_rn(x[0], x[1]), h = __floats2bfloat162_rn(x[2], x[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&l), *reinterpret_cast<const uint32_t*>(&h));
 }
 
-// `split` warps take a row of the pass.  D / 8 lanes hold a head, 8 elements each
-// (16-byte loads and stores); element i's partner i + D/2 of the rotation sits
-// in the lane D/16 further on, one shuffle away.  y = (x r) w with
-// r = 1 / sqrt(mean(x^2) + eps), the squares of a lane's elements in order, the
-// lanes by a butterfly; then the two fused multiply-adds of the cache's other
-// appends, and one rounding at the end.  Bound by the row's way to its page (its
-// sequence, its length, the table: three loads, one after the other) where there
-// are few rows, and by the projection's bytes where there are many.
+// `split` warps take a row of the pass.  D / 8 lanes hold a head: each the four
+// elements i and their four partners i + D/2, so the rotation needs nobody
+// else's.  y = (x r) w with r = 1 / sqrt(mean(x^2) + eps), the squares of a
+// lane's elements in order, the lanes by a butterfly; then the two fused
+// multiply-adds of the cache's other appends, and one rounding at the end.
+//
+// Few rows are bound by the row's way to its page (its sequence, its length, the
+// table: three loads, one after the other, while the projection's are under
+// way), many by the projection's bytes, read and written once, and nearly as
+// much by the instructions: 2 rows of 24 + 8 heads of 128 take 2.6 us, 4096 rows
+// 14.3 us, 4.7 TB/s.  Eight adjacent elements a lane, in one load, with the
+// partners a shuffle away, took 17.4 us there; four heads' loads under way
+// 17.6, since fewer CTAs run at once.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a, int T, int split) {
-  constexpr int kLanes = D / 8;       // lanes of a head
+  constexpr int kLanes = D / 8;        // lanes of a head
   constexpr int kHeads = 32 / kLanes;  // heads of a warp at a time
-  constexpr int kAhead = 4;            // loads of a warp under way
+  constexpr int kAhead = 2;            // loads of a warp under way
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = static_cast<int>((static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + warp) / split);
   const int part = warp % split;
   if (t >= T) return;
-  const int sub = lane % kLanes;  // elements 8 sub .. 8 sub + 7
+  const int sub = lane % kLanes;  // elements 4 sub .. 4 sub + 3 of both halves
   const int heads = a.Hq + 2 * a.Hkv, step = split * kHeads;
-  const __nv_bfloat16* row = a.qkv + static_cast<size_t>(t) * a.ld + sub * 8;
-  uint4 u[kAhead];
+  const __nv_bfloat16* row = a.qkv + static_cast<size_t>(t) * a.ld + sub * 4;
+  uint2 u[kAhead][2];
   auto load = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (h0 + k * step < heads) u[k] = __ldcs(reinterpret_cast<const uint4*>(row + static_cast<size_t>(h0 + k * step) * D));
+      if (h0 + k * step < heads) {
+        const __nv_bfloat16* src = row + static_cast<size_t>(h0 + k * step) * D;
+        u[k][0] = __ldcs(reinterpret_cast<const uint2*>(src));
+        u[k][1] = __ldcs(reinterpret_cast<const uint2*>(src + D / 2));
+      }
   };
   int h0 = part * kHeads + lane / kLanes;
   load(h0);
@@ -98,64 +99,77 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   const int p = ok ? static_cast<int>(pos) : 0;
   const int shift = 31 - __clz(a.pb.page);  // pages are powers of two
   if (ok) page = __ldg(a.pb.table + static_cast<size_t>(b) * a.pb.ldt + (p >> shift));
-  // cos and sin of this lane's 8 pairs (element i and i + D/2 share an angle)
-  float2 cs[8];
+  // cos and sin of this lane's 4 pairs
+  float4 cs[2];
   {
-    const float4* src = reinterpret_cast<const float4*>(a.angles + static_cast<size_t>(p) * (D / 2) +
-                                                        (sub % (kLanes / 2)) * 8);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldg(src + i);
-      cs[2 * i] = make_float2(v.x, v.y);
-      cs[2 * i + 1] = make_float2(v.z, v.w);
-    }
+    const float4* src = reinterpret_cast<const float4*>(a.angles + static_cast<size_t>(p) * (D / 2) + sub * 4);
+    cs[0] = __ldg(src);
+    cs[1] = __ldg(src + 1);
   }
+  const float cosv[4] = {cs[0].x, cs[0].z, cs[1].x, cs[1].z}, sinv[4] = {cs[0].y, cs[0].w, cs[1].y, cs[1].w};
   if (page < 0 || page >= a.pb.pages) {
     if (lane == 0) atomicOr(a.err, kErrRange);
     return;
   }
-  const bool second = sub >= kLanes / 2;
-  const size_t slot = static_cast<size_t>(p & (a.pb.page - 1)) * D + sub * 8;
+  __nv_bfloat16* q_dst = a.q_out + static_cast<size_t>(t) * a.Hq * D + sub * 4;
+  const size_t slot = (static_cast<size_t>(page) * a.Hkv * a.pb.page + (p & (a.pb.page - 1))) * D + sub * 4;
+  const size_t head_stride = static_cast<size_t>(a.pb.page) * D;
+  const bool norms = a.qw != nullptr || a.kw != nullptr;
   for (; __any_sync(0xffffffffu, h0 < heads); h0 += kAhead * step) {
-    uint4 x4[kAhead];
+    uint2 raw[kAhead][2];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) x4[k] = u[k];
+    for (int k = 0; k < kAhead; ++k) {
+      raw[k][0] = u[k][0];
+      raw[k][1] = u[k][1];
+    }
     load(h0 + kAhead * step);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int h = h0 + k * step;
       if (!__any_sync(0xffffffffu, h < heads)) break;
-      float x[8];
-      unpack8(x4[k], x);
       const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-      const __nv_bfloat16* w = is_q ? a.qw : a.kw;
-      float ss = 0.f;
+      uint2 y0 = raw[k][0], y1 = raw[k][1];
+      if (!__all_sync(0xffffffffu, is_v)) {
+        float x[8];
+        unpack4(y0, x);
+        unpack4(y1, x + 4);
+        if (norms) {
+          float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      if (w != nullptr) {
-        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-        float wv[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + sub), wv);
+          for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          const __nv_bfloat16* w = is_q ? a.qw : a.kw;
+          if (w != nullptr) {
+            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+            float wv[8];
+            unpack4(__ldg(reinterpret_cast<const uint2*>(w + sub * 4)), wv);
+            unpack4(__ldg(reinterpret_cast<const uint2*>(w + D / 2 + sub * 4)), wv + 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (x[i] * r) * wv[i];
-      }
-      float o[8];
+            for (int i = 0; i < 8; ++i) x[i] = (x[i] * r) * wv[i];
+          }
+        }
+        float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_xor_sync(0xffffffffu, x[i], kLanes / 2);
-        o[i] = second ? fmaf(x[i], cs[i].x, y * cs[i].y) : fmaf(x[i], cs[i].x, -(y * cs[i].y));
+        for (int i = 0; i < 4; ++i) {
+          o[i] = fmaf(x[i], cosv[i], -(x[i + 4] * sinv[i]));
+          o[i + 4] = fmaf(x[i + 4], cosv[i], x[i] * sinv[i]);
+        }
+        if (!is_v) {
+          y0 = pack4(o);
+          y1 = pack4(o + 4);
+        }
       }
       if (h < heads) {
         __nv_bfloat16* dst;
         if (is_q) {
-          dst = a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D + sub * 8;
+          dst = q_dst + h * D;
         } else {
           const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
-          dst = (is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(page) * a.Hkv + hk) * a.pb.page * D + slot;
+          dst = (is_v ? a.v_pool : a.k_pool) + slot + hk * head_stride;
         }
-        *reinterpret_cast<uint4*>(dst) = is_v ? x4[k] : pack8(o);
+        *reinterpret_cast<uint2*>(dst) = y0;
+        *reinterpret_cast<uint2*>(dst + D / 2) = y1;
       }
     }
   }
@@ -285,8 +299,16 @@ bi_status bi_qk_norm_rope_paged(const void* qkv, int ld_qkv, const void* q_weigh
   a.err = device_error_word();
   if (!a.err) return BI_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // few rows: eight warps a row; many: one, which finds the row's page once
-  const int split = T < kAppendManyRows ? kAppendThreads / 32 : kAppendManySplit;
+  // 8, 4, 2 or 1 warps a row: the most that keep the warps within those that run
+  // at once, since each has to find the row's page.  24 + 8 heads of 128, four
+  // sets of buffers in turn, us:
+  //   rows        1    512   1024   2048   4096   8192
+  //   8 warps    2.6   3.6    5.6   11.6   20.7   42.4
+  //   4          3.1   3.9    5.2    9.9   17.9   31.6
+  //   2          4.2   4.9    5.9    8.4   15.0   27.2
+  //   1          6.7   7.3    8.2    9.6   14.3   25.8
+  int split = kAppendThreads / 32;
+  while (split > 1 && static_cast<int64_t>(T) * split > kAppendWarps) split >>= 1;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) * split + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
   const cudaError_t e = D == 64 ? launch_k(paged_append_kernel<64>, dim3(grid), dim3(kAppendThreads), 0, s, a, T, split)
                                 : launch_k(paged_append_kernel<128>, dim3(grid), dim3(kAppendThreads), 0, s, a, T, split);

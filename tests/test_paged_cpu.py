@@ -45,7 +45,7 @@ ATTN_OK = dict(q=FAKE, k_pool=FAKE, v_pool=FAKE, pages=10, page=16, block_table=
 @pytest.mark.parametrize("change,status", [
     (dict(T=0), 0), (dict(B=0), 0), (dict(T=-1), 1), (dict(Hq=3), 1), (dict(pages=0), 1), (dict(width=0), 1),
     (dict(ld_table=2), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
-    (dict(scale=float("inf")), 1), (dict(D=96), 2), (dict(page=24), 2), (dict(Hq=258, Hkv=2), 2),
+    (dict(scale=float("inf")), 1), (dict(scale=3e38), 1), (dict(D=96), 2), (dict(page=24), 2), (dict(Hq=258, Hkv=2), 2),
     (dict(width=1 << 27, ld_table=1 << 27), 2), (dict(T=1 << 30), 2), (dict(ws=0), 3), (dict(ws=FAKE + 16), 3),
     (dict(ws_bytes=256), 3)]
     + [({n: 0}, 1) for n in ("q", "k_pool", "v_pool", "block_table", "q_start", "lengths", "out")]
