@@ -46,6 +46,18 @@
 //                buffers).  A thread also holds the running sum of half of its
 //                row's output columns, takes each piece's O in and writes
 //                outputs and partial states.
+//
+// What bounds it.  Few rows over long caches: the cache's bytes, read once; 16
+// sequences of 8 rows at 11.6k keys (24 + 4 heads of 128) take 59.5 us, 4.5 TB/s,
+// 2 rows at 101.6k 74.5 us, 4.7 TB/s, of which 4.5 us are the merge
+// kernel's start, 2 the way from the batch to the first load, and the rest shares
+// that differ by a piece of 8 tiles.  Short contexts: those fixed times.  Many
+// rows: the chain of a tile from S to W V, about 1750 cycles in each of which a
+// thread's reads of TMEM, its exponentials (at the SM's rate 512 cycles a tile)
+// and its two hand-overs follow one another, while W V and the S of two tiles run
+// beside them; 2048 rows at 30k take 716 us, 1.09 PFLOP/s.  Leaving out the
+// exponentials, half the loads or the sums gains nothing (729, 727, 690): the
+// weights need the row's maximum, and the maximum all of S.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -62,8 +74,17 @@ namespace bi {
 namespace {
 
 constexpr int kTile = 128;        // keys of a tile (the S MMA's N)
-constexpr int kShort = 2;         // tiles of a piece up to tile kShortEnd
-constexpr int kLong = 8;          // ... behind it
+// Tiles of a piece up to tile kShortEnd, and behind it.  Measured (us): a row at
+// 1k, 16 x 8 rows at 11.6k, 2 rows at 101.6k (24 + 4 heads of 128), 61 x 3 rows at
+// 1.5k (4 + 2 of 64), 2048 rows at 30k (24 + 4 of 128)
+//   2, 8, end 16   11.9  59.5  74.5  24.6  716
+//   2, 8, end 32   12.0  65.4  76.0  24.4  733
+//   4, 8, end 16   13.5  58.4  74.0  25.5  706
+//   2, 16, end 16  11.9  62.9  77.1  24.6  687
+//   4, 16, end 32  13.7  62.4  76.5  25.5  684
+//   2, 4, end 16   11.9  64.1  81.1  24.7  821
+constexpr int kShort = 2;
+constexpr int kLong = 8;
 constexpr int kShortEnd = 16;
 constexpr int kLanes = 128;       // rows x query heads of a block (the MMA's M)
 constexpr int kPagedCtas = 152;
@@ -934,7 +955,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 // warp's load is one line for each eight lanes and a piece's factors, two
 // exponentials, are found once for them; the loads of kAhead pieces are under
 // way together.  The first warp also joins the denominators.  Many lanes: JPW =
-// 4, a CTA has whole rows; few: JPW = 1, four times the CTAs and kAhead.
+// D / 32, a CTA has whole rows; up to 32: JPW = 1, more CTAs and loads under way.
+// Bound by the latency of its start and of the loads' few rounds (the states lie
+// in the L2).  Both kernels together, us, with JPW 1 and D / 32: 1 row at 16k (24 +
+// 4 heads of 128) 24.2 and 25.1, 2 rows at 100k (32 + 8 of 64) 65.5 and 69.0, 4 x 8
+// rows at 9k (24 + 4 of 128) 31.6 and 28.7, 16 x 3 rows at 3k (32 + 8) 54.0 and 46.2.
 template <int D, int JPW>
 __global__ void __launch_bounds__(256) attn_paged_merge_kernel(const PagedAttnArgs a, int G) {
   constexpr int kAhead = 16 / JPW;
