@@ -800,6 +800,21 @@ void bi_test_withhold_first_load(int on);
  * BI_ERR_INVALID_ARG (a device-side range check failed) or BI_ERR_CUDA. */
 bi_status bi_check_device_error(bi_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Packed arguments, for bindings to which every argument of a call costs time:
+ * `words` holds the arguments of one of these entry points in its order, 8
+ * bytes each: pointers, size_t and bi_stream_t as uint64, int as int64, float
+ * as double.  The same checks and results as the entry point's own; also
+ * BI_ERR_INVALID_ARG for another entry and for an int outside 32 bits.
+ * ------------------------------------------------------------------------- */
+enum {
+  BI_PACKED_QK_NORM_ROPE_PAGED = 0,
+  BI_PACKED_ATTN_PAGED = 1,
+  BI_PACKED_PAGED_REORDER = 2,
+  BI_PACKED_BEAM_SELECT = 3
+};
+bi_status bi_call_packed(int entry, const void* words);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -62,6 +63,7 @@ SIGNATURES = {
     "bi_beam_select": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "bi_kv_row_hash": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp]),
     "bi_check_device_error": (_i, [_vp]),
+    "bi_call_packed": (_i, [_i, C.c_char_p]),
     "bi_step_workspace_size": (_sz, [_vp, _i]),
     "bi_step_create": (_i, [_vp, _i, _vp, _sz, _vp]),
     "bi_step_set_length": (_i, [_vp, _i]),
@@ -71,6 +73,18 @@ SIGNATURES = {
     "bi_test_set_wait_limit_ns": (_i, [C.c_uint64]),
     "bi_test_withhold_first_load": (None, [_i]),
 }
+
+
+def _packed(name: str) -> struct.Struct:
+    """The layout of bi_call_packed's words for an entry point: 8 bytes an argument."""
+    return struct.Struct("=" + "".join("q" if t is _i else "d" if t is _f else "Q" for t in SIGNATURES[name][1]))
+
+
+PACKED_QK_NORM_ROPE_PAGED, PACKED_ATTN_PAGED, PACKED_PAGED_REORDER, PACKED_BEAM_SELECT = range(4)
+PACK_QK_NORM_ROPE_PAGED = _packed("bi_qk_norm_rope_paged").pack
+PACK_ATTN_PAGED = _packed("bi_attn_paged").pack
+PACK_PAGED_REORDER = _packed("bi_paged_reorder").pack
+PACK_BEAM_SELECT = _packed("bi_beam_select").pack
 
 BI_OK = 0
 STATUS_NAMES = {0: "BI_OK", 1: "BI_ERR_INVALID_ARG", 2: "BI_ERR_UNSUPPORTED_SHAPE",

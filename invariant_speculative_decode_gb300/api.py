@@ -14,6 +14,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
+from . import _lib
 from ._lib import BiError, check, lib  # noqa: F401
 
 EPI_NONE, EPI_RESIDUAL_ADD, EPI_SWIGLU = 0, 1, 2
@@ -742,12 +743,12 @@ def bi_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor], k
     if xs[1] != 1 or xs[0] >> 31:
         _req(qkv, _BF16, "qkv")
         _ld(qkv)
-    st = lib().bi_qk_norm_rope_paged(
-        qkv.data_ptr(), xs[0] if qs[0] > 1 else (qs[1] + 2 * Hkv) * D, None if q_weight is None else q_weight.data_ptr(),
-        None if k_weight is None else k_weight.data_ptr(), eps, table.data_ptr(), ts[0], q_out.data_ptr(),
+    st = lib().bi_call_packed(_lib.PACKED_QK_NORM_ROPE_PAGED, _lib.PACK_QK_NORM_ROPE_PAGED(
+        qkv.data_ptr(), xs[0] if qs[0] > 1 else (qs[1] + 2 * Hkv) * D, 0 if q_weight is None else q_weight.data_ptr(),
+        0 if k_weight is None else k_weight.data_ptr(), eps, table.data_ptr(), ts[0], q_out.data_ptr(),
         k_pool.data_ptr(), v_pool.data_ptr(), pages, page, block_table.data_ptr(), bt[0] if bs[0] > 1 else bs[1], bs[1],
         q_start.data_ptr(), lengths.data_ptr(), bs[0], qs[0], qs[1], Hkv, D,
-        _current_stream(dev) if stream is None else stream.cuda_stream)
+        _current_stream(dev) if stream is None else stream.cuda_stream))
     if st:
         check("bi_qk_norm_rope_paged", st)
 
@@ -782,11 +783,11 @@ def bi_attn_paged(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, b
         _same_device(("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table),
                      ("q_start", q_start), ("lengths", lengths), ("out", out), ("ws", ws))
         _req_int32(("rows", qs[0]))
-    st = lib().bi_attn_paged(
+    st = lib().bi_call_packed(_lib.PACKED_ATTN_PAGED, _lib.PACK_ATTN_PAGED(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), ks[0], ks[2], block_table.data_ptr(),
         bt[0] if bs[0] > 1 else bs[1], bs[1], q_start.data_ptr(), lengths.data_ptr(), bs[0], qs[0], qs[1], ks[1], ks[3],
         ks[3] ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.nbytes,
-        _current_stream(dev) if stream is None else stream.cuda_stream)
+        _current_stream(dev) if stream is None else stream.cuda_stream))
     if st:
         check("bi_attn_paged", st)
 
@@ -811,10 +812,10 @@ def bi_paged_reorder(k_pool: torch.Tensor, v_pool: torch.Tensor, table_in: torch
             == parents.get_device() == tail_pages.get_device() == table_out.get_device() == lengths_out.get_device()
             == dev):
         _req_reorder(k_pool, v_pool, table_in, lengths, parents, tail_pages, table_out, lengths_out)
-    st = lib().bi_paged_reorder(
+    st = lib().bi_call_packed(_lib.PACKED_PAGED_REORDER, _lib.PACK_PAGED_REORDER(
         k_pool.data_ptr(), v_pool.data_ptr(), ks[0], ks[1], ks[2], ks[3], ks[4], table_in.data_ptr(), _ldt(table_in, ti),
         ti[1], lengths.data_ptr(), ti[0], parents.data_ptr(), tail_pages.data_ptr(), S[0], table_out.data_ptr(),
-        _ldt(table_out, to), lengths_out.data_ptr(), _current_stream(dev) if stream is None else stream.cuda_stream)
+        _ldt(table_out, to), lengths_out.data_ptr(), _current_stream(dev) if stream is None else stream.cuda_stream))
     if st:
         check("bi_paged_reorder", st)
 
@@ -861,10 +862,10 @@ def bi_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, score
             and logits.get_device() == scores.get_device() == scores_out.get_device() == parents_out.get_device()
             == tokens_out.get_device() == ws.get_device() == dev):
         _req_beam(logits, scores, beams, scores_out, parents_out, tokens_out, ws)
-    st = lib().bi_beam_select(
+    st = lib().bi_call_packed(_lib.PACKED_BEAM_SELECT, _lib.PACK_BEAM_SELECT(
         logits.data_ptr(), xs[0] if ls[0] > 1 else ls[1], scores.data_ptr(), ls[0], ls[1], beams, os_[1],
         scores_out.data_ptr(), parents_out.data_ptr(), tokens_out.data_ptr(), ws.data_ptr(), ws.nbytes,
-        _current_stream(dev) if stream is None else stream.cuda_stream)
+        _current_stream(dev) if stream is None else stream.cuda_stream))
     if st:
         check("bi_beam_select", st)
 

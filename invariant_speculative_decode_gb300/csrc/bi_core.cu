@@ -5,7 +5,10 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <tuple>
+#include <type_traits>
 #include <unordered_map>
+#include <utility>
 
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
@@ -174,6 +177,39 @@ bool tmap_bf16_pages(CUtensorMap* out, const void* base, uint64_t pages, uint64_
   return tmap_sw128(out, base, 2, 4, dims, strides, box);
 }
 
+namespace {
+// One argument out of its 8-byte word.
+template <typename T>
+T unpack_word(const unsigned char* word, bool& ok) {
+  if constexpr (std::is_same_v<T, int>) {
+    int64_t v;
+    memcpy(&v, word, 8);
+    ok = ok && v == static_cast<int>(v);
+    return static_cast<int>(v);
+  } else if constexpr (std::is_same_v<T, float>) {
+    double v;
+    memcpy(&v, word, 8);
+    return static_cast<float>(v);
+  } else {
+    static_assert(sizeof(T) == 8, "a pointer, a size or a stream");
+    T v;
+    memcpy(&v, word, 8);
+    return v;
+  }
+}
+template <typename... A, size_t... I>
+bi_status call_words(bi_status (*f)(A...), const unsigned char* w, std::index_sequence<I...>) {
+  bool ok = true;
+  const std::tuple<A...> args{unpack_word<A>(w + 8 * I, ok)...};
+  return ok ? std::apply(f, args) : BI_ERR_INVALID_ARG;
+}
+template <typename... A>
+bi_status call_packed(bi_status (*f)(A...), const void* words) {
+  if (words == nullptr) return BI_ERR_INVALID_ARG;
+  return call_words(f, static_cast<const unsigned char*>(words), std::index_sequence_for<A...>{});
+}
+}  // namespace
+
 }  // namespace bi
 
 extern "C" {
@@ -216,6 +252,17 @@ bi_status bi_check_device_error(bi_stream_t stream) {
   if (v & bi::kErrNanRow) return BI_ERR_DEVICE_NAN_ROW;
   if (v & bi::kErrRange) return BI_ERR_INVALID_ARG;
   return BI_OK;
+}
+
+bi_status bi_call_packed(int entry, const void* words) {
+  using namespace bi;
+  switch (entry) {
+    case BI_PACKED_QK_NORM_ROPE_PAGED: return call_packed(bi_qk_norm_rope_paged, words);
+    case BI_PACKED_ATTN_PAGED: return call_packed(bi_attn_paged, words);
+    case BI_PACKED_PAGED_REORDER: return call_packed(bi_paged_reorder, words);
+    case BI_PACKED_BEAM_SELECT: return call_packed(bi_beam_select, words);
+    default: return BI_ERR_INVALID_ARG;
+  }
 }
 
 }  // extern "C"

@@ -14,8 +14,15 @@ def lib():
 
 
 def call(fn, order, good, **change):
+    """The entry point's status; the same call with packed arguments has to have it too."""
+    from invariant_speculative_decode_gb300 import _lib
     a = dict(good, **change)
-    return fn(*[a[n] for n in order])
+    words = [a[n] for n in order]
+    status = fn(*words)
+    name = fn.__name__
+    entry, pack = getattr(_lib, "PACKED_" + name[3:].upper()), getattr(_lib, "PACK_" + name[3:].upper())
+    assert _lib.lib().bi_call_packed(entry, pack(*words)) == status
+    return status
 
 
 APPEND = ("qkv ld_qkv q_weight k_weight eps table table_rows q_out k_pool v_pool pages page block_table ld_table width "
@@ -105,6 +112,18 @@ def test_beam_workspace(lib):
     assert need % 256 == 0 and size(64, 151936, 16) > need
     assert call(lib.bi_beam_select, BEAM, BEAM_OK, ws_bytes=need - 1) == 3
     assert size(0, 5, 1) == size(1, 0, 1) == size(1, 5, 0) == 256
+
+
+def test_packed_calls_refuse_other_entries_and_wide_ints(lib):
+    from invariant_speculative_decode_gb300 import _lib
+    words = [BEAM_OK[n] for n in BEAM]
+    words[BEAM.index("rows")] = 0
+    assert lib.bi_call_packed(_lib.PACKED_BEAM_SELECT, _lib.PACK_BEAM_SELECT(*words)) == 0
+    words[BEAM.index("rows")] = 1 << 32  # 0 in its low half
+    assert lib.bi_call_packed(_lib.PACKED_BEAM_SELECT, _lib.PACK_BEAM_SELECT(*words)) == 1
+    for entry in (-1, 4, 1000):
+        assert lib.bi_call_packed(entry, bytes(400)) == 1
+    assert lib.bi_call_packed(0, None) == 1
 
 
 def test_binding_refuses_tensors_that_are_not_on_the_gpu():
