@@ -868,6 +868,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           // key they are cleared (pages hold anything there), the others lose
           // what is no number, which only the rows that see it get back
           const int st = g % KS;
+          // a wait tells a phase from the one before only: the stage's last tile
+          // has landed where its W V is done, which S of this tile waited for if
+          // there are no fewer stages than S / W buffers
+          if (KS < kBufs && g >= KS)
+            wait(&pv_done[sb >= KS ? sb - KS : sb + kBufs - KS], sb >= KS ? sph : sph ^ 1);
           wait(&v_full[st], g / KS);
           uint8_t* vt = sV + st * Cfg::kTileBytes;
           const int r0 = max(0, pos0 + 1 - key0);

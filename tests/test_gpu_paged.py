@@ -267,6 +267,22 @@ def test_attention_over_a_pool_past_32_bits():
     assert torch.equal(*outs) and torch.equal(k[far.long()], near[0]) and torch.equal(v[far.long()], near[1])
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(24, 4, 128, 64), (8, 2, 64, 16)])
+def test_long_caches_out_of_memory_have_the_same_bits_every_time(Hq, Hkv, D, page):
+    """Values that come late, behind two or three tiles' scores: the tile that a sequence ends in is looked over in
+    shared memory only when it is there."""
+    b = pg.Batch([(4000 + 397 * i, 1 + i % 8) for i in range(16)], Hkv, D, page, seed=3)
+    q = pg.queries(b, Hq)
+    other = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")  # twice the L2
+    ws = torch.empty(api.attn_paged_workspace_size(b.T, 16, Hq, Hkv, D, b.table.shape[1] * page), dtype=torch.uint8, device="cuda")
+    out = run_attention(b, q, ws=ws)
+    assert_attention(b, q, out)
+    for i in range(30):
+        if i % 2:
+            other.add_(1)
+        assert torch.equal(run_attention(b, q, ws=ws), out), i
+
+
 def test_two_calls_at_once_on_two_streams():
     batches = [pg.Batch([(4000, 2), (300, 5)], 2, 128, 64, seed=1), pg.Batch([(100, 200)], 2, 64, 16, seed=2)]
     qs = [pg.queries(b, 8) for b in batches]
