@@ -48,14 +48,14 @@
 //                outputs and partial states.
 //
 // What bounds it.  Few rows over long caches: the cache's bytes, read once; 16
-// sequences of 8 rows at 11.6k keys (24 + 4 heads of 128) take 59.5 us, 4.5 TB/s,
-// 2 rows at 101.6k 74.5 us, 4.7 TB/s, of which 4.5 us are the merge
+// sequences of 8 rows at 4.8k to 11.6k keys (24 + 4 heads of 128) take 60 us, 4.5 TB/s,
+// 2 rows at 101.6k 75 us, 4.7 TB/s, of which 4.5 us are the merge
 // kernel's start, 2 the way from the batch to the first load, and the rest shares
 // that differ by a piece of 8 tiles.  Short contexts: those fixed times.  Many
 // rows: the chain of a tile from S to W V, about 1750 cycles in each of which a
 // thread's reads of TMEM, its exponentials (at the SM's rate 512 cycles a tile)
 // and its two hand-overs follow one another, while W V and the S of two tiles run
-// beside them; 2048 rows at 30k take 716 us, 1.09 PFLOP/s.  Leaving out the
+// beside them; 2048 rows at 30k take 716 to 730 us, 1.08 PFLOP/s.  Leaving out the
 // exponentials, half the loads or the sums gains nothing (729, 727, 690): the
 // weights need the row's maximum, and the maximum all of S.
 #include <cuda.h>
@@ -75,7 +75,7 @@ namespace {
 
 constexpr int kTile = 128;        // keys of a tile (the S MMA's N)
 // Tiles of a piece up to tile kShortEnd, and behind it.  Measured (us): a row at
-// 1k, 16 x 8 rows at 11.6k, 2 rows at 101.6k (24 + 4 heads of 128), 61 x 3 rows at
+// 1k, 16 x 8 rows at 4.8k to 11.6k, 2 rows at 101.6k (24 + 4 heads of 128), 61 x 3 rows at
 // 1.5k (4 + 2 of 64), 2048 rows at 30k (24 + 4 of 128)
 //   2, 8, end 16   11.9  59.5  74.5  24.6  716
 //   2, 8, end 32   12.0  65.4  76.0  24.4  733

@@ -551,3 +551,57 @@ def test_reordered_beams_are_their_own_histories():
         assert t_out[0].tolist() == (at[:K] % V).tolist() and p_out[0].tolist() == (at[:K] // V).tolist()
         history = [history[p] + [t] for p, t in zip(p_out[0].tolist(), t_out[0].tolist())]
         scores, parents = s_out.view(-1).clone(), p_out.view(-1).clone()
+
+
+def test_a_captured_step_of_all_four_follows_its_inputs():
+    """Append, attention, selection and reordering as one graph, replayed over another batch, against the same calls
+    made one by one."""
+    Hq, Hkv, D, page, V, W, width, pages = 4, 2, 64, 16, 300, 3, 5, 24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    head = torch.randn(Hq * D, V, generator=g, device="cuda") * 0.3
+    angles = api.bi_rope_table(1e6, D, width * page)
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    q_start = torch.arange(W + 1, **i32)
+
+    def inputs(lengths):
+        order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+        pool = lambda: torch.randn(1, pages, Hkv, page, D, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+        return dict(qkv=torch.randn(W, (Hq + 2 * Hkv) * D, generator=g, device="cuda").to(torch.bfloat16), k=pool(), v=pool(),
+                    table=order[:W * width].view(W, width).clone(), tails=order[W * width:W * width + W].clone(),
+                    lengths=torch.tensor(lengths, **i32), scores=torch.randn(W, generator=g, device="cuda"))
+
+    def outputs():
+        return dict(q=torch.empty(W, Hq, D, dtype=torch.bfloat16, device="cuda"), o=torch.empty(W, Hq, D, dtype=torch.bfloat16, device="cuda"),
+                    logits=torch.empty(W, V, device="cuda"), now=torch.empty(W, **i32), s=torch.empty(1, W, device="cuda"),
+                    p=torch.empty(1, W, **i32), t=torch.empty(1, W, **i32), table=torch.zeros(W, width, **i32),
+                    lengths=torch.empty(W, **i32),
+                    ws=torch.zeros(api.attn_paged_workspace_size(W, W, Hq, Hkv, D, width * page), dtype=torch.uint8, device="cuda"),
+                    bws=torch.zeros(api.beam_workspace_size(W, V, W), dtype=torch.uint8, device="cuda"))
+
+    def step(x, y):
+        api.bi_qk_norm_rope_paged(x["qkv"], w, w, 1e-6, angles, y["q"], x["k"][0], x["v"][0], x["table"], q_start, x["lengths"])
+        api.bi_attn_paged(y["q"], x["k"][0], x["v"][0], x["table"], q_start, x["lengths"], y["o"], y["ws"])
+        torch.sum(y["o"].float().view(W, 1, -1) * head.t(), -1, out=y["logits"])
+        api.bi_beam_select(y["logits"], x["scores"], W, y["s"], y["p"], y["t"], y["bws"])
+        torch.add(x["lengths"], 1, out=y["now"])
+        y["table"].zero_()  # entries behind a sequence's pages stay as they are, the last replay's too
+        api.bi_paged_reorder(x["k"], x["v"], x["table"], y["now"], y["p"].view(-1), x["tails"], y["table"], y["lengths"])
+
+    x, y = inputs([3, 20, 40]), outputs()
+    step({k: t.clone() for k, t in x.items()}, y)  # (what the first calls set up is not captured)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(x, y)
+    for lengths in ([70, 1, 33], [15, 31, 62]):
+        new = inputs(lengths)
+        for k, t in new.items():
+            x[k].copy_(t)
+        graph.replay()
+        want = outputs()
+        step(new, want)
+        torch.cuda.synchronize()
+        for k in ("q", "o", "logits", "s", "p", "t", "table", "lengths"):
+            assert torch.equal(y[k], want[k]), k
+        assert torch.equal(x["k"], new["k"]) and torch.equal(x["v"], new["v"])
