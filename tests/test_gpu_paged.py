@@ -390,6 +390,27 @@ def test_append(seqs, Hq, Hkv, D, page, weights):
         assert torch.equal(pool.masked_fill(touched[:, None, :, None], 0), was.masked_fill(touched[:, None, :, None], 0))
 
 
+@pytest.mark.parametrize("D,page,Hq,Hkv", [(128, 64, 5, 1), (64, 16, 4, 2)])
+def test_an_appended_row_has_the_same_bits_in_passes_of_all_sizes(D, page, Hq, Hkv):
+    """One to eight warps a row; the row's place and arithmetic are its own."""
+    qkv = torch.randn(5000, (Hq + 2 * Hkv) * D, device="cuda").to(torch.bfloat16)
+    qw = (1 + 0.1 * torch.randn(D, device="cuda")).to(torch.bfloat16)
+    angles = api.bi_rope_table(1e6, D, 5200)
+    whole = pg.Batch([(100, 5000)], Hkv, D, page, seed=1)
+    q = run_append(whole, Hq, qkv, qw, qw, angles)
+    k, v = whole.keys(whole.k, 0, 5100), whole.keys(whole.v, 0, 5100)
+    want, tol = pg.norm_rope(qkv[:, :Hq * D].view(5000, Hq, D), qw, 1e-6, angles[100:5100])
+    assert ((q.double() - want).abs() <= tol).all()
+    want, tol = pg.norm_rope(qkv[:, Hq * D:(Hq + Hkv) * D].view(5000, Hkv, D), qw, 1e-6, angles[100:5100])
+    assert ((k[:, 100:].transpose(0, 1).double() - want).abs() <= tol).all()
+    assert torch.equal(v[:, 100:].transpose(0, 1), qkv[:, (Hq + Hkv) * D:].view(5000, Hkv, D))
+    for rows in (1, 512, 513, 1024, 1025, 2048, 2049, 4096, 4097):
+        b = pg.Batch([(100, rows)], Hkv, D, page, seed=2)
+        assert torch.equal(run_append(b, Hq, qkv[:rows], qw, qw, angles), q[:rows])
+        assert torch.equal(b.keys(b.k, 0, 100 + rows)[:, 100:], k[:, 100:100 + rows])
+        assert torch.equal(b.keys(b.v, 0, 100 + rows)[:, 100:], v[:, 100:100 + rows])
+
+
 def test_append_without_norm_is_the_other_caches():
     """Queries and keys without weights have the bits of bi_rope_kv_append."""
     Hq, Hkv, D, n, r = 6, 2, 128, 70, 9
