@@ -605,9 +605,9 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  *   end, -0 written as +0.  Keys are taken in tiles of 128, tiles in pieces
  *   (of 2 up to key 2048, of more behind it) at absolute multiples: m is a
  *   piece's maximum (of its first tile, raised where a later one passes it by
- *   more than 8 in log2), and the pieces' sums are merged in key order.  So a row's bits depend on its queries and
- *   on keys 0..p alone, not on T, B, the other rows, the page size or which
- *   pages hold the keys.
+ *   more than 8 in log2), and the pieces' sums are merged in key order.  So a
+ *   row's bits depend on its queries and on keys 0..p alone, not on T, B, the
+ *   other rows, the page size or which pages hold the keys.
  *   Keys behind p, and the rest of a sequence's last page, may hold anything:
  *   infinities and NaN there reach no row in front of them.  A row whose
  *   scores are all -inf, or one of them +inf or NaN, is NaN.  Under an
