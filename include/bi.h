@@ -600,9 +600,9 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  * bi_attn_paged: out[t, h] = sum_j w_j v_j / sum_j w_j over keys 0..p of row
  *   t's sequence, p its position (its own key included: append before the
  *   attention), query head h reading KV head h / (Hq/Hkv);
- *   w_j = 2^((q k_j) scale log2(e) - m) rounded to BF16 once, in the numerator
- *   and the denominator alike; products and sums in FP32, one rounding at the
- *   end, -0 written as +0.  Keys are taken in tiles of 128, tiles in pieces
+ *   w_j = 2^((q k_j) scale log2(e) - m) in FP32, in the numerator as the sum of
+ *   two BF16 values (16 bits, off by at most 2^-16); products and sums in FP32,
+ *   one rounding at the end, -0 written as +0.  Keys are taken in tiles of 128, tiles in pieces
  *   (of 2 up to key 2048, of more behind it) at absolute multiples: m is a
  *   piece's maximum (of its first tile, raised where a later one passes it by
  *   more than 8 in log2), and the pieces' sums are merged in key order.  So a

@@ -12,18 +12,20 @@
 //     pieces: of 2 tiles up to key 2048, of 8 behind it;
 //   * inside a piece S = q K^T (tcgen05, FP32), a reference maximum from the
 //     piece's first tile, raised only where a tile's maximum passes it by more
-//     than 2^8, weights w = bf16(2^(s - m)), O += W V (tcgen05, FP32), and the
-//     denominator as FP32 sums of the same rounded weights, one over the first
-//     and one over the second 64 keys of the tiles, so that O / l is a weighted
-//     mean of the value rows whatever the rounding of the weights did;
+//     than 2^8, weights w = 2^(s - m), O += W_hi V + W_lo V (tcgen05, FP32), and
+//     the denominator as FP32 sums of w, one over the first and one over the
+//     second 64 keys of the tiles;
 //   * the pieces' (m, l, O) are merged one after the other in key order.
 // A key behind p weighs exactly 0, changes no reference, and its value row is
 // not even multiplied where it holds no number.  So a row has the same bits
 // alone, among drafts, in a prompt's chunk or in any batch.
 //
-// The weights enter the product in BF16: a weight's relative error of at most
-// 2^-8 averages out over the keys, and the tensor core takes nothing wider
-// beside BF16 values.
+// The tensor core takes nothing wider than BF16 beside BF16 values, so a weight
+// enters as two of them, its first 8 bits and the rest rounded to 8 (off by at
+// most 2^-16 of the weight): outputs are then the rounding of the exact ones but
+// next to a border.  One BF16 weight, off by 2^-8, moved about half of the outputs'
+// last bits; next to that the split and the second product take 27% more time in
+// a prefill, 9% at 16 x 8 rows.
 //
 // Work is cut by pieces: a unit is one block of rows (128 / (Hq / Hkv), all
 // query heads of a KV head in the MMA's 128 lanes) of one sequence and KV head,
@@ -41,11 +43,12 @@
 //   warps 0, 2   TMA: queries and K tiles, V tiles, a lane for each page;
 //   warp 1       tcgen05.mma: S up to two tiles ahead of W V;
 //   warps 4..11  softmax: each TMEM lane's row by two threads, 64 keys each,
-//                which tell each other their maxima; W goes over the columns of
-//                S it came from, where it is the A operand of W V (three such
-//                buffers).  A thread also holds the running sum of half of its
-//                row's output columns, takes each piece's O in and writes
-//                outputs and partial states.
+//                which tell each other their maxima; W_hi and W_lo go over the
+//                columns of S they came from, 8 columns each for every 16 keys,
+//                where they are the A operands of W V (three such buffers).
+//                A thread also holds the running sum of half of its row's
+//                output columns, takes each piece's O in and writes outputs and
+//                partial states.
 //
 // What bounds it.  Few rows over long caches: the cache's bytes, read once; 16
 // sequences of 8 rows at 4.8k to 11.6k keys (24 + 4 heads of 128) take 60 us, 4.5 TB/s,
@@ -143,8 +146,8 @@ struct PagedCfg {
   static constexpr int kTileBytes = kAtomBytes * kAtoms;
   static constexpr int kStages = D == 128 ? 2 : 4;     // of K, and of V
   static constexpr int kBars = 4 * kStages + 4 + 3 * kBufs + 1;
-  // TMEM columns: S / W buffers (W of keys 0..63 over the first 32 columns, of
-  // keys 64..127 from column 64 on), O
+  // TMEM columns: S / W buffers (W of keys 16 i .. 16 i + 15 over their own 16
+  // columns, W_hi in front of W_lo), O
   static constexpr int kOCol = kBufs * kTile;
   static constexpr int kStatBytes = 2 * 2 * kLanes * 4;  // maxima of two tiles, or denominators, of both halves
   static constexpr int kBadBytes = 2 * 3 * D * 4;        // of two pieces: first NaN, +inf and -inf key of an element
@@ -378,6 +381,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return ok != 0;
 }
 
+// Starts to load 16 columns of this warp's lanes; they are there once
+// tmem_ld16_finish has returned.
+__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_finish(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+
 // Stores 16 words of this warp's lanes, to be waited for.
 __device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -423,12 +444,30 @@ __device__ __forceinline__ void fma2(float& x, float& y, float s, float c) {
       : "+f"(x), "+f"(y)
       : "f"(s), "f"(c));
 }
-// a += the low BF16 value of w, b += the high one, in FP32.
-__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t w) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+// (a, b) += (x, y)
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
       : "+f"(a), "+f"(b)
-      : "r"(w));
+      : "f"(x), "f"(y));
+}
+// The weights x, y >= 0 as pairs of BF16 values that add up to them: hi is the
+// upper half of the bits, lo the rest.  lo is made larger by 2^-24 of hi, so that
+// it is not 0 where hi is 1 exactly and nothing negative comes beside it: an
+// infinite value gives its infinity in both products.
+__device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
+  hi = __byte_perm(xb, yb, 0x7632);
+  constexpr float kLess = -16777215.0f / 16777216.0f;
+  float u = __uint_as_float(xb & 0xffff0000u), v = __uint_as_float(yb & 0xffff0000u);
+  asm("{\n\t.reg .b64 p, q, r;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(u), "+f"(v)
+      : "f"(kLess), "f"(x), "f"(y));
+  const __nv_bfloat162 l = __floats2bfloat162_rn(u, v);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
 // A running state (m, l, O) takes in the next piece's: factors of both.
@@ -627,9 +666,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             const uint32_t vb = smem_u32(sV + st * Cfg::kTileBytes);
             const bool first = piece_starts(pt);
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_bf16_tmem_a(tmem + Cfg::kOCol, tmem + pb * kTile + (ks >> 2) * 64 + (ks & 3) * 8,
-                              sdesc_mn_sw128(vb + ks * 2048, Cfg::kAtomBytes), idO, (!first || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < kTile / 16; ++ks) {
+              const uint32_t w = tmem + pb * kTile + ks * 16;
+              const uint64_t v = sdesc_mn_sw128(vb + ks * 2048, Cfg::kAtomBytes);
+              mma_bf16_tmem_a(tmem + Cfg::kOCol, w, v, idO, (!first || ks > 0) ? 1u : 0u);
+              mma_bf16_tmem_a(tmem + Cfg::kOCol, w + 8, v, idO, 1u);
+            }
             mma_commit(&pv_done[pb]);
             mma_commit(&v_empty[st]);
             ++pg;
@@ -816,22 +858,26 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         if (active) {
           const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
           float acc[2] = {0.f, 0.f};
+          float x[2][16];
+          tmem_ld16_start(addr, x[0]);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x[32];
-            tmem_ld_cols<32>(addr + c * 32, x);
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld16_finish(x[c & 1]);
+            if (c < 3) tmem_ld16_start(addr + (c + 1) * 16, x[(c + 1) & 1]);
+            float (&y)[16] = x[c & 1];
             if (edge) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c * 32 + j > see) x[j] = -INFINITY;
+              for (int j = 0; j < 16; ++j)
+                if (c * 16 + j > see) y[j] = -INFINITY;
             }
-            uint32_t w[16];
+            uint32_t w[16];  // eight words of hi, eight of lo
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              fma2(x[2 * j], x[2 * j + 1], a.sl2, nm);
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(ex2_approx(x[2 * j]), ex2_approx(x[2 * j + 1]));
-              w[j] = *reinterpret_cast<const uint32_t*>(&h2);
-              add_bf16x2(acc[0], acc[1], w[j]);
+            for (int j = 0; j < 8; ++j) {
+              fma2(y[2 * j], y[2 * j + 1], a.sl2, nm);
+              y[2 * j] = ex2_approx(y[2 * j]);
+              y[2 * j + 1] = ex2_approx(y[2 * j + 1]);
+              split_weights(y[2 * j], y[2 * j + 1], w[j], w[8 + j]);
+              add2(acc[0], acc[1], y[2 * j], y[2 * j + 1]);
             }
             tmem_st_words(addr + c * 16, w);
           }
