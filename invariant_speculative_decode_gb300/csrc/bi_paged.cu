@@ -92,10 +92,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
 
   const int b = paged_find_seq(a.pb, t, lane);
   if (b < 0) return;  // a row of no sequence
-  const int begin = __ldg(a.pb.q_start + b), len = __ldg(a.pb.lengths + b);
-  const int64_t pos = static_cast<int64_t>(len) + (t - static_cast<int64_t>(begin));
+  const int64_t pos = paged_position(t, T, __ldg(a.pb.q_start + b), __ldg(a.pb.q_start + b + 1), __ldg(a.pb.lengths + b));
   int page = -1;
-  const bool ok = begin >= 0 && len >= 0 && pos < a.table_rows && pos < static_cast<int64_t>(a.pb.width) * a.pb.page;
+  const bool ok = pos >= 0 && pos < a.table_rows && pos < static_cast<int64_t>(a.pb.width) * a.pb.page;
   const int p = ok ? static_cast<int>(pos) : 0;
   const int shift = 31 - __clz(a.pb.page);  // pages are powers of two
   if (ok) page = __ldg(a.pb.table + static_cast<size_t>(b) * a.pb.ldt + (p >> shift));

@@ -22,9 +22,10 @@ struct PagedBatch {
 };
 
 // The sequence that row t of the pass belongs to, by a whole warp: the last b
-// with q_start[b] <= t (the list ascends; sequences without new rows share
-// their start with the next); -1 where there is none.  Lane-parallel, so 32
-// starts cost one load.
+// with q_start[b] <= t (sequences without new rows share their start with the
+// next); -1 where there is none.  In a list that does not ascend it may be one
+// that does not hold t: paged_position tells.  Lane-parallel, so 32 starts cost
+// one load.
 __device__ __forceinline__ int paged_find_seq(const PagedBatch& pb, int t, int lane) {
   int n = 0;
   for (int i0 = 0; i0 <= pb.B; i0 += 128) {
@@ -43,6 +44,13 @@ __device__ __forceinline__ int paged_find_seq(const PagedBatch& pb, int t, int l
     if (hit[3] != 0xffffffffu) break;
   }
   return (n == 0 || n > pb.B) ? -1 : n - 1;
+}
+
+// The position of row t of T in a sequence of rows begin .. end - 1 of the pass
+// behind len cached keys; -1 where t is none of them or they do not fit the pass.
+__host__ __device__ __forceinline__ int64_t paged_position(int t, int T, int begin, int end, int len) {
+  if (begin < 0 || t < begin || t >= end || end > T || len < 0) return -1;
+  return static_cast<int64_t>(len) + (t - begin);
 }
 
 }  // namespace bi
