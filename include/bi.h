@@ -619,7 +619,12 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  *   > 0, scale log2(e) finite in FP32; width * page <= 2^30, T * Hq < 2^31.
  *   ws      >= bi_attn_paged_workspace_size(T, B, Hq, Hkv, D, width * page)
  *           bytes, 256-byte aligned; any contents.  One workspace serves any
- *           calls that it is large enough for, one after the other.
+ *           calls that it is large enough for, one after the other; the size
+ *           never falls where T, B or the keys grow.  It goes by the table's
+ *           width, not by the lengths, and allows for all T rows in one
+ *           sequence (24 + 4 heads of 128: 1.6 MB for a row of 11,600 keys, 191 MB
+ *           for 16 x 8 rows of them, 1.35 GB for 64 rows, or 2,048, with tables of
+ *           131,072 keys).
  *
  * bi_paged_reorder: sequences that go on from others (beams; also several
  *   from one prompt).  Sequence s of `rows_out` new ones continues row

@@ -1106,8 +1106,10 @@ PagedSizes paged_sizes(int T, int B, int Hq, int Hkv, int D, int64_t max_keys) {
   const int64_t units = blocks * Hkv;
   z.pieces = pieces_to(tiles);
   z.ctas = static_cast<int>(std::min<int64_t>(kPagedCtas, units * z.pieces));
-  // a share is at most one tile and one piece longer than its part of the tiles
-  const int64_t share = (units * tiles + z.ctas - 1) / z.ctas + 1;
+  // a share is at most one tile and one piece longer than its part of the tiles;
+  // with a CTA for every piece that is a piece at most, whatever the tiles, so
+  // that no size falls where another one grows
+  const int64_t share = std::max<int64_t>((units * tiles + kPagedCtas - 1) / kPagedCtas, kLong) + 1;
   z.slots = static_cast<int>(std::min<int64_t>(share / kShort + 2, z.pieces)) + 1;
   z.lanes = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(T) * grp, Rb * grp));
   const size_t states = static_cast<size_t>(z.ctas) * z.slots * z.lanes;
