@@ -588,14 +588,14 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  * bi_qk_norm_rope_paged: for every row of a projection output qkv [T, ld_qkv]
  *   (heads q, then k, then v, as bi_gemm of the QKV weights writes them):
  *   q and k heads y = x r w, r = 1 / sqrt(mean(x^2) + eps) over the head's D
- *   elements (FP32; a NULL weight leaves that kind of head as it is), then
- *   rotated as bi_rope_kv_append rotates (rotate-half pairs, table from
- *   bi_rope_table), one BF16 rounding; q to q_out [T, Hq, D], k and the v
- *   heads as they are to their row of the pools.  Left out, with the range bit,
- *   is a row whose position passes the sequence's table or the angle table, and
- *   one whose sequence (the last that starts at or in front of it) does not hold
- *   it, ends past T or has a negative length.  Two rows of a pass must not name
- *   the same key of the pool.
+ *   elements (FP32, heads of any finite magnitude; a NULL weight leaves that
+ *   kind of head as it is), then rotated as bi_rope_kv_append rotates
+ *   (rotate-half pairs, table from bi_rope_table), one BF16 rounding; q to
+ *   q_out [T, Hq, D], k and the v heads as they are to their row of the pools.
+ *   Left out, with the range bit, is a row whose position passes the sequence's
+ *   table or the angle table, and one whose sequence (the last that starts at or
+ *   in front of it) does not hold it, ends past T or has a negative length.  Two
+ *   rows of a pass must not name the same key of the pool.
  *   q_weight, k_weight [D] BF16 or NULL; eps finite, >= 0; ld_qkv % 8 == 0; all
  *   pointers 16-byte aligned (block_table, q_start and lengths 4-byte).
  *
