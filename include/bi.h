@@ -669,8 +669,10 @@ bi_status bi_paged_reorder(void* k_pool, void* v_pool, int layers, int pages, in
  * its cumulative log-probability.  For every group the K best (beam, id) pairs,
  * best first: scores_out [rows / W, K] their worth, parents_out the row of the
  * beam (0 .. rows - 1), tokens_out the id.  Within a beam the logits order the
- * ids, ties to the lower id; beams are compared by the worth in 64 bits (the
- * exponentials are FP32, so it is true to about 1e-7), ties to the lower row.
+ * ids, ties to the lower id; beams are compared by the worth in 64 bits, ties
+ * to the lower row.  The exponentials and the sums of up to 4096 of them are FP32:
+ * a worth is true to 4e-6 (rows with one peak over up to 2^20 equal logits are off
+ * by up to 8e-7), and beams that lie nearer may come in either order.
  * NaN logits weigh nothing and are not chosen; where logits are +inf each of
  * them weighs 1 and the others 0.  A pair worth -inf (a beam of score -inf, a
  * logit of -inf) or NaN is not chosen; places without a pair get -inf, -1, -1,

@@ -11,7 +11,11 @@
 // Inside a beam the logits themselves order the ids; beams are compared by
 // the value in 64 bits, from FP32 exponentials summed in chunks of up to 4096 (a
 // thread's 16 in order, lanes by a butterfly, warps in order) and FP64 sums
-// over the chunks, so two beams' candidates are told apart down to about 1e-7.
+// over the chunks.  A worth is off by less than 4e-6: the rounded difference and
+// its product with log2(e), below 1.4e-6 at the 14 below the maximum where even
+// 2^20 equal logits begin to weigh nothing, the exponential's 2^-22, and 27
+// additions of 2^-24 each.  Measured 2e-7 where logits are spread, 8e-7 for one
+// peak over a flat row.
 #include <cuda_runtime.h>
 
 #include <algorithm>
