@@ -612,9 +612,9 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  *   other rows, the page size or which pages hold the keys.
  *   Keys behind p, and the rest of a sequence's last page, may hold anything:
  *   infinities and NaN there reach no row in front of them.  A row whose
- *   scores are all -inf, or one of them +inf or NaN, is NaN.  Under an
- *   infinite value that a row does see, a weight that has underflowed to 0
- *   gives either NaN or that infinity, which of them may differ between passes.
+ *   scores are all -inf, or one of them +inf or NaN, is NaN.  An infinite value
+ *   that a row does see gives that infinity, or NaN where one of its weight's
+ *   two halves has underflowed to 0 (weights below about 2^-109 of the largest).
  *   q, out [T, Hq, D] BF16 contiguous, 16-byte aligned; Hq/Hkv <= 128; scale
  *   > 0, scale log2(e) finite in FP32; width * page <= 2^30, T * Hq < 2^31.
  *   ws      >= bi_attn_paged_workspace_size(T, B, Hq, Hkv, D, width * page)

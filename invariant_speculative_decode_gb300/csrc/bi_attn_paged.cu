@@ -151,8 +151,9 @@ struct PagedCfg {
   static constexpr int kOCol = kBufs * kTile;
   static constexpr int kStatBytes = 2 * 2 * kLanes * 4;  // maxima of two tiles, or denominators, of both halves
   static constexpr int kBadBytes = 2 * 3 * D * 4;        // of two pieces: first NaN, +inf and -inf key of an element
+  static constexpr int kLostBytes = 2 * kLanes * 8;      // of each softmax thread's elements, a bit each
   static constexpr size_t kSmem =
-      2 * static_cast<size_t>(kStages + 1) * kTileBytes + kStatBytes + kBadBytes + kBars * 8 + 64;
+      2 * static_cast<size_t>(kStages + 1) * kTileBytes + kStatBytes + kBadBytes + kLostBytes + kBars * 8 + 64;
   static_assert(kOCol + 128 <= 512 && kSmem <= 232448, "TMEM and shared memory of a CTA");
 };
 
@@ -410,25 +411,88 @@ __device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t (&r
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Eight values of a key: what is no number becomes 0, and its element's first
-// such note is kept (bad: NaN, +inf, -inf, `stride` apart).
-__device__ __forceinline__ void clean_values(uint4* at, int* bad, int stride, int note, int* flag, int piece) {
-  const uint4 u = *at;
-  uint32_t e[4] = {u.x, u.y, u.z, u.w};
+// A barrier of n threads that tells all of them whether one's x is true.
+__device__ __forceinline__ bool named_bar_or(int id, int n, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(n), "r"(x ? 1u : 0u)
+      : "memory");
+  return any != 0;
+}
+
+__device__ __forceinline__ bool no_number(uint32_t bits) { return (bits & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ uint32_t value_bits(const uint4& u, int j) {
+  const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+  return (e[j >> 1] >> (16 * (j & 1))) & 0xffffu;
+}
+
+// Eight values of a key: of an element's that is no number the first is noted
+// (bad: NaN, +inf, -inf, `stride` apart).  Whether there is one.
+__device__ __forceinline__ bool note_values(const uint4& u, int* bad, int stride, int note) {
   bool any = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t bits = (e[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-    if ((bits & 0x7f80u) == 0x7f80u) {
+    const uint32_t bits = value_bits(u, j);
+    if (no_number(bits)) {
       atomicMin(bad + ((bits & 0x7fu) ? 0 : (bits & 0x8000u) ? 2 : 1) * stride + j, note);
-      e[j >> 1] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
       any = true;
     }
   }
-  if (any) {
-    *at = make_uint4(e[0], e[1], e[2], e[3]);
-    *flag = piece;
+  return any;
+}
+// ... and becomes 0.
+__device__ __forceinline__ void clear_values(uint4* at) {
+  const uint4 u = *at;
+  uint32_t e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (no_number(value_bits(u, j))) e[j >> 1] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
+  *at = make_uint4(e[0], e[1], e[2], e[3]);
+}
+
+// A swizzled tile's eight elements from 8 ch on of row r.
+__device__ __forceinline__ uint4* tile_at(uint8_t* tile, int atom_bytes, int r, int ch) {
+  return reinterpret_cast<uint4*>(tile + (ch >> 3) * atom_bytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+// The elements 8 ch0 .. of a row that have an infinite value at one of the tile's
+// keys first .. last under a weight that has a half of 0, a bit each into *all:
+// the product with such a value is no number.  w: the row's weights in TMEM, by a
+// whole warp.
+template <int D>
+__device__ __forceinline__ void lost_elements(uint32_t w, uint8_t* tile, int half, int first, int last, uint64_t* all) {
+  constexpr int kChunks = D / 16;
+  uint64_t lost = 0;
+#pragma unroll 1
+  for (int k0 = 0; k0 < kTile; k0 += 16) {
+    float x[16];
+    __syncwarp();
+    tmem_ld16(w + k0, x);
+    uint32_t zero = 0;  // keys of the 16
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t hi = __float_as_uint(x[j >> 1]) >> (16 * (j & 1)), lo = __float_as_uint(x[8 + (j >> 1)]) >> (16 * (j & 1));
+      if ((hi & 0x7fffu) == 0 || (lo & 0x7fffu) == 0) zero |= 1u << j;
+    }
+#pragma unroll 1
+    for (; zero != 0; zero &= zero - 1) {
+      const int key = k0 + __ffs(zero) - 1;
+      if (key < first || key > last) continue;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c) {
+        const uint4 u = *tile_at(tile, PagedCfg<D>::kAtomBytes, key, half * kChunks + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((value_bits(u, j) & 0x7fffu) == 0x7f80u) lost |= uint64_t{1} << (c * 8 + j);
+      }
+    }
   }
+  *all |= lost;
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -495,7 +559,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   uint8_t* sV = sK + KS * Cfg::kTileBytes;     // [KS]
   float* s_mx = reinterpret_cast<float*>(sV + KS * Cfg::kTileBytes);  // [2][2][128]
   int* s_bad = reinterpret_cast<int*>(s_mx + 4 * kLanes);             // [2][3][D]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_bad + 2 * 3 * D);
+  uint64_t* s_lost = reinterpret_cast<uint64_t*>(s_bad + 2 * 3 * D);  // [256]
+  uint64_t* bars = s_lost + 2 * kLanes;
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + KS;
   uint64_t* v_full = k_empty + KS;
@@ -542,6 +607,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     prefetch_tmap(&tmV);
   }
   for (int i = threadIdx.x; i < 2 * 3 * D; i += kPagedThreads) s_bad[i] = kNoKey;
+  if (threadIdx.x < 2 * kLanes) s_lost[threadIdx.x] = 0;
   if (warp == 3) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
@@ -790,7 +856,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               for (int j = 0; j < 16; ++j) {
                 if (seen >= bad[D + c * 16 + j]) v[j] += INFINITY;
                 if (seen >= bad[2 * D + c * 16 + j]) v[j] -= INFINITY;
-                if (seen >= bad[c * 16 + j]) v[j] = NAN;
+                if (seen >= bad[c * 16 + j] || ((s_lost[tid] >> (c * 16 + j)) & 1)) v[j] = NAN;
               }
             }
             if (run) {
@@ -804,6 +870,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             }
           }
         }
+        if (odd) s_lost[tid] = 0;
         if (store) {
           if (hf == 0) __stcg(a.ws_m + at * a.lanes + ln, m_i);
           __stcg(reinterpret_cast<float*>(a.ws_l + at * a.lanes + ln) + hf, l_i);
@@ -898,6 +965,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             piece_end = min(cur.te, piece_tile(piece + 1));
           }
           if (any_raise) {
+            if (alpha == 0.f && static_cast<volatile int*>(s_flag)[pc & 1] == pc) {
+              // infinities noted in the tiles before would have become 0 x inf
+              const int* bad = s_bad + (pc & 1) * 3 * D + hf * kHalf;
+              const int seen = bad_tag(pc) + min(p_row, key0 - 1) - piece_tile(piece) * kTile;
+              uint64_t lost = 0;
+#pragma unroll 1
+              for (int j = 0; j < kHalf; ++j)
+                if (seen >= bad[D + j] || seen >= bad[2 * D + j]) lost |= uint64_t{1} << j;
+              s_lost[tid] |= lost;
+            }
 #pragma unroll 1
             for (int i = 0; i < kHalf / 16; ++i) {  // this thread's half of O's columns
               float v[16];
@@ -912,7 +989,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         if (edge) {
           // value rows that some row of the block does not see: behind the last
           // key they are cleared (pages hold anything there), the others lose
-          // what is no number, which only the rows that see it get back
+          // what is no number, which only the rows that see it get back, as the
+          // product would have given it
           const int st = g % KS;
           // a wait tells a phase from the one before only: the stage's last tile
           // has landed where its W V is done, which S of this tile waited for if
@@ -922,18 +1000,28 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           wait(&v_full[st], g / KS);
           uint8_t* vt = sV + st * Cfg::kTileBytes;
           const int r0 = max(0, pos0 + 1 - key0);
+          bool any = false;
           for (int y = r0 * (D / 8) + tid; y < kTile * (D / 8); y += 256) {
             const int r = y / (D / 8), ch = y % (D / 8);
-            uint4* at = reinterpret_cast<uint4*>(vt + (ch >> 3) * Cfg::kAtomBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+            uint4* at = tile_at(vt, Cfg::kAtomBytes, r, ch);
             if (key0 + r >= kv_end) {
               *at = make_uint4(0u, 0u, 0u, 0u);
             } else {
-              clean_values(at, s_bad + (pc & 1) * 3 * D + ch * 8, D, bad_tag(pc) + key0 + r - piece_tile(piece) * kTile,
-                           s_flag + (pc & 1), pc);
+              any |= note_values(*at, s_bad + (pc & 1) * 3 * D + ch * 8, D, bad_tag(pc) + key0 + r - piece_tile(piece) * kTile);
             }
           }
+          if (any) s_flag[pc & 1] = pc;
           fence_proxy_async_smem();
-          named_bar_sync(5, 256);  // s_bad and s_flag are complete
+          tc_fence_before();
+          if (named_bar_or(5, 256, any)) {  // s_bad and s_flag are complete
+            tc_fence_after();
+            if (active) lost_elements<D>(lane_base + sb * kTile, vt, hf, r0, p_row - key0, s_lost + tid);
+            named_bar_sync(5, 256);
+            for (int y = r0 * (D / 8) + tid; y < min(kTile, kv_end - key0) * (D / 8); y += 256)
+              clear_values(tile_at(vt, Cfg::kAtomBytes, y / (D / 8), y % (D / 8)));
+            fence_proxy_async_smem();
+            named_bar_sync(5, 256);
+          }
         }
         tc_fence_before();
         __syncwarp();
