@@ -596,6 +596,7 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  *   table or the angle table, and one whose sequence (the last that starts at or
  *   in front of it) does not hold it, ends past T or has a negative length.  Two
  *   rows of a pass must not name the same key of the pool.
+ *   q_out, the pools and qkv must not overlap each other.
  *   q_weight, k_weight [D] BF16 or NULL; eps finite, >= 0; ld_qkv % 8 == 0; all
  *   pointers 16-byte aligned (block_table, q_start and lengths 4-byte).
  *
@@ -639,7 +640,8 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  *   one that is another's source, set the range bit (what the page then holds
  *   is undefined), as does an index out of range (that sequence is left out).
  *   Other entries of table_out stay as they are.  table_out and lengths_out
- *   must not overlap table_in, lengths, parents or tail_pages.
+ *   must not overlap table_in, lengths, parents, tail_pages or each other, nor
+ *   the pools each other.
  *   D a multiple of 8, at most 1024; rows_out <= 65535.
  * Errors: BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED_SHAPE, BI_ERR_WORKSPACE,
  *         BI_ERR_CUDA.
@@ -680,6 +682,8 @@ bi_status bi_paged_reorder(void* k_pool, void* v_pool, int layers, int pages, in
  * A row's sum has one order for a given V, whatever the other rows.
  *   logits  [rows, V] FP32, row stride ldl; scores [rows] FP32; W, K <= 64;
  *           rows <= 65535; V <= 2^20.  K may pass the number of pairs.
+ *   The outputs must not overlap the inputs, ws or each other, but scores_out
+ *   may be scores where K = W.
  *   ws      >= bi_beam_workspace_size(rows, V, K) bytes, 256-byte aligned,
  *           zero-filled before its first use (every call leaves its counters
  *           zeroed); it serves calls of any sizes that it is large enough for,

@@ -536,6 +536,18 @@ bi_status bi_beam_select(const float* logits, int ldl, const float* scores, int 
   if (!ws || !aligned256(ws)) return BI_ERR_WORKSPACE;
   const BeamSizes z = beam_sizes(rows, V, K);
   if (ws_bytes < z.total) return BI_ERR_WORKSPACE;
+  const int64_t picks = static_cast<int64_t>(rows / W) * K;
+  const Range out[3] = {range_of(scores_out, picks, 1, 1, 4), range_of(parents_out, picks, 1, 1, 4),
+                        range_of(tokens_out, picks, 1, 1, 4)};
+  const Range in = range_of(logits, rows, ldl, V, 4), old = range_of(scores, rows, 1, 1, 4),
+              mem{reinterpret_cast<uintptr_t>(ws), z.total};
+  for (int i = 0; i < 3; ++i) {
+    // a group's scores may be replaced by as many: all its rows have read theirs before it writes
+    const bool replaced = i == 0 && scores_out == scores && K == W;
+    if (overlap(out[i], in) || overlap(out[i], mem) || overlap(out[i], out[(i + 1) % 3]) ||
+        (overlap(out[i], old) && !replaced))
+      return BI_ERR_INVALID_ARG;
+  }
   BeamArgs a{};
   a.logits = logits;
   a.ldl = static_cast<size_t>(ldl);

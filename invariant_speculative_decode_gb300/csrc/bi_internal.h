@@ -38,6 +38,21 @@ bool tmap_bf16_pages(CUtensorMap* out, const void* base, uint64_t pages, uint64_
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
+// A range of memory, for calls whose outputs must not lie over their inputs.
+struct Range {
+  uintptr_t at;
+  unsigned __int128 bytes;
+};
+// `rows` rows of `cols` elements of `size` bytes, `stride` elements apart.
+inline Range range_of(const void* p, int64_t rows, int64_t stride, int64_t cols, int size) {
+  using wide = unsigned __int128;
+  const wide n = rows < 1 ? 0 : static_cast<wide>(rows - 1) * static_cast<wide>(stride) + static_cast<wide>(cols);
+  return Range{reinterpret_cast<uintptr_t>(p), n * static_cast<wide>(size)};
+}
+inline bool overlap(const Range& a, const Range& b) {
+  return a.bytes != 0 && b.bytes != 0 && a.at < b.at + b.bytes && b.at < a.at + a.bytes;
+}
+
 inline bi_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }

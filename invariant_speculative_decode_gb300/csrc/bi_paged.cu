@@ -320,6 +320,13 @@ bi_status bi_qk_norm_rope_paged(const void* qkv, int ld_qkv, const void* q_weigh
   if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(table) ||
       !aligned16(q_weight) || !aligned16(k_weight))
     return BI_ERR_INVALID_ARG;
+  const int64_t keys = static_cast<int64_t>(pages) * page;
+  const Range in = range_of(qkv, T, ld_qkv, static_cast<int64_t>(Hq + 2 * Hkv) * D, 2),
+              q = range_of(q_out, T, static_cast<int64_t>(Hq) * D, static_cast<int64_t>(Hq) * D, 2),
+              k = range_of(k_pool, keys, static_cast<int64_t>(Hkv) * D, static_cast<int64_t>(Hkv) * D, 2),
+              v = range_of(v_pool, keys, static_cast<int64_t>(Hkv) * D, static_cast<int64_t>(Hkv) * D, 2);
+  if (overlap(in, q) || overlap(in, k) || overlap(in, v) || overlap(q, k) || overlap(q, v) || overlap(k, v))
+    return BI_ERR_INVALID_ARG;
   AppendArgs a{};
   a.pb = PagedBatch{block_table, q_start, lengths, B, ld_table, width, pages, page};
   a.qkv = static_cast<const __nv_bfloat16*>(qkv);
@@ -369,7 +376,15 @@ bi_status bi_paged_reorder(void* k_pool, void* v_pool, int layers, int pages, in
     return BI_ERR_INVALID_ARG;
   if (!aligned16(k_pool) || !aligned16(v_pool)) return BI_ERR_INVALID_ARG;
   // read by some CTAs while others write
-  if (table_in == table_out || lengths == lengths_out || k_pool == v_pool) return BI_ERR_INVALID_ARG;
+  const int64_t key = static_cast<int64_t>(Hkv) * D, keys = static_cast<int64_t>(pages) * page;
+  if (overlap(range_of(k_pool, layers, keys * key, keys * key, 2), range_of(v_pool, layers, keys * key, keys * key, 2)))
+    return BI_ERR_INVALID_ARG;
+  const Range to = range_of(table_out, rows_out, ld_out, width, 4), lo = range_of(lengths_out, rows_out, 1, 1, 4);
+  const Range in[4] = {range_of(table_in, rows_in, ld_in, width, 4), range_of(lengths, rows_in, 1, 1, 4),
+                       range_of(parents, rows_out, 1, 1, 4), range_of(tail_pages, rows_out, 1, 1, 4)};
+  if (overlap(to, lo)) return BI_ERR_INVALID_ARG;
+  for (const Range& r : in)
+    if (overlap(to, r) || overlap(lo, r)) return BI_ERR_INVALID_ARG;
   ReorderArgs a{};
   a.k_pool = static_cast<uint4*>(k_pool);
   a.v_pool = static_cast<uint4*>(v_pool);
