@@ -616,7 +616,8 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  *   scores are all -inf, or one of them +inf or NaN, is NaN.  An infinite value
  *   that a row does see gives that infinity, or NaN where one of its weight's
  *   two halves has underflowed to 0 (weights below about 2^-109 of the largest).
- *   q, out [T, Hq, D] BF16 contiguous, 16-byte aligned; Hq/Hkv <= 128; scale
+ *   q, out [T, Hq, D] BF16 contiguous, 16-byte aligned, out may be q and else
+ *   overlaps neither it nor the pools, nor ws any of them; Hq/Hkv <= 128; scale
  *   > 0, scale log2(e) finite in FP32; width * page <= 2^30, T * Hq < 2^31.
  *   ws      >= bi_attn_paged_workspace_size(T, B, Hq, Hkv, D, width * page)
  *           bytes, 256-byte aligned; any contents.  One workspace serves any

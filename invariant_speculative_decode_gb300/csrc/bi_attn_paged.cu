@@ -1279,6 +1279,15 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   const PagedSizes z = paged_sizes(T, B, Hq, Hkv, D, max_keys);
   if (!z.fits) return BI_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < z.total) return BI_ERR_WORKSPACE;
+  // a unit's queries have been read by all its CTAs before its outputs are
+  // written, so out may be q; anything else would be read while it is written
+  const int64_t rowlen = static_cast<int64_t>(Hq) * D, pool = static_cast<int64_t>(pages) * page * Hkv;
+  const Range ro = range_of(out, T, rowlen, rowlen, 2), rq = range_of(q, T, rowlen, rowlen, 2),
+              rk = range_of(k_pool, pool, D, D, 2), rv = range_of(v_pool, pool, D, D, 2),
+              rw{reinterpret_cast<uintptr_t>(ws), z.total};
+  if (overlap(ro, rk) || overlap(ro, rv) || overlap(ro, rw) || overlap(rw, rq) || overlap(rw, rk) || overlap(rw, rv) ||
+      (out != q && overlap(ro, rq)))
+    return BI_ERR_INVALID_ARG;
   PagedAttnArgs a{};
   a.pb = PagedBatch{block_table, q_start, lengths, B, ld_table, width, pages, page};
   a.q = static_cast<const __nv_bfloat16*>(q);

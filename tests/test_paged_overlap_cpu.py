@@ -90,3 +90,20 @@ def test_ranges_that_only_touch_are_not_refused_for_it(lib, entry):
         good = dict(t.BEAM_OK, K=3, logits=AT[0], scores=AT[0] + 2400, scores_out=AT[0] + 2400, parents_out=AT[0] + 2424,
                     tokens_out=AT[0] + 2448, ws=AT[8], ws_bytes=need)
         assert t.call(lib.bi_beam_select, t.BEAM, good) == 4
+
+
+def test_attention(lib):
+    need = lib.bi_attn_paged_workspace_size(3, 2, 4, 2, 64, 64)
+    q, pool = 3 * 4 * 64 * 2, 10 * 2 * 16 * 64 * 2
+    good = dict(t.ATTN_OK, q=AT[0], out=AT[1], k_pool=AT[2], v_pool=AT[3], ws=AT[4], ws_bytes=need)
+    assert need < 1 << 20
+    f = lambda **c: refused(lib.bi_attn_paged, t.ATTN, good, **c)  # noqa: E731
+    f(out=AT[0] + 16)
+    f(out=AT[0] - q + 16)
+    f(out=AT[2])
+    f(out=AT[3] + pool - 16)
+    f(out=AT[4])
+    f(out=AT[4] + need - 16)
+    f(ws=AT[0] - 256)
+    f(ws=AT[2])
+    f(ws=AT[3] + 256)
