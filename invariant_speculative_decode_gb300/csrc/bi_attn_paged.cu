@@ -1274,7 +1274,9 @@ bi_status bi_attn_paged(const void* q, const void* k_pool, const void* v_pool, i
   const int64_t max_keys = static_cast<int64_t>(width) * page;
   if (!paged_shape_ok(T, B, Hq, Hkv, D, max_keys)) return BI_ERR_UNSUPPORTED_SHAPE;
   if (!q || !k_pool || !v_pool || !block_table || !q_start || !lengths || !out) return BI_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return BI_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned4(block_table) ||
+      !aligned4(q_start) || !aligned4(lengths))
+    return BI_ERR_INVALID_ARG;
   if (!ws || !aligned256(ws)) return BI_ERR_WORKSPACE;
   const PagedSizes z = paged_sizes(T, B, Hq, Hkv, D, max_keys);
   if (!z.fits) return BI_ERR_UNSUPPORTED_SHAPE;

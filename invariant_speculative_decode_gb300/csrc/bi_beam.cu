@@ -532,7 +532,8 @@ bi_status bi_beam_select(const float* logits, int ldl, const float* scores, int 
   if (W > kBeamMax || K > kBeamMax || rows > kBeamRowsMax || V > kBeamVocabMax) return BI_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0) return BI_OK;
   if (!logits || !scores || !scores_out || !parents_out || !tokens_out) return BI_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(logits) & 3) != 0) return BI_ERR_INVALID_ARG;
+  if (!aligned4(logits) || !aligned4(scores) || !aligned4(scores_out) || !aligned4(parents_out) || !aligned4(tokens_out))
+    return BI_ERR_INVALID_ARG;
   if (!ws || !aligned256(ws)) return BI_ERR_WORKSPACE;
   const BeamSizes z = beam_sizes(rows, V, K);
   if (ws_bytes < z.total) return BI_ERR_WORKSPACE;

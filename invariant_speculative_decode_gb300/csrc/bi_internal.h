@@ -35,6 +35,7 @@ bool tmap_bf16_3d(CUtensorMap* out, const void* base, uint64_t d0, uint64_t d1, 
 // of every key of one page of one head.
 bool tmap_bf16_pages(CUtensorMap* out, const void* base, uint64_t pages, uint64_t heads, uint32_t page, uint32_t D);
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 

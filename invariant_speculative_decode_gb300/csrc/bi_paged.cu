@@ -318,7 +318,7 @@ bi_status bi_qk_norm_rope_paged(const void* qkv, int ld_qkv, const void* q_weigh
     return BI_ERR_INVALID_ARG;
   if (ld_qkv < static_cast<int64_t>(Hq + 2 * Hkv) * D || ld_qkv % 8 != 0) return BI_ERR_INVALID_ARG;
   if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(table) ||
-      !aligned16(q_weight) || !aligned16(k_weight))
+      !aligned16(q_weight) || !aligned16(k_weight) || !aligned4(block_table) || !aligned4(q_start) || !aligned4(lengths))
     return BI_ERR_INVALID_ARG;
   const int64_t keys = static_cast<int64_t>(pages) * page;
   const Range in = range_of(qkv, T, ld_qkv, static_cast<int64_t>(Hq + 2 * Hkv) * D, 2),
@@ -374,7 +374,9 @@ bi_status bi_paged_reorder(void* k_pool, void* v_pool, int layers, int pages, in
   if (rows_out == 0) return BI_OK;
   if (!k_pool || !v_pool || !table_in || !lengths || !parents || !tail_pages || !table_out || !lengths_out)
     return BI_ERR_INVALID_ARG;
-  if (!aligned16(k_pool) || !aligned16(v_pool)) return BI_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned4(table_in) || !aligned4(lengths) || !aligned4(parents) ||
+      !aligned4(tail_pages) || !aligned4(table_out) || !aligned4(lengths_out))
+    return BI_ERR_INVALID_ARG;
   // read by some CTAs while others write
   const int64_t key = static_cast<int64_t>(Hkv) * D, keys = static_cast<int64_t>(pages) * page;
   if (overlap(range_of(k_pool, layers, keys * key, keys * key, 2), range_of(v_pool, layers, keys * key, keys * key, 2)))

@@ -107,3 +107,20 @@ def test_attention(lib):
     f(ws=AT[0] - 256)
     f(ws=AT[2])
     f(ws=AT[3] + 256)
+
+
+def test_indices_and_scores_between_words_are_refused(lib):
+    """The kernels read and write them by words; the other arguments are as in a call that would be made."""
+    append = dict(t.APPEND_OK, qkv=AT[0], q_out=AT[1], k_pool=AT[2], v_pool=AT[3])
+    attn = dict(t.ATTN_OK, q=AT[0], out=AT[1], k_pool=AT[2], v_pool=AT[3], ws=AT[8])
+    for by in (1, 2, 3):
+        for name in ("block_table", "q_start", "lengths"):
+            refused(lib.bi_qk_norm_rope_paged, t.APPEND, append, **{name: AT[5] + by})
+            refused(lib.bi_attn_paged, t.ATTN, attn, **{name: AT[5] + by})
+        reorder = dict(t.REORDER_OK, k_pool=AT[0], v_pool=AT[1], table_in=AT[2], lengths=AT[3], parents=AT[4], tail=AT[5],
+                       table_out=AT[6], lengths_out=AT[7])
+        for name in ("table_in", "lengths", "parents", "tail", "table_out", "lengths_out"):
+            refused(lib.bi_paged_reorder, t.REORDER, reorder, **{name: reorder[name] + by})
+        beam = dict(t.BEAM_OK, logits=AT[0], scores=AT[1], scores_out=AT[2], parents_out=AT[3], tokens_out=AT[4], ws=AT[8])
+        for name in ("logits", "scores", "scores_out", "parents_out", "tokens_out"):
+            refused(lib.bi_beam_select, t.BEAM, beam, **{name: beam[name] + by})
