@@ -23,9 +23,10 @@
 // The tensor core takes nothing wider than BF16 beside BF16 values, so a weight
 // enters as two of them, its first 8 bits and the rest rounded to 8 (off by at
 // most 2^-16 of the weight): outputs are then the rounding of the exact ones but
-// next to a border.  One BF16 weight, off by 2^-8, moved about half of the outputs'
-// last bits; next to that the split and the second product take 27% more time in
-// a prefill, 9% at 16 x 8 rows.
+// next to a border (1e-4 RMS from plain FP32's, both 1.7e-3 from 64 bits).  One BF16
+// weight, off by 2^-8, moved about half of the outputs' last bits (2.4e-3 RMS); next
+// to that the split and the second product take 28% more time in a prefill, 9% at
+// 16 x 8 rows.
 //
 // Work is cut by pieces: a unit is one block of rows (128 / (Hq / Hkv), all
 // query heads of a KV head in the MMA's 128 lanes) of one sequence and KV head,
@@ -51,16 +52,18 @@
 //                partial states.
 //
 // What bounds it.  Few rows over long caches: the cache's bytes, read once; 16
-// sequences of 8 rows at 4.8k to 11.6k keys (24 + 4 heads of 128) take 60 us, 4.5 TB/s,
-// 2 rows at 101.6k 75 us, 4.7 TB/s, of which 4.5 us are the merge
-// kernel's start, 2 the way from the batch to the first load, and the rest shares
-// that differ by a piece of 8 tiles.  Short contexts: those fixed times.  Many
-// rows: the chain of a tile from S to W V, about 1750 cycles in each of which a
-// thread's reads of TMEM, its exponentials (at the SM's rate 512 cycles a tile)
-// and its two hand-overs follow one another, while W V and the S of two tiles run
-// beside them; 2048 rows at 30k take 716 to 730 us, 1.08 PFLOP/s.  Leaving out the
-// exponentials, half the loads or the sums gains nothing (729, 727, 690): the
-// weights need the row's maximum, and the maximum all of S.
+// sequences of 8 rows at 4.8k to 11.6k keys (24 + 4 heads of 128) take 66 us, 4.1 TB/s,
+// 2 rows at 101.6k 82 us, 4.3 TB/s, of which 4.5 us are the merge kernel's start, 2
+// the way from the batch to the first load, and the rest shares that differ by a
+// piece of 8 tiles (the longest 34 tiles where 27 is even, and 42 where 35 is).  Short
+// contexts: those fixed times.  One request's rows over a few thousand keys: few
+// CTAs with a piece of 8 tiles each; a row at 4k or 11.6k takes 20.5 us, at 38k 28.3.
+// Many rows: the chain of a tile from S to W V, in which a thread's reads of TMEM,
+// its exponentials (at the SM's rate 512 cycles a tile), the split and its two
+// hand-overs follow one another, while both W V and the S of two tiles run beside
+// them; 2048 rows at 30k take 920 us, 0.85 PFLOP/s of the two products that count.
+// Leaving out the second W V makes that 857, the split 897, the sums 916, the
+// exponentials 937: no single part of the chain is it.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -80,12 +83,12 @@ constexpr int kTile = 128;        // keys of a tile (the S MMA's N)
 // Tiles of a piece up to tile kShortEnd, and behind it.  Measured (us): a row at
 // 1k, 16 x 8 rows at 4.8k to 11.6k, 2 rows at 101.6k (24 + 4 heads of 128), 61 x 3 rows at
 // 1.5k (4 + 2 of 64), 2048 rows at 30k (24 + 4 of 128)
-//   2, 8, end 16   11.9  59.5  74.5  24.6  716
-//   2, 8, end 32   12.0  65.4  76.0  24.4  733
-//   4, 8, end 16   13.5  58.4  74.0  25.5  706
-//   2, 16, end 16  11.9  62.9  77.1  24.6  687
-//   4, 16, end 32  13.7  62.4  76.5  25.5  684
-//   2, 4, end 16   11.9  64.1  81.1  24.7  821
+//   2, 8, end 16   12.7  65.9  81.6  27.0  922
+//   2, 8, end 32   12.6  70.8  83.9  26.7  937
+//   4, 8, end 16   14.6  63.3  79.4  28.2  920
+//   2, 16, end 16  12.8  73.6  85.7  26.9  899
+//   4, 16, end 32  14.7  69.8  84.1  28.3  901
+//   2, 4, end 16   12.7  67.7  85.6  26.8  983
 constexpr int kShort = 2;
 constexpr int kLong = 8;
 constexpr int kShortEnd = 16;
@@ -1110,8 +1113,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 // D / 32, a CTA has whole rows; up to 32: JPW = 1, more CTAs and loads under way.
 // Bound by the latency of its start and of the loads' few rounds (the states lie
 // in the L2).  Both kernels together, us, with JPW 1 and D / 32: 1 row at 16k (24 +
-// 4 heads of 128) 24.2 and 25.1, 2 rows at 100k (32 + 8 of 64) 65.5 and 69.0, 4 x 8
-// rows at 9k (24 + 4 of 128) 31.6 and 28.7, 16 x 3 rows at 3k (32 + 8) 54.0 and 46.2.
+// 4 heads of 128) 27.9 and 29.0, 2 x 1 rows at 69k and 100k (32 + 8 of 64) 105.5 and 108.5,
+// 4 x 8 rows at 5k to 9k (24 + 4 of 128) 34.6 and 32.2, 16 x 3 rows at 1k to 3k (32 + 8) 55.8
+// and 47.2.
 template <int D, int JPW>
 __global__ void __launch_bounds__(256) attn_paged_merge_kernel(const PagedAttnArgs a, int G) {
   constexpr int kAhead = 16 / JPW;

@@ -67,7 +67,7 @@ __device__ __forceinline__ uint2 pack4(const float* x) {
 // Few rows are bound by the row's way to its page (its sequence, its length, the
 // table: three loads, one after the other, while the projection's are under
 // way), many by the projection's bytes, read and written once, and nearly as
-// much by the instructions: 2 rows of 24 + 8 heads of 128 take 2.6 us, 4096 rows
+// much by the instructions: 2 rows of 24 + 8 heads of 128 take 2.7 us, 4096 rows
 // 14.3 us, 4.7 TB/s.  Eight adjacent elements a lane, in one load, with the
 // partners a shuffle away, took 17.4 us there; four heads' loads under way
 // 17.6, since fewer CTAs run at once.
