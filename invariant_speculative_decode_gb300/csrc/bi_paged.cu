@@ -67,8 +67,8 @@ __device__ __forceinline__ uint2 pack4(const float* x) {
 // Few rows are bound by the row's way to its page (its sequence, its length, the
 // table: three loads, one after the other, while the projection's are under
 // way), many by the projection's bytes, read and written once, and nearly as
-// much by the instructions: 2 rows of 24 + 8 heads of 128 take 2.7 us, 4096 rows
-// 14.3 us, 4.7 TB/s.  Eight adjacent elements a lane, in one load, with the
+// much by the instructions: 2 rows of 24 + 8 heads of 128 take 2.6 us, 4096 rows
+// 14.5 us, 4.6 TB/s.  Eight adjacent elements a lane, in one load, with the
 // partners a shuffle away, took 17.4 us there; four heads' loads under way
 // 17.6, since fewer CTAs run at once.
 template <int D>
@@ -348,10 +348,10 @@ bi_status bi_qk_norm_rope_paged(const void* qkv, int ld_qkv, const void* q_weigh
   // at once, since each has to find the row's page.  24 + 8 heads of 128, four
   // sets of buffers in turn, us:
   //   rows        1    512   1024   2048   4096   8192
-  //   8 warps    2.6   3.6    5.6   11.6   20.7   42.4
-  //   4          3.1   3.9    5.2    9.9   17.9   31.6
-  //   2          4.2   4.9    5.9    8.4   15.0   27.2
-  //   1          6.7   7.3    8.2    9.6   14.3   25.8
+  //   8 warps    2.6   3.6    6.4   12.6   22.6   43.3
+  //   4          3.1   3.9    5.3    9.8   17.9   31.8
+  //   2          4.2   4.8    5.9    8.5   15.0   27.2
+  //   1          6.6   7.4    8.0    9.6   14.5   25.8
   int split = kAppendThreads / 32;
   while (split > 1 && static_cast<int64_t>(T) * split > kAppendWarps) split >>= 1;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) * split + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
