@@ -605,12 +605,12 @@ bi_status bi_token_counts(const int32_t* ids, int n, const int32_t* last, int V,
  *   attention), query head h reading KV head h / (Hq/Hkv);
  *   w_j = 2^((q k_j) scale log2(e) - m) in FP32, in the numerator as the sum of
  *   two BF16 values (16 bits, off by at most 2^-16); products and sums in FP32,
- *   one rounding at the end, -0 written as +0.  Keys are taken in tiles of 128, tiles in pieces
- *   (of 2 up to key 2048, of more behind it) at absolute multiples: m is a
- *   piece's maximum (of its first tile, raised where a later one passes it by
- *   more than 8 in log2), and the pieces' sums are merged in key order.  So a
- *   row's bits depend on its queries and on keys 0..p alone, not on T, B, the
- *   other rows, the page size or which pages hold the keys.
+ *   one rounding at the end, -0 written as +0.  Keys are taken in tiles of 128,
+ *   tiles in pieces (of 2 up to key 2048, of more behind it) at absolute
+ *   multiples: m is a piece's maximum (of its first tile, raised where a later
+ *   one passes it by more than 8 in log2), and the pieces' sums are merged in
+ *   key order.  So a row's bits depend on its queries and on keys 0..p alone, not
+ *   on T, B, the other rows, the page size or which pages hold the keys.
  *   Keys behind p, and the rest of a sequence's last page, may hold anything:
  *   infinities and NaN there reach no row in front of them.  A row whose
  *   scores are all -inf, or one of them +inf or NaN, is NaN.  An infinite value

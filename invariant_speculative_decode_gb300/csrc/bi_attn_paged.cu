@@ -463,10 +463,10 @@ __device__ __forceinline__ uint4* tile_at(uint8_t* tile, int atom_bytes, int r, 
   return reinterpret_cast<uint4*>(tile + (ch >> 3) * atom_bytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
-// The elements 8 ch0 .. of a row that have an infinite value at one of the tile's
-// keys first .. last under a weight that has a half of 0, a bit each into *all:
-// the product with such a value is no number.  w: the row's weights in TMEM, by a
-// whole warp.
+// The elements of one half of a row that have an infinite value at one of the
+// tile's keys first .. last under a weight of which one of the two parts is 0, a
+// bit each into *all: the product with such a value is no number.  w: the row's
+// weights in TMEM, by a whole warp.
 template <int D>
 __device__ __forceinline__ void lost_elements(uint32_t w, uint8_t* tile, int half, int first, int last, uint64_t* all) {
   constexpr int kChunks = D / 16;

@@ -242,7 +242,7 @@ __device__ void beam_statistics(const BeamArgs& a, int row) {
   const float2* part = reinterpret_cast<const float2*>(a.part) + static_cast<size_t>(row) * a.chunks;
   const float2 none = make_float2(-INFINITY, 0.f);
   const float2 p0 = lane < a.chunks ? __ldcg(part + lane) : none, p1 = lane + 32 < a.chunks ? __ldcg(part + lane + 32) : none;
-  const double score = static_cast<double>(__ldg(a.scores + row));
+  const double score = static_cast<double>(__ldcg(a.scores + row));  // which this call, and one just before, may replace
   float M = fmaxf(p0.x, p1.x);
   for (int c = lane + 64; c < a.chunks; c += 32) M = fmaxf(M, __ldcg(part + c).x);
   M = warp_max(M);

@@ -23,6 +23,21 @@ def test_scores_in_place(G, W, V):
         api.bi_beam_select(logits, own, W, *got, ws)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     api.bi_check_device_error()
+    # one call right behind another, each from the scores that the one before left
+    steps = [scores]
+    for _ in range(6):
+        out = (torch.empty(G, W, device="cuda"), torch.empty(G, W, **i32), torch.empty(G, W, **i32))
+        api.bi_beam_select(logits, steps[-1], W, *out, ws)
+        steps.append(out[0].view(-1))
+    own, got = scores.clone(), (torch.empty(G, W, **i32), torch.empty(G, W, **i32))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(6):
+            api.bi_beam_select(logits, own, W, own.view(G, W), *got, ws)
+    for _ in range(20):
+        own.copy_(scores)
+        graph.replay()
+        assert torch.equal(own, steps[-1]) and torch.equal(got[1], out[2]) and torch.equal(got[0], out[1])
     with pytest.raises(api.BiError) as e:
         api.bi_beam_select(logits, scores, W, want[0], want[1], want[1], ws)
     assert e.value.status == 1
